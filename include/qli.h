@@ -294,6 +294,136 @@ qli_status qli_gather_kv(const qli_problem* p, const int32_t* seq_lens_q, const 
                          int64_t entry_bytes, int64_t kv_stride, void* out, int32_t* counts, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/*
+ * The attention side: what makes a layer's queries and keys, the KV cache in 4 bits, and the
+ * attention over the entries that the indexer selected.  The README ends at the indices ("the
+ * output is the attention's input"); these calls take the step before and the step after.  They
+ * share the indexer's problem (batch, rows, page geometry, block_table, compressed positions).
+ */
+typedef enum { QLI_ACT_BF16 = 0, QLI_ACT_F16 = 1 } qli_act_dtype;  /* bfloat16, float16 activations */
+typedef enum { QLI_KV_INT4 = 0, QLI_KV_E2M1 = 1 } qli_kv_dtype;    /* 4-bit codes of the KV cache */
+
+/* Attributes of qli_norm_rope. */
+typedef struct {
+    int32_t num_heads_q;        /* query heads per token, in [0, 1024] */
+    int32_t num_heads_k;        /* key heads per token, in [0, 1024] */
+    int32_t head_dim;           /* D: 64, 128 or 256 */
+    int32_t rotary_dim;         /* R: leading elements of a head that are rotated, a multiple of 8 in [0, D] */
+    int32_t max_positions;      /* rows of cos_sin */
+    int32_t dtype;              /* qli_act_dtype of activations and weights */
+    int32_t interleaved;        /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+    int32_t norm;               /* 1: root-mean-square norm of each head first; 0: rotation only */
+    float eps;                  /* added to the mean square, finite and >= 0 */
+} qli_rotation;
+
+/* Fill `r` with 64 + 8 heads of 128, all rotated, bfloat16, norm on, eps 1e-6, 4096 positions. */
+void qli_rotation_init(qli_rotation* r);
+
+/* Check `r` on the host: QLI_OK or QLI_ERR_INVALID_ARG; `why` (may be NULL) as in qli_validate. */
+qli_status qli_rotation_validate(const qli_rotation* r, const char** why);
+
+/*
+ * Norm of each query and key head and the position rotation, in one pass.  For every token t and
+ * head vector x (D elements):
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight                       (norm = 1; else y = x)
+ *     (y_a, y_b) <- (y_a c_i - y_b s_i, y_b c_i + y_a s_i),  i < R/2, (a, b) the i-th pair
+ *     c_i = cos_sin[positions[t]][i],  s_i = cos_sin[positions[t]][R/2 + i]
+ *
+ * in fp32, rounded once at the end; elements from R on are not rotated.  `q` [tokens, num_heads_q,
+ * D] and `k` [tokens, num_heads_k, D] with `q_stride` / `k_stride` elements between tokens (0 =
+ * contiguous, else a multiple of 8 of at least the heads' size), so that both may be views of one
+ * packed projection; q_out / k_out likewise.  An output may be its own input (same address and
+ * stride).  q_weight, k_weight [D] of the activations' type (unused, may be NULL, when norm = 0);
+ * positions int32 [tokens]; cos_sin float32 [max_positions, R], cosines first (may be NULL when
+ * R = 0).  16-byte aligned arrays; a side with no heads may have NULL pointers.  A position outside
+ * [0, max_positions) writes zeros for that token and sets error bit 1 in `workspace`'s device error
+ * word when `workspace` is given.  One kernel on `stream`; tokens = 0 enqueues nothing.
+ */
+qli_status qli_norm_rope(const qli_rotation* r, int64_t tokens, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* q_weight, const void* k_weight, const int32_t* positions,
+                         const float* cos_sin, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attributes of the KV cache and of the attention that reads it. */
+typedef struct {
+    int32_t num_heads_q;        /* query heads: num_heads_kv times the group size, at most 256 */
+    int32_t num_heads_kv;       /* KV heads, in [1, 64]; query head h reads KV head h / group size */
+    int32_t head_dim;           /* D of queries, keys and values: 64 or 128 */
+    int32_t dtype;              /* qli_act_dtype of query, keys, values and output */
+    int32_t kv_dtype;           /* qli_kv_dtype of the cache */
+    float softmax_scale;        /* factor of the logits, finite and >= 0; 0 = 1 / sqrt(D) */
+    float k_scale, v_scale;     /* factors of the cached keys / values, finite and > 0 (a calibration
+                                   constant that keeps a block's largest magnitude well inside the
+                                   scales' range 2^-6 ... 448 times 6 or 7; 1 if in doubt) */
+    int64_t kv_stride;          /* bytes between pages: 0 = block_size * entry bytes, else a multiple
+                                   of 16 of at least that */
+} qli_attention;
+
+/* Fill `a` with 64 query heads over 8 KV heads of 128, bfloat16, E2M1, factors 1, contiguous pages. */
+void qli_attention_init(qli_attention* a);
+
+/* Check `a` on the host: QLI_OK or QLI_ERR_INVALID_ARG; `why` (may be NULL) as in qli_validate. */
+qli_status qli_attention_validate(const qli_attention* a, const char** why);
+
+/* Bytes of one cache entry (all heads of one position), a multiple of 16; 0 if `a` is invalid. */
+size_t qli_kv_entry_bytes(const qli_attention* a);
+
+/*
+ * The paged KV cache in 4 bits.  `kv` is num_blocks pages of block_size entries (pages kv_stride
+ * bytes apart), 16-byte aligned and addressed by the same block_table as the key pool.  An entry
+ * holds, for each KV head in order,
+ *
+ *     K codes [D/2 bytes]  V codes [D/2]  K scales [D/16]  V scales [D/16]
+ *
+ * and is padded to a multiple of 16 bytes; element 2i of a vector is the low nibble of code byte i.
+ * Every 16 elements share one scale in float8_e4m3fn.  With y = x / k_scale (v_scale) in fp32 and
+ * Q = 7 (INT4, two's complement) or 6 (E2M1: a sign bit and the magnitudes 0 .5 1 1.5 2 3 4 6):
+ *
+ *     s = e4m3(min(max |y| / Q, 448)),   code = y / s  (fp32 division) rounded to nearest and
+ *     saturated to +-Q; both roundings to ties-to-even; s = 0 gives zero codes
+ *
+ * so x ~= k_scale * s * code.  Non-finite inputs are outside the definition.
+ *
+ * qli_kv_write: token t's keys `k[t]` and values `v[t]` ([num_heads_kv, D] each, k_stride /
+ * v_stride elements between tokens: 0 = contiguous, else a multiple of 8 of at least the heads'
+ * size; 16-byte aligned) go to compressed position token_pos[t] of batch token_batch[t].  Nothing
+ * else of the pool changes (an entry's padding included).  Positions, batches, pages and errors as
+ * in qli_quantize_keys.  One kernel on `stream`; tokens = 0 enqueues nothing.
+ *
+ * qli_kv_read: the reverse; k[t], v[t] receive k_scale * s * code, rounded once to the activations'
+ * type.  A token with an invalid batch, position or page gets zeros and sets the same error bits.
+ */
+qli_status qli_kv_write(const qli_problem* p, const qli_attention* a, int64_t tokens, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const int32_t* token_batch, const int32_t* token_pos,
+                        const int32_t* block_table, void* kv, void* workspace, size_t workspace_bytes, void* stream);
+qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tokens, const int32_t* token_batch,
+                       const int32_t* token_pos, const int32_t* block_table, const void* kv, void* k,
+                       int64_t k_stride, void* v, int64_t v_stride, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Attention over the selected entries.  For row r (batch b as in qli_gather_kv), query head h and
+ * its KV head g, over the entries i < sparse_count whose index j = sparse_indices[r][i] is valid,
+ * K_i and V_i the cached vectors of position j of batch b:
+ *
+ *     z_i = softmax_scale * (query[r][h] . K_i),   out[r][h] = sum_i softmax(z)_i V_i,
+ *     lse[r][h] = ln sum_i exp(z_i)
+ *
+ * An index listed twice counts twice.  A row without a valid index gets zeros and lse = -infinity.
+ * Validity and errors as in qli_gather_kv: -1 is skipped silently, any other index out of range (or
+ * in a row that belongs to no batch) is skipped with error bit 1, a page outside the pool with bit
+ * 2.  `query` [rows, num_heads_q, D] with q_stride elements between rows (0 = contiguous, else a
+ * multiple of 8 of at least num_heads_q * D); `out` [rows, num_heads_q, D] contiguous; `lse`
+ * (optional) float32 [rows, num_heads_q].  query, kv and out 16-byte aligned.  Logits, softmax
+ * statistics and accumulators are fp32.  Enqueued on `stream`; the result does not depend on
+ * scheduling.
+ */
+qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, const void* query, int64_t q_stride,
+                                const int32_t* seq_lens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                                const int32_t* sparse_indices, const void* kv, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Zero the workspace's device error word (enqueued on `stream`).  Call once after allocating a
  * workspace, before its first qli_score_topk. */
 qli_status qli_workspace_init(void* workspace, size_t workspace_bytes, void* stream);

@@ -26,6 +26,8 @@ INT8, FP8_E4M3 = 0, 1
 F16, F32 = 0, 1
 BSND, TND = 0, 1
 SPLIT_AUTO, SPLIT_ON, SPLIT_OFF = 0, 1, 2       # qli_split_topk
+ACT_BF16, ACT_F16 = 0, 1                        # qli_act_dtype
+KV_INT4, KV_E2M1 = 0, 1                         # qli_kv_dtype
 INT64_MAX = (1 << 63) - 1
 
 # symbols include/qli.h declares
@@ -34,6 +36,9 @@ EXPORTS = ("qli_problem_init", "qli_validate", "qli_metadata_words", "qli_worksp
            "qli_workspace_init", "qli_get_device_error",
            "qli_plan_create", "qli_plan_launch", "qli_plan_destroy",
            "qli_quantize", "qli_quantize_keys", "qli_gather_kv",
+           "qli_rotation_init", "qli_rotation_validate", "qli_norm_rope",
+           "qli_attention_init", "qli_attention_validate", "qli_kv_entry_bytes", "qli_kv_write", "qli_kv_read",
+           "qli_sparse_attention",
            "qli_status_string", "qli_version")
 
 
@@ -53,6 +58,19 @@ class Problem(ctypes.Structure):
                             ("max_seqlen_q", ctypes.c_int32), ("max_seqlen_k", ctypes.c_int32),
                             ("key_stride", ctypes.c_int32), ("mask_complete_blocks", ctypes.c_int32),
                             ("split_topk", ctypes.c_int32)]
+
+
+class Rotation(ctypes.Structure):
+    """Mirror of ``qli_rotation``."""
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_heads_q", "num_heads_k", "head_dim", "rotary_dim", "max_positions", "dtype", "interleaved",
+        "norm")] + [("eps", ctypes.c_float)]
+
+
+class Attention(ctypes.Structure):
+    """Mirror of ``qli_attention``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_heads_q", "num_heads_kv", "head_dim", "dtype", "kv_dtype")] + [
+        (n, ctypes.c_float) for n in ("softmax_scale", "k_scale", "v_scale")] + [("kv_stride", ctypes.c_int64)]
 
 
 def _load():
@@ -109,6 +127,26 @@ def _load():
     L.qli_gather_kv.argtypes = [P, i32p, i32p, i32p, i32p, vp, ctypes.c_int64, ctypes.c_int64, vp, i32p, vp, sz,
                                 vp]
     L.qli_gather_kv.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    R, A = ctypes.POINTER(Rotation), ctypes.POINTER(Attention)
+    L.qli_rotation_init.argtypes = [R]
+    L.qli_rotation_init.restype = None
+    L.qli_rotation_validate.argtypes = [R, ctypes.POINTER(ctypes.c_char_p)]
+    L.qli_rotation_validate.restype = ctypes.c_int
+    L.qli_norm_rope.argtypes = [R, i64, vp, i64, vp, i64, vp, vp, i32p, vp, vp, i64, vp, i64, vp, sz, vp]
+    L.qli_norm_rope.restype = ctypes.c_int
+    L.qli_attention_init.argtypes = [A]
+    L.qli_attention_init.restype = None
+    L.qli_attention_validate.argtypes = [A, ctypes.POINTER(ctypes.c_char_p)]
+    L.qli_attention_validate.restype = ctypes.c_int
+    L.qli_kv_entry_bytes.argtypes = [A]
+    L.qli_kv_entry_bytes.restype = sz
+    L.qli_kv_write.argtypes = [P, A, i64, vp, i64, vp, i64, i32p, i32p, i32p, vp, vp, sz, vp]
+    L.qli_kv_write.restype = ctypes.c_int
+    L.qli_kv_read.argtypes = [P, A, i64, i32p, i32p, i32p, vp, vp, i64, vp, i64, vp, sz, vp]
+    L.qli_kv_read.restype = ctypes.c_int
+    L.qli_sparse_attention.argtypes = [P, A, vp, i64, i32p, i32p, i32p, i32p, vp, vp, vp, vp, sz, vp]
+    L.qli_sparse_attention.restype = ctypes.c_int
     return L
 
 
@@ -255,6 +293,134 @@ def gather_kv(p: Problem, seq_lens_q, seq_lens_k, block_table, sparse_indices, k
         ctypes.byref(p), _ptr(seq_lens_q), _ptr(seq_lens_k), _ptr(block_table), _ptr(sparse_indices), _ptr(kv),
         int(entry_bytes), int(kv_stride), _ptr(out), _ptr(counts), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+# ------------------------------------------------------------------------------ the attention side
+def _rows(t, what, dtype, tokens, heads, dim):
+    """(address, elements between tokens) of a [tokens, heads, dim] tensor whose heads are contiguous
+    (a view of a packed projection keeps its token stride); TypeError / ValueError otherwise."""
+    import torch
+    if t is None:
+        return None, 0
+    want = torch.float16 if dtype == ACT_F16 else torch.bfloat16
+    if t.dtype != want:
+        raise TypeError("%s: expected %s, got %s" % (what, want, t.dtype))
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, tokens, heads, dim, tuple(t.shape)))
+    if tokens <= 1:
+        stride = 0
+    else:
+        stride = t.stride(0)
+        if stride < heads * dim:                 # 0 would read as contiguous
+            raise ValueError("%s: tokens overlap (stride %d)" % (what, stride))
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError("%s: a token's heads must be contiguous" % what)
+    return t.data_ptr(), stride
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def make_norm_rope(*, num_heads_q, num_heads_k, head_dim, rotary_dim, max_positions, dtype=ACT_BF16,
+                   interleaved=False, norm=True, eps=1e-6) -> Rotation:
+    r = Rotation()
+    _get_lib().qli_rotation_init(ctypes.byref(r))
+    r.num_heads_q = num_heads_q
+    r.num_heads_k = num_heads_k
+    r.head_dim = head_dim
+    r.rotary_dim = rotary_dim
+    r.max_positions = max_positions
+    r.dtype = dtype
+    r.interleaved = 1 if interleaved else 0
+    r.norm = 1 if norm else 0
+    r.eps = eps
+    return r
+
+
+def validate_norm_rope(r: Rotation):
+    why = ctypes.c_char_p()
+    st = _get_lib().qli_rotation_validate(ctypes.byref(r), ctypes.byref(why))
+    return st, why.value.decode() if why.value else ""
+
+
+def norm_rope(r: Rotation, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace=None,
+              stream=None) -> int:
+    """qli_norm_rope: ``q`` [tokens, num_heads_q, head_dim] and ``k`` [tokens, num_heads_k, head_dim] (views
+    of a packed projection are fine) normalised and rotated into ``q_out`` / ``k_out`` (which may be
+    ``q`` / ``k``); ``positions`` int32 [tokens], ``cos_sin`` float32 [max_positions, rotary_dim]."""
+    n = positions.numel()
+    qa, qs = _rows(q, "q", r.dtype, n, r.num_heads_q, r.head_dim)
+    ka, ks = _rows(k, "k", r.dtype, n, r.num_heads_k, r.head_dim)
+    qo, qos = _rows(q_out, "q_out", r.dtype, n, r.num_heads_q, r.head_dim)
+    ko, kos = _rows(k_out, "k_out", r.dtype, n, r.num_heads_k, r.head_dim)
+    return _get_lib().qli_norm_rope(
+        ctypes.byref(r), n, qa, qs, ka, ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+        _ptr(cos_sin), qo, qos, ko, kos, _ptr(workspace), _bytes(workspace), _stream(stream))
+
+
+def make_attention(*, num_heads_q, num_heads_kv, head_dim, dtype=ACT_BF16, kv_dtype=KV_E2M1, softmax_scale=0.0,
+                   k_scale=1.0, v_scale=1.0, kv_stride=0) -> Attention:
+    a = Attention()
+    _get_lib().qli_attention_init(ctypes.byref(a))
+    a.num_heads_q = num_heads_q
+    a.num_heads_kv = num_heads_kv
+    a.head_dim = head_dim
+    a.dtype = dtype
+    a.kv_dtype = kv_dtype
+    a.softmax_scale = softmax_scale
+    a.k_scale = k_scale
+    a.v_scale = v_scale
+    a.kv_stride = kv_stride
+    return a
+
+
+def validate_attention(a: Attention):
+    why = ctypes.c_char_p()
+    st = _get_lib().qli_attention_validate(ctypes.byref(a), ctypes.byref(why))
+    return st, why.value.decode() if why.value else ""
+
+
+def kv_entry_bytes(a: Attention) -> int:
+    return int(_get_lib().qli_kv_entry_bytes(ctypes.byref(a)))
+
+
+def kv_write(p: Problem, a: Attention, k, v, token_batch, token_pos, block_table, kv, workspace=None,
+             stream=None) -> int:
+    """qli_kv_write: quantise ``k`` and ``v`` ([tokens, num_heads_kv, head_dim], views of a packed
+    projection are fine) into the paged 4-bit cache ``kv`` at each token's (batch, compressed position)."""
+    n = token_batch.numel()
+    ka, ks = _rows(k, "k", a.dtype, n, a.num_heads_kv, a.head_dim)
+    va, vs = _rows(v, "v", a.dtype, n, a.num_heads_kv, a.head_dim)
+    return _get_lib().qli_kv_write(
+        ctypes.byref(p), ctypes.byref(a), n, ka, ks, va, vs, _ptr(token_batch), _ptr(token_pos),
+        _ptr(block_table), _ptr(kv), _ptr(workspace), _bytes(workspace), _stream(stream))
+
+
+def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k, v, workspace=None,
+            stream=None) -> int:
+    """qli_kv_read: the cached keys and values of each token's (batch, compressed position) into ``k`` and
+    ``v`` ([tokens, num_heads_kv, head_dim])."""
+    n = token_batch.numel()
+    ka, ks = _rows(k, "k", a.dtype, n, a.num_heads_kv, a.head_dim)
+    va, vs = _rows(v, "v", a.dtype, n, a.num_heads_kv, a.head_dim)
+    return _get_lib().qli_kv_read(
+        ctypes.byref(p), ctypes.byref(a), n, _ptr(token_batch), _ptr(token_pos), _ptr(block_table),
+        _ptr(kv), ka, ks, va, vs, _ptr(workspace), _bytes(workspace), _stream(stream))
+
+
+def sparse_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, block_table, sparse_indices, kv, out,
+                     lse=None, workspace=None, stream=None) -> int:
+    """qli_sparse_attention: ``out`` [rows, num_heads_q, head_dim] (and ``lse`` float32 [rows, num_heads_q])
+    of ``query`` over the entries of the 4-bit cache ``kv`` that ``sparse_indices`` names."""
+    n = p.batch * p.max_q_tokens if p.layout_q == BSND else p.total_q_tokens
+    qa, qs = _rows(query, "query", a.dtype, n, a.num_heads_q, a.head_dim)
+    oa, os_ = _rows(out, "out", a.dtype, n, a.num_heads_q, a.head_dim)
+    if os_ not in (0, a.num_heads_q * a.head_dim):
+        raise ValueError("out: must be contiguous")
+    return _get_lib().qli_sparse_attention(
+        ctypes.byref(p), ctypes.byref(a), qa, qs, _ptr(seq_lens_q), _ptr(seq_lens_k), _ptr(block_table),
+        _ptr(sparse_indices), _ptr(kv), oa, _ptr(lse), _ptr(workspace), _bytes(workspace), _stream(stream))
 
 
 def workspace_init(workspace, stream=None) -> int:

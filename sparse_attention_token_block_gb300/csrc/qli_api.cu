@@ -4,7 +4,9 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -30,6 +32,8 @@ namespace {
 std::atomic<int> g_test_stall{0};
 std::atomic<int> g_test_topk_ctas{0};
 #endif
+
+constexpr int64_t kMaxTokens = INT64_C(1) << 30;      // of one call that takes a token list (grid limit)
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
@@ -80,6 +84,69 @@ qli_status check(const qli_problem* p, const char** why)
 #undef QLI_REJECT
     if (why) *why = "ok";
     return QLI_OK;
+}
+
+#define QLI_REJECT(cond, msg)           \
+    do {                                \
+        if (cond) {                     \
+            if (why) *why = msg;        \
+            return QLI_ERR_INVALID_ARG; \
+        }                               \
+    } while (0)
+
+qli_status check_rotation(const qli_rotation* r, const char** why)
+{
+    QLI_REJECT(r == nullptr, "rotation is NULL");
+    QLI_REJECT(r->num_heads_q < 0 || r->num_heads_q > 1024 || r->num_heads_k < 0 || r->num_heads_k > 1024,
+               "num_heads_q and num_heads_k must be in [0, 1024]");
+    QLI_REJECT(r->head_dim != 64 && r->head_dim != 128 && r->head_dim != 256, "head_dim must be 64, 128 or 256");
+    QLI_REJECT(r->rotary_dim < 0 || r->rotary_dim > r->head_dim || r->rotary_dim % 8 != 0,
+               "rotary_dim must be a multiple of 8 in [0, head_dim]");
+    QLI_REJECT(r->max_positions < 1, "max_positions must be >= 1");
+    QLI_REJECT(r->dtype != QLI_ACT_BF16 && r->dtype != QLI_ACT_F16, "dtype must be bf16 or f16");
+    QLI_REJECT(r->interleaved != 0 && r->interleaved != 1, "interleaved must be 0 or 1");
+    QLI_REJECT(r->norm != 0 && r->norm != 1, "norm must be 0 or 1");
+    QLI_REJECT(!(r->eps >= 0.0f) || r->eps > FLT_MAX, "eps must be finite and >= 0");
+    if (why) *why = "ok";
+    return QLI_OK;
+}
+
+size_t entry_bytes_of(const qli_attention* a)
+{
+    return ((size_t)a->num_heads_kv * kv_unit_bytes(a->head_dim) + 15) & ~size_t(15);
+}
+
+qli_status check_attention(const qli_attention* a, const char** why)
+{
+    QLI_REJECT(a == nullptr, "attention is NULL");
+    QLI_REJECT(a->num_heads_kv < 1 || a->num_heads_kv > 64, "num_heads_kv must be in [1, 64]");
+    QLI_REJECT(a->num_heads_q < 1 || a->num_heads_q > 256 || a->num_heads_q % a->num_heads_kv != 0,
+               "num_heads_q must be a multiple of num_heads_kv in [1, 256]");
+    QLI_REJECT(a->head_dim != 64 && a->head_dim != 128, "head_dim must be 64 or 128");
+    QLI_REJECT(a->dtype != QLI_ACT_BF16 && a->dtype != QLI_ACT_F16, "dtype must be bf16 or f16");
+    QLI_REJECT(a->kv_dtype != QLI_KV_INT4 && a->kv_dtype != QLI_KV_E2M1, "kv_dtype must be int4 or e2m1");
+    QLI_REJECT(!(a->softmax_scale >= 0.0f) || a->softmax_scale > FLT_MAX, "softmax_scale must be finite and >= 0");
+    QLI_REJECT(!(a->k_scale >= FLT_MIN) || a->k_scale > FLT_MAX, "k_scale must be finite, normal and > 0");
+    QLI_REJECT(!(a->v_scale >= FLT_MIN) || a->v_scale > FLT_MAX, "v_scale must be finite, normal and > 0");
+    QLI_REJECT(a->kv_stride < 0 || a->kv_stride % 16 != 0, "kv_stride must be 0 or a multiple of 16");
+    if (why) *why = "ok";
+    return QLI_OK;
+}
+#undef QLI_REJECT
+
+// Token stride in elements of `heads` vectors of `dim` (0 = contiguous); -1 when it is not allowed
+int64_t token_stride(int64_t stride, int64_t heads, int64_t dim)
+{
+    if (stride == 0) return heads * dim;
+    return (stride >= heads * dim && stride % 8 == 0) ? stride : -1;
+}
+
+// Page stride of the KV cache in bytes, -1 when the attributes' stride is below a page
+int64_t kv_page_bytes(const qli_problem* p, const qli_attention* a)
+{
+    const int64_t page = (int64_t)p->block_size * (int64_t)entry_bytes_of(a);
+    if (a->kv_stride == 0) return page;
+    return a->kv_stride >= page ? a->kv_stride : -1;
 }
 
 // Query tokens scored together by one MMA (N = 64 per token): one for one query token per
@@ -503,6 +570,200 @@ qli_status qli_gather_kv(const qli_problem* p, const int32_t* seq_lens_q, const 
     cudaError_t e = launch_gather(P, seq_lens_q, seq_lens_k, block_table, sparse_indices, kv, entry_bytes,
                                   kv_stride ? kv_stride : page_bytes, out, counts, static_cast<uint32_t*>(workspace),
                                   static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+void qli_rotation_init(qli_rotation* r)
+{
+    if (!r) return;
+    std::memset(r, 0, sizeof(*r));
+    r->num_heads_q = 64;
+    r->num_heads_k = 8;
+    r->head_dim = 128;
+    r->rotary_dim = 128;
+    r->max_positions = 4096;
+    r->dtype = QLI_ACT_BF16;
+    r->norm = 1;
+    r->eps = 1e-6f;
+}
+
+qli_status qli_rotation_validate(const qli_rotation* r, const char** why) { return check_rotation(r, why); }
+
+qli_status qli_norm_rope(const qli_rotation* r, int64_t tokens, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* q_weight, const void* k_weight, const int32_t* positions,
+                         const float* cos_sin, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                         void* workspace, size_t workspace_bytes, void* stream)
+{
+    qli_status s = check_rotation(r, nullptr);
+    if (s != QLI_OK) return s;
+    if (tokens < 0 || tokens > kMaxTokens) return QLI_ERR_INVALID_ARG;
+    if (workspace && (workspace_bytes < kWsHeaderBytes || !aligned(workspace, 256))) return QLI_ERR_INVALID_ARG;
+    NormRopeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const void* weight[2] = {q_weight, k_weight};
+    const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
+    const int32_t heads[2] = {r->num_heads_q, r->num_heads_k};
+    for (int i = 0; i < 2; ++i) {
+        a.heads[i] = heads[i];
+        if (heads[i] == 0) continue;
+        a.in[i] = in[i];
+        a.out[i] = out[i];
+        a.weight[i] = r->norm ? weight[i] : nullptr;
+        a.in_stride[i] = token_stride(is[i], heads[i], r->head_dim);
+        a.out_stride[i] = token_stride(os[i], heads[i], r->head_dim);
+        if (a.in_stride[i] < 0 || a.out_stride[i] < 0) return QLI_ERR_INVALID_ARG;
+        if (tokens == 0) continue;
+        if (!in[i] || !out[i] || !aligned(in[i], 16) || !aligned(out[i], 16)) return QLI_ERR_INVALID_ARG;
+        if (r->norm && (!weight[i] || !aligned(weight[i], 16))) return QLI_ERR_INVALID_ARG;
+    }
+    if (tokens == 0 || heads[0] + heads[1] == 0) return QLI_OK;
+    if (!positions || !aligned(positions, 4)) return QLI_ERR_INVALID_ARG;
+    if (r->rotary_dim > 0 && (!cos_sin || !aligned(cos_sin, 16))) return QLI_ERR_INVALID_ARG;
+    int sms = device_sms(nullptr);
+    if (sms < 0) return QLI_ERR_CUDA;
+    if (sms == 0) return QLI_ERR_NO_DEVICE;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.err = static_cast<uint32_t*>(workspace);
+    a.tokens = tokens;
+    a.rotary = r->rotary_dim;
+    a.max_positions = r->max_positions;
+    a.interleaved = r->interleaved;
+    a.norm = r->norm;
+    a.eps = r->eps;
+    cudaError_t e = launch_norm_rope(a, r->head_dim, r->dtype == QLI_ACT_F16, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+void qli_attention_init(qli_attention* a)
+{
+    if (!a) return;
+    std::memset(a, 0, sizeof(*a));
+    a->num_heads_q = 64;
+    a->num_heads_kv = 8;
+    a->head_dim = 128;
+    a->dtype = QLI_ACT_BF16;
+    a->kv_dtype = QLI_KV_E2M1;
+    a->k_scale = 1.0f;
+    a->v_scale = 1.0f;
+}
+
+qli_status qli_attention_validate(const qli_attention* a, const char** why) { return check_attention(a, why); }
+
+size_t qli_kv_entry_bytes(const qli_attention* a)
+{
+    return check_attention(a, nullptr) == QLI_OK ? entry_bytes_of(a) : 0;
+}
+
+namespace {
+
+// Argument checks that writing and reading the cache share; fills `A` (nothing to do when tokens = 0)
+qli_status kv_args(const qli_problem* p, const qli_attention* a, int64_t tokens, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const int32_t* token_batch, const int32_t* token_pos,
+                   const int32_t* block_table, const void* kv, void* workspace, size_t workspace_bytes, KvArgs* A)
+{
+    qli_status s = check(p, nullptr);
+    if (s != QLI_OK) return s;
+    s = check_attention(a, nullptr);
+    if (s != QLI_OK) return s;
+    if (tokens < 0 || tokens > kMaxTokens) return QLI_ERR_INVALID_ARG;
+    if (workspace && (workspace_bytes < kWsHeaderBytes || !aligned(workspace, 256))) return QLI_ERR_INVALID_ARG;
+    A->stride[0] = token_stride(k_stride, a->num_heads_kv, a->head_dim);
+    A->stride[1] = token_stride(v_stride, a->num_heads_kv, a->head_dim);
+    A->page_bytes = kv_page_bytes(p, a);
+    if (A->stride[0] < 0 || A->stride[1] < 0 || A->page_bytes < 0) return QLI_ERR_INVALID_ARG;
+    if (tokens == 0) return QLI_OK;
+    if (!k || !v || !token_batch || !token_pos || !block_table || !kv) return QLI_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv, 16)) return QLI_ERR_INVALID_ARG;
+    int sms = device_sms(nullptr);
+    if (sms < 0) return QLI_ERR_CUDA;
+    if (sms == 0) return QLI_ERR_NO_DEVICE;
+    A->p = params_of(p);
+    A->heads_kv = a->num_heads_kv;
+    A->head_dim = a->head_dim;
+    A->f16 = a->dtype == QLI_ACT_F16;
+    A->e2m1 = a->kv_dtype == QLI_KV_E2M1;
+    A->k_scale = a->k_scale;
+    A->v_scale = a->v_scale;
+    A->entry_bytes = (int64_t)entry_bytes_of(a);
+    A->tokens = tokens;
+    A->token_batch = token_batch;
+    A->token_pos = token_pos;
+    A->block_table = block_table;
+    A->err = static_cast<uint32_t*>(workspace);
+    return QLI_OK;
+}
+
+}  // namespace
+
+qli_status qli_kv_write(const qli_problem* p, const qli_attention* a, int64_t tokens, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const int32_t* token_batch, const int32_t* token_pos,
+                        const int32_t* block_table, void* kv, void* workspace, size_t workspace_bytes, void* stream)
+{
+    KvArgs A;
+    qli_status s = kv_args(p, a, tokens, k, k_stride, v, v_stride, token_batch, token_pos, block_table, kv, workspace,
+                           workspace_bytes, &A);
+    if (s != QLI_OK || tokens == 0) return s;
+    cudaError_t e = launch_kv_write(A, k, v, kv, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tokens, const int32_t* token_batch,
+                       const int32_t* token_pos, const int32_t* block_table, const void* kv, void* k,
+                       int64_t k_stride, void* v, int64_t v_stride, void* workspace, size_t workspace_bytes,
+                       void* stream)
+{
+    KvArgs A;
+    qli_status s = kv_args(p, a, tokens, k, k_stride, v, v_stride, token_batch, token_pos, block_table, kv, workspace,
+                           workspace_bytes, &A);
+    if (s != QLI_OK || tokens == 0) return s;
+    cudaError_t e = launch_kv_read(A, kv, k, v, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, const void* query, int64_t q_stride,
+                                const int32_t* seq_lens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                                const int32_t* sparse_indices, const void* kv, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream)
+{
+    qli_status s = check(p, nullptr);
+    if (s != QLI_OK) return s;
+    s = check_attention(a, nullptr);
+    if (s != QLI_OK) return s;
+    if (workspace && (workspace_bytes < kWsHeaderBytes || !aligned(workspace, 256))) return QLI_ERR_INVALID_ARG;
+    AttentionArgs A;
+    A.p = params_of(p);
+    A.q_stride = token_stride(q_stride, a->num_heads_q, a->head_dim);
+    A.page_bytes = kv_page_bytes(p, a);
+    if (A.q_stride < 0 || A.page_bytes < 0) return QLI_ERR_INVALID_ARG;
+    if (A.p.rows == 0) return QLI_OK;
+    if (!query || !sparse_indices || !out || !aligned(query, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
+        return QLI_ERR_INVALID_ARG;
+    if (A.p.batch > 0 && (!block_table || !kv || !aligned(kv, 16))) return QLI_ERR_INVALID_ARG;
+    if (A.p.layout_tnd && A.p.batch > 0 && !seq_lens_q) return QLI_ERR_INVALID_ARG;
+    if ((int64_t)A.p.rows * a->num_heads_q >= (INT64_C(1) << 28)) return QLI_ERR_UNSUPPORTED;    // grid limit
+    int sms = device_sms(nullptr);
+    if (sms < 0) return QLI_ERR_CUDA;
+    if (sms == 0) return QLI_ERR_NO_DEVICE;
+    A.query = query;
+    A.seq_lens_q = seq_lens_q;
+    A.seq_lens_k = seq_lens_k;
+    A.block_table = block_table;
+    A.idx = sparse_indices;
+    A.kv = static_cast<const uint8_t*>(kv);
+    A.out = out;
+    A.lse = lse;
+    A.err = static_cast<uint32_t*>(workspace);
+    A.entry_bytes = (int32_t)entry_bytes_of(a);
+    A.heads_q = a->num_heads_q;
+    A.heads_kv = a->num_heads_kv;
+    A.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : 1.0f / sqrtf((float)a->head_dim);
+    A.k_scale = a->k_scale;
+    A.v_scale = a->v_scale;
+    cudaError_t e = launch_attention(A, a->head_dim, a->dtype == QLI_ACT_F16, a->kv_dtype == QLI_KV_E2M1, sms,
+                                     static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 

@@ -46,37 +46,6 @@ struct GatherArgs {
     int32_t kw;                       // entries per warp run
 };
 
-// Batch of global row r, or -1: BSND r / S1; TND the b with cum[b-1] <= r < cum[b] (cum[-1] = 0),
-// found by binary search for the first prefix sum above r and then checked, so prefix sums that
-// are not non-decreasing can never yield an index outside [0, batch).
-__device__ __forceinline__ int64_t row_batch(const GatherArgs& a, int64_t r)
-{
-    const Params& p = a.p;
-    if (!p.layout_tnd) return p.s1 > 0 ? r / p.s1 : -1;
-    int lo = 0, hi = p.batch;                  // first b in [lo, hi) with cum[b] > r
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.seq_lens_q[mid] > r) hi = mid;
-        else lo = mid + 1;
-    }
-    if (lo >= p.batch) return -1;
-    const int64_t first = lo > 0 ? a.seq_lens_q[lo - 1] : 0, end = a.seq_lens_q[lo];
-    return (first <= r && r < end && end <= p.total_q) ? lo : -1;
-}
-
-// Exclusive upper bound of valid j in batch b (-1 when the batch's length is invalid).
-__device__ __forceinline__ int64_t index_limit(const GatherArgs& a, int64_t b)
-{
-    const Params& p = a.p;
-    int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
-    if (a.seq_lens_k) {
-        const int64_t sk = a.seq_lens_k[b];
-        const int64_t lc = sk < 0 ? -1 : (sk + p.cmp_ratio - 1) / p.cmp_ratio;
-        limit = lc < limit ? lc : limit;
-    }
-    return limit;
-}
-
 // Chunk offset of index j's entry in the pool, -1 for a zero entry; error bits into *bits.
 __device__ __forceinline__ int64_t entry_source(const GatherArgs& a, int64_t b, int64_t limit, int64_t j,
                                                 uint32_t* bits)
@@ -110,8 +79,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(GatherArgs a)
         int64_t src = -1;
         const int64_t e = e0 + lane;
         if (lane < a.kw && e < a.total) {
-            const int64_t b = row_batch(a, e / k);
-            const int64_t limit = b >= 0 ? index_limit(a, b) : -1;
+            const int64_t b = row_batch(a.p, a.seq_lens_q, e / k);
+            const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
             src = entry_source(a, b, limit, a.idx[e], &bits);
         }
         // copy: chunk t of the run belongs to entry t / n16
@@ -143,8 +112,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(GatherArgs a)
     // through shared memory
     if (a.counts && blockIdx.x < a.p.rows) {
         const int64_t r = blockIdx.x;
-        const int64_t b = row_batch(a, r);                 // uniform over the CTA
-        const int64_t limit = b >= 0 ? index_limit(a, b) : -1;
+        const int64_t b = row_batch(a.p, a.seq_lens_q, r);                 // uniform over the CTA
+        const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
         int c = 0;
         if (limit > 0) {
             const int64_t bs = a.p.block_size;

@@ -232,6 +232,36 @@ __device__ __forceinline__ BatchExtent batch_extent(const Params& p, const int32
     return e;
 }
 
+// Batch of global row r, or -1: BSND r / S1; TND the b with cum[b-1] <= r < cum[b] (cum[-1] = 0),
+// found by binary search for the first prefix sum above r and then checked, so prefix sums that
+// are not non-decreasing can never yield an index outside [0, batch).
+__device__ __forceinline__ int64_t row_batch(const Params& p, const int32_t* seq_lens_q, int64_t r)
+{
+    if (!p.layout_tnd) return p.s1 > 0 ? r / p.s1 : -1;
+    int lo = 0, hi = p.batch;                  // first b in [lo, hi) with cum[b] > r
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_lens_q[mid] > r) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo >= p.batch) return -1;
+    const int64_t first = lo > 0 ? seq_lens_q[lo - 1] : 0, end = seq_lens_q[lo];
+    return (first <= r && r < end && end <= p.total_q) ? lo : -1;
+}
+
+// Exclusive upper bound of valid compressed positions in batch b (-1 when the batch's length is
+// negative); seq_lens_k may be NULL, then only the block_table's capacity bounds them.
+__device__ __forceinline__ int64_t index_limit(const Params& p, const int32_t* seq_lens_k, int64_t b)
+{
+    int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
+    if (seq_lens_k) {
+        const int64_t sk = seq_lens_k[b];
+        const int64_t lc = sk < 0 ? -1 : (sk + p.cmp_ratio - 1) / p.cmp_ratio;
+        limit = lc < limit ? lc : limit;
+    }
+    return limit;
+}
+
 // Key tiles of the query group of batch rows [r0, min(r0 + gt, sq)): ceil(n / kTileKeys), n the
 // visible keys of its last row (the largest in the group under either mask)
 __host__ __device__ inline int64_t group_tiles(const Params& p, int64_t sq, int64_t sk, int64_t lc, int64_t r0)
@@ -339,6 +369,59 @@ cudaError_t launch_quantize_vectors(const void* x_bf16, int64_t nvec, void* code
 cudaError_t launch_quantize_keys(const Params& p, const void* k_bf16, int64_t tokens, const int32_t* tok_batch,
                                  const int32_t* tok_pos, const int32_t* block_table, void* pool, void* k_scale,
                                  uint32_t* err, cudaStream_t st);
+// Norm and rotation (qli_norm_rope.cu): a null side has no heads
+struct NormRopeArgs {
+    const void* in[2];          // queries, keys
+    void* out[2];
+    const void* weight[2];
+    int64_t in_stride[2], out_stride[2];      // elements between tokens
+    const int32_t* positions;
+    const float* cos_sin;
+    uint32_t* err;
+    int64_t tokens;
+    int32_t heads[2];
+    int32_t rotary, max_positions, interleaved, norm;
+    float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, bool f16, int sms, cudaStream_t st);
+
+// The 4-bit KV cache (qli_kv_cache.cu) and the attention over it (qli_attention.cu).  An entry holds
+// per KV head kv_unit_bytes(D): K codes, V codes, K scales, V scales.
+constexpr int kKvBlock = 16;               // elements that share a scale
+__host__ __device__ constexpr int kv_unit_bytes(int d) { return d + 2 * (d / kKvBlock); }
+struct KvArgs {
+    Params p;
+    int32_t heads_kv, head_dim, f16, e2m1;
+    float k_scale, v_scale;
+    int64_t entry_bytes, page_bytes;       // entry and page strides
+    int64_t tokens;
+    int64_t stride[2];                     // elements between tokens of k, v
+    const int32_t* token_batch;
+    const int32_t* token_pos;
+    const int32_t* block_table;
+    uint32_t* err;
+};
+cudaError_t launch_kv_write(const KvArgs& a, const void* k, const void* v, void* kv, cudaStream_t st);
+cudaError_t launch_kv_read(const KvArgs& a, const void* kv, void* k, void* v, cudaStream_t st);
+
+struct AttentionArgs {
+    Params p;
+    const void* query;
+    int64_t q_stride;                      // elements between rows
+    const int32_t* seq_lens_q;
+    const int32_t* seq_lens_k;
+    const int32_t* block_table;
+    const int32_t* idx;                    // [rows, sparse_count]
+    const uint8_t* kv;
+    void* out;
+    float* lse;                            // optional
+    uint32_t* err;                         // optional sticky error word
+    int64_t page_bytes;
+    int32_t entry_bytes;
+    int32_t heads_q, heads_kv;
+    float softmax_scale, k_scale, v_scale;
+};
+cudaError_t launch_attention(const AttentionArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st);
 cudaError_t launch_gather(const Params& p, const int32_t* seq_lens_q, const int32_t* seq_lens_k,
                           const int32_t* block_table, const int32_t* idx, const void* kv, int64_t entry_bytes,
                           int64_t kv_stride, void* out, int32_t* counts, uint32_t* err, cudaStream_t st);

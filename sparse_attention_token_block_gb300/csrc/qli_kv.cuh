@@ -1,0 +1,98 @@
+// qli_kv.cuh -- the 4-bit codes of the KV cache: quantising one block of 16 elements, decoding codes
+// and scales, and finding an entry through the block_table.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qli_internal.cuh"
+#include "qli_ptx.cuh"
+
+namespace qli {
+
+// Two activations packed in a word -> fp32 (exact), and back (rounded to nearest even)
+template <bool F16>
+__device__ __forceinline__ float2 act2_to_float2(uint32_t w)
+{
+    if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t float2_to_act2(float lo, float hi)
+{
+    if (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A scale byte (float8_e4m3fn) as fp32, and the scale of a block: e4m3(min(a, 448)) as a byte
+__device__ __forceinline__ float e4m3_to_float(uint32_t byte)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+}
+
+__device__ __forceinline__ uint32_t float_to_e4m3(float a)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(a));
+    return r & 0xFFu;
+}
+
+// Eight E2M1 codes in a word -> f16x2 words of elements (0, 1), (2, 3), (4, 5), (6, 7) (exact)
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+
+// Code c of a word as fp32
+template <bool E2M1>
+__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8])
+{
+    if (E2M1) {
+        uint32_t h[4];
+        e2m1x8_to_f16x2(w, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)((int32_t)(w << (28 - 4 * i)) >> 28);
+    }
+}
+
+// Byte offset of compressed position `pos` of batch `b` in the pool, -1 when the batch, the
+// position (against `limit`) or the page is invalid (with the error bit)
+__device__ __forceinline__ int64_t kv_entry_offset(const Params& p, const int32_t* block_table, int64_t b, int64_t pos,
+                                                   int64_t limit, int64_t page_bytes, int64_t entry_bytes,
+                                                   uint32_t* bits)
+{
+    if (b < 0 || b >= p.batch || pos < 0 || pos >= limit) {
+        *bits |= kErrLength;
+        return -1;
+    }
+    const uint32_t bs = (uint32_t)p.block_size, block = (uint32_t)pos / bs;       // pos < 2^31
+    const int64_t page = block_table[b * p.max_blocks_per_seq + block];
+    if (page < 0 || page >= p.num_blocks) {
+        *bits |= kErrPage;
+        return -1;
+    }
+    return page * page_bytes + (int64_t)((uint32_t)pos - block * bs) * entry_bytes;
+}
+
+}  // namespace qli
