@@ -2,11 +2,35 @@
 // names, the entries held in 4 bits:
 //     z_i = scale * q_h . K_i,   out_h = sum_i softmax(z)_i V_i,   lse_h = ln sum_i exp(z_i)
 //
-// One CTA per (row, KV head, eight of its query heads).  A tile of 32 listed entries is decoded
-// into shared memory in fp32; each of the four warps carries two query heads, one entry per lane for
-// the logits and D / 32 output elements per lane for the weighted sum, with the running maximum and
-// sum of the softmax.
+// A cluster of `splits` CTAs works on one row (or a slice of its KV heads), each on a slice of the
+// list.  A CTA first resolves its slice -- index, bounds, block_table -- into a compact list of the
+// valid entries; a producer warp then streams those entries into a ring of shared-memory stages, one
+// bulk copy per entry (all of the CTA's KV heads lie side by side in it).  Each of eight consumer
+// warps carries one unit, a KV head with up to 8 * NT of its query heads, over its share of the
+// entries:
+//
+//   * logits:  S^T (16 entries x 8 heads) = K Q^T.  A lane decodes 4-bit keys straight into the A
+//     fragment: lane (r, c) of a warp holds rows r and r + 8, so it takes 1/4 of two key vectors as one
+//     shared-memory load each; which of its columns meets which step of the product is free as long as
+//     the query fragment, loaded once, follows the same order.
+//   * softmax: running maximum and sum per head in fp32 (base 2).  The accumulators are rescaled only
+//     when some logit exceeds the maximum in use by more than 8 (then p stays within 2^8, inside
+//     fp16's range at full precision), so most tiles skip the exchange between lanes.
+//   * output:  O^T (D x 8 heads) += V^T P^T.  P goes from accumulator to B fragment by 8 x 8
+//     transposes.  V^T's A fragment pairs two entries per register: the nibbles of two entries are
+//     interleaved before they are decoded.
+//
+// Heads never fill the M side of a product, entries do, so groups of 8 query heads waste nothing of
+// the tensor cores.  4-bit values times e4m3 scales are exact in fp16 (at most 6 significant bits,
+// 2^-10 to 2688); queries are scaled by a power of two of their head's largest magnitude, so that
+// bfloat16 fits fp16 too (elements below 2^-14 of the largest lose bits of 2^-25 of it).
+//
+// Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over
+// the cluster) and are joined in a fixed order.  Every wait is bounded (0.2 s): on expiry the kernel
+// records kErrTimeout, writes NaN, lets its copies land and returns.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "qli_kv.cuh"
 
@@ -14,122 +38,568 @@ namespace qli {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
-constexpr int kAttnTile = 32;
-constexpr int kAttnHeads = 8;
+constexpr int kWarps = 8;                         // consumer warps
+constexpr int kBuilders = 32 * kWarps;            // threads that resolve the list
+constexpr int kThreads = kBuilders + 32;          // and the producer warp
+constexpr int kMt = 2;                            // tiles of 16 entries per warp and stage
+constexpr int kMaxStages = 8;
+constexpr int kMaxPerThread = kMaxSparse / kBuilders;
+constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
+constexpr uint64_t kWaitLimitNs = 200000000ull;
 
-template <bool F16, bool E2M1, int D>
-__global__ void __launch_bounds__(kAttnThreads) attention_kernel(AttentionArgs a)
+// How a launch is laid out (host)
+struct Layout {
+    int32_t chunks;        // units per KV head: ceil(group / (8 NT))
+    int32_t units;         // heads_kv * chunks
+    int32_t per_cta;       // units per CTA, at most kWarps
+    int32_t ctas;          // CTAs a row's units take: ceil(units / per_cta)
+    int32_t parts;         // warps that share a unit: kWarps / per_cta
+    int32_t splits;        // CTAs of the cluster, each with a slice of the list
+    int32_t per_split;     // list positions per slice
+    int32_t stages;
+    int32_t row_bytes;     // entry stride in a stage, 32 or 96 beyond a multiple of 128
+    int32_t list_off, ring_off;   // shared-memory offsets
+};
+
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int32_t warp_count[kWarps];
+    int32_t issued;        // stages the producer filled
+    uint32_t abort;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
 {
-    __shared__ float ks[kAttnTile][D + 1], vs[kAttnTile][D];
-    __shared__ float qs[kAttnHeads][D];
-    __shared__ int64_t src[kAttnTile];
-    ptx::pdl_wait();
-    const int group = a.heads_q / a.heads_kv, chunks = (group + kAttnHeads - 1) / kAttnHeads;
-    const int64_t unit = (int64_t)a.heads_kv * chunks, r = blockIdx.x / unit;
-    const int uh = (int)(blockIdx.x - r * unit), kvh = uh / chunks, h0 = kvh * group + (uh - kvh * chunks) * kAttnHeads;
-    const int nh = min(kAttnHeads, (kvh + 1) * group - h0);
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const uint16_t* q = static_cast<const uint16_t*>(a.query) + r * a.q_stride + (int64_t)h0 * D;
-    for (int i = tid; i < kAttnHeads * D / 2; i += kAttnThreads) {
-        const int h = 2 * i / D;
-        float2 f = make_float2(0.0f, 0.0f);
-        if (h < nh) f = act2_to_float2<F16>(reinterpret_cast<const uint32_t*>(q)[i]);
-        qs[h][2 * i % D] = f.x * a.softmax_scale;              // (first, so that the products stay in range)
-        qs[h][2 * i % D + 1] = f.y * a.softmax_scale;
-    }
-    const int64_t b = row_batch(a.p, a.seq_lens_q, r);
-    const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
-    const int k = a.p.sparse_count;
-    const int32_t* idx = a.idx + r * k;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, acc[2][D / 32];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[j][e] = 0.0f;
-    uint32_t bits = 0;
-    for (int t0 = 0; t0 < k; t0 += kAttnTile) {
-        __syncthreads();
-        if (tid < kAttnTile) {
-            const int j = t0 + tid < k ? idx[t0 + tid] : -1;
-            src[tid] = j == -1 ? -1
-                               : kv_entry_offset(a.p, a.block_table, b, j, limit, a.page_bytes, a.entry_bytes, &bits);
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        if (ptx::mbar_try_wait_sleep(bar, parity, 100000u)) return true;
+        if (*abort) return false;
+        if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
         }
-        __syncthreads();
-        for (int i = tid; i < kAttnTile * D / 8; i += kAttnThreads) {
-            const int t = i / (D / 8), c = i - t * (D / 8);
-            float kf[8] = {0, 0, 0, 0, 0, 0, 0, 0}, vf[8] = {0, 0, 0, 0, 0, 0, 0, 0}, sk = 0.0f, sv = 0.0f;
-            if (src[t] >= 0) {
-                const uint8_t* e = a.kv + src[t] + kvh * kv_unit_bytes(D);
-                decode8<E2M1>(*reinterpret_cast<const uint32_t*>(e + 4 * c), kf);
-                decode8<E2M1>(*reinterpret_cast<const uint32_t*>(e + D / 2 + 4 * c), vf);
-                sk = e4m3_to_float(e[D + c / 2]) * a.k_scale;
-                sv = e4m3_to_float(e[D + D / 16 + c / 2]) * a.v_scale;
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                ks[t][8 * c + x] = kf[x] * sk;
-                vs[t][8 * c + x] = vf[x] * sv;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int h = 2 * wid + j;
-            if (h >= nh) continue;
-            float z = 0.0f;
-            for (int d = 0; d < D; ++d) z = fmaf(qs[h][d], ks[lane][d], z);
-            z = src[lane] >= 0 ? z : -INFINITY;
-            float top = z;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float mn = fmaxf(m[j], top);
-            if (mn == -INFINITY) continue;                     // nothing valid so far
-            const float p = __expf(z - mn), f = __expf(m[j] - mn);
-            m[j] = mn;
-            l[j] = l[j] * f + p;                               // per lane; summed at the end
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[j][e] *= f;
-            for (int t = 0; t < kAttnTile; ++t) {
-                const float pt = __shfl_sync(0xffffffffu, p, t);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[j][e] = fmaf(pt, vs[t][32 * e + lane], acc[j][e]);
-            }
-        }
-    }
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if (bits && lane == 0 && a.err) atomicOr(a.err, bits);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int h = 2 * wid + j;
-        if (h >= nh) continue;
-        float total = l[j];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-        uint16_t* out = static_cast<uint16_t*>(a.out) + (r * a.heads_q + h0 + h) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            out[32 * e + lane] = (uint16_t)float2_to_act2<F16>(acc[j][e] * inv, 0.0f);
-        if (a.lse && lane == 0) a.lse[r * a.heads_q + h0 + h] = total > 0.0f ? m[j] + logf(total) : -INFINITY;
     }
 }
 
-template <bool F16, bool E2M1>
-cudaError_t launch_type(const AttentionArgs& a, int head_dim, cudaStream_t st)
+// Entry (of a group of eight) that row r of an 8-row fragment holds.  Rows 2c and 2c + 1 hold entries
+// c and 4 + (c + 2) % 4: with an entry stride of 32 or 96 modulo 128 bytes, the four entries that a
+// quarter-warp reads of V and the two that it reads of K then lie in different banks.
+__device__ __forceinline__ int entry_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
 {
-    const int group = a.heads_q / a.heads_kv, chunks = (group + kAttnHeads - 1) / kAttnHeads;
-    const int64_t grid = (int64_t)a.p.rows * a.heads_kv * chunks;
-    auto kernel = head_dim == 64 ? attention_kernel<F16, E2M1, 64> : attention_kernel<F16, E2M1, 128>;
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kAttnThreads), 0, st, a);
+    static_assert(N == 1 || N == 2, "one or two words");
+    if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+template <bool F16, bool E2M1, int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L)
+{
+    constexpr int kUnit = kv_unit_bytes(D);
+    constexpr int NW = D / 32;                    // words of key codes per lane and entry
+    constexpr int MO = D / 16;                    // 16-row tiles of the output
+    constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
+    extern __shared__ __align__(128) uint8_t smem[];
+    Control& ctl = *reinterpret_cast<Control*>(smem);
+    uint32_t* list = reinterpret_cast<uint32_t*>(smem + L.list_off);
+    uint8_t* ring = smem + L.ring_off;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
+    const int64_t task = blockIdx.x / L.splits, row = task / L.ctas;
+    const int u0 = (int)(task - row * L.ctas) * L.per_cta, nu = min(L.per_cta, L.units - u0);
+    const int group = a.heads_q / a.heads_kv;
+    // the bytes of an entry that hold the CTA's KV heads
+    const int lo = (u0 / L.chunks) * kUnit & ~15, hi = (((u0 + nu - 1) / L.chunks + 1) * kUnit + 15) & ~15;
+    const int tile = 16 * kMt * L.parts;
+    const int stage_bytes = tile * L.row_bytes;
+
+    if (tid == 0) {
+        for (int s = 0; s < L.stages; ++s) {
+            ptx::mbar_init(&ctl.full[s], 1);
+            ptx::mbar_init(&ctl.empty[s], nu * L.parts);
+        }
+        ctl.issued = 0;
+        ctl.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::pdl_wait();
+
+    // ---- the slice's valid entries, in list order, as slots page * block_size + position in the page
+    const int k0 = rank * L.per_split, n = max(0, min(L.per_split, a.p.sparse_count - k0));
+    uint32_t slot[kMaxPerThread];
+    int mine = 0;
+    if (wid < kWarps) {
+        const int64_t b = row_batch(a.p, a.seq_lens_q, row);
+        const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
+        const int32_t* idx = a.idx + row * a.p.sparse_count + k0;
+        const int32_t* table = a.block_table + b * a.p.max_blocks_per_seq;
+        const int per = (n + kBuilders - 1) / kBuilders, at = tid * per;
+        const uint32_t bs = (uint32_t)a.p.block_size;
+        int32_t j[kMaxPerThread], page[kMaxPerThread];
+        uint32_t bits = 0;
+#pragma unroll
+        for (int e = 0; e < kMaxPerThread; ++e) j[e] = e < per && at + e < n ? idx[at + e] : -1;
+#pragma unroll
+        for (int e = 0; e < kMaxPerThread; ++e) {
+            const bool ok = j[e] >= 0 && j[e] < limit;
+            if (j[e] != -1 && !ok) bits |= kErrLength;
+            page[e] = ok ? table[(uint32_t)j[e] / bs] : -1;
+            if (!ok) j[e] = -1;
+        }
+#pragma unroll
+        for (int e = 0; e < kMaxPerThread; ++e) {
+            const bool ok = j[e] >= 0 && page[e] >= 0 && page[e] < a.p.num_blocks;
+            if (j[e] >= 0 && !ok) bits |= kErrPage;
+            slot[e] = ok ? (uint32_t)page[e] * bs + (uint32_t)j[e] % bs : 0xFFFFFFFFu;
+            mine += ok ? 1 : 0;
+        }
+        bits = __reduce_or_sync(0xffffffffu, bits);
+        if (bits && lane == 0 && a.err) atomicOr(a.err, bits);
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) ctl.warp_count[wid] = sum;
+        mine = sum - mine;                        // entries of the warp's earlier lanes
+    }
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == wid) mine += total;
+        total += ctl.warp_count[w];
+    }
+    if (wid < kWarps) {
+#pragma unroll
+        for (int e = 0; e < kMaxPerThread; ++e)
+            if (slot[e] != 0xFFFFFFFFu) list[mine++] = slot[e];
+    }
+    __syncthreads();
+    const int tiles = (total + tile - 1) / tile;
+
+    const int active = nu * L.parts;              // consumer warps with work
+    const int unit = wid / L.parts, part = wid - unit * L.parts;
+    const int kvh = (u0 + unit) / L.chunks;
+    const int h0 = kvh * group + (u0 + unit - kvh * L.chunks) * 8 * NT;      // the unit's first query head
+    const int nh = min(8 * NT, (kvh + 1) * group - h0);
+    const int r = lane >> 2, c = lane & 3;
+    float o[NT][MO][4], m[NT][2], l[NT][2];
+    if (wid == kWarps) {
+        // ------------------------------------------------------------------------------ producer
+        const uint32_t bs = (uint32_t)a.p.block_size, bytes = (uint32_t)(hi - lo);
+        for (int it = 0; it < tiles; ++it) {
+            const int st = it % L.stages, use = it / L.stages;
+            const bool free = use == 0 || wait_bounded(&ctl.empty[st], (use - 1) & 1, &ctl.abort, a.err);
+            if (!__all_sync(0xffffffffu, free)) break;
+            // whole tiles of 16: the last one is filled up with its last entry (masked by the consumers)
+            const int cnt = min(tile, total - it * tile), fill = (cnt + 15) & ~15;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(&ctl.full[st], fill * bytes);
+                ctl.issued = it + 1;
+            }
+            __syncwarp();
+            for (int t = lane; t < fill; t += 32) {
+                const uint32_t s = list[it * tile + min(t, cnt - 1)], page = s / bs;
+                ptx::bulk_load(ring + st * stage_bytes + t * L.row_bytes,
+                               a.kv + (int64_t)page * a.page_bytes + (int64_t)(s - page * bs) * a.entry_bytes + lo, bytes,
+                               &ctl.full[st]);
+            }
+        }
+    } else if (wid < active) {
+        // ------------------------------------------------------------------------------ consumers
+        // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
+        uint32_t q[NT][NW][4];
+        float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
+        const uint16_t* qrow = static_cast<const uint16_t*>(a.query) + row * a.q_stride + (int64_t)h0 * D;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uint32_t w[NW][4];
+            const bool live = 8 * t + r < nh;
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (live) v = *reinterpret_cast<const uint4*>(qrow + (int64_t)(8 * t + r) * D + c * (D / 4) + 8 * j);
+                w[j][0] = v.x;
+                w[j][1] = v.y;
+                w[j][2] = v.z;
+                w[j][3] = v.w;
+            }
+            float big = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = act2_to_float2<F16>(w[j][i]);
+                    big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+            const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of big)
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = act2_to_float2<F16>(w[j][i]);
+                    x[2 * i] = v.x * down;
+                    x[2 * i + 1] = v.y * down;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[t][j][i] = E2M1 ? float2_to_act2<true>(x[2 * i], x[2 * i + 1]) : float2_to_act2<true>(x[i], x[i + 4]);
+            }
+            const float up = __uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f);
+            f[t][0] = fminf(__shfl_sync(0xffffffffu, up, 8 * c), 3.0e38f);
+            f[t][1] = fminf(__shfl_sync(0xffffffffu, up, 8 * c + 4), 3.0e38f);
+#pragma unroll
+            for (int i = 0; i < MO; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
+            m[t][0] = m[t][1] = -FLT_MAX;
+            l[t][0] = l[t][1] = 0.0f;
+        }
+        const uint8_t* base = ring + kvh * kUnit - lo;
+        const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
+        for (int it = 0; it < tiles; ++it) {
+            const int st = it % L.stages;
+            const bool landed = wait_bounded(&ctl.full[st], (it / L.stages) & 1, &ctl.abort, a.err);
+            if (!__all_sync(0xffffffffu, landed)) break;
+            const int cnt = min(tile, total - it * tile);
+#pragma unroll 1
+            for (int mt = 0; mt < kMt; ++mt) {
+                const int e0 = 16 * (mt * L.parts + part);
+                if (e0 >= cnt) break;
+                const uint8_t* p0 = base + st * stage_bytes + e0 * L.row_bytes;
+                // ---- logits
+                float s[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+                {
+                    const uint8_t* x0 = p0 + tk * L.row_bytes;
+                    const uint8_t* x1 = x0 + 8 * L.row_bytes;
+                    uint32_t w0[NW], w1[NW], g0[2], g1[2];         // codes, scales of the lane's two halves
+                    if constexpr (D == 128) {
+                        const uint4 v0 = *reinterpret_cast<const uint4*>(x0 + 16 * c), v1 = *reinterpret_cast<const uint4*>(x1 + 16 * c);
+                        w0[0] = v0.x, w0[1] = v0.y, w0[2] = v0.z, w0[3] = v0.w;
+                        w1[0] = v1.x, w1[1] = v1.y, w1[2] = v1.z, w1[3] = v1.w;
+                        const uint32_t h0x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x0 + D + 2 * c));
+                        const uint32_t h1x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x1 + D + 2 * c));
+                        g0[0] = __byte_perm(h0x, 0, 0x1010), g0[1] = __byte_perm(h0x, 0, 0x3232);
+                        g1[0] = __byte_perm(h1x, 0, 0x1010), g1[1] = __byte_perm(h1x, 0, 0x3232);
+                    } else {
+                        const uint2 v0 = *reinterpret_cast<const uint2*>(x0 + 8 * c), v1 = *reinterpret_cast<const uint2*>(x1 + 8 * c);
+                        w0[0] = v0.x, w0[1] = v0.y;
+                        w1[0] = v1.x, w1[1] = v1.y;
+                        // both rows' scales in one conversion
+                        const uint32_t hx = e4m3x2_to_f16x2(x0[D + c] | (uint32_t)x1[D + c] << 8);
+                        g0[0] = g0[1] = __byte_perm(hx, 0, 0x1010);
+                        g1[0] = g1[1] = __byte_perm(hx, 0, 0x3232);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint32_t x[4], y[4];
+                        decode_pairs<E2M1>(w0[j], x);
+                        decode_pairs<E2M1>(w1[j], y);
+                        const int half = j / (NW / 2);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = ptx::mul_f16x2(x[i], g0[half]);
+                            y[i] = ptx::mul_f16x2(y[i], g1[half]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            ptx::mma_16816(s[t], x[0], y[0], x[1], y[1], q[t][j][0], q[t][j][1]);
+                            ptx::mma_16816(s[t], x[2], y[2], x[3], y[3], q[t][j][2], q[t][j][3]);
+                        }
+                    }
+                }
+                // ---- softmax: entries past the end get -infinity
+                bool over = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][e] *= f[t][e & 1];
+                    if (e0 + 16 > cnt) {
+                        if (e0 + tk >= cnt) s[t][0] = s[t][1] = -INFINITY;
+                        if (e0 + 8 + tk >= cnt) s[t][2] = s[t][3] = -INFINITY;
+                    }
+                    over |= fmaxf(s[t][0], s[t][2]) > m[t][0] + kRescale || fmaxf(s[t][1], s[t][3]) > m[t][1] + kRescale;
+                }
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = fmaxf(s[t][e], s[t][e + 2]);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            top = fmaxf(top, m[t][e]);
+                            const float g = ptx::ex2(m[t][e] - top);
+                            m[t][e] = top;
+                            l[t][e] *= g;
+#pragma unroll
+                            for (int i = 0; i < MO; ++i) {
+                                o[t][i][e] *= g;
+                                o[t][i][e + 2] *= g;
+                            }
+                        }
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][e] = ptx::ex2(s[t][e] - m[t][e & 1]);
+                    l[t][0] += s[t][0] + s[t][2];
+                    l[t][1] += s[t][1] + s[t][3];
+                    // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
+                    pb[t][0] = ptx::transpose_8x8(float2_to_act2<true>(s[t][0], s[t][1]));
+                    pb[t][1] = ptx::transpose_8x8(float2_to_act2<true>(s[t][2], s[t][3]));
+                }
+                // ---- output
+                {
+                    const uint8_t* va = p0 + ta * L.row_bytes;
+                    const uint8_t* vb = p0 + tb * L.row_bytes;
+                    constexpr int kHi = 8;
+                    const int off = D / 2 + r * (D / 16), soff = D + D / 16 + (D == 128 ? r : r >> 1);
+                    const uint32_t sab = e4m3x2_to_f16x2(va[soff] | (uint32_t)vb[soff] << 8);
+                    const uint32_t scd = e4m3x2_to_f16x2(va[kHi * L.row_bytes + soff] | (uint32_t)vb[kHi * L.row_bytes + soff] << 8);
+                    uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
+                    load_words<NW / 2>(va + off, wa);
+                    load_words<NW / 2>(vb + off, wb);
+                    load_words<NW / 2>(va + kHi * L.row_bytes + off, wc);
+                    load_words<NW / 2>(vb + kHi * L.row_bytes + off, wd);
+#pragma unroll
+                    for (int j = 0; j < NW / 2; ++j) {
+                        uint32_t x[8], y[8];
+                        decode_across<E2M1>(wa[j], wb[j], x);
+                        decode_across<E2M1>(wc[j], wd[j], y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = ptx::mul_f16x2(x[2 * i], sab), a1 = ptx::mul_f16x2(x[2 * i + 1], sab);
+                            const uint32_t a2 = ptx::mul_f16x2(y[2 * i], scd), a3 = ptx::mul_f16x2(y[2 * i + 1], scd);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) ptx::mma_16816(o[t][4 * j + i], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctl.empty[st]);
+        }
+        // the sums over the lanes that share a head's column
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+            }
+    }
+
+    // ---- join and write.  Lane (r, c) holds elements r * D / 8 ... of heads 2c and 2c + 1 of each block.
+    __syncthreads();
+    const bool failed = ctl.abort != 0;
+    if (failed) {                                  // copies that are still under way land before the CTA ends
+        for (int it = max(0, ctl.issued - L.stages); it < ctl.issued; ++it) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(&ctl.full[it % L.stages], (it / L.stages) & 1) &&
+                   ptx::globaltimer() - t0 < kWaitLimitNs) {
+            }
+        }
+        __syncthreads();
+    }
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.heads_q * D;
+    if (L.parts * L.splits == 1) {
+        if (wid >= active) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * t + 2 * c + e;
+                if (h >= nh) continue;
+                const float sum = failed ? __int_as_float(0x7FC00000) : l[t][e];
+                const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+                uint32_t w[MO];
+#pragma unroll
+                for (int i = 0; i < MO; ++i) w[i] = float2_to_act2<F16>(o[t][i][e] * inv, o[t][i][e + 2] * inv);
+                uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)(h0 + h) * D + r * (D / 8));
+#pragma unroll
+                for (int i = 0; i < MO / 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (a.lse && r == 0)
+                    a.lse[row * a.heads_q + h0 + h] = sum == 0.0f ? -INFINITY : (m[t][e] + log2f(sum)) * 0.6931471805599453f;
+            }
+        return;
+    }
+    // partial outputs [warp][8 NT heads][kHeadStride], then (maximum, sum) [warp][8 NT heads]
+    float* part_o = reinterpret_cast<float*>(ring);
+    float* part_ml = part_o + active * 8 * NT * kHeadStride;
+    if (wid < active) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = wid * 8 * NT + 8 * t + 2 * c + e;
+                float4* dst = reinterpret_cast<float4*>(part_o + h * kHeadStride + r * (D / 8));
+#pragma unroll
+                for (int i = 0; i < MO / 2; ++i)
+                    dst[i] = make_float4(o[t][2 * i][e], o[t][2 * i][e + 2], o[t][2 * i + 1][e], o[t][2 * i + 1][e + 2]);
+                if (r == 0) {
+                    part_ml[2 * h] = m[t][e];
+                    part_ml[2 * h + 1] = failed ? __int_as_float(0x7FC00000) : l[t][e];
+                }
+            }
+    }
+    if (L.splits > 1) ptx::cluster_sync();
+    else __syncthreads();
+    const int pieces = nu * 8 * NT * (D / 8);      // 8 elements of a head each
+    for (int i = rank * kThreads + tid; i < pieces; i += L.splits * kThreads) {
+        const int uh = i / (D / 8), d8 = i - uh * (D / 8), un = uh / (8 * NT), h = uh - un * 8 * NT;
+        const int kv = (u0 + un) / L.chunks, first = kv * group + (u0 + un - kv * L.chunks) * 8 * NT;
+        if (first + h >= (kv + 1) * group) continue;
+        float top = -FLT_MAX;
+        for (int s = 0; s < L.splits; ++s)
+            for (int pt = 0; pt < L.parts; ++pt) {
+                const float* ml = part_ml + 2 * ((un * L.parts + pt) * 8 * NT + h);
+                top = fmaxf(top, L.splits > 1 ? __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(ml, s))) : *ml);
+            }
+        float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < L.splits; ++s)
+            for (int pt = 0; pt < L.parts; ++pt) {
+                const int w = (un * L.parts + pt) * 8 * NT + h;
+                const float* ml = part_ml + 2 * w;
+                const float* src = part_o + w * kHeadStride + 8 * d8;
+                float pm, pl;
+                float4 x, y;
+                if (L.splits > 1) {
+                    const uint32_t am = ptx::cluster_addr(ml, s), as = ptx::cluster_addr(src, s);
+                    pm = __uint_as_float(ptx::ld_cluster(am));
+                    pl = __uint_as_float(ptx::ld_cluster(am + 4));
+                    x = ptx::ld_cluster4(as);
+                    y = ptx::ld_cluster4(as + 16);
+                } else {
+                    pm = ml[0];
+                    pl = ml[1];
+                    x = *reinterpret_cast<const float4*>(src);
+                    y = *reinterpret_cast<const float4*>(src + 4);
+                }
+                const float g = ptx::ex2(pm - top);
+                sum = fmaf(g, pl, sum);
+                acc[0] = fmaf(g, x.x, acc[0]), acc[1] = fmaf(g, x.y, acc[1]), acc[2] = fmaf(g, x.z, acc[2]);
+                acc[3] = fmaf(g, x.w, acc[3]), acc[4] = fmaf(g, y.x, acc[4]), acc[5] = fmaf(g, y.y, acc[5]);
+                acc[6] = fmaf(g, y.z, acc[6]), acc[7] = fmaf(g, y.w, acc[7]);
+            }
+        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = float2_to_act2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        *reinterpret_cast<uint4*>(out + (int64_t)(first + h) * D + 8 * d8) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (a.lse && d8 == 0)
+            a.lse[row * a.heads_q + first + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncwarp();
+    if (L.splits > 1) ptx::cluster_sync();         // no CTA leaves while another reads its partial results
+}
+
+// Shared-memory row stride of `bytes` copied bytes: 32 or 96 beyond a multiple of 128
+int row_stride(int bytes)
+{
+    const int s32 = (bytes - 32 + 127) / 128 * 128 + 32, s96 = (bytes - 96 + 127) / 128 * 128 + 96;
+    const int a = bytes <= 32 ? 32 : s32, b = bytes <= 96 ? 96 : s96;
+    return a < b ? a : b;
+}
+
+template <bool F16, bool E2M1, int D, int NT>
+cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
+{
+    const int group = a.heads_q / a.heads_kv;
+    Layout L;
+    L.chunks = (group + 8 * NT - 1) / (8 * NT);
+    L.units = a.heads_kv * L.chunks;
+    const int k = a.p.sparse_count;
+    const int64_t rows = a.p.rows;
+    L.ctas = (L.units + kWarps - 1) / kWarps;
+    L.per_cta = (L.units + L.ctas - 1) / L.ctas;
+    L.splits = 1;
+    const int slots = (NT == 1 ? 2 : 1) * sms;
+    while (L.splits < 8 && rows * L.ctas * L.splits * 2 <= slots && k > 64 * L.splits) L.splits *= 2;
+    L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
+    L.parts = kWarps / L.per_cta;
+    L.per_split = (k + L.splits - 1) / L.splits;
+    // the widest range of an entry that a CTA copies
+    int widest = 0;
+    for (int u0 = 0; u0 < L.units; u0 += L.per_cta) {
+        const int u1 = (u0 + L.per_cta < L.units ? u0 + L.per_cta : L.units) - 1, unit = kv_unit_bytes(D);
+        const int lo = (u0 / L.chunks) * unit & ~15, hi = ((u1 / L.chunks + 1) * unit + 15) & ~15;
+        widest = hi - lo > widest ? hi - lo : widest;
+    }
+    L.row_bytes = row_stride(widest);
+    const int stage = 16 * kMt * L.parts * L.row_bytes;
+    const int room = (NT == 1 ? 100 : 200) * 1024;
+    L.list_off = (sizeof(Control) + 127) & ~127;
+    L.ring_off = (L.list_off + 4 * L.per_split + 127) & ~127;
+    L.stages = (room - L.ring_off) / stage;
+    L.stages = L.stages < 2 ? 2 : (L.stages > kMaxStages ? kMaxStages : L.stages);
+    int ring = L.stages * stage;
+    const int join = kWarps * 8 * NT * ((D + 4) + 2) * 4;
+    if (L.parts * L.splits > 1 && ring < join) ring = join;
+    const int smem = L.ring_off + ring;
+    const int64_t grid = rows * L.ctas * L.splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    auto kernel = attention_kernel<F16, E2M1, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, L);
+}
+
+template <bool F16, bool E2M1>
+cudaError_t launch_type(const AttentionArgs& a, int head_dim, int sms, cudaStream_t st)
+{
+    // query heads per unit: as few blocks of eight as hold the group, within the registers (an
+    // accumulator of D x 8 NT fp32 per warp)
+    const int group = a.heads_q / a.heads_kv;
+    if (head_dim == 64) {
+        if (group <= 8) return launch_shape<F16, E2M1, 64, 1>(a, sms, st);
+        if (group <= 16) return launch_shape<F16, E2M1, 64, 2>(a, sms, st);
+        return launch_shape<F16, E2M1, 64, 4>(a, sms, st);
+    }
+    return group <= 8 ? launch_shape<F16, E2M1, 128, 1>(a, sms, st) : launch_shape<F16, E2M1, 128, 2>(a, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attention(const AttentionArgs& a, int head_dim, bool f16, bool e2m1, int, cudaStream_t st)
+cudaError_t launch_attention(const AttentionArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
 {
-    if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, st) : launch_type<true, false>(a, head_dim, st);
-    return e2m1 ? launch_type<false, true>(a, head_dim, st) : launch_type<false, false>(a, head_dim, st);
+    if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
+    return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
 }
 
 }  // namespace qli

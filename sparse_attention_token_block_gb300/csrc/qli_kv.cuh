@@ -29,12 +29,18 @@ __device__ __forceinline__ uint32_t float2_to_act2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two scale bytes as fp16 (exact), the low byte in the low half
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t bytes)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bytes)));
+    return h;
+}
+
 // A scale byte (float8_e4m3fn) as fp32, and the scale of a block: e4m3(min(a, 448)) as a byte
 __device__ __forceinline__ float e4m3_to_float(uint32_t byte)
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(byte) & 0xFFFFu)));
 }
 
 __device__ __forceinline__ uint32_t float_to_e4m3(float a)
@@ -73,6 +79,51 @@ __device__ __forceinline__ void decode8(uint32_t w, float (&v)[8])
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)((int32_t)(w << (28 - 4 * i)) >> 28);
+    }
+}
+
+// Eight codes of one vector in a word as four fp16 pairs, exactly: E2M1 elements (2i, 2i + 1), int4
+// elements (i, i + 4).  The int4 nibbles u = code + 8 are placed as fractions of fp16 numbers (1024 + u
+// at bits 0-3; 1024 + 16 u at bits 4-7).
+template <bool E2M1>
+__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t (&o)[4])
+{
+    if (E2M1) {
+        e2m1x8_to_f16x2(w, o);
+        return;
+    }
+    const uint32_t u = w ^ 0x88888888u, v = u >> 8;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"((u & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[1]) : "r"((u & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"((v & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[3]) : "r"((v & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+}
+
+// Eight codes each of two vectors as eight fp16 pairs (a's element e, b's element e), exactly
+template <bool E2M1>
+__device__ __forceinline__ void decode_across(uint32_t a, uint32_t b, uint32_t (&o)[8])
+{
+    if (E2M1) {
+        // bytes of (a's nibble, b's nibble) for the even and the odd elements
+        const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+        uint32_t x[4], y[4];
+        e2m1x8_to_f16x2(even, x);
+        e2m1x8_to_f16x2(odd, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = x[i];
+            o[2 * i + 1] = y[i];
+        }
+        return;
+    }
+    const uint32_t lo = __byte_perm(a, b, 0x5410), hi = __byte_perm(a, b, 0x7632);
+    uint32_t x[4], y[4];
+    decode_pairs<false>(lo, x);             // (a's element i, b's element i) of the low halves
+    decode_pairs<false>(hi, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[i] = x[i];
+        o[4 + i] = y[i];
     }
 }
 
