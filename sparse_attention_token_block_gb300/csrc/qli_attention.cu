@@ -4,10 +4,12 @@
 //
 // A cluster of `splits` CTAs works on one row (or a slice of its KV heads), each on a slice of the
 // list.  A CTA first resolves its slice -- index, bounds, block_table -- into a compact list of the
-// valid entries; a producer warp then streams those entries into a ring of shared-memory stages, one
-// bulk copy per entry (all of the CTA's KV heads lie side by side in it).  Each of eight consumer
-// warps carries one unit, a KV head with up to 8 * NT of its query heads, over its share of the
-// entries:
+// valid entries' addresses.  Each of its eight warps then carries one unit, a KV head with up to
+// 8 * NT of its query heads, over its share of the entries, 16 at a time, on its own: it copies its
+// head's bytes of each entry (144 for D = 128) into a ring of its own with 16-byte asynchronous
+// copies, kStages tiles deep, and meets no other warp until the end.  (One bulk copy per entry from
+// a producer warp, all heads in one copy, measured slower: an SM takes about 44 cycles per bulk copy
+// whatever its size.)
 //
 //   * logits:  S^T (16 entries x 8 heads) = K Q^T.  A lane decodes 4-bit keys straight into the A
 //     fragment: lane (r, c) of a warp holds rows r and r + 8, so it takes 1/4 of two key vectors as one
@@ -26,8 +28,7 @@
 // bfloat16 fits fp16 too (elements below 2^-14 of the largest lose bits of 2^-25 of it).
 //
 // Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over
-// the cluster) and are joined in a fixed order.  Every wait is bounded (0.2 s): on expiry the kernel
-// records kErrTimeout, writes NaN, lets its copies land and returns.
+// the cluster) and are joined in a fixed order.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -38,14 +39,11 @@ namespace qli {
 
 namespace {
 
-constexpr int kWarps = 8;                         // consumer warps
-constexpr int kBuilders = 32 * kWarps;            // threads that resolve the list
-constexpr int kThreads = kBuilders + 32;          // and the producer warp
-constexpr int kMt = 2;                            // tiles of 16 entries per warp and stage
-constexpr int kMaxStages = 8;
-constexpr int kMaxPerThread = kMaxSparse / kBuilders;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 4;                        // tiles of 16 entries in a warp's ring
+constexpr int kMaxPerThread = kMaxSparse / kThreads;
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
-constexpr uint64_t kWaitLimitNs = 200000000ull;
 
 // How a launch is laid out (host)
 struct Layout {
@@ -56,32 +54,13 @@ struct Layout {
     int32_t parts;         // warps that share a unit: kWarps / per_cta
     int32_t splits;        // CTAs of the cluster, each with a slice of the list
     int32_t per_split;     // list positions per slice
-    int32_t stages;
-    int32_t row_bytes;     // entry stride in a stage, 32 or 96 beyond a multiple of 128
-    int32_t list_off, ring_off;   // shared-memory offsets
+    int32_t ring_off;      // shared-memory offset of the rings, behind the list
 };
 
-struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    int32_t warp_count[kWarps];
-    int32_t issued;        // stages the producer filled
-    uint32_t abort;
-};
-
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
-{
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    while (true) {
-        if (ptx::mbar_try_wait_sleep(bar, parity, 100000u)) return true;
-        if (*abort) return false;
-        if (ptx::globaltimer() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            if (err) atomicOr(err, kErrTimeout);
-            return false;
-        }
-    }
-}
+// One KV head's bytes of an entry, widened to 16-byte pieces (they start on a multiple of 8 for
+// D = 64), and the stride of entries in a ring: 32 or 96 beyond a multiple of 128
+constexpr int pieces_of(int d) { return d == 128 ? 9 : 5; }
+constexpr int row_bytes_of(int d) { return d == 128 ? 160 : 96; }
 
 // Entry (of a group of eight) that row r of an 8-row fragment holds.  Rows 2c and 2c + 1 hold entries
 // c and 4 + (c + 2) % 4: with an entry stride of 32 or 96 modulo 128 bytes, the four entries that a
@@ -102,50 +81,36 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
 }
 
 template <bool F16, bool E2M1, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L)
 {
     constexpr int kUnit = kv_unit_bytes(D);
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
+    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kTile = 16 * kRow;
+    constexpr int kCopies = (16 * kPieces + 31) / 32;               // copies per lane and tile
     extern __shared__ __align__(128) uint8_t smem[];
-    Control& ctl = *reinterpret_cast<Control*>(smem);
-    uint32_t* list = reinterpret_cast<uint32_t*>(smem + L.list_off);
-    uint8_t* ring = smem + L.ring_off;
+    __shared__ int32_t warp_count[kWarps];
+    int64_t* list = reinterpret_cast<int64_t*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
     const int64_t task = blockIdx.x / L.splits, row = task / L.ctas;
     const int u0 = (int)(task - row * L.ctas) * L.per_cta, nu = min(L.per_cta, L.units - u0);
     const int group = a.heads_q / a.heads_kv;
-    // the bytes of an entry that hold the CTA's KV heads
-    const int lo = (u0 / L.chunks) * kUnit & ~15, hi = (((u0 + nu - 1) / L.chunks + 1) * kUnit + 15) & ~15;
-    const int tile = 16 * kMt * L.parts;
-    const int stage_bytes = tile * L.row_bytes;
-
-    if (tid == 0) {
-        for (int s = 0; s < L.stages; ++s) {
-            ptx::mbar_init(&ctl.full[s], 1);
-            ptx::mbar_init(&ctl.empty[s], nu * L.parts);
-        }
-        ctl.issued = 0;
-        ctl.abort = 0;
-        ptx::fence_mbar_init();
-    }
     ptx::pdl_wait();
 
-    // ---- the slice's valid entries, in list order, as slots page * block_size + position in the page
+    // ---- the slice's valid entries, in list order, as byte offsets into the pool
     const int k0 = rank * L.per_split, n = max(0, min(L.per_split, a.p.sparse_count - k0));
-    uint32_t slot[kMaxPerThread];
+    int32_t j[kMaxPerThread], page[kMaxPerThread];
     int mine = 0;
-    if (wid < kWarps) {
+    const uint32_t bs = (uint32_t)a.p.block_size;
+    {
         const int64_t b = row_batch(a.p, a.seq_lens_q, row);
         const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
         const int32_t* idx = a.idx + row * a.p.sparse_count + k0;
         const int32_t* table = a.block_table + b * a.p.max_blocks_per_seq;
-        const int per = (n + kBuilders - 1) / kBuilders, at = tid * per;
-        const uint32_t bs = (uint32_t)a.p.block_size;
-        int32_t j[kMaxPerThread], page[kMaxPerThread];
+        const int per = (n + kThreads - 1) / kThreads, at = tid * per;
         uint32_t bits = 0;
 #pragma unroll
         for (int e = 0; e < kMaxPerThread; ++e) j[e] = e < per && at + e < n ? idx[at + e] : -1;
@@ -160,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         for (int e = 0; e < kMaxPerThread; ++e) {
             const bool ok = j[e] >= 0 && page[e] >= 0 && page[e] < a.p.num_blocks;
             if (j[e] >= 0 && !ok) bits |= kErrPage;
-            slot[e] = ok ? (uint32_t)page[e] * bs + (uint32_t)j[e] % bs : 0xFFFFFFFFu;
+            if (!ok) j[e] = -1;
             mine += ok ? 1 : 0;
         }
         bits = __reduce_or_sync(0xffffffffu, bits);
@@ -171,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += v;
         }
-        if (lane == 31) ctl.warp_count[wid] = sum;
+        if (lane == 31) warp_count[wid] = sum;
         mine = sum - mine;                        // entries of the warp's earlier lanes
     }
     __syncthreads();
@@ -179,15 +144,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w == wid) mine += total;
-        total += ctl.warp_count[w];
+        total += warp_count[w];
     }
-    if (wid < kWarps) {
 #pragma unroll
-        for (int e = 0; e < kMaxPerThread; ++e)
-            if (slot[e] != 0xFFFFFFFFu) list[mine++] = slot[e];
-    }
+    for (int e = 0; e < kMaxPerThread; ++e)
+        if (j[e] >= 0)
+            list[mine++] = page[e] * a.page_bytes + (int64_t)((uint32_t)j[e] % bs) * a.entry_bytes;
     __syncthreads();
-    const int tiles = (total + tile - 1) / tile;
 
     const int active = nu * L.parts;              // consumer warps with work
     const int unit = wid / L.parts, part = wid - unit * L.parts;
@@ -196,29 +159,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     const int nh = min(8 * NT, (kvh + 1) * group - h0);
     const int r = lane >> 2, c = lane & 3;
     float o[NT][MO][4], m[NT][2], l[NT][2];
-    if (wid == kWarps) {
-        // ------------------------------------------------------------------------------ producer
-        const uint32_t bs = (uint32_t)a.p.block_size, bytes = (uint32_t)(hi - lo);
-        for (int it = 0; it < tiles; ++it) {
-            const int st = it % L.stages, use = it / L.stages;
-            const bool free = use == 0 || wait_bounded(&ctl.empty[st], (use - 1) & 1, &ctl.abort, a.err);
-            if (!__all_sync(0xffffffffu, free)) break;
-            // whole tiles of 16: the last one is filled up with its last entry (masked by the consumers)
-            const int cnt = min(tile, total - it * tile), fill = (cnt + 15) & ~15;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(&ctl.full[st], fill * bytes);
-                ctl.issued = it + 1;
+    if (wid < active) {
+        // this lane's 16-byte copies of a tile: piece x % kPieces of entry x / kPieces
+        const int tiles = (total + 15) / 16;
+        const int head_lo = kvh * kUnit & ~15;
+        uint8_t* ring = smem + L.ring_off + wid * kStages * kTile;
+        auto copy_tile = [&](int tl, int stage) {
+            if (tl < tiles) {
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int x = lane + 32 * i, e = x / kPieces, pc = x - e * kPieces;
+                    // the last tile is filled up with its last entry (masked below)
+                    if (x < 16 * kPieces)
+                        ptx::cp_async<16>(ring + stage * kTile + e * kRow + 16 * pc,
+                                          a.kv + list[min(16 * tl + e, total - 1)] + head_lo + 16 * pc);
+                }
             }
-            __syncwarp();
-            for (int t = lane; t < fill; t += 32) {
-                const uint32_t s = list[it * tile + min(t, cnt - 1)], page = s / bs;
-                ptx::bulk_load(ring + st * stage_bytes + t * L.row_bytes,
-                               a.kv + (int64_t)page * a.page_bytes + (int64_t)(s - page * bs) * a.entry_bytes + lo, bytes,
-                               &ctl.full[st]);
-            }
-        }
-    } else if (wid < active) {
-        // ------------------------------------------------------------------------------ consumers
+            ptx::cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy_tile(part + i * L.parts, i);
         // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
@@ -271,25 +231,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             m[t][0] = m[t][1] = -FLT_MAX;
             l[t][0] = l[t][1] = 0.0f;
         }
-        const uint8_t* base = ring + kvh * kUnit - lo;
+        const uint8_t* base = ring + kvh * kUnit - head_lo;
         const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
-        for (int it = 0; it < tiles; ++it) {
-            const int st = it % L.stages;
-            const bool landed = wait_bounded(&ctl.full[st], (it / L.stages) & 1, &ctl.abort, a.err);
-            if (!__all_sync(0xffffffffu, landed)) break;
-            const int cnt = min(tile, total - it * tile);
+        int stage = 0;
 #pragma unroll 1
-            for (int mt = 0; mt < kMt; ++mt) {
-                const int e0 = 16 * (mt * L.parts + part);
-                if (e0 >= cnt) break;
-                const uint8_t* p0 = base + st * stage_bytes + e0 * L.row_bytes;
+        for (int tl = part; tl < tiles; tl += L.parts) {
+            ptx::cp_async_wait<kStages - 2>();     // the lane's copies of this tile have landed ...
+            __syncwarp();                          // ... and the others'; the tile before it is free
+            copy_tile(tl + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
+            const int e0 = 16 * tl, cnt = total;
+            const uint8_t* p0 = base + stage * kTile;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            {
                 // ---- logits
                 float s[NT][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
                 {
-                    const uint8_t* x0 = p0 + tk * L.row_bytes;
-                    const uint8_t* x1 = x0 + 8 * L.row_bytes;
+                    const uint8_t* x0 = p0 + tk * kRow;
+                    const uint8_t* x1 = x0 + 8 * kRow;
                     uint32_t w0[NW], w1[NW], g0[2], g1[2];         // codes, scales of the lane's two halves
                     if constexpr (D == 128) {
                         const uint4 v0 = *reinterpret_cast<const uint4*>(x0 + 16 * c), v1 = *reinterpret_cast<const uint4*>(x1 + 16 * c);
@@ -371,17 +331,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 }
                 // ---- output
                 {
-                    const uint8_t* va = p0 + ta * L.row_bytes;
-                    const uint8_t* vb = p0 + tb * L.row_bytes;
+                    const uint8_t* va = p0 + ta * kRow;
+                    const uint8_t* vb = p0 + tb * kRow;
                     constexpr int kHi = 8;
                     const int off = D / 2 + r * (D / 16), soff = D + D / 16 + (D == 128 ? r : r >> 1);
                     const uint32_t sab = e4m3x2_to_f16x2(va[soff] | (uint32_t)vb[soff] << 8);
-                    const uint32_t scd = e4m3x2_to_f16x2(va[kHi * L.row_bytes + soff] | (uint32_t)vb[kHi * L.row_bytes + soff] << 8);
+                    const uint32_t scd = e4m3x2_to_f16x2(va[kHi * kRow + soff] | (uint32_t)vb[kHi * kRow + soff] << 8);
                     uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
                     load_words<NW / 2>(va + off, wa);
                     load_words<NW / 2>(vb + off, wb);
-                    load_words<NW / 2>(va + kHi * L.row_bytes + off, wc);
-                    load_words<NW / 2>(vb + kHi * L.row_bytes + off, wd);
+                    load_words<NW / 2>(va + kHi * kRow + off, wc);
+                    load_words<NW / 2>(vb + kHi * kRow + off, wd);
 #pragma unroll
                     for (int j = 0; j < NW / 2; ++j) {
                         uint32_t x[8], y[8];
@@ -397,8 +357,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ctl.empty[st]);
         }
         // the sums over the lanes that share a head's column
 #pragma unroll
@@ -412,17 +370,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     }
 
     // ---- join and write.  Lane (r, c) holds elements r * D / 8 ... of heads 2c and 2c + 1 of each block.
-    __syncthreads();
-    const bool failed = ctl.abort != 0;
-    if (failed) {                                  // copies that are still under way land before the CTA ends
-        for (int it = max(0, ctl.issued - L.stages); it < ctl.issued; ++it) {
-            const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(&ctl.full[it % L.stages], (it / L.stages) & 1) &&
-                   ptx::globaltimer() - t0 < kWaitLimitNs) {
-            }
-        }
-        __syncthreads();
-    }
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.heads_q * D;
     if (L.parts * L.splits == 1) {
         if (wid >= active) return;
@@ -432,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             for (int e = 0; e < 2; ++e) {
                 const int h = 8 * t + 2 * c + e;
                 if (h >= nh) continue;
-                const float sum = failed ? __int_as_float(0x7FC00000) : l[t][e];
+                const float sum = l[t][e];
                 const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
                 uint32_t w[MO];
 #pragma unroll
@@ -446,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         return;
     }
     // partial outputs [warp][8 NT heads][kHeadStride], then (maximum, sum) [warp][8 NT heads]
-    float* part_o = reinterpret_cast<float*>(ring);
+    __syncthreads();                               // the rings are free
+    float* part_o = reinterpret_cast<float*>(smem + L.ring_off);
     float* part_ml = part_o + active * 8 * NT * kHeadStride;
     if (wid < active) {
 #pragma unroll
@@ -460,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     dst[i] = make_float4(o[t][2 * i][e], o[t][2 * i][e + 2], o[t][2 * i + 1][e], o[t][2 * i + 1][e + 2]);
                 if (r == 0) {
                     part_ml[2 * h] = m[t][e];
-                    part_ml[2 * h + 1] = failed ? __int_as_float(0x7FC00000) : l[t][e];
+                    part_ml[2 * h + 1] = l[t][e];
                 }
             }
     }
@@ -515,14 +463,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     if (L.splits > 1) ptx::cluster_sync();         // no CTA leaves while another reads its partial results
 }
 
-// Shared-memory row stride of `bytes` copied bytes: 32 or 96 beyond a multiple of 128
-int row_stride(int bytes)
-{
-    const int s32 = (bytes - 32 + 127) / 128 * 128 + 32, s96 = (bytes - 96 + 127) / 128 * 128 + 96;
-    const int a = bytes <= 32 ? 32 : s32, b = bytes <= 96 ? 96 : s96;
-    return a < b ? a : b;
-}
-
 template <bool F16, bool E2M1, int D, int NT>
 cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
 {
@@ -535,26 +475,13 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.ctas = (L.units + kWarps - 1) / kWarps;
     L.per_cta = (L.units + L.ctas - 1) / L.ctas;
     L.splits = 1;
-    const int slots = (NT == 1 ? 2 : 1) * sms;
+    const int slots = (NT * D <= 128 ? 2 : 1) * sms;
     while (L.splits < 8 && rows * L.ctas * L.splits * 2 <= slots && k > 64 * L.splits) L.splits *= 2;
     L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
     L.parts = kWarps / L.per_cta;
     L.per_split = (k + L.splits - 1) / L.splits;
-    // the widest range of an entry that a CTA copies
-    int widest = 0;
-    for (int u0 = 0; u0 < L.units; u0 += L.per_cta) {
-        const int u1 = (u0 + L.per_cta < L.units ? u0 + L.per_cta : L.units) - 1, unit = kv_unit_bytes(D);
-        const int lo = (u0 / L.chunks) * unit & ~15, hi = ((u1 / L.chunks + 1) * unit + 15) & ~15;
-        widest = hi - lo > widest ? hi - lo : widest;
-    }
-    L.row_bytes = row_stride(widest);
-    const int stage = 16 * kMt * L.parts * L.row_bytes;
-    const int room = (NT == 1 ? 100 : 200) * 1024;
-    L.list_off = (sizeof(Control) + 127) & ~127;
-    L.ring_off = (L.list_off + 4 * L.per_split + 127) & ~127;
-    L.stages = (room - L.ring_off) / stage;
-    L.stages = L.stages < 2 ? 2 : (L.stages > kMaxStages ? kMaxStages : L.stages);
-    int ring = L.stages * stage;
+    L.ring_off = (8 * L.per_split + 127) & ~127;
+    int ring = kWarps * kStages * 16 * row_bytes_of(D);
     const int join = kWarps * 8 * NT * ((D + 4) + 2) * 4;
     if (L.parts * L.splits > 1 && ring < join) ring = join;
     const int smem = L.ring_off + ring;
