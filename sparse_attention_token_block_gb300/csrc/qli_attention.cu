@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;                        // tiles of 16 entries in a warp's ring
 constexpr int kMaxPerThread = kMaxSparse / kThreads;
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
 
@@ -61,17 +60,35 @@ struct Layout {
 // D = 64), and the stride of entries in a ring: 32 or 96 beyond a multiple of 128
 constexpr int pieces_of(int d) { return d == 128 ? 9 : 5; }
 constexpr int row_bytes_of(int d) { return d == 128 ? 160 : 96; }
+constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }          // of 32 entries each (two CTAs fit an SM)
 
 // Entry (of a group of eight) that row r of an 8-row fragment holds.  Rows 2c and 2c + 1 hold entries
 // c and 4 + (c + 2) % 4: with an entry stride of 32 or 96 modulo 128 bytes, the four entries that a
 // quarter-warp reads of V and the two that it reads of K then lie in different banks.
 __device__ __forceinline__ int entry_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
 
+// A value of another CTA's shared memory (of this CTA's when there is no cluster)
+__device__ __forceinline__ float peer_load(const float* p, int rank, int splits)
+{
+    return splits > 1 ? __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(p, rank))) : *p;
+}
+
+__device__ __forceinline__ float4 peer_load4(const float* p, int rank, int splits)
+{
+    return splits > 1 ? ptx::ld_cluster4(ptx::cluster_addr(p, rank)) : *reinterpret_cast<const float4*>(p);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
 {
-    static_assert(N == 1 || N == 2, "one or two words");
-    if constexpr (N == 2) {
+    static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (N == 2) {
         const uint2 v = *reinterpret_cast<const uint2*>(p);
         w[0] = v.x;
         w[1] = v.y;
@@ -88,8 +105,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
-    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kTile = 16 * kRow;
-    constexpr int kCopies = (16 * kPieces + 31) / 32;               // copies per lane and tile
+    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kPair = 32 * kRow, kStages = stages_of(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t warp_count[kWarps];
     int64_t* list = reinterpret_cast<int64_t*>(smem);
@@ -148,8 +164,12 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
 #pragma unroll
     for (int e = 0; e < kMaxPerThread; ++e)
-        if (j[e] >= 0)
-            list[mine++] = page[e] * a.page_bytes + (int64_t)((uint32_t)j[e] % bs) * a.entry_bytes;
+        if (j[e] >= 0) {
+            const int64_t at = page[e] * a.page_bytes + (int64_t)((uint32_t)j[e] % bs) * a.entry_bytes;
+            list[mine++] = at;
+            if (mine == total)                    // filled up to 32 with the last one (masked below)
+                for (int x = mine; x & 31; ++x) list[x] = at;
+        }
     __syncthreads();
 
     const int active = nu * L.parts;              // consumer warps with work
@@ -160,25 +180,33 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     const int r = lane >> 2, c = lane & 3;
     float o[NT][MO][4], m[NT][2], l[NT][2];
     if (wid < active) {
-        // this lane's 16-byte copies of a tile: piece x % kPieces of entry x / kPieces
-        const int tiles = (total + 15) / 16;
+        // The lane's 16-byte copies of 32 entries: four lanes take 64 bytes in a row of one entry, eight
+        // entries at a time, and the one piece that is left over goes by entry = lane.  Code bytes of odd
+        // heads start 16 bytes past a sector, so there the left-over piece is the first one.
+        const int pairs = (total + 31) / 32;
         const int head_lo = kvh * kUnit & ~15;
-        uint8_t* ring = smem + L.ring_off + wid * kStages * kTile;
-        auto copy_tile = [&](int tl, int stage) {
-            if (tl < tiles) {
+        const int quad_at = (D == 128 && (kvh & 1)) ? 16 : 0, rest_at = quad_at ? 0 : 16 * (kPieces - 1);
+        uint8_t* ring = smem + L.ring_off + wid * kStages * kPair;
+        const uint8_t* src = a.kv + head_lo + quad_at + 16 * (lane & 3);
+        const uint8_t* src_rest = a.kv + head_lo + rest_at;
+        uint8_t* dst = ring + (lane >> 2) * kRow + quad_at + 16 * (lane & 3);
+        uint8_t* dst_rest = ring + lane * kRow + rest_at;
+        auto copy_pair = [&](int pi, int stage) {
+            if (pi < pairs) {
+                const int64_t* at = list + 32 * pi;
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int x = lane + 32 * i, e = x / kPieces, pc = x - e * kPieces;
-                    // the last tile is filled up with its last entry (masked below)
-                    if (x < 16 * kPieces)
-                        ptx::cp_async<16>(ring + stage * kTile + e * kRow + 16 * pc,
-                                          a.kv + list[min(16 * tl + e, total - 1)] + head_lo + 16 * pc);
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* x = src + at[(lane >> 2) + 8 * i];
+#pragma unroll
+                    for (int y = 0; y < kPieces / 4; ++y)
+                        ptx::cp_async<16>(dst + stage * kPair + 8 * i * kRow + 64 * y, x + 64 * y);
                 }
+                ptx::cp_async<16>(dst_rest + stage * kPair, src_rest + at[lane]);
             }
             ptx::cp_async_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) copy_tile(part + i * L.parts, i);
+        for (int i = 0; i < kStages - 1; ++i) copy_pair(part + i * L.parts, i);
         // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
@@ -231,129 +259,147 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
             m[t][0] = m[t][1] = -FLT_MAX;
             l[t][0] = l[t][1] = 0.0f;
         }
-        const uint8_t* base = ring + kvh * kUnit - head_lo;
         const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
+        const uint8_t* kp = ring + kvh * kUnit - head_lo + tk * kRow;          // the lane's key rows, value entries
+        const uint8_t* vp = ring + kvh * kUnit - head_lo;
         int stage = 0;
 #pragma unroll 1
-        for (int tl = part; tl < tiles; tl += L.parts) {
-            ptx::cp_async_wait<kStages - 2>();     // the lane's copies of this tile have landed ...
-            __syncwarp();                          // ... and the others'; the tile before it is free
-            copy_tile(tl + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
-            const int e0 = 16 * tl, cnt = total;
-            const uint8_t* p0 = base + stage * kTile;
+        for (int pi = part; pi < pairs; pi += L.parts) {
+            ptx::cp_async_wait<kStages - 2>();     // the lane's copies of these entries have landed ...
+            __syncwarp();                          // ... and the others'; the entries before them are done with
+            copy_pair(pi + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
+            const uint8_t* kx = kp + stage * kPair;
+            const uint8_t* vx = vp + stage * kPair;
             stage = stage == kStages - 1 ? 0 : stage + 1;
-            {
-                // ---- logits
-                float s[NT][4];
+            // ---- logits of two tiles of 16 entries
+            float s[2][NT][4];
+            uint32_t w[2][2][NW], g[2][2][2];      // tile, row r or r + 8: codes and the two halves' scales
 #pragma unroll
-                for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-                {
-                    const uint8_t* x0 = p0 + tk * kRow;
-                    const uint8_t* x1 = x0 + 8 * kRow;
-                    uint32_t w0[NW], w1[NW], g0[2], g1[2];         // codes, scales of the lane's two halves
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint8_t* x = kx + (16 * u + 8 * y) * kRow;
+                    load_words<NW>(x + (D / 8) * c, w[u][y]);
                     if constexpr (D == 128) {
-                        const uint4 v0 = *reinterpret_cast<const uint4*>(x0 + 16 * c), v1 = *reinterpret_cast<const uint4*>(x1 + 16 * c);
-                        w0[0] = v0.x, w0[1] = v0.y, w0[2] = v0.z, w0[3] = v0.w;
-                        w1[0] = v1.x, w1[1] = v1.y, w1[2] = v1.z, w1[3] = v1.w;
-                        const uint32_t h0x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x0 + D + 2 * c));
-                        const uint32_t h1x = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x1 + D + 2 * c));
-                        g0[0] = __byte_perm(h0x, 0, 0x1010), g0[1] = __byte_perm(h0x, 0, 0x3232);
-                        g1[0] = __byte_perm(h1x, 0, 0x1010), g1[1] = __byte_perm(h1x, 0, 0x3232);
+                        const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x + D + 2 * c));
+                        g[u][y][0] = __byte_perm(h, 0, 0x1010);
+                        g[u][y][1] = __byte_perm(h, 0, 0x3232);
                     } else {
-                        const uint2 v0 = *reinterpret_cast<const uint2*>(x0 + 8 * c), v1 = *reinterpret_cast<const uint2*>(x1 + 8 * c);
-                        w0[0] = v0.x, w0[1] = v0.y;
-                        w1[0] = v1.x, w1[1] = v1.y;
-                        // both rows' scales in one conversion
-                        const uint32_t hx = e4m3x2_to_f16x2(x0[D + c] | (uint32_t)x1[D + c] << 8);
-                        g0[0] = g0[1] = __byte_perm(hx, 0, 0x1010);
-                        g1[0] = g1[1] = __byte_perm(hx, 0, 0x3232);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NW; ++j) {
-                        uint32_t x[4], y[4];
-                        decode_pairs<E2M1>(w0[j], x);
-                        decode_pairs<E2M1>(w1[j], y);
-                        const int half = j / (NW / 2);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            x[i] = ptx::mul_f16x2(x[i], g0[half]);
-                            y[i] = ptx::mul_f16x2(y[i], g1[half]);
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            ptx::mma_16816(s[t], x[0], y[0], x[1], y[1], q[t][j][0], q[t][j][1]);
-                            ptx::mma_16816(s[t], x[2], y[2], x[3], y[3], q[t][j][2], q[t][j][3]);
-                        }
+                        g[u][y][0] = g[u][y][1] = __byte_perm(e4m3x2_to_f16x2(x[D + c]), 0, 0x1010);
                     }
                 }
-                // ---- softmax: entries past the end get -infinity
-                bool over = false;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] *= f[t][e & 1];
-                    if (e0 + 16 > cnt) {
-                        if (e0 + tk >= cnt) s[t][0] = s[t][1] = -INFINITY;
-                        if (e0 + 8 + tk >= cnt) s[t][2] = s[t][3] = -INFINITY;
+                for (int t = 0; t < NT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t x[4], y[4];
+                    decode_pairs<E2M1>(w[u][0][j], x);
+                    decode_pairs<E2M1>(w[u][1][j], y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = ptx::mul_f16x2(x[i], g[u][0][j / (NW / 2)]);
+                        y[i] = ptx::mul_f16x2(y[i], g[u][1][j / (NW / 2)]);
                     }
-                    over |= fmaxf(s[t][0], s[t][2]) > m[t][0] + kRescale || fmaxf(s[t][1], s[t][3]) > m[t][1] + kRescale;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        ptx::mma_16816(s[u][t], x[0], y[0], x[1], y[1], q[t][j][0], q[t][j][1]);
+                        ptx::mma_16816(s[u][t], x[2], y[2], x[3], y[3], q[t][j][2], q[t][j][3]);
+                    }
                 }
-                if (__any_sync(0xffffffffu, over)) {
+            // ---- softmax: entries past the end get -infinity
+            const int left = total - 32 * pi;      // 32 or more except in the last pair
+            float z[2][NT][4], over = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[u][t][e] = fmaf(s[u][t][e], f[t][e & 1], -m[t][e & 1]);
+            if (left < 32) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float top = fmaxf(s[t][e], s[t][e + 2]);
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                            top = fmaxf(top, m[t][e]);
-                            const float g = ptx::ex2(m[t][e] - top);
-                            m[t][e] = top;
-                            l[t][e] *= g;
+                        for (int e = 0; e < 4; ++e)
+                            if (16 * u + 8 * (e >> 1) + tk >= left) z[u][t][e] = -INFINITY;
+            }
 #pragma unroll
-                            for (int i = 0; i < MO; ++i) {
-                                o[t][i][e] *= g;
-                                o[t][i][e + 2] *= g;
-                            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    over = fmaxf(over, fmaxf(fmaxf(z[u][t][0], z[u][t][1]), fmaxf(z[u][t][2], z[u][t][3])));
+            if (__any_sync(0xffffffffu, over > kRescale)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = m[t][e];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int y = e; y < 4; y += 2)
+                                if (z[u][t][y] > -INFINITY) top = fmaxf(top, s[u][t][y] * f[t][e]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float down = ptx::ex2(m[t][e] - top);
+                        m[t][e] = top;
+                        l[t][e] *= down;
+#pragma unroll
+                        for (int i = 0; i < MO; ++i) {
+                            o[t][i][e] *= down;
+                            o[t][i][e + 2] *= down;
                         }
-                }
-                uint32_t pb[NT][2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int y = e; y < 4; y += 2)
+                                if (z[u][t][y] > -INFINITY) z[u][t][y] = fmaf(s[u][t][y], f[t][e], -top);
+                    }
+            }
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] = ptx::ex2(s[t][e] - m[t][e & 1]);
-                    l[t][0] += s[t][0] + s[t][2];
-                    l[t][1] += s[t][1] + s[t][3];
+                    for (int e = 0; e < 4; ++e) z[u][t][e] = ptx::ex2(z[u][t][e]);
+                    l[t][0] += z[u][t][0] + z[u][t][2];
+                    l[t][1] += z[u][t][1] + z[u][t][3];
                     // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
-                    pb[t][0] = ptx::transpose_8x8(float2_to_act2<true>(s[t][0], s[t][1]));
-                    pb[t][1] = ptx::transpose_8x8(float2_to_act2<true>(s[t][2], s[t][3]));
+                    pb[u][t][0] = ptx::transpose_8x8(float2_to_act2<true>(z[u][t][0], z[u][t][1]));
+                    pb[u][t][1] = ptx::transpose_8x8(float2_to_act2<true>(z[u][t][2], z[u][t][3]));
                 }
-                // ---- output
-                {
-                    const uint8_t* va = p0 + ta * kRow;
-                    const uint8_t* vb = p0 + tb * kRow;
-                    constexpr int kHi = 8;
-                    const int off = D / 2 + r * (D / 16), soff = D + D / 16 + (D == 128 ? r : r >> 1);
-                    const uint32_t sab = e4m3x2_to_f16x2(va[soff] | (uint32_t)vb[soff] << 8);
-                    const uint32_t scd = e4m3x2_to_f16x2(va[kHi * kRow + soff] | (uint32_t)vb[kHi * kRow + soff] << 8);
-                    uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
-                    load_words<NW / 2>(va + off, wa);
-                    load_words<NW / 2>(vb + off, wb);
-                    load_words<NW / 2>(va + kHi * kRow + off, wc);
-                    load_words<NW / 2>(vb + kHi * kRow + off, wd);
+            // ---- output
 #pragma unroll
-                    for (int j = 0; j < NW / 2; ++j) {
-                        uint32_t x[8], y[8];
-                        decode_across<E2M1>(wa[j], wb[j], x);
-                        decode_across<E2M1>(wc[j], wd[j], y);
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t* va = vx + (16 * u + ta) * kRow;
+                const uint8_t* vb = vx + (16 * u + tb) * kRow;
+                const int off = D / 2 + r * (D / 16), soff = D + D / 16 + (D == 128 ? r : r >> 1);
+                const uint32_t sab = e4m3x2_to_f16x2(va[soff] | (uint32_t)vb[soff] << 8);
+                const uint32_t scd = e4m3x2_to_f16x2(va[8 * kRow + soff] | (uint32_t)vb[8 * kRow + soff] << 8);
+                uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
+                load_words<NW / 2>(va + off, wa);
+                load_words<NW / 2>(vb + off, wb);
+                load_words<NW / 2>(va + 8 * kRow + off, wc);
+                load_words<NW / 2>(vb + 8 * kRow + off, wd);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t a0 = ptx::mul_f16x2(x[2 * i], sab), a1 = ptx::mul_f16x2(x[2 * i + 1], sab);
-                            const uint32_t a2 = ptx::mul_f16x2(y[2 * i], scd), a3 = ptx::mul_f16x2(y[2 * i + 1], scd);
+                for (int j = 0; j < NW / 2; ++j) {
+                    uint32_t x[8], y[8];
+                    decode_across<E2M1>(wa[j], wb[j], x);
+                    decode_across<E2M1>(wc[j], wd[j], y);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) ptx::mma_16816(o[t][4 * j + i], a0, a1, a2, a3, pb[t][0], pb[t][1]);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = ptx::mul_f16x2(x[2 * i], sab), a1 = ptx::mul_f16x2(x[2 * i + 1], sab);
+                        const uint32_t a2 = ptx::mul_f16x2(y[2 * i], scd), a3 = ptx::mul_f16x2(y[2 * i + 1], scd);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            ptx::mma_16816(o[t][4 * j + i], a0, a1, a2, a3, pb[u][t][0], pb[u][t][1]);
                     }
                 }
             }
@@ -414,50 +460,53 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
     if (L.splits > 1) ptx::cluster_sync();
     else __syncthreads();
-    const int pieces = nu * 8 * NT * (D / 8);      // 8 elements of a head each
-    for (int i = rank * kThreads + tid; i < pieces; i += L.splits * kThreads) {
-        const int uh = i / (D / 8), d8 = i - uh * (D / 8), un = uh / (8 * NT), h = uh - un * 8 * NT;
+    // every CTA: the weight 2^(m - top) * v_scale / sum of each partial result of each head
+    float* weight = part_ml + active * 8 * NT * 2;          // [split * parts + part][nu * 8 NT]
+    const int heads = nu * 8 * NT, partials = L.splits * L.parts;
+    for (int hh = tid; hh < heads; hh += kThreads) {
+        const int un = hh / (8 * NT), h = hh - un * 8 * NT;
+        const int kv = (u0 + un) / L.chunks, first = kv * group + (u0 + un - kv * L.chunks) * 8 * NT;
+        float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll 4
+        for (int x = 0; x < partials; ++x) {
+            const int sp = x / L.parts;
+            const float pm = peer_load(part_ml + 2 * ((un * L.parts + x - sp * L.parts) * 8 * NT + h), sp, L.splits);
+            weight[x * heads + hh] = pm;
+            top = fmaxf(top, pm);
+        }
+#pragma unroll 4
+        for (int x = 0; x < partials; ++x) {
+            const int sp = x / L.parts;
+            const float pl = peer_load(part_ml + 2 * ((un * L.parts + x - sp * L.parts) * 8 * NT + h) + 1, sp, L.splits);
+            const float g = ptx::ex2(weight[x * heads + hh] - top);
+            weight[x * heads + hh] = g;
+            sum = fmaf(g, pl, sum);
+        }
+        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        for (int x = 0; x < partials; ++x) weight[x * heads + hh] *= inv;
+        if (a.lse && rank == 0 && first + h < (kv + 1) * group)
+            a.lse[row * a.heads_q + first + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+    for (int i = rank * kThreads + tid; i < heads * (D / 8); i += L.splits * kThreads) {      // 8 elements of a head
+        const int hh = i / (D / 8), d8 = i - hh * (D / 8), un = hh / (8 * NT), h = hh - un * 8 * NT;
         const int kv = (u0 + un) / L.chunks, first = kv * group + (u0 + un - kv * L.chunks) * 8 * NT;
         if (first + h >= (kv + 1) * group) continue;
-        float top = -FLT_MAX;
-        for (int s = 0; s < L.splits; ++s)
-            for (int pt = 0; pt < L.parts; ++pt) {
-                const float* ml = part_ml + 2 * ((un * L.parts + pt) * 8 * NT + h);
-                top = fmaxf(top, L.splits > 1 ? __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(ml, s))) : *ml);
-            }
-        float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < L.splits; ++s)
-            for (int pt = 0; pt < L.parts; ++pt) {
-                const int w = (un * L.parts + pt) * 8 * NT + h;
-                const float* ml = part_ml + 2 * w;
-                const float* src = part_o + w * kHeadStride + 8 * d8;
-                float pm, pl;
-                float4 x, y;
-                if (L.splits > 1) {
-                    const uint32_t am = ptx::cluster_addr(ml, s), as = ptx::cluster_addr(src, s);
-                    pm = __uint_as_float(ptx::ld_cluster(am));
-                    pl = __uint_as_float(ptx::ld_cluster(am + 4));
-                    x = ptx::ld_cluster4(as);
-                    y = ptx::ld_cluster4(as + 16);
-                } else {
-                    pm = ml[0];
-                    pl = ml[1];
-                    x = *reinterpret_cast<const float4*>(src);
-                    y = *reinterpret_cast<const float4*>(src + 4);
-                }
-                const float g = ptx::ex2(pm - top);
-                sum = fmaf(g, pl, sum);
-                acc[0] = fmaf(g, x.x, acc[0]), acc[1] = fmaf(g, x.y, acc[1]), acc[2] = fmaf(g, x.z, acc[2]);
-                acc[3] = fmaf(g, x.w, acc[3]), acc[4] = fmaf(g, y.x, acc[4]), acc[5] = fmaf(g, y.y, acc[5]);
-                acc[6] = fmaf(g, y.z, acc[6]), acc[7] = fmaf(g, y.w, acc[7]);
-            }
-        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int x = 0; x < partials; ++x) {
+            const int sp = x / L.parts;
+            const float* from = part_o + ((un * L.parts + x - sp * L.parts) * 8 * NT + h) * kHeadStride + 8 * d8;
+            const float4 v = peer_load4(from, sp, L.splits), w = peer_load4(from + 4, sp, L.splits);
+            const float g = weight[x * heads + hh];
+            acc[0] = fmaf(g, v.x, acc[0]), acc[1] = fmaf(g, v.y, acc[1]), acc[2] = fmaf(g, v.z, acc[2]);
+            acc[3] = fmaf(g, v.w, acc[3]), acc[4] = fmaf(g, w.x, acc[4]), acc[5] = fmaf(g, w.y, acc[5]);
+            acc[6] = fmaf(g, w.z, acc[6]), acc[7] = fmaf(g, w.w, acc[7]);
+        }
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = float2_to_act2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        for (int e = 0; e < 4; ++e) w[e] = float2_to_act2<F16>(acc[2 * e], acc[2 * e + 1]);
         *reinterpret_cast<uint4*>(out + (int64_t)(first + h) * D + 8 * d8) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (a.lse && d8 == 0)
-            a.lse[row * a.heads_q + first + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
     __syncwarp();
     if (L.splits > 1) ptx::cluster_sync();         // no CTA leaves while another reads its partial results
@@ -480,9 +529,9 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
     L.parts = kWarps / L.per_cta;
     L.per_split = (k + L.splits - 1) / L.splits;
-    L.ring_off = (8 * L.per_split + 127) & ~127;
-    int ring = kWarps * kStages * 16 * row_bytes_of(D);
-    const int join = kWarps * 8 * NT * ((D + 4) + 2) * 4;
+    L.ring_off = 8 * ((L.per_split + 31) & ~31);
+    int ring = kWarps * stages_of(D) * 32 * row_bytes_of(D);
+    const int join = kWarps * 8 * NT * ((D + 4) + 2 + L.splits) * 4;      // partial outputs, (m, l), weights
     if (L.parts * L.splits > 1 && ring < join) ring = join;
     const int smem = L.ring_off + ring;
     const int64_t grid = rows * L.ctas * L.splits;
