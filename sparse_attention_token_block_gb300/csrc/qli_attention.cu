@@ -42,6 +42,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPerThread = kMaxSparse / kThreads;
+constexpr int kMaxSplits = 8;                     // a portable cluster
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
 
 // How a launch is laid out (host)
@@ -53,7 +54,8 @@ struct Layout {
     int32_t parts;         // warps that share a unit: kWarps / per_cta
     int32_t splits;        // CTAs of the cluster, each with a slice of the list
     int32_t per_split;     // list positions per slice
-    int32_t ring_off;      // shared-memory offset of the rings, behind the list
+    uint32_t block_recip;  // floor(2^32 / block_size)
+    int32_t mask_off, ring_off;   // shared-memory offsets of the masks and the rings, behind the list
 };
 
 // One KV head's bytes of an entry, widened to 16-byte pieces (they start on a multiple of 8 for
@@ -66,17 +68,6 @@ constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }          // of 32 en
 // c and 4 + (c + 2) % 4: with an entry stride of 32 or 96 modulo 128 bytes, the four entries that a
 // quarter-warp reads of V and the two that it reads of K then lie in different banks.
 __device__ __forceinline__ int entry_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
-
-// A value of another CTA's shared memory (of this CTA's when there is no cluster)
-__device__ __forceinline__ float peer_load(const float* p, int rank, int splits)
-{
-    return splits > 1 ? __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(p, rank))) : *p;
-}
-
-__device__ __forceinline__ float4 peer_load4(const float* p, int rank, int splits)
-{
-    return splits > 1 ? ptx::ld_cluster4(ptx::cluster_addr(p, rank)) : *reinterpret_cast<const float4*>(p);
-}
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
@@ -105,71 +96,60 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
-    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kPair = 32 * kRow, kStages = stages_of(D);
+    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kStep = 32 * kRow, kStages = stages_of(D);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int32_t warp_count[kWarps];
     int64_t* list = reinterpret_cast<int64_t*>(smem);
+    uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L.mask_off);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
-    const int64_t task = blockIdx.x / L.splits, row = task / L.ctas;
+    const uint32_t task = blockIdx.x / (uint32_t)L.splits, row = task / (uint32_t)L.ctas;
     const int u0 = (int)(task - row * L.ctas) * L.per_cta, nu = min(L.per_cta, L.units - u0);
     const int group = a.heads_q / a.heads_kv;
     ptx::pdl_wait();
 
-    // ---- the slice's valid entries, in list order, as byte offsets into the pool
+    // ---- the slice's entries as byte offsets into the pool, 32 positions of the list per warp at a
+    // time: the mask of the valid ones, and in the others' places the offset of a valid one (what is
+    // copied from there is masked), so that every byte a step reads is some listed entry's
     const int k0 = rank * L.per_split, n = max(0, min(L.per_split, a.p.sparse_count - k0));
-    int32_t j[kMaxPerThread], page[kMaxPerThread];
-    int mine = 0;
-    const uint32_t bs = (uint32_t)a.p.block_size;
+    const int steps = (n + 31) / 32;
     {
+        const int32_t* idx = a.idx + (int64_t)row * a.p.sparse_count + k0;
+        int32_t j[kMaxPerThread], page[kMaxPerThread];
+#pragma unroll
+        for (int e = 0; e < kMaxPerThread; ++e) {
+            const int at = 32 * (wid + kWarps * e) + lane;
+            j[e] = at < n ? idx[at] : -1;
+        }
         const int64_t b = row_batch(a.p, a.seq_lens_q, row);
         const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : -1;
-        const int32_t* idx = a.idx + row * a.p.sparse_count + k0;
         const int32_t* table = a.block_table + b * a.p.max_blocks_per_seq;
-        const int per = (n + kThreads - 1) / kThreads, at = tid * per;
+        const uint32_t bs = (uint32_t)a.p.block_size;
         uint32_t bits = 0;
-#pragma unroll
-        for (int e = 0; e < kMaxPerThread; ++e) j[e] = e < per && at + e < n ? idx[at + e] : -1;
 #pragma unroll
         for (int e = 0; e < kMaxPerThread; ++e) {
             const bool ok = j[e] >= 0 && j[e] < limit;
             if (j[e] != -1 && !ok) bits |= kErrLength;
-            page[e] = ok ? table[(uint32_t)j[e] / bs] : -1;
-            if (!ok) j[e] = -1;
+            // j / block_size: the reciprocal rounded down gives the quotient or one less
+            uint32_t blk = __umulhi((uint32_t)j[e], L.block_recip), pos = (uint32_t)j[e] - blk * bs;
+            if (pos >= bs) ++blk, pos -= bs;
+            page[e] = ok ? table[blk] : -1;
+            j[e] = ok ? (int32_t)pos : -1;
         }
 #pragma unroll
         for (int e = 0; e < kMaxPerThread; ++e) {
+            const int st = wid + kWarps * e;
+            if (st >= steps) break;
             const bool ok = j[e] >= 0 && page[e] >= 0 && page[e] < a.p.num_blocks;
             if (j[e] >= 0 && !ok) bits |= kErrPage;
-            if (!ok) j[e] = -1;
-            mine += ok ? 1 : 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+            int64_t at = page[e] * a.page_bytes + (int64_t)j[e] * a.entry_bytes;
+            const int64_t some = __shfl_sync(0xffffffffu, at, mask ? __ffs(mask) - 1 : 0);
+            list[32 * st + lane] = ok ? at : some;
+            if (lane == 0) masks[st] = mask;
         }
         bits = __reduce_or_sync(0xffffffffu, bits);
         if (bits && lane == 0 && a.err) atomicOr(a.err, bits);
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (lane == 31) warp_count[wid] = sum;
-        mine = sum - mine;                        // entries of the warp's earlier lanes
     }
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == wid) mine += total;
-        total += warp_count[w];
-    }
-#pragma unroll
-    for (int e = 0; e < kMaxPerThread; ++e)
-        if (j[e] >= 0) {
-            const int64_t at = page[e] * a.page_bytes + (int64_t)((uint32_t)j[e] % bs) * a.entry_bytes;
-            list[mine++] = at;
-            if (mine == total)                    // filled up to 32 with the last one (masked below)
-                for (int x = mine; x & 31; ++x) list[x] = at;
-        }
     __syncthreads();
 
     const int active = nu * L.parts;              // consumer warps with work
@@ -183,34 +163,33 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
         // The lane's 16-byte copies of 32 entries: four lanes take 64 bytes in a row of one entry, eight
         // entries at a time, and the one piece that is left over goes by entry = lane.  Code bytes of odd
         // heads start 16 bytes past a sector, so there the left-over piece is the first one.
-        const int pairs = (total + 31) / 32;
         const int head_lo = kvh * kUnit & ~15;
         const int quad_at = (D == 128 && (kvh & 1)) ? 16 : 0, rest_at = quad_at ? 0 : 16 * (kPieces - 1);
-        uint8_t* ring = smem + L.ring_off + wid * kStages * kPair;
+        uint8_t* ring = smem + L.ring_off + wid * kStages * kStep;
         const uint8_t* src = a.kv + head_lo + quad_at + 16 * (lane & 3);
         const uint8_t* src_rest = a.kv + head_lo + rest_at;
         uint8_t* dst = ring + (lane >> 2) * kRow + quad_at + 16 * (lane & 3);
         uint8_t* dst_rest = ring + lane * kRow + rest_at;
-        auto copy_pair = [&](int pi, int stage) {
-            if (pi < pairs) {
-                const int64_t* at = list + 32 * pi;
+        auto copy_step = [&](int st, int stage) {
+            if (st < steps && masks[st]) {
+                const int64_t* at = list + 32 * st;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint8_t* x = src + at[(lane >> 2) + 8 * i];
 #pragma unroll
                     for (int y = 0; y < kPieces / 4; ++y)
-                        ptx::cp_async<16>(dst + stage * kPair + 8 * i * kRow + 64 * y, x + 64 * y);
+                        ptx::cp_async<16>(dst + stage * kStep + 8 * i * kRow + 64 * y, x + 64 * y);
                 }
-                ptx::cp_async<16>(dst_rest + stage * kPair, src_rest + at[lane]);
+                ptx::cp_async<16>(dst_rest + stage * kStep, src_rest + at[lane]);
             }
             ptx::cp_async_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) copy_pair(part + i * L.parts, i);
+        for (int i = 0; i < kStages - 1; ++i) copy_step(part + i * L.parts, i);
         // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
-        const uint16_t* qrow = static_cast<const uint16_t*>(a.query) + row * a.q_stride + (int64_t)h0 * D;
+        const uint16_t* qrow = static_cast<const uint16_t*>(a.query) + (int64_t)row * a.q_stride + (int64_t)h0 * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             uint32_t w[NW][4];
@@ -264,13 +243,15 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
         const uint8_t* vp = ring + kvh * kUnit - head_lo;
         int stage = 0;
 #pragma unroll 1
-        for (int pi = part; pi < pairs; pi += L.parts) {
+        for (int st = part; st < steps; st += L.parts) {
             ptx::cp_async_wait<kStages - 2>();     // the lane's copies of these entries have landed ...
             __syncwarp();                          // ... and the others'; the entries before them are done with
-            copy_pair(pi + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
-            const uint8_t* kx = kp + stage * kPair;
-            const uint8_t* vx = vp + stage * kPair;
+            copy_step(st + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
+            const uint8_t* kx = kp + stage * kStep;
+            const uint8_t* vx = vp + stage * kStep;
             stage = stage == kStages - 1 ? 0 : stage + 1;
+            const uint32_t mask = masks[st];
+            if (mask == 0) continue;
             // ---- logits of two tiles of 16 entries
             float s[2][NT][4];
             uint32_t w[2][2][NW], g[2][2][2];      // tile, row r or r + 8: codes and the two halves' scales
@@ -310,8 +291,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
                         ptx::mma_16816(s[u][t], x[2], y[2], x[3], y[3], q[t][j][2], q[t][j][3]);
                     }
                 }
-            // ---- softmax: entries past the end get -infinity
-            const int left = total - 32 * pi;      // 32 or more except in the last pair
+            // ---- softmax: masked entries get -infinity
             float z[2][NT][4], over = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -319,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[u][t][e] = fmaf(s[u][t][e], f[t][e & 1], -m[t][e & 1]);
-            if (left < 32) {
+            if (mask != 0xffffffffu) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (16 * u + 8 * (e >> 1) + tk >= left) z[u][t][e] = -INFINITY;
+                            if (!(mask >> (16 * u + 8 * (e >> 1) + tk) & 1)) z[u][t][e] = -INFINITY;
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -416,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
 
     // ---- join and write.  Lane (r, c) holds elements r * D / 8 ... of heads 2c and 2c + 1 of each block.
-    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.heads_q * D;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)row * a.heads_q * D;
     if (L.parts * L.splits == 1) {
         if (wid >= active) return;
 #pragma unroll
@@ -434,14 +414,16 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < MO / 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (a.lse && r == 0)
-                    a.lse[row * a.heads_q + h0 + h] = sum == 0.0f ? -INFINITY : (m[t][e] + log2f(sum)) * 0.6931471805599453f;
+                    a.lse[(int64_t)row * a.heads_q + h0 + h] = sum == 0.0f ? -INFINITY : (m[t][e] + log2f(sum)) * 0.6931471805599453f;
             }
         return;
     }
-    // partial outputs [warp][8 NT heads][kHeadStride], then (maximum, sum) [warp][8 NT heads]
+    // partial outputs [warp][8 NT heads][kHeadStride], (maximum, sum) [warp][8 NT heads], and the same
+    // pairs of the CTA's units once its warps are joined
     __syncthreads();                               // the rings are free
     float* part_o = reinterpret_cast<float*>(smem + L.ring_off);
-    float* part_ml = part_o + active * 8 * NT * kHeadStride;
+    float2* part_ml = reinterpret_cast<float2*>(part_o + kWarps * 8 * NT * kHeadStride);
+    float2* unit_ml = part_ml + kWarps * 8 * NT;
     if (wid < active) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -452,64 +434,88 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < MO / 2; ++i)
                     dst[i] = make_float4(o[t][2 * i][e], o[t][2 * i][e + 2], o[t][2 * i + 1][e], o[t][2 * i + 1][e + 2]);
-                if (r == 0) {
-                    part_ml[2 * h] = m[t][e];
-                    part_ml[2 * h + 1] = l[t][e];
-                }
+                if (r == 0) (L.parts > 1 ? part_ml : unit_ml)[h] = make_float2(m[t][e], l[t][e]);
             }
     }
-    if (L.splits > 1) ptx::cluster_sync();
-    else __syncthreads();
-    // every CTA: the weight 2^(m - top) * v_scale / sum of each partial result of each head
-    float* weight = part_ml + active * 8 * NT * 2;          // [split * parts + part][nu * 8 NT]
-    const int heads = nu * 8 * NT, partials = L.splits * L.parts;
-    for (int hh = tid; hh < heads; hh += kThreads) {
-        const int un = hh / (8 * NT), h = hh - un * 8 * NT;
-        const int kv = (u0 + un) / L.chunks, first = kv * group + (u0 + un - kv * L.chunks) * 8 * NT;
-        float top = -FLT_MAX, sum = 0.0f;
-#pragma unroll 4
-        for (int x = 0; x < partials; ++x) {
-            const int sp = x / L.parts;
-            const float pm = peer_load(part_ml + 2 * ((un * L.parts + x - sp * L.parts) * 8 * NT + h), sp, L.splits);
-            weight[x * heads + hh] = pm;
-            top = fmaxf(top, pm);
-        }
-#pragma unroll 4
-        for (int x = 0; x < partials; ++x) {
-            const int sp = x / L.parts;
-            const float pl = peer_load(part_ml + 2 * ((un * L.parts + x - sp * L.parts) * 8 * NT + h) + 1, sp, L.splits);
-            const float g = ptx::ex2(weight[x * heads + hh] - top);
-            weight[x * heads + hh] = g;
-            sum = fmaf(g, pl, sum);
-        }
+    const int pieces = nu * 8 * NT * (D / 4);      // 4 elements of a head
+    auto finish = [&](int hh, int d4, const float4& v, float top, float sum) {
+        const int un = hh / (8 * NT), h = hh - un * 8 * NT, kv = (u0 + un) / L.chunks;
+        const int head = kv * group + (u0 + un - kv * L.chunks) * 8 * NT + h;
+        if (head >= (kv + 1) * group) return;
         const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-        for (int x = 0; x < partials; ++x) weight[x * heads + hh] *= inv;
-        if (a.lse && rank == 0 && first + h < (kv + 1) * group)
-            a.lse[row * a.heads_q + first + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    }
-    __syncthreads();
-    for (int i = rank * kThreads + tid; i < heads * (D / 8); i += L.splits * kThreads) {      // 8 elements of a head
-        const int hh = i / (D / 8), d8 = i - hh * (D / 8), un = hh / (8 * NT), h = hh - un * 8 * NT;
-        const int kv = (u0 + un) / L.chunks, first = kv * group + (u0 + un - kv * L.chunks) * 8 * NT;
-        if (first + h >= (kv + 1) * group) continue;
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-        for (int x = 0; x < partials; ++x) {
-            const int sp = x / L.parts;
-            const float* from = part_o + ((un * L.parts + x - sp * L.parts) * 8 * NT + h) * kHeadStride + 8 * d8;
-            const float4 v = peer_load4(from, sp, L.splits), w = peer_load4(from + 4, sp, L.splits);
-            const float g = weight[x * heads + hh];
-            acc[0] = fmaf(g, v.x, acc[0]), acc[1] = fmaf(g, v.y, acc[1]), acc[2] = fmaf(g, v.z, acc[2]);
-            acc[3] = fmaf(g, v.w, acc[3]), acc[4] = fmaf(g, w.x, acc[4]), acc[5] = fmaf(g, w.y, acc[5]);
-            acc[6] = fmaf(g, w.z, acc[6]), acc[7] = fmaf(g, w.w, acc[7]);
-        }
-        uint32_t w[4];
+        *reinterpret_cast<uint2*>(out + (int64_t)head * D + 4 * d4) =
+            make_uint2(float2_to_act2<F16>(v.x * inv, v.y * inv), float2_to_act2<F16>(v.z * inv, v.w * inv));
+        if (a.lse && d4 == 0)
+            a.lse[(int64_t)row * a.heads_q + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    };
+    if (L.parts > 1) {
+        // the warps of each unit; the joined result replaces the first warp's
+        __syncthreads();
+        for (int i = tid; i < pieces; i += kThreads) {
+            const int hh = i / (D / 4), d4 = i % (D / 4), un = hh / (8 * NT);
+            const int at = hh + un * (L.parts - 1) * 8 * NT;       // of the unit's first warp
+            float2 ml[kWarps];
+            float4 v[kWarps];
+            float top = -FLT_MAX, sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = float2_to_act2<F16>(acc[2 * e], acc[2 * e + 1]);
-        *reinterpret_cast<uint4*>(out + (int64_t)(first + h) * D + 8 * d8) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int x = 0; x < kWarps; ++x) {
+                ml[x] = make_float2(-FLT_MAX, 0.0f);
+                v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x < L.parts) {
+                    ml[x] = part_ml[at + x * 8 * NT];
+                    v[x] = *reinterpret_cast<const float4*>(part_o + (at + x * 8 * NT) * kHeadStride + 4 * d4);
+                }
+                top = fmaxf(top, ml[x].x);
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float g = ptx::ex2(ml[x].x - top);
+                sum = fmaf(g, ml[x].y, sum);
+                acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
+                acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
+            }
+            if (L.splits == 1) {
+                finish(hh, d4, acc, top, sum);
+            } else {
+                *reinterpret_cast<float4*>(part_o + at * kHeadStride + 4 * d4) = acc;
+                if (d4 == 0) unit_ml[at] = make_float2(top, sum);
+            }
+        }
+        if (L.splits == 1) return;
+        __syncwarp();
+    }
+    ptx::cluster_sync();
+    for (int i = rank * kThreads + tid; i < pieces; i += L.splits * kThreads) {
+        const int hh = i / (D / 4), d4 = i % (D / 4), un = hh / (8 * NT);
+        const int at = hh + un * (L.parts - 1) * 8 * NT;
+        const uint32_t from_ml = ptx::smem_addr(unit_ml + at), from_o = ptx::smem_addr(part_o + at * kHeadStride + 4 * d4);
+        float2 ml[kMaxSplits];
+        float4 v[kMaxSplits];
+        float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) {
+            ml[x] = make_float2(-FLT_MAX, 0.0f);
+            v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (x < L.splits) {
+                ml[x] = ptx::ld_cluster2(ptx::cluster_addr(from_ml, x));
+                v[x] = ptx::ld_cluster4(ptx::cluster_addr(from_o, x));
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) top = fmaxf(top, ml[x].x);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) {
+            const float g = ptx::ex2(ml[x].x - top);
+            sum = fmaf(g, ml[x].y, sum);
+            acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
+            acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
+        }
+        finish(hh, d4, acc, top, sum);
     }
     __syncwarp();
-    if (L.splits > 1) ptx::cluster_sync();         // no CTA leaves while another reads its partial results
+    ptx::cluster_sync();                           // no CTA leaves while another reads its partial results
 }
 
 template <bool F16, bool E2M1, int D, int NT>
@@ -525,13 +531,16 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.per_cta = (L.units + L.ctas - 1) / L.ctas;
     L.splits = 1;
     const int slots = (NT * D <= 128 ? 2 : 1) * sms;
-    while (L.splits < 8 && rows * L.ctas * L.splits * 2 <= slots && k > 64 * L.splits) L.splits *= 2;
+    while (L.splits < kMaxSplits && rows * L.ctas * L.splits * 2 <= slots && k > 64 * L.splits) L.splits *= 2;
     L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
     L.parts = kWarps / L.per_cta;
     L.per_split = (k + L.splits - 1) / L.splits;
-    L.ring_off = 8 * ((L.per_split + 31) & ~31);
+    const int steps = (L.per_split + 31) / 32;
+    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
+    L.mask_off = 8 * 32 * steps;
+    L.ring_off = (L.mask_off + 4 * steps + 127) & ~127;
     int ring = kWarps * stages_of(D) * 32 * row_bytes_of(D);
-    const int join = kWarps * 8 * NT * ((D + 4) + 2 + L.splits) * 4;      // partial outputs, (m, l), weights
+    const int join = kWarps * 8 * NT * ((D + 4) + 2 + 2) * 4;        // partial outputs, (maximum, sum) twice
     if (L.parts * L.splits > 1 && ring < join) ring = join;
     const int smem = L.ring_off + ring;
     const int64_t grid = rows * L.ctas * L.splits;

@@ -237,7 +237,7 @@ __device__ __forceinline__ BatchExtent batch_extent(const Params& p, const int32
 // are not non-decreasing can never yield an index outside [0, batch).
 __device__ __forceinline__ int64_t row_batch(const Params& p, const int32_t* seq_lens_q, int64_t r)
 {
-    if (!p.layout_tnd) return p.s1 > 0 ? r / p.s1 : -1;
+    if (!p.layout_tnd) return p.s1 > 0 ? (uint32_t)r / (uint32_t)p.s1 : -1;      // r < 2^31
     int lo = 0, hi = p.batch;                  // first b in [lo, hi) with cum[b] > r
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -256,7 +256,7 @@ __device__ __forceinline__ int64_t index_limit(const Params& p, const int32_t* s
     int64_t limit = (int64_t)p.max_blocks_per_seq * p.block_size;
     if (seq_lens_k) {
         const int64_t sk = seq_lens_k[b];
-        const int64_t lc = sk < 0 ? -1 : (sk + p.cmp_ratio - 1) / p.cmp_ratio;
+        const int64_t lc = sk < 0 ? -1 : (sk + p.cmp_ratio - 1) >> (31 - __clz(p.cmp_ratio));
         limit = lc < limit ? lc : limit;
     }
     return limit;

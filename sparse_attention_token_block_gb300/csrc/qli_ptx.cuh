@@ -432,17 +432,26 @@ __device__ __forceinline__ uint32_t cluster_rank()
 }
 
 // The shared::cluster address of `p` (a shared-memory address of this CTA's layout) in CTA `rank`
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t p, uint32_t rank)
 {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(p), "r"(rank));
     return a;
 }
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) { return cluster_addr(smem_addr(p), rank); }
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
 {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
 }
 
