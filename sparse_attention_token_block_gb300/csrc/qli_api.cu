@@ -297,8 +297,22 @@ bool encode_key_map(CUtensorMap* tm, const void* key, const Params& p)
     return r == CUDA_SUCCESS;
 }
 
-
 }  // namespace
+
+bool encode_row_map(void* tmap, const void* pool, int64_t entry_bytes, int64_t rows, int box_bytes)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)entry_bytes / 8, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)entry_bytes};
+    cuuint32_t box[2] = {(cuuint32_t)box_bytes / 8, 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(static_cast<CUtensorMap*>(tmap), CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(pool), dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace qli
 
 using namespace qli;

@@ -3,13 +3,13 @@
 //     z_i = scale * q_h . K_i,   out_h = sum_i softmax(z)_i V_i,   lse_h = ln sum_i exp(z_i)
 //
 // A cluster of `splits` CTAs works on one row (or a slice of its KV heads), each on a slice of the
-// list.  A CTA first resolves its slice -- index, bounds, block_table -- into a compact list of the
-// valid entries' addresses.  Each of its eight warps then carries one unit, a KV head with up to
-// 8 * NT of its query heads, over its share of the entries, 16 at a time, on its own: it copies its
-// head's bytes of each entry (144 for D = 128) into a ring of its own with 16-byte asynchronous
-// copies, kStages tiles deep, and meets no other warp until the end.  (One bulk copy per entry from
-// a producer warp, all heads in one copy, measured slower: an SM takes about 44 cycles per bulk copy
-// whatever its size.)
+// list.  A CTA first resolves its slice -- index, bounds, block_table -- into rows of the pool.  Each
+// of its eight warps then carries one unit, a KV head with up to 8 * NT of its query heads, over its
+// share of the entries, 32 a step, and meets no other warp until the end: its head's bytes of those
+// entries come into a ring of its own by TMA row gathers, four entries an instruction.  (In a probe
+// from L2, 16-byte asynchronous copies of a head's 144 bytes stop at 7.8 TB/s, a shared-memory write
+// per 32-byte sector; row gathers of them reach 14.5 TB/s.  A bulk copy per entry costs about 45 issue
+// slots.)
 //
 //   * logits:  S^T (16 entries x 8 heads) = K Q^T.  A lane decodes 4-bit keys straight into the A
 //     fragment: lane (r, c) of a warp holds rows r and r + 8, so it takes 1/4 of two key vectors as one
@@ -28,10 +28,13 @@
 // bfloat16 fits fp16 too (elements below 2^-14 of the largest lose bits of 2^-25 of it).
 //
 // Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over
-// the cluster) and are joined in a fixed order.
+// the cluster) and are joined in a fixed order.  Every wait for a copy is bounded (0.2 s): on expiry the
+// kernel records kErrTimeout, writes NaN, lets its copies land and returns.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <cstring>
 
 #include "qli_kv.cuh"
 
@@ -43,6 +46,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPerThread = kMaxSparse / kThreads;
 constexpr int kMaxSplits = 8;                     // a portable cluster
+constexpr uint64_t kWaitLimitNs = 200000000ull;
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
 
 // How a launch is laid out (host)
@@ -55,14 +59,37 @@ struct Layout {
     int32_t splits;        // CTAs of the cluster, each with a slice of the list
     int32_t per_split;     // list positions per slice
     uint32_t block_recip;  // floor(2^32 / block_size)
+    int32_t page_rows;     // entries from one page to the next; 0: no whole number, no row gathers
     int32_t mask_off, ring_off;   // shared-memory offsets of the masks and the rings, behind the list
 };
 
-// One KV head's bytes of an entry, widened to 16-byte pieces (they start on a multiple of 8 for
-// D = 64), and the stride of entries in a ring: 32 or 96 beyond a multiple of 128
-constexpr int pieces_of(int d) { return d == 128 ? 9 : 5; }
-constexpr int row_bytes_of(int d) { return d == 128 ? 160 : 96; }
-constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }          // of 32 entries each (two CTAs fit an SM)
+// One KV head's bytes of an entry, from a multiple of 16 on (heads of 72 bytes start on a multiple of
+// 8), and their stride in a ring: 32 or 96 beyond a multiple of 128
+constexpr int head_bytes(int d) { return d == 128 ? 144 : 80; }
+constexpr int row_bytes(int d) { return d == 128 ? 160 : 96; }
+constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }        // steps in a ring (two CTAs fit an SM)
+
+// The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        const bool done = ptx::mbar_try_wait_sleep(bar, parity, 100000u);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort, err);
+}
 
 // Entry (of a group of eight) that row r of an 8-row fragment holds.  Rows 2c and 2c + 1 hold entries
 // c and 4 + (c + 2) % 4: with an entry stride of 32 or 96 modulo 128 bytes, the four entries that a
@@ -90,28 +117,36 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
 
 template <bool F16, bool E2M1, int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
-    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L)
+    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L,
+                     const __grid_constant__ CUtensorMap rows)
 {
     constexpr int kUnit = kv_unit_bytes(D);
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
-    constexpr int kPieces = pieces_of(D), kRow = row_bytes_of(D), kStep = 32 * kRow, kStages = stages_of(D);
+    constexpr int kRow = row_bytes(D), kStep = 32 * kRow, kStages = stages_of(D);
+    __shared__ uint64_t bars[kWarps][kStages];
+    __shared__ uint32_t abort;
     extern __shared__ __align__(128) uint8_t smem[];
-    int64_t* list = reinterpret_cast<int64_t*>(smem);
+    int32_t* list = reinterpret_cast<int32_t*>(smem);
     uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L.mask_off);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
     const uint32_t task = blockIdx.x / (uint32_t)L.splits, row = task / (uint32_t)L.ctas;
     const int u0 = (int)(task - row * L.ctas) * L.per_cta, nu = min(L.per_cta, L.units - u0);
-    const int group = a.heads_q / a.heads_kv;
+    const int group = a.heads_q / a.heads_kv, active = nu * L.parts;       // warps with work
+    if (tid == 0) abort = 0;
+    if (lane == 0) {
+        for (int x = 0; x < kStages; ++x) ptx::mbar_init(&bars[wid][x], L.page_rows ? 1 : 32);
+        ptx::fence_mbar_init();
+    }
     ptx::pdl_wait();
 
-    // ---- the slice's entries as byte offsets into the pool, 32 positions of the list per warp at a
-    // time: the mask of the valid ones, and in the others' places the offset of a valid one (what is
-    // copied from there is masked), so that every byte a step reads is some listed entry's
+    // ---- the slice's entries as rows of the pool, 32 positions of the list per warp at a time: the mask
+    // of the valid ones, and in the others' places a valid one's row (what is copied from there is
+    // masked), so that every byte a step reads is some listed entry's
     const int k0 = rank * L.per_split, n = max(0, min(L.per_split, a.p.sparse_count - k0));
-    const int steps = (n + 31) / 32;
+    const int chunks = (n + 31) / 32;             // of the list
     {
         const int32_t* idx = a.idx + (int64_t)row * a.p.sparse_count + k0;
         int32_t j[kMaxPerThread], page[kMaxPerThread];
@@ -138,12 +173,13 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
 #pragma unroll
         for (int e = 0; e < kMaxPerThread; ++e) {
             const int st = wid + kWarps * e;
-            if (st >= steps) break;
+            if (st >= chunks) break;
             const bool ok = j[e] >= 0 && page[e] >= 0 && page[e] < a.p.num_blocks;
             if (j[e] >= 0 && !ok) bits |= kErrPage;
             const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-            int64_t at = page[e] * a.page_bytes + (int64_t)j[e] * a.entry_bytes;
-            const int64_t some = __shfl_sync(0xffffffffu, at, mask ? __ffs(mask) - 1 : 0);
+            // (without row gathers the row is page * block_size + position, taken apart again below)
+            const int32_t at = page[e] * (L.page_rows ? L.page_rows : a.p.block_size) + j[e];
+            const int32_t some = __shfl_sync(0xffffffffu, at, mask ? __ffs(mask) - 1 : 0);
             list[32 * st + lane] = ok ? at : some;
             if (lane == 0) masks[st] = mask;
         }
@@ -152,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
     __syncthreads();
 
-    const int active = nu * L.parts;              // consumer warps with work
     const int unit = wid / L.parts, part = wid - unit * L.parts;
     const int kvh = (u0 + unit) / L.chunks;
     const int h0 = kvh * group + (u0 + unit - kvh * L.chunks) * 8 * NT;      // the unit's first query head
@@ -160,32 +195,40 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     const int r = lane >> 2, c = lane & 3;
     float o[NT][MO][4], m[NT][2], l[NT][2];
     if (wid < active) {
-        // The lane's 16-byte copies of 32 entries: four lanes take 64 bytes in a row of one entry, eight
-        // entries at a time, and the one piece that is left over goes by entry = lane.  Code bytes of odd
-        // heads start 16 bytes past a sector, so there the left-over piece is the first one.
-        const int head_lo = kvh * kUnit & ~15;
-        const int quad_at = (D == 128 && (kvh & 1)) ? 16 : 0, rest_at = quad_at ? 0 : 16 * (kPieces - 1);
+        // the chunks of 32 positions part, part + parts, ... are this warp's steps; a chunk without a valid
+        // entry is not copied
+        const int steps = (chunks - part + L.parts - 1) / L.parts, lo = kvh * kUnit & ~15;
         uint8_t* ring = smem + L.ring_off + wid * kStages * kStep;
-        const uint8_t* src = a.kv + head_lo + quad_at + 16 * (lane & 3);
-        const uint8_t* src_rest = a.kv + head_lo + rest_at;
-        uint8_t* dst = ring + (lane >> 2) * kRow + quad_at + 16 * (lane & 3);
-        uint8_t* dst_rest = ring + lane * kRow + rest_at;
+        uint64_t* bar = bars[wid];
         auto copy_step = [&](int st, int stage) {
-            if (st < steps && masks[st]) {
-                const int64_t* at = list + 32 * st;
+            const int ch = st * L.parts + part;
+            const bool go = masks[ch] != 0;
+            if (L.page_rows) {
+                if (ptx::elect_one()) {
+                    ptx::mbar_arrive_expect_tx(&bar[stage], go ? kStep : 0);
+                    if (go) {
+                        const int4* at = reinterpret_cast<const int4*>(list + 32 * ch);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* x = src + at[(lane >> 2) + 8 * i];
-#pragma unroll
-                    for (int y = 0; y < kPieces / 4; ++y)
-                        ptx::cp_async<16>(dst + stage * kStep + 8 * i * kRow + 64 * y, x + 64 * y);
+                        for (int g = 0; g < 8; ++g) {
+                            const int4 y = at[g];
+                            ptx::tma_gather4(ring + stage * kStep + 4 * g * kRow, &rows, lo / 8, y.x, y.y, y.z, y.w, &bar[stage]);
+                        }
+                    }
                 }
-                ptx::cp_async<16>(dst_rest + stage * kStep, src_rest + at[lane]);
-            }
-            ptx::cp_async_commit();
-        };
+                __syncwarp();
+            } else {
+                // a lane per entry, 16 bytes at a time
+                if (go) {
+                    const int slot = list[32 * ch + lane], pg = slot / a.p.block_size;
+                    const uint8_t* src = a.kv + pg * a.page_bytes + (int64_t)(slot - pg * a.p.block_size) * a.entry_bytes + lo;
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) copy_step(part + i * L.parts, i);
+                    for (int x = 0; x < head_bytes(D); x += 16)
+                        ptx::cp_async<16>(ring + stage * kStep + lane * kRow + x, src + x);
+                }
+                ptx::cp_async_arrive_noinc(&bar[stage]);
+            }
+        };
+        for (int st = 0; st < min(kStages, steps); ++st) copy_step(st, st);
         // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
@@ -239,19 +282,22 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
             l[t][0] = l[t][1] = 0.0f;
         }
         const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
-        const uint8_t* kp = ring + kvh * kUnit - head_lo + tk * kRow;          // the lane's key rows, value entries
-        const uint8_t* vp = ring + kvh * kUnit - head_lo;
-        int stage = 0;
+        const uint8_t* head = ring + kvh * kUnit - lo;
+        const uint8_t* kc0 = head + tk * kRow + (D / 8) * c;                       // the lane's key codes and scales,
+        const uint8_t* ks0 = head + tk * kRow + D + (D == 128 ? 2 * c : c);
+        const uint8_t* vc0 = head + ta * kRow + D / 2 + (D / 16) * r;              // value codes and scales
+        const uint8_t* vs0 = head + ta * kRow + D + D / 16 + (D == 128 ? r : r >> 1);
+        const int vb = (tb - ta) * kRow;
+        int stage = 0, parity = 0;
 #pragma unroll 1
-        for (int st = part; st < steps; st += L.parts) {
-            ptx::cp_async_wait<kStages - 2>();     // the lane's copies of these entries have landed ...
-            __syncwarp();                          // ... and the others'; the entries before them are done with
-            copy_step(st + (kStages - 1) * L.parts, stage == 0 ? kStages - 1 : stage - 1);
-            const uint8_t* kx = kp + stage * kStep;
-            const uint8_t* vx = vp + stage * kStep;
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-            const uint32_t mask = masks[st];
-            if (mask == 0) continue;
+        for (int st = 0; st < steps; ++st) {
+            if (!wait_bounded(&bar[stage], parity, &abort, a.err)) break;
+            const uint32_t mask = masks[st * L.parts + part];
+            if (mask) {
+            const uint8_t* kc = kc0 + stage * kStep;
+            const uint8_t* ks = ks0 + stage * kStep;
+            const uint8_t* va = vc0 + stage * kStep;
+            const uint8_t* vs = vs0 + stage * kStep;
             // ---- logits of two tiles of 16 entries
             float s[2][NT][4];
             uint32_t w[2][2][NW], g[2][2][2];      // tile, row r or r + 8: codes and the two halves' scales
@@ -259,14 +305,14 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const uint8_t* x = kx + (16 * u + 8 * y) * kRow;
-                    load_words<NW>(x + (D / 8) * c, w[u][y]);
+                    load_words<NW>(kc + (16 * u + 8 * y) * kRow, w[u][y]);
+                    const uint8_t* x = ks + (16 * u + 8 * y) * kRow;
                     if constexpr (D == 128) {
-                        const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x + D + 2 * c));
+                        const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x));
                         g[u][y][0] = __byte_perm(h, 0, 0x1010);
                         g[u][y][1] = __byte_perm(h, 0, 0x3232);
                     } else {
-                        g[u][y][0] = g[u][y][1] = __byte_perm(e4m3x2_to_f16x2(x[D + c]), 0, 0x1010);
+                        g[u][y][0] = g[u][y][1] = __byte_perm(e4m3x2_to_f16x2(*x), 0, 0x1010);
                     }
                 }
 #pragma unroll
@@ -358,16 +404,14 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
             // ---- output
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* va = vx + (16 * u + ta) * kRow;
-                const uint8_t* vb = vx + (16 * u + tb) * kRow;
-                const int off = D / 2 + r * (D / 16), soff = D + D / 16 + (D == 128 ? r : r >> 1);
-                const uint32_t sab = e4m3x2_to_f16x2(va[soff] | (uint32_t)vb[soff] << 8);
-                const uint32_t scd = e4m3x2_to_f16x2(va[8 * kRow + soff] | (uint32_t)vb[8 * kRow + soff] << 8);
+                const uint8_t* x0 = vs + 16 * u * kRow;
+                const uint32_t sab = e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[vb] << 8);
+                const uint32_t scd = e4m3x2_to_f16x2(x0[8 * kRow] | (uint32_t)x0[vb + 8 * kRow] << 8);
                 uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
-                load_words<NW / 2>(va + off, wa);
-                load_words<NW / 2>(vb + off, wb);
-                load_words<NW / 2>(va + 8 * kRow + off, wc);
-                load_words<NW / 2>(vb + 8 * kRow + off, wd);
+                load_words<NW / 2>(va + 16 * u * kRow, wa);
+                load_words<NW / 2>(va + 16 * u * kRow + vb, wb);
+                load_words<NW / 2>(va + (16 * u + 8) * kRow, wc);
+                load_words<NW / 2>(va + (16 * u + 8) * kRow + vb, wd);
 #pragma unroll
                 for (int j = 0; j < NW / 2; ++j) {
                     uint32_t x[8], y[8];
@@ -383,6 +427,13 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
                     }
                 }
             }
+            }
+            __syncwarp();                          // every lane is done with the stage
+            if (st + kStages < steps) copy_step(st + kStages, stage);
+            if (++stage == kStages) {
+                stage = 0;
+                parity ^= 1;
+            }
         }
         // the sums over the lanes that share a head's column
 #pragma unroll
@@ -396,6 +447,17 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
 
     // ---- join and write.  Lane (r, c) holds elements r * D / 8 ... of heads 2c and 2c + 1 of each block.
+    __syncthreads();                               // the rings are free
+    const bool failed = abort != 0;
+    if (failed) {                                  // copies that are still under way land before the CTA ends
+        // (which phase a barrier is in is not known here: give the copies the time of a wait)
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kWaitLimitNs) {
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = __int_as_float(0x7FC00000);
+    }
     uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)row * a.heads_q * D;
     if (L.parts * L.splits == 1) {
         if (wid >= active) return;
@@ -420,7 +482,6 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     }
     // partial outputs [warp][8 NT heads][kHeadStride], (maximum, sum) [warp][8 NT heads], and the same
     // pairs of the CTA's units once its warps are joined
-    __syncthreads();                               // the rings are free
     float* part_o = reinterpret_cast<float*>(smem + L.ring_off);
     float2* part_ml = reinterpret_cast<float2*>(part_o + kWarps * 8 * NT * kHeadStride);
     float2* unit_ml = part_ml + kWarps * 8 * NT;
@@ -527,19 +588,35 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.units = a.heads_kv * L.chunks;
     const int k = a.p.sparse_count;
     const int64_t rows = a.p.rows;
-    L.ctas = (L.units + kWarps - 1) / kWarps;
-    L.per_cta = (L.units + L.ctas - 1) / L.ctas;
-    L.splits = 1;
+    // CTAs per row: as many slices of the units as still run in one wave (fewer units per CTA: more warps
+    // share a unit, so each reads a shorter part of the list; long decode, 32 rows x 8 units: 8 units
+    // per CTA 80 us, 2 units 25.6, 1 unit 23.4).  The list itself is split over a cluster while each SM
+    // has at most one CTA and each warp keeps a step of its own (1 row: 14.6 us unsplit, 7.4 with 8
+    // splits; 8 rows: 15.2, 11.9 with 2, 12.3 with 4, 17.7 with 8).
     const int slots = (NT * D <= 128 ? 2 : 1) * sms;
-    while (L.splits < kMaxSplits && rows * L.ctas * L.splits * 2 <= slots && k > 64 * L.splits) L.splits *= 2;
+    L.per_cta = 1;
+    while (L.per_cta < kWarps && rows * ((L.units + L.per_cta - 1) / L.per_cta) > slots) L.per_cta *= 2;
     L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
+    L.per_cta = (L.units + L.ctas - 1) / L.ctas;
     L.parts = kWarps / L.per_cta;
+    L.splits = 1;
+    while (L.splits < kMaxSplits && rows * L.ctas * L.splits * 2 <= sms && k >= 32 * L.parts * L.splits * 2) L.splits *= 2;
     L.per_split = (k + L.splits - 1) / L.splits;
     const int steps = (L.per_split + 31) / 32;
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
-    L.mask_off = 8 * 32 * steps;
+    L.mask_off = 4 * 32 * steps;
     L.ring_off = (L.mask_off + 4 * steps + 127) & ~127;
-    int ring = kWarps * stages_of(D) * 32 * row_bytes_of(D);
+    int ring = kWarps * stages_of(D) * 32 * row_bytes(D);
+    // row gathers need one stride for all entries of the pool
+    CUtensorMap rows_map;
+    std::memset(&rows_map, 0, sizeof(rows_map));
+    L.page_rows = 0;
+    if (a.page_bytes % a.entry_bytes == 0 && a.page_bytes / a.entry_bytes * a.p.num_blocks <= INT32_MAX) {
+        L.page_rows = (int32_t)(a.page_bytes / a.entry_bytes);
+        if (!encode_row_map(&rows_map, a.kv, a.entry_bytes, (int64_t)L.page_rows * (a.p.num_blocks - 1) + a.p.block_size,
+                            row_bytes(D)))
+            return cudaErrorUnknown;
+    }
     const int join = kWarps * 8 * NT * ((D + 4) + 2 + 2) * 4;        // partial outputs, (maximum, sum) twice
     if (L.parts * L.splits > 1 && ring < join) ring = join;
     const int smem = L.ring_off + ring;
@@ -562,7 +639,7 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, L);
+    return cudaLaunchKernelEx(&cfg, kernel, a, L, rows_map);
 }
 
 template <bool F16, bool E2M1>

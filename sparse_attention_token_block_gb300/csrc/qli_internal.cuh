@@ -404,6 +404,10 @@ struct KvArgs {
 cudaError_t launch_kv_write(const KvArgs& a, const void* k, const void* v, void* kv, cudaStream_t st);
 cudaError_t launch_kv_read(const KvArgs& a, const void* kv, void* k, void* v, cudaStream_t st);
 
+// Tensor map (a CUtensorMap) of a pool of `rows` entries of `entry_bytes` bytes in a row: 8-byte elements,
+// boxes one entry high and `box_bytes` wide (at most 2048; past the entry's end they are filled with zeros)
+bool encode_row_map(void* tmap, const void* pool, int64_t entry_bytes, int64_t rows, int box_bytes);
+
 struct AttentionArgs {
     Params p;
     const void* query;

@@ -120,6 +120,22 @@ def test_many_rows_tnd_compressed(Q, e2m1, f16, dim):
     _check(case, got, q, idx, pool, hkv, e2m1, f16, 0.11, factors)
 
 
+@pytest.mark.parametrize("heads", [(8, 1, 128), (64, 8, 128), (24, 3, 64), (32, 4, 64)])
+@pytest.mark.parametrize("gap", [0, 1, 3])
+def test_page_strides_of_whole_entries(Q, heads, gap):
+    """Pages that lie a whole number of entries apart."""
+    hq, hkv, dim = heads
+    case = cache_case(batch=3, s1=1, seq_lens_k=[300, 90, 33], block_size=32, sparse_count=96, seed=hq)
+    pool = cache(case, hkv, dim, True, seed=1)
+    eb = pool.shape[2]
+    raw = np.random.default_rng(4).integers(0, 256, (case.num_blocks, (32 + gap) * eb), dtype=np.uint8)
+    raw[:, :32 * eb] = pool.reshape(case.num_blocks, -1)
+    idx = W.random_indices(case, seed=2)
+    q = _query(3, hq, dim, False, 3)
+    got = _run(Q, case, q, idx, raw, hkv, True, False, kv_stride=(32 + gap) * eb)
+    _check(case, got, q, idx, pool, hkv, True, False)
+
+
 def test_scattered_padding_duplicates_and_empty_rows(Q):
     """-1 anywhere in a list, whole tiles of it, rows of nothing else, one entry listed many times."""
     rng = np.random.default_rng(8)
