@@ -9,7 +9,9 @@
 // entries come into a ring of its own by TMA row gathers, four entries an instruction.  (In a probe
 // from L2, 16-byte asynchronous copies of a head's 144 bytes stop at 7.8 TB/s, a shared-memory write
 // per 32-byte sector; row gathers of them reach 14.5 TB/s.  A bulk copy per entry costs about 45 issue
-// slots.)
+// slots.)  Where the eight warps of a CTA carry eight KV heads side by side (kShared), the ring is the
+// CTA's: every warp gathers four whole entries a step, one instruction instead of eight, and the warps
+// hand the stages on through barriers.
 //
 //   * logits:  S^T (16 entries x 8 heads) = K Q^T.  A lane decodes 4-bit keys straight into the A
 //     fragment: lane (r, c) of a warp holds rows r and r + 8, so it takes 1/4 of two key vectors as one
@@ -66,7 +68,10 @@ struct Layout {
 // One KV head's bytes of an entry, from a multiple of 16 on (heads of 72 bytes start on a multiple of
 // 8), and their stride in a ring: 32 or 96 beyond a multiple of 128
 constexpr int head_bytes(int d) { return d == 128 ? 144 : 80; }
-constexpr int row_bytes(int d) { return d == 128 ? 160 : 96; }
+constexpr int row_bytes(int d, bool shared)
+{
+    return shared ? kWarps * kv_unit_bytes(d) + 32 : (d == 128 ? 160 : 96);
+}
 constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }        // steps in a ring (two CTAs fit an SM)
 
 // The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up
@@ -115,7 +120,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
     }
 }
 
-template <bool F16, bool E2M1, int D, int NT>
+template <bool F16, bool E2M1, int D, int NT, bool kShared>
 __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L,
                      const __grid_constant__ CUtensorMap rows)
@@ -124,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
-    constexpr int kRow = row_bytes(D), kStep = 32 * kRow, kStages = stages_of(D);
+    constexpr int kRow = row_bytes(D, kShared), kStep = 32 * kRow, kStages = stages_of(D);
+    // of each warp's ring; kShared: [0] the ring's, [1] its stages handed back
     __shared__ uint64_t bars[kWarps][kStages];
     __shared__ uint32_t abort;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     const int group = a.heads_q / a.heads_kv, active = nu * L.parts;       // warps with work
     if (tid == 0) abort = 0;
     if (lane == 0) {
-        for (int x = 0; x < kStages; ++x) ptx::mbar_init(&bars[wid][x], L.page_rows ? 1 : 32);
+        for (int x = 0; x < kStages; ++x) ptx::mbar_init(&bars[wid][x], kShared ? kWarps : (L.page_rows ? 1 : 32));
         ptx::fence_mbar_init();
     }
     ptx::pdl_wait();
@@ -197,13 +203,20 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     if (wid < active) {
         // the chunks of 32 positions part, part + parts, ... are this warp's steps; a chunk without a valid
         // entry is not copied
-        const int steps = (chunks - part + L.parts - 1) / L.parts, lo = kvh * kUnit & ~15;
-        uint8_t* ring = smem + L.ring_off + wid * kStages * kStep;
-        uint64_t* bar = bars[wid];
+        const int steps = (chunks - part + L.parts - 1) / L.parts, lo = (kShared ? u0 : kvh) * kUnit & ~15;
+        uint8_t* ring = smem + L.ring_off + (kShared ? 0 : wid * kStages * kStep);
+        uint64_t* bar = bars[kShared ? 0 : wid];
         auto copy_step = [&](int st, int stage) {
             const int ch = st * L.parts + part;
             const bool go = masks[ch] != 0;
-            if (L.page_rows) {
+            if constexpr (kShared) {
+                if (ptx::elect_one()) {
+                    ptx::mbar_arrive_expect_tx(&bar[stage], go ? 4 * kRow : 0);
+                    const int4 y = *reinterpret_cast<const int4*>(list + 32 * ch + 4 * wid);
+                    if (go) ptx::tma_gather4(ring + stage * kStep + 4 * wid * kRow, &rows, lo / 8, y.x, y.y, y.z, y.w, &bar[stage]);
+                }
+                __syncwarp();
+            } else if (L.page_rows) {
                 if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(&bar[stage], go ? kStep : 0);
                     if (go) {
@@ -291,6 +304,12 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
         int stage = 0, parity = 0;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
+            if (kShared && st > 0 && st - 1 + kStages < steps) {
+                // the step before freed its stage (of the other parity when it was the last of a round)
+                const int freed = stage == 0 ? kStages - 1 : stage - 1;
+                if (!wait_bounded(&bars[1][freed], stage == 0 ? parity ^ 1 : parity, &abort, a.err)) break;
+                copy_step(st - 1 + kStages, freed);
+            }
             if (!wait_bounded(&bar[stage], parity, &abort, a.err)) break;
             const uint32_t mask = masks[st * L.parts + part];
             if (mask) {
@@ -429,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
             }
             }
             __syncwarp();                          // every lane is done with the stage
-            if (st + kStages < steps) copy_step(st + kStages, stage);
+            if constexpr (kShared) {
+                if (lane == 0) ptx::mbar_arrive(&bars[1][stage]);
+            } else if (st + kStages < steps) {
+                copy_step(st + kStages, stage);
+            }
             if (++stage == kStages) {
                 stage = 0;
                 parity ^= 1;
@@ -579,6 +602,45 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     ptx::cluster_sync();                           // no CTA leaves while another reads its partial results
 }
 
+template <bool F16, bool E2M1, int D, int NT, bool kShared>
+cudaError_t launch_layout(const AttentionArgs& a, Layout L, cudaStream_t st)
+{
+    const int64_t rows = a.p.rows;
+    const int steps = (L.per_split + 31) / 32;
+    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
+    L.mask_off = 4 * 32 * steps;
+    L.ring_off = (L.mask_off + 4 * steps + 127) & ~127;
+    int ring = (kShared ? 1 : kWarps) * stages_of(D) * 32 * row_bytes(D, kShared);
+    CUtensorMap rows_map;
+    std::memset(&rows_map, 0, sizeof(rows_map));
+    if (L.page_rows && !encode_row_map(&rows_map, a.kv, a.entry_bytes,
+                                       (int64_t)L.page_rows * (a.p.num_blocks - 1) + a.p.block_size, row_bytes(D, kShared)))
+        return cudaErrorUnknown;
+    const int join = kWarps * 8 * NT * ((D + 4) + 2 + 2) * 4;        // partial outputs, (maximum, sum) twice
+    if (L.parts * L.splits > 1 && ring < join) ring = join;
+    const int smem = L.ring_off + ring;
+    const int64_t grid = rows * L.ctas * L.splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    auto kernel = attention_kernel<F16, E2M1, D, NT, kShared>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, L, rows_map);
+}
+
 template <bool F16, bool E2M1, int D, int NT>
 cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
 {
@@ -602,44 +664,15 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.splits = 1;
     while (L.splits < kMaxSplits && rows * L.ctas * L.splits * 2 <= sms && k >= 32 * L.parts * L.splits * 2) L.splits *= 2;
     L.per_split = (k + L.splits - 1) / L.splits;
-    const int steps = (L.per_split + 31) / 32;
-    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
-    L.mask_off = 4 * 32 * steps;
-    L.ring_off = (L.mask_off + 4 * steps + 127) & ~127;
-    int ring = kWarps * stages_of(D) * 32 * row_bytes(D);
     // row gathers need one stride for all entries of the pool
-    CUtensorMap rows_map;
-    std::memset(&rows_map, 0, sizeof(rows_map));
     L.page_rows = 0;
-    if (a.page_bytes % a.entry_bytes == 0 && a.page_bytes / a.entry_bytes * a.p.num_blocks <= INT32_MAX) {
+    if (a.page_bytes % a.entry_bytes == 0 && a.page_bytes / a.entry_bytes * a.p.num_blocks <= INT32_MAX)
         L.page_rows = (int32_t)(a.page_bytes / a.entry_bytes);
-        if (!encode_row_map(&rows_map, a.kv, a.entry_bytes, (int64_t)L.page_rows * (a.p.num_blocks - 1) + a.p.block_size,
-                            row_bytes(D)))
-            return cudaErrorUnknown;
+    if constexpr (NT == 1) {
+        if (L.page_rows && L.chunks == 1 && L.per_cta == kWarps && L.units % kWarps == 0)
+            return launch_layout<F16, E2M1, D, NT, true>(a, L, st);
     }
-    const int join = kWarps * 8 * NT * ((D + 4) + 2 + 2) * 4;        // partial outputs, (maximum, sum) twice
-    if (L.parts * L.splits > 1 && ring < join) ring = join;
-    const int smem = L.ring_off + ring;
-    const int64_t grid = rows * L.ctas * L.splits;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    auto kernel = attention_kernel<F16, E2M1, D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = L.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = L.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, L, rows_map);
+    return launch_layout<F16, E2M1, D, NT, false>(a, L, st);
 }
 
 template <bool F16, bool E2M1>

@@ -99,13 +99,21 @@ __device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t (&o)[4])
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[3]) : "r"((v & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
 }
 
+// The low nibble of every byte of a, the high nibble of every byte of b (one instruction)
+__device__ __forceinline__ uint32_t select_low_nibbles(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(r) : "r"(a), "r"(b));        // (a & c) | (b & ~c)
+    return r;
+}
+
 // Eight codes each of two vectors as eight fp16 pairs (a's element e, b's element e), exactly
 template <bool E2M1>
 __device__ __forceinline__ void decode_across(uint32_t a, uint32_t b, uint32_t (&o)[8])
 {
     if (E2M1) {
         // bytes of (a's nibble, b's nibble) for the even and the odd elements
-        const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+        const uint32_t even = select_low_nibbles(a, b << 4), odd = select_low_nibbles(a >> 4, b);
         uint32_t x[4], y[4];
         e2m1x8_to_f16x2(even, x);
         e2m1x8_to_f16x2(odd, y);
