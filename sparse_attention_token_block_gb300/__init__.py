@@ -184,11 +184,20 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream=None):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without building a Stream object
+        device = torch.cuda.current_device
+        _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current_stream()
 
 
 def problem_init() -> Problem:
@@ -296,26 +305,30 @@ def gather_kv(p: Problem, seq_lens_q, seq_lens_k, block_table, sparse_indices, k
 
 
 # ------------------------------------------------------------------------------ the attention side
+_act_dtypes = None
+
+
 def _rows(t, what, dtype, tokens, heads, dim):
     """(address, elements between tokens) of a [tokens, heads, dim] tensor whose heads are contiguous
     (a view of a packed projection keeps its token stride); TypeError / ValueError otherwise."""
-    import torch
     if t is None:
         return None, 0
-    want = torch.float16 if dtype == ACT_F16 else torch.bfloat16
-    if t.dtype != want:
-        raise TypeError("%s: expected %s, got %s" % (what, want, t.dtype))
-    if tuple(t.shape) != (tokens, heads, dim):
+    global _act_dtypes
+    if _act_dtypes is None:
+        import torch
+        _act_dtypes = (torch.bfloat16, torch.float16)
+    if t.dtype is not _act_dtypes[1 if dtype == ACT_F16 else 0]:
+        raise TypeError("%s: expected %s, got %s" % (what, _act_dtypes[1 if dtype == ACT_F16 else 0], t.dtype))
+    if t.shape != (tokens, heads, dim):
         raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, tokens, heads, dim, tuple(t.shape)))
+    step, head, elem = t.stride()
     if tokens <= 1:
-        stride = 0
-    else:
-        stride = t.stride(0)
-        if stride < heads * dim:                 # 0 would read as contiguous
-            raise ValueError("%s: tokens overlap (stride %d)" % (what, stride))
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        step = 0
+    elif step < heads * dim:                     # 0 would read as contiguous
+        raise ValueError("%s: tokens overlap (stride %d)" % (what, step))
+    if (elem != 1 or (heads > 1 and head != dim)) and t.numel():
         raise ValueError("%s: a token's heads must be contiguous" % what)
-    return t.data_ptr(), stride
+    return t.data_ptr(), step
 
 
 def _bytes(workspace):

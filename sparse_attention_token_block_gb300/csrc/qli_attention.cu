@@ -35,6 +35,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstring>
 
@@ -48,6 +49,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPerThread = kMaxSparse / kThreads;
 constexpr int kMaxSplits = 8;                     // a portable cluster
+constexpr int kMaxSmem = 220 * 1024;              // dynamic, of a CTA
 constexpr uint64_t kWaitLimitNs = 200000000ull;
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
 
@@ -72,7 +74,11 @@ constexpr int row_bytes(int d, bool shared)
 {
     return shared ? kWarps * kv_unit_bytes(d) + 32 : (d == 128 ? 160 : 96);
 }
-constexpr int stages_of(int d) { return d == 128 ? 2 : 3; }        // steps in a ring (two CTAs fit an SM)
+constexpr int kStages = 2;                                          // steps in a ring
+
+// Resident CTAs per SM, as the accumulators (D x 8 NT fp32 per warp) and the rings allow.  (D = 64 with
+// three: int4 prefill of 1024 and 2048 rows 237 -> 212 us against two.)
+constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 3 : (nt * d <= 128 ? 2 : 1); }
 
 // The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
@@ -121,7 +127,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
 }
 
 template <bool F16, bool E2M1, int D, int NT, bool kShared>
-__global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Layout L,
                      const __grid_constant__ CUtensorMap rows)
 {
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1)
     constexpr int NW = D / 32;                    // words of key codes per lane and entry
     constexpr int MO = D / 16;                    // 16-row tiles of the output
     constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
-    constexpr int kRow = row_bytes(D, kShared), kStep = 32 * kRow, kStages = stages_of(D);
+    constexpr int kRow = row_bytes(D, kShared), kStep = 32 * kRow;
     // of each warp's ring; kShared: [0] the ring's, [1] its stages handed back
     __shared__ uint64_t bars[kWarps][kStages];
     __shared__ uint32_t abort;
@@ -610,7 +616,7 @@ cudaError_t launch_layout(const AttentionArgs& a, Layout L, cudaStream_t st)
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
     L.mask_off = 4 * 32 * steps;
     L.ring_off = (L.mask_off + 4 * steps + 127) & ~127;
-    int ring = (kShared ? 1 : kWarps) * stages_of(D) * 32 * row_bytes(D, kShared);
+    int ring = (kShared ? 1 : kWarps) * kStages * 32 * row_bytes(D, kShared);
     CUtensorMap rows_map;
     std::memset(&rows_map, 0, sizeof(rows_map));
     if (L.page_rows && !encode_row_map(&rows_map, a.kv, a.entry_bytes,
@@ -622,8 +628,17 @@ cudaError_t launch_layout(const AttentionArgs& a, Layout L, cudaStream_t st)
     const int64_t grid = rows * L.ctas * L.splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     auto kernel = attention_kernel<F16, E2M1, D, NT, kShared>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the kernel's shared-memory limit, raised once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? UINT64_C(1) << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -655,7 +670,7 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     // per CTA 80 us, 2 units 25.6, 1 unit 23.4).  The list itself is split over a cluster while each SM
     // has at most one CTA and each warp keeps a step of its own (1 row: 14.6 us unsplit, 7.4 with 8
     // splits; 8 rows: 15.2, 11.9 with 2, 12.3 with 4, 17.7 with 8).
-    const int slots = (NT * D <= 128 ? 2 : 1) * sms;
+    const int slots = ctas_per_sm(D, NT) * sms;
     L.per_cta = 1;
     while (L.per_cta < kWarps && rows * ((L.units + L.per_cta - 1) / L.per_cta) > slots) L.per_cta *= 2;
     L.ctas = (L.units + L.per_cta - 1) / L.per_cta;
