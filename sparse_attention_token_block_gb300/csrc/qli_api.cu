@@ -676,7 +676,7 @@ namespace {
 // Argument checks that writing and reading the cache share; fills `A` (nothing to do when tokens = 0)
 qli_status kv_args(const qli_problem* p, const qli_attention* a, int64_t tokens, const void* k, int64_t k_stride,
                    const void* v, int64_t v_stride, const int32_t* token_batch, const int32_t* token_pos,
-                   const int32_t* block_table, const void* kv, void* workspace, size_t workspace_bytes, KvArgs* A)
+                   const int32_t* block_table, const void* kv, void* workspace, size_t workspace_bytes, KvArgs* A, int* sms)
 {
     qli_status s = check(p, nullptr);
     if (s != QLI_OK) return s;
@@ -691,9 +691,9 @@ qli_status kv_args(const qli_problem* p, const qli_attention* a, int64_t tokens,
     if (tokens == 0) return QLI_OK;
     if (!k || !v || !token_batch || !token_pos || !block_table || !kv) return QLI_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv, 16)) return QLI_ERR_INVALID_ARG;
-    int sms = device_sms(nullptr);
-    if (sms < 0) return QLI_ERR_CUDA;
-    if (sms == 0) return QLI_ERR_NO_DEVICE;
+    *sms = device_sms(nullptr);
+    if (*sms < 0) return QLI_ERR_CUDA;
+    if (*sms == 0) return QLI_ERR_NO_DEVICE;
     A->p = params_of(p);
     A->heads_kv = a->num_heads_kv;
     A->head_dim = a->head_dim;
@@ -717,10 +717,11 @@ qli_status qli_kv_write(const qli_problem* p, const qli_attention* a, int64_t to
                         const int32_t* block_table, void* kv, void* workspace, size_t workspace_bytes, void* stream)
 {
     KvArgs A;
+    int sms = 0;
     qli_status s = kv_args(p, a, tokens, k, k_stride, v, v_stride, token_batch, token_pos, block_table, kv, workspace,
-                           workspace_bytes, &A);
+                           workspace_bytes, &A, &sms);
     if (s != QLI_OK || tokens == 0) return s;
-    cudaError_t e = launch_kv_write(A, k, v, kv, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_kv_write(A, sms, k, v, kv, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
@@ -730,10 +731,11 @@ qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tok
                        void* stream)
 {
     KvArgs A;
+    int sms = 0;
     qli_status s = kv_args(p, a, tokens, k, k_stride, v, v_stride, token_batch, token_pos, block_table, kv, workspace,
-                           workspace_bytes, &A);
+                           workspace_bytes, &A, &sms);
     if (s != QLI_OK || tokens == 0) return s;
-    cudaError_t e = launch_kv_read(A, kv, k, v, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_kv_read(A, sms, kv, k, v, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 

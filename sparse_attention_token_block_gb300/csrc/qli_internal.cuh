@@ -237,7 +237,7 @@ __device__ __forceinline__ BatchExtent batch_extent(const Params& p, const int32
 // are not non-decreasing can never yield an index outside [0, batch).
 __device__ __forceinline__ int64_t row_batch(const Params& p, const int32_t* seq_lens_q, int64_t r)
 {
-    if (!p.layout_tnd) return p.s1 > 0 ? (uint32_t)r / (uint32_t)p.s1 : -1;      // r < 2^31
+    if (!p.layout_tnd) return p.s1 > 0 ? (int64_t)((uint32_t)r / (uint32_t)p.s1) : -1;      // r < 2^31
     int lo = 0, hi = p.batch;                  // first b in [lo, hi) with cum[b] > r
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -401,8 +401,8 @@ struct KvArgs {
     const int32_t* block_table;
     uint32_t* err;
 };
-cudaError_t launch_kv_write(const KvArgs& a, const void* k, const void* v, void* kv, cudaStream_t st);
-cudaError_t launch_kv_read(const KvArgs& a, const void* kv, void* k, void* v, cudaStream_t st);
+cudaError_t launch_kv_write(const KvArgs& a, int sms, const void* k, const void* v, void* kv, cudaStream_t st);
+cudaError_t launch_kv_read(const KvArgs& a, int sms, const void* kv, void* k, void* v, cudaStream_t st);
 
 // Tensor map (a CUtensorMap) of a pool of `rows` entries of `entry_bytes` bytes in a row: 8-byte elements,
 // boxes one entry high and `box_bytes` wide (at most 2048; past the entry's end they are filled with zeros)

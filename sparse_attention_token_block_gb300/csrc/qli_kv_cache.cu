@@ -4,10 +4,17 @@
 // Per block of 16 elements:  y = x / g (g = k_scale or v_scale);  s = e4m3(min(max |y| / Q, 448)),
 // Q = 7 (int4) or 6 (E2M1);  code = y / s in fp32 rounded to nearest even and saturated to +-Q.
 //
-// Streams over HBM: 2 bytes per element on the activations' side and 0.5625 on the cache's.  One
-// thread per block of 16 elements: its maximum needs no exchange between lanes, and a token's
-// blocks (K heads, then V heads) follow one another over the threads, so both sides coalesce.
+// Streams over HBM: 2 bytes per element on the activations' side and 0.5625 on the cache's.  A thread
+// holds half a block, eight elements: 16 bytes of activations and 4 of codes, so every load and store
+// of a warp is one contiguous range of a token (a whole block per thread wrote 16 bytes at a stride of
+// 32), and a block's maximum takes one exchange with the neighbouring lane.  A token's half-blocks (K
+// heads, then V heads) follow one another over the threads.  A CTA looks up the entries of up to
+// kMaxTokens tokens first (batch, position, block_table, pool are four dependent loads; one lookup per
+// four tokens left the read of 65536 tokens at 89 us), then each thread streams its half-block of
+// those tokens, kUnroll at a time.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "qli_kv.cuh"
 
@@ -16,143 +23,214 @@ namespace qli {
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr int kMaxTokens = 32;             // tokens of a CTA
+constexpr int kUnroll = 4;                 // half-blocks of a thread under way
 
-// Block i of a token: K or V (kv), head h, block b of D / 16
-struct BlockPos {
-    int kv, h, b;
+// Half-block i of a token: byte offsets in the entry, element offset in K or V
+struct HalfPos {
+    int kv;                                // 0: K, 1: V
+    int element, code, scale;
 };
-__device__ __forceinline__ BlockPos block_pos(int i, int heads, int nb)
+__device__ __forceinline__ HalfPos half_pos(int i, int heads, int dim)
 {
-    BlockPos r;
-    r.kv = i >= heads * nb ? 1 : 0;
-    i -= r.kv * heads * nb;
-    r.h = i / nb;
-    r.b = i - r.h * nb;
+    const int per = dim / 8;               // half-blocks of a vector
+    HalfPos r;
+    r.kv = i >= heads * per ? 1 : 0;
+    i -= r.kv * heads * per;
+    const int h = i / per, x = i - h * per, unit = kv_unit_bytes(dim);
+    r.element = 8 * i;
+    r.code = h * unit + r.kv * (dim / 2) + 4 * x;
+    r.scale = h * unit + dim + r.kv * (dim / kKvBlock) + x / 2;
     return r;
 }
 
-// The entry of token t: byte offset into the pool, or -1 with the error bit set (once per token)
-__device__ __forceinline__ int64_t token_entry(const KvArgs& a, int64_t t, bool report)
+// The entries of the CTA's n tokens from t0 on: byte offsets into the pool, -1 for invalid tokens (with
+// the error bit)
+__device__ __forceinline__ void find_entries(const KvArgs& a, int64_t t0, int n, int64_t* entry)
 {
-    uint32_t bits = 0;
-    const int64_t off = kv_entry_offset(a.p, a.block_table, a.token_batch[t], a.token_pos[t],
-                                        (int64_t)a.p.max_blocks_per_seq * a.p.block_size, a.page_bytes, a.entry_bytes, &bits);
-    if (bits && report && a.err) atomicOr(a.err, bits);
-    return off;
+    if (threadIdx.x < n) {
+        uint32_t bits = 0;
+        const int64_t t = t0 + threadIdx.x;
+        entry[threadIdx.x] = kv_entry_offset(a.p, a.block_table, a.token_batch[t], a.token_pos[t],
+                                             (int64_t)a.p.max_blocks_per_seq * a.p.block_size, a.page_bytes,
+                                             a.entry_bytes, &bits);
+        if (bits && a.err) atomicOr(a.err, bits);
+    }
+}
+
+// Codes of eight elements y (packed pairs) and the scale byte of their block
+template <bool E2M1>
+__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float amax, uint32_t& scale)
+{
+    constexpr float kTop = E2M1 ? 6.0f : 7.0f;
+    scale = float_to_e4m3(fminf(__fdiv_rn(amax, kTop), 448.0f));
+    const float s = e4m3_to_float(scale);
+    if (s == 0.0f) return 0u;
+    float q[8];
+    if (amax <= FLT_MAX) {
+        // s is 2^-9 or more: the division as a reciprocal and remainder corrections
+        const float r = __frcp_rn(s);
+        const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-s, -s);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) ptx::unpack2(ptx::quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), q[i], q[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(y[i], s);
+    }
+    uint32_t code = 0;
+    if (E2M1) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            // (the corrections can lose the sign of a zero quotient, which the code keeps)
+            const float lo = copysignf(q[i], y[i]), hi = copysignf(q[i + 1], y[i + 1]);
+            uint32_t byte;
+            asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
+                : "=r"(byte)
+                : "f"(hi), "f"(lo));
+            code |= byte << (4 * i);
+        }
+    } else {
+        // q + 1.5 * 2^23 rounds q to an integer (ties to even), whose two's complement ends the sum's bits
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            code |= (__float_as_uint(fminf(fmaxf(q[i], -7.0f), 7.0f) + 12582912.0f) & 15u) << (4 * i);
+    }
+    return code;
 }
 
 template <bool F16, bool E2M1>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const uint16_t* __restrict__ k,
                                                               const uint16_t* __restrict__ v, uint8_t* __restrict__ pool,
-                                                              int tokens_per_cta)
+                                                              int slots, int tokens)
 {
+    __shared__ int64_t entry[kMaxTokens];
     ptx::pdl_wait();
-    const int nb = a.head_dim / kKvBlock, blocks = 2 * a.heads_kv * nb, unit = kv_unit_bytes(a.head_dim);
-    constexpr float kTop = E2M1 ? 6.0f : 7.0f;
-    for (int i = threadIdx.x; i < tokens_per_cta * blocks; i += kKvThreads) {
-        const int tl = i / blocks, ib = i - tl * blocks;
-        const int64_t t = (int64_t)blockIdx.x * tokens_per_cta + tl;
-        if (t >= a.tokens) break;
-        const int64_t entry = token_entry(a, t, ib == 0);
-        if (entry < 0) continue;
-        const BlockPos w = block_pos(ib, a.heads_kv, nb);
-        const uint4* src = reinterpret_cast<const uint4*>((w.kv ? v : k) + t * a.stride[w.kv] +
-                                                          (int64_t)w.h * a.head_dim + w.b * kKvBlock);
-        const uint4 u0 = src[0], u1 = src[1];
-        const uint32_t x[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    const int halves = 2 * a.heads_kv * (a.head_dim / 8);
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int n = (int)min((int64_t)tokens, a.tokens - t0);
+    find_entries(a, t0, n, entry);
+    __syncthreads();
+    const uint32_t pair = 3u << (threadIdx.x & 30);
+    for (int i = threadIdx.x; i < slots * halves; i += kKvThreads) {       // (an even number: a block's two lanes stay together)
+        const int slot = i / halves, ih = i - slot * halves;
+        const HalfPos w = half_pos(ih, a.heads_kv, a.head_dim);
+        const int64_t stride = a.stride[w.kv];
+        const uint16_t* src = (w.kv ? v : k) + w.element + t0 * stride;
         const float g = w.kv ? a.v_scale : a.k_scale;
-        float y[16], amax = 0.0f;
+        for (int l0 = slot; l0 < n; l0 += kUnroll * slots) {
+            uint4 x[kUnroll];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 f = act2_to_float2<F16>(x[j]);
-            y[2 * j] = __fdiv_rn(f.x, g);
-            y[2 * j + 1] = __fdiv_rn(f.y, g);
-            amax = fmaxf(amax, fmaxf(fabsf(y[2 * j]), fabsf(y[2 * j + 1])));
-        }
-        const uint32_t sb = float_to_e4m3(fminf(__fdiv_rn(amax, kTop), 448.0f));
-        const float s = e4m3_to_float(sb);
-        uint32_t code[2] = {0u, 0u};
-        if (s > 0.0f) {
+            for (int u = 0; u < kUnroll; ++u) {
+                const int l = l0 + u * slots;
+                x[u] = l < n ? __ldcs(reinterpret_cast<const uint4*>(src + l * stride)) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                const float q0 = __fdiv_rn(y[j], s), q1 = __fdiv_rn(y[j + 1], s);
-                uint32_t byte;
-                if (E2M1) {
-                    asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\t"
-                        "mov.b32 %0, {d, 0, 0, 0};\n\t}"
-                        : "=r"(byte)
-                        : "f"(q1), "f"(q0));
-                } else {
-                    const int c0 = __float2int_rn(fminf(fmaxf(q0, -7.0f), 7.0f));
-                    const int c1 = __float2int_rn(fminf(fmaxf(q1, -7.0f), 7.0f));
-                    byte = (c0 & 15) | ((c1 & 15) << 4);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int l = l0 + u * slots;
+                if (l >= n) break;
+                const uint32_t word[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                float y[8], amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = act2_to_float2<F16>(word[j]);
+                    y[2 * j] = f.x;
+                    y[2 * j + 1] = f.y;
                 }
-                code[j >> 3] |= byte << ((j & 7) * 4);
+                if (g != 1.0f) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], g);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+                amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
+                uint32_t scale;
+                const uint32_t code = quantize8<E2M1>(y, amax, scale);
+                const int64_t at = entry[l];
+                if (at < 0) continue;
+                *reinterpret_cast<uint32_t*>(pool + at + w.code) = code;
+                if (!(ih & 1)) pool[at + w.scale] = (uint8_t)scale;
             }
         }
-        uint8_t* dst = pool + entry + w.h * unit;
-        *reinterpret_cast<uint2*>(dst + w.kv * (a.head_dim / 2) + w.b * 8) = make_uint2(code[0], code[1]);
-        dst[a.head_dim + w.kv * nb + w.b] = (uint8_t)sb;
     }
 }
 
 template <bool F16, bool E2M1>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvArgs a, const uint8_t* __restrict__ pool,
-                                                             uint16_t* __restrict__ k, uint16_t* __restrict__ v,
-                                                             int tokens_per_cta)
+                                                             uint16_t* __restrict__ k, uint16_t* __restrict__ v, int slots,
+                                                             int tokens)
 {
+    __shared__ int64_t entry[kMaxTokens];
     ptx::pdl_wait();
-    const int nb = a.head_dim / kKvBlock, blocks = 2 * a.heads_kv * nb, unit = kv_unit_bytes(a.head_dim);
-    for (int i = threadIdx.x; i < tokens_per_cta * blocks; i += kKvThreads) {
-        const int tl = i / blocks, ib = i - tl * blocks;
-        const int64_t t = (int64_t)blockIdx.x * tokens_per_cta + tl;
-        if (t >= a.tokens) break;
-        const int64_t entry = token_entry(a, t, ib == 0);
-        const BlockPos w = block_pos(ib, a.heads_kv, nb);
-        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (entry >= 0) {
-            const uint8_t* src = pool + entry + w.h * unit;
-            const uint2 c = *reinterpret_cast<const uint2*>(src + w.kv * (a.head_dim / 2) + w.b * 8);
-            const float s = e4m3_to_float(src[a.head_dim + w.kv * nb + w.b]), g = w.kv ? a.v_scale : a.k_scale;
-            float f[8];
+    const int halves = 2 * a.heads_kv * (a.head_dim / 8);
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int n = (int)min((int64_t)tokens, a.tokens - t0);
+    find_entries(a, t0, n, entry);
+    __syncthreads();
+    for (int i = threadIdx.x; i < slots * halves; i += kKvThreads) {
+        const int slot = i / halves, ih = i - slot * halves;
+        const HalfPos w = half_pos(ih, a.heads_kv, a.head_dim);
+        const int64_t stride = a.stride[w.kv];
+        uint16_t* dst = (w.kv ? v : k) + w.element + t0 * stride;
+        const float g = w.kv ? a.v_scale : a.k_scale;
+        for (int l0 = slot; l0 < n; l0 += kUnroll * slots) {
+            uint32_t code[kUnroll], scale[kUnroll];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                decode8<E2M1>(j ? c.y : c.x, f);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int l = l0 + u * slots;
+                const int64_t at = l < n ? entry[l] : -1;
+                code[u] = at >= 0 ? *reinterpret_cast<const uint32_t*>(pool + at + w.code) : 0u;
+                scale[u] = at >= 0 ? pool[at + w.scale] : 0u;             // (an invalid token: zeros times zero)
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * j + e] = float2_to_act2<F16>(f[2 * e] * s * g, f[2 * e + 1] * s * g);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int l = l0 + u * slots;
+                if (l >= n) break;
+                const float s = e4m3_to_float(scale[u]);
+                float f[8];
+                decode8<E2M1>(code[u], f);
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = float2_to_act2<F16>(f[2 * e] * s * g, f[2 * e + 1] * s * g);
+                __stcs(reinterpret_cast<uint4*>(dst + l * stride), make_uint4(o[0], o[1], o[2], o[3]));
             }
         }
-        uint4* dst = reinterpret_cast<uint4*>((w.kv ? v : k) + t * a.stride[w.kv] + (int64_t)w.h * a.head_dim +
-                                              w.b * kKvBlock);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
-int tokens_per_cta(const KvArgs& a)
+// Token slots that a CTA's threads cover at once, and the tokens of a CTA: up to kMaxTokens while about
+// eight CTAs per SM remain
+struct Split {
+    int slots, tokens;
+};
+Split split_of(const KvArgs& a, int sms)
 {
-    const int blocks = 2 * a.heads_kv * (a.head_dim / kKvBlock);
-    return blocks >= kKvThreads ? 1 : kKvThreads / blocks;
+    const int halves = 2 * a.heads_kv * (a.head_dim / 8);
+    Split s;
+    s.slots = halves >= kKvThreads ? 1 : kKvThreads / halves;
+    if (s.slots > kMaxTokens) s.slots = kMaxTokens;
+    const int64_t per = ceil_div64(a.tokens, 8 * sms);
+    s.tokens = per < s.slots ? s.slots : (per > kMaxTokens ? kMaxTokens : (int)per);
+    return s;
 }
 
 }  // namespace
 
-cudaError_t launch_kv_write(const KvArgs& a, const void* k, const void* v, void* kv, cudaStream_t st)
+cudaError_t launch_kv_write(const KvArgs& a, int sms, const void* k, const void* v, void* kv, cudaStream_t st)
 {
-    const int tpc = tokens_per_cta(a);
+    const Split s = split_of(a, sms);
     auto kernel = a.f16 ? (a.e2m1 ? kv_write_kernel<true, true> : kv_write_kernel<true, false>)
                         : (a.e2m1 ? kv_write_kernel<false, true> : kv_write_kernel<false, false>);
-    return launch_pdl(kernel, dim3((unsigned)ceil_div64(a.tokens, tpc)), dim3(kKvThreads), 0, st, a,
-                      static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), static_cast<uint8_t*>(kv), tpc);
+    return launch_pdl(kernel, dim3((unsigned)ceil_div64(a.tokens, s.tokens)), dim3(kKvThreads), 0, st, a,
+                      static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), static_cast<uint8_t*>(kv), s.slots, s.tokens);
 }
 
-cudaError_t launch_kv_read(const KvArgs& a, const void* kv, void* k, void* v, cudaStream_t st)
+cudaError_t launch_kv_read(const KvArgs& a, int sms, const void* kv, void* k, void* v, cudaStream_t st)
 {
-    const int tpc = tokens_per_cta(a);
+    const Split s = split_of(a, sms);
     auto kernel = a.f16 ? (a.e2m1 ? kv_read_kernel<true, true> : kv_read_kernel<true, false>)
                         : (a.e2m1 ? kv_read_kernel<false, true> : kv_read_kernel<false, false>);
-    return launch_pdl(kernel, dim3((unsigned)ceil_div64(a.tokens, tpc)), dim3(kKvThreads), 0, st, a,
-                      static_cast<const uint8_t*>(kv), static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), tpc);
+    return launch_pdl(kernel, dim3((unsigned)ceil_div64(a.tokens, s.tokens)), dim3(kKvThreads), 0, st, a,
+                      static_cast<const uint8_t*>(kv), static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), s.slots, s.tokens);
 }
 
 }  // namespace qli

@@ -62,6 +62,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// The quotient x / s correctly rounded to fp32 (what an IEEE division gives), for 2^-126 <= s <
+// 2^125, from r = RN(1/s): q = RN(x * r), then two remainder corrections q <- RN(q + (x - q * s) * r)
+// with the remainder formed exactly by a fused multiply-add.  By Markstein's theorem (r within half
+// an ulp of 1/s and q within one ulp of x / s give the correctly rounded quotient) the second
+// correction is exact; the first brings RN(x * r), which can lie up to 1.5 ulp from x / s, within
+// one ulp.  Quotients below 2^-126 in magnitude may differ from the division's, but every such
+// quotient gives the code +-0 either way.  X, R and NS (= -s) hold two lanes each.
+__device__ __forceinline__ uint64_t quotient2(uint64_t X, uint64_t R, uint64_t NS)
+{
+    uint64_t Q = mul2(X, R);
+    Q = fma2(fma2(Q, NS, X), R, Q);
+    return fma2(fma2(Q, NS, X), R, Q);
+}
+
+__device__ __forceinline__ bool reciprocal_ok(float s) { return s >= 1.17549435e-38f && s < 4.2535296e37f; }
+
 // ------------------------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count)
 {

@@ -28,6 +28,8 @@ using ptx::add2;
 using ptx::fma2;
 using ptx::mul2;
 using ptx::pack2;
+using ptx::quotient2;
+using ptx::reciprocal_ok;
 using ptx::unpack2;
 
 constexpr int kGroup = 8;                             // lanes per vector
@@ -75,22 +77,6 @@ __device__ __forceinline__ uint32_t low_bytes(uint64_t p, uint64_t q)
     const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
 }
-
-// The quotient x / s correctly rounded to fp32 (what an IEEE division gives), for 2^-126 <= s <
-// 2^125, from r = RN(1/s): q = RN(x * r), then two remainder corrections q <- RN(q + (x - q * s) * r)
-// with the remainder formed exactly by a fused multiply-add.  By Markstein's theorem (r within half
-// an ulp of 1/s and q within one ulp of x / s give the correctly rounded quotient) the second
-// correction is exact; the first brings RN(x * r), which can lie up to 1.5 ulp from x / s, within
-// one ulp.  Quotients below 2^-126 in magnitude may differ from the division's, but every such
-// quotient gives the code +-0 either way.  X, R and NS (= -s) hold two lanes each.
-__device__ __forceinline__ uint64_t quotient2(uint64_t X, uint64_t R, uint64_t NS)
-{
-    uint64_t Q = mul2(X, R);
-    Q = fma2(fma2(Q, NS, X), R, Q);
-    return fma2(fma2(Q, NS, X), R, Q);
-}
-
-__device__ __forceinline__ bool reciprocal_ok(float s) { return s >= 1.17549435e-38f && s < 4.2535296e37f; }
 
 // Quantize the group's vector; (a, b) hold this lane's 16 elements.  Every lane of the warp must
 // call it (the shuffles span the warp; offsets below 8 stay within a group).
