@@ -58,7 +58,29 @@ __device__ __forceinline__ void find_entries(const KvArgs& a, int64_t t0, int n,
     }
 }
 
-// Codes of eight elements y (packed pairs) and the scale byte of their block
+// y <- y / d for eight elements whose largest quotient is `top`: a reciprocal and remainder corrections
+// where they give the correctly rounded quotient, else divisions.  The corrections can lose the sign
+// of a zero quotient; kSign keeps it.
+template <bool kSign>
+__device__ __forceinline__ void divide8(float (&y)[8], float d, float top)
+{
+    if (top <= FLT_MAX && ptx::reciprocal_ok(d)) {
+        const float r = __frcp_rn(d);
+        const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-d, -d);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float lo, hi;
+            ptx::unpack2(ptx::quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), lo, hi);
+            y[i] = kSign ? copysignf(lo, y[i]) : lo;
+            y[i + 1] = kSign ? copysignf(hi, y[i + 1]) : hi;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], d);
+    }
+}
+
+// Codes of eight elements y and the scale byte of their block
 template <bool E2M1>
 __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float amax, uint32_t& scale)
 {
@@ -67,26 +89,17 @@ __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float amax, u
     const float s = e4m3_to_float(scale);
     if (s == 0.0f) return 0u;
     float q[8];
-    if (amax <= FLT_MAX) {
-        // s is 2^-9 or more: the division as a reciprocal and remainder corrections
-        const float r = __frcp_rn(s);
-        const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-s, -s);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) ptx::unpack2(ptx::quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), q[i], q[i + 1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(y[i], s);
-    }
+    for (int i = 0; i < 8; ++i) q[i] = y[i];
+    divide8<E2M1>(q, s, amax);
     uint32_t code = 0;
     if (E2M1) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            // (the corrections can lose the sign of a zero quotient, which the code keeps)
-            const float lo = copysignf(q[i], y[i]), hi = copysignf(q[i + 1], y[i + 1]);
             uint32_t byte;
             asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
                 : "=r"(byte)
-                : "f"(hi), "f"(lo));
+                : "f"(q[i + 1]), "f"(q[i]));
             code |= byte << (4 * i);
         }
     } else {
@@ -136,13 +149,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
                     y[2 * j] = f.x;
                     y[2 * j + 1] = f.y;
                 }
-                if (g != 1.0f) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], g);
-                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
                 amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
+                if (g != 1.0f) {
+                    // (the division is monotone: the largest quotient is the largest magnitude's)
+                    amax = __fdiv_rn(amax, g);
+                    divide8<E2M1>(y, g, amax);
+                }
                 uint32_t scale;
                 const uint32_t code = quantize8<E2M1>(y, amax, scale);
                 const int64_t at = entry[l];
