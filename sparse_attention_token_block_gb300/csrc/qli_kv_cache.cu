@@ -80,28 +80,61 @@ __device__ __forceinline__ void divide8(float (&y)[8], float d, float top)
     }
 }
 
-// Codes of eight elements y and the scale byte of their block
+// The correctly rounded quotients y / d of a finite y and a d of at most four significant bits (a scale,
+// 6 or 7), from r within an ulp of 1 / d: q = RN(y r) is within two ulps of y / d, its remainder
+// y - q d is exact in a fused multiply-add, and q + (y - q d) r lies within 2^-21 ulp of y / d.
+// Rounded, that is the quotient rounded: y / d is no midpoint of two fp32 numbers (a 25-bit number
+// times d has more bits than y) and no nearer to one than 2^-5 ulp.  Quotients below 2^-126 may
+// differ, but give code 0 and scale 0 either way.
+__device__ __forceinline__ uint64_t short_quotient2(uint64_t Y, uint64_t R, uint64_t ND)
+{
+    const uint64_t Q = ptx::mul2(Y, R);
+    return ptx::fma2(ptx::fma2(Q, ND, Y), R, Q);
+}
+
+// Codes of eight elements y and the scale byte of their block, whose largest magnitude is amax
 template <bool E2M1>
 __device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float amax, uint32_t& scale)
 {
-    constexpr float kTop = E2M1 ? 6.0f : 7.0f;
-    scale = float_to_e4m3(fminf(__fdiv_rn(amax, kTop), 448.0f));
-    const float s = e4m3_to_float(scale);
+    constexpr float kTop = E2M1 ? 6.0f : 7.0f, kTopInv = 1.0f / kTop;
+    if (!(amax <= FLT_MAX)) {                          // y = x / g overflowed: the largest scale, codes +-Q or 0
+        scale = 0x7E;
+        uint32_t code = 0;
+        for (int i = 0; i < 8; ++i) {
+            const float q = fminf(fmaxf(__fdiv_rn(y[i], 448.0f), -kTop), kTop);
+            uint32_t c = (uint32_t)__float2int_rn(q) & 15u;
+            if (E2M1) {
+                asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
+                    : "=r"(c)
+                    : "f"(0.0f), "f"(q));
+                c &= 15u;
+            }
+            code |= c << (4 * i);
+        }
+        return code;
+    }
+    float s, dummy;
+    ptx::unpack2(short_quotient2(ptx::pack2(amax, 0.0f), ptx::pack2(kTopInv, kTopInv), ptx::pack2(-kTop, -kTop)), s, dummy);
+    scale = float_to_e4m3(fminf(s, 448.0f));
+    s = e4m3_to_float(scale);
     if (s == 0.0f) return 0u;
+    const float r = ptx::rcp_approx(s);
+    const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-s, -s);
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = y[i];
-    divide8<E2M1>(q, s, amax);
+    for (int i = 0; i < 8; i += 2) ptx::unpack2(short_quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), q[i], q[i + 1]);
     uint32_t code = 0;
     if (E2M1) {
+        uint32_t byte[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            uint32_t byte;
+        for (int i = 0; i < 4; ++i) {
+            // (the correction can lose the sign of a zero quotient, which the code keeps)
+            const float lo = copysignf(q[2 * i], y[2 * i]), hi = copysignf(q[2 * i + 1], y[2 * i + 1]);
             asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
-                : "=r"(byte)
-                : "f"(q[i + 1]), "f"(q[i]));
-            code |= byte << (4 * i);
+                : "=r"(byte[i])
+                : "f"(hi), "f"(lo));
         }
+        code = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
     } else {
         // q + 1.5 * 2^23 rounds q to an integer (ties to even), whose two's complement ends the sum's bits
 #pragma unroll
@@ -123,24 +156,27 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
     const int n = (int)min((int64_t)tokens, a.tokens - t0);
     find_entries(a, t0, n, entry);
     __syncthreads();
-    const uint32_t pair = 3u << (threadIdx.x & 30);
-    for (int i = threadIdx.x; i < slots * halves; i += kKvThreads) {       // (an even number: a block's two lanes stay together)
-        const int slot = i / halves, ih = i - slot * halves;
+    const int covered = slots * halves;
+    for (int base = 0; base < covered; base += kKvThreads) {
+        // (threads past the end follow along with nothing to load or store: whole warps take part in the exchange)
+        const int i = min(base + (int)threadIdx.x, covered - 1), slot = i / halves, ih = i - slot * halves;
+        const bool live = base + (int)threadIdx.x < covered;
         const HalfPos w = half_pos(ih, a.heads_kv, a.head_dim);
         const int64_t stride = a.stride[w.kv];
         const uint16_t* src = (w.kv ? v : k) + w.element + t0 * stride;
         const float g = w.kv ? a.v_scale : a.k_scale;
-        for (int l0 = slot; l0 < n; l0 += kUnroll * slots) {
+        for (int l0 = 0; l0 < n; l0 += kUnroll * slots) {
             uint4 x[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int l = l0 + u * slots;
-                x[u] = l < n ? __ldcs(reinterpret_cast<const uint4*>(src + l * stride)) : make_uint4(0u, 0u, 0u, 0u);
+                const int l = l0 + slot + u * slots;
+                x[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (live && l < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + l * stride));
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int l = l0 + u * slots;
-                if (l >= n) break;
+                if (l0 + u * slots >= n) break;                        // the same for every thread
+                const int l = l0 + slot + u * slots;
                 const uint32_t word[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
                 float y[8], amax = 0.0f;
 #pragma unroll
@@ -151,7 +187,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
-                amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 if (g != 1.0f) {
                     // (the division is monotone: the largest quotient is the largest magnitude's)
                     amax = __fdiv_rn(amax, g);
@@ -159,10 +195,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
                 }
                 uint32_t scale;
                 const uint32_t code = quantize8<E2M1>(y, amax, scale);
-                const int64_t at = entry[l];
-                if (at < 0) continue;
-                *reinterpret_cast<uint32_t*>(pool + at + w.code) = code;
-                if (!(ih & 1)) pool[at + w.scale] = (uint8_t)scale;
+                const int64_t at = live && l < n ? entry[l] : -1;
+                if (at >= 0) {
+                    *reinterpret_cast<uint32_t*>(pool + at + w.code) = code;
+                    if (!(ih & 1)) pool[at + w.scale] = (uint8_t)scale;
+                }
             }
         }
     }

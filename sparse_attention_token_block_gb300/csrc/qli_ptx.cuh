@@ -442,6 +442,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// 1 / x within one ulp, x and 1 / x normal
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 2^x (about 2 ulp; 2^-infinity = 0)
 __device__ __forceinline__ float ex2(float x)
 {
