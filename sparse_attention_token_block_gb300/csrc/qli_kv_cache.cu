@@ -154,8 +154,6 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
     const int halves = 2 * a.heads_kv * (a.head_dim / 8);
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int n = (int)min((int64_t)tokens, a.tokens - t0);
-    find_entries(a, t0, n, entry);
-    __syncthreads();
     const int covered = slots * halves;
     for (int base = 0; base < covered; base += kKvThreads) {
         // (threads past the end follow along with nothing to load or store: whole warps take part in the exchange)
@@ -172,6 +170,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
                 const int l = l0 + slot + u * slots;
                 x[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (live && l < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + l * stride));
+            }
+            if (base == 0 && l0 == 0) {                                // (behind the first loads)
+                find_entries(a, t0, n, entry);
+                __syncthreads();
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
