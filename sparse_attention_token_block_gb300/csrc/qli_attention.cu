@@ -152,7 +152,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         for (int x = 0; x < kStages; ++x) ptx::mbar_init(&bars[wid][x], kShared ? kWarps : (L.page_rows ? 1 : 32));
         ptx::fence_mbar_init();
     }
+    if (tid == 0 && L.page_rows) ptx::prefetch_tensormap(&rows);
+    const int unit = wid / L.parts, part = wid - unit * L.parts;
+    const int kvh = (u0 + unit) / L.chunks;
+    const int h0 = kvh * group + (u0 + unit - kvh * L.chunks) * 8 * NT;      // the unit's first query head
+    const int nh = min(8 * NT, (kvh + 1) * group - h0);
+    const int r = lane >> 2, c = lane & 3;
     ptx::pdl_wait();
+    // the query heads' elements, under way while the list is resolved: head r of each block of eight,
+    // this lane's quarter of D
+    uint4 qraw[NT][NW];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            qraw[t][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (wid < active && 8 * t + r < nh)
+                qraw[t][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.query) + (int64_t)row * a.q_stride +
+                                                             (int64_t)(h0 + 8 * t + r) * D + c * (D / 4) + 8 * j);
+        }
 
     // ---- the slice's entries as rows of the pool, 32 positions of the list per warp at a time: the mask
     // of the valid ones, and in the others' places a valid one's row (what is copied from there is
@@ -200,11 +218,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     }
     __syncthreads();
 
-    const int unit = wid / L.parts, part = wid - unit * L.parts;
-    const int kvh = (u0 + unit) / L.chunks;
-    const int h0 = kvh * group + (u0 + unit - kvh * L.chunks) * 8 * NT;      // the unit's first query head
-    const int nh = min(8 * NT, (kvh + 1) * group - h0);
-    const int r = lane >> 2, c = lane & 3;
     float o[NT][MO][4], m[NT][2], l[NT][2];
     if (wid < active) {
         // the chunks of 32 positions part, part + parts, ... are this warp's steps; a chunk without a valid
@@ -247,24 +260,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 ptx::cp_async_arrive_noinc(&bar[stage]);
             }
         };
-        for (int st = 0; st < min(kStages, steps); ++st) copy_step(st, st);
-        // query fragments: head r of each block of eight, this lane's quarter of D, scaled by a power of two
+        if (steps > 0) copy_step(0, 0);
+        // query fragments, scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
-        const uint16_t* qrow = static_cast<const uint16_t*>(a.query) + (int64_t)row * a.q_stride + (int64_t)h0 * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             uint32_t w[NW][4];
-            const bool live = 8 * t + r < nh;
 #pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (live) v = *reinterpret_cast<const uint4*>(qrow + (int64_t)(8 * t + r) * D + c * (D / 4) + 8 * j);
-                w[j][0] = v.x;
-                w[j][1] = v.y;
-                w[j][2] = v.z;
-                w[j][3] = v.w;
-            }
+            for (int j = 0; j < NW; ++j) w[j][0] = qraw[t][j].x, w[j][1] = qraw[t][j].y, w[j][2] = qraw[t][j].z, w[j][3] = qraw[t][j].w;
             float big = 0.0f;
 #pragma unroll
             for (int j = 0; j < NW; ++j)
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             m[t][0] = m[t][1] = -FLT_MAX;
             l[t][0] = l[t][1] = 0.0f;
         }
+        for (int st = 1; st < min(kStages, steps); ++st) copy_step(st, st);
         const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
         const uint8_t* head = ring + kvh * kUnit - lo;
         const uint8_t* kc0 = head + tk * kRow + (D / 8) * c;                       // the lane's key codes and scales,
