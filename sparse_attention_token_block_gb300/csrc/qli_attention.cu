@@ -239,12 +239,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(&bar[stage], go ? kStep : 0);
                     if (go) {
-                        const int4* at = reinterpret_cast<const int4*>(list + 32 * ch);
+                        int4 y[8];                // all loads first: the gathers keep the compiler from moving them up
 #pragma unroll
-                        for (int g = 0; g < 8; ++g) {
-                            const int4 y = at[g];
-                            ptx::tma_gather4(ring + stage * kStep + 4 * g * kRow, &rows, lo / 8, y.x, y.y, y.z, y.w, &bar[stage]);
-                        }
+                        for (int g = 0; g < 8; ++g) y[g] = reinterpret_cast<const int4*>(list + 32 * ch)[g];
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            ptx::tma_gather4(ring + stage * kStep + 4 * g * kRow, &rows, lo / 8, y[g].x, y[g].y, y[g].z, y[g].w,
+                                             &bar[stage]);
                     }
                 }
                 __syncwarp();
