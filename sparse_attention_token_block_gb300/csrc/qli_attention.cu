@@ -228,17 +228,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         auto copy_step = [&](int st, int stage) {
             const int ch = st * L.parts + part;
             const bool go = masks[ch] != 0;
+            const bool stall = a.p.test_stall == 1;            // test switch: nothing arrives, the waits run out
             if constexpr (kShared) {
                 if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(&bar[stage], go ? 4 * kRow : 0);
                     const int4 y = *reinterpret_cast<const int4*>(list + 32 * ch + 4 * wid);
-                    if (go) ptx::tma_gather4(ring + stage * kStep + 4 * wid * kRow, &rows, lo / 8, y.x, y.y, y.z, y.w, &bar[stage]);
+                    if (go && !stall) ptx::tma_gather4(ring + stage * kStep + 4 * wid * kRow, &rows, lo / 8, y.x, y.y, y.z, y.w, &bar[stage]);
                 }
                 __syncwarp();
             } else if (L.page_rows) {
                 if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(&bar[stage], go ? kStep : 0);
-                    if (go) {
+                    if (go && !stall) {
                         int4 y[8];                // all loads first: the gathers keep the compiler from moving them up
 #pragma unroll
                         for (int g = 0; g < 8; ++g) y[g] = reinterpret_cast<const int4*>(list + 32 * ch)[g];

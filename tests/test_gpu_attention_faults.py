@@ -1,0 +1,57 @@
+"""Failure detection of the sparse attention on the GPU without a fault: with the testing build's stall
+switch no row gather is issued, so every bounded wait runs out; the kernel must report
+QLI_ERR_DEVICE_TIMEOUT, write NaN and leave the CUDA context usable."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CHILD = r"""
+import sys
+sys.path.insert(0, %r)
+import torch
+import sparse_attention_token_block_gb300 as Q
+Q.use_testing_library()
+Q.lib.qli_testing_set_stall(%d)
+rows = %d
+p = Q.make_problem(batch=rows, max_q_tokens=1, num_blocks=4, block_size=64, max_blocks_per_seq=4, sparse_count=64,
+                   sparse_mode=0, cmp_ratio=1, max_seqlen_q=1, max_seqlen_k=256)
+a = Q.make_attention(num_heads_q=8, num_heads_kv=8, head_dim=64)
+dev = dict(device="cuda")
+pool = torch.zeros(4, 64, Q.kv_entry_bytes(a), dtype=torch.uint8, **dev)
+q = torch.ones(rows, 8, 64, dtype=torch.bfloat16, **dev)
+out = torch.zeros_like(q)
+table = torch.arange(4, dtype=torch.int32, **dev).repeat(rows, 1)
+idx = torch.arange(64, dtype=torch.int32, **dev).repeat(rows, 1)
+lens = torch.full((rows,), 256, dtype=torch.int32, **dev)
+ws = torch.zeros(64, dtype=torch.int32, **dev)
+Q.check(Q.sparse_attention(p, a, q, None, lens, table, idx, pool, out, None, ws), "sparse_attention")
+st, bits = Q.get_device_error(ws)
+print("STATUS", st, bits, int(torch.isnan(out.float()).all().item()), int((out == 0).all().item()))
+print("AFTER", torch.ones(1024, **dev).sum().item())
+"""
+
+
+@pytest.fixture(scope="module")
+def built():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_attention_token_block_gb300 import build as B
+    B.build()
+
+
+# 2 rows: a ring per warp; 460 rows (more than three CTAs of one head each per SM): the shared ring
+@pytest.mark.parametrize("rows", [2, 460])
+@pytest.mark.parametrize("stall", [1, 0])
+def test_waits_run_out(built, rows, stall):
+    out = subprocess.run([sys.executable, "-c", CHILD % (ROOT, stall, rows)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0, out.stderr[-2000:]
+    status = [x for x in out.stdout.splitlines() if x.startswith("STATUS")][0].split()[1:]
+    assert status == (["6", "4", "1", "0"] if stall else ["0", "0", "0", "1"])
+    assert "AFTER 1024.0" in out.stdout
