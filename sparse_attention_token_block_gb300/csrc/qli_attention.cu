@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             const uint8_t* vs = vs0 + stage * kStep;
             // ---- logits of two tiles of 16 entries
             float s[2][NT][4];
-            uint32_t w[2][2][NW], g[2][2][2];      // tile, row r or r + 8: codes and the two halves' scales
+            uint32_t w[2][2][NW];                  // tile, row r or r + 8: codes
+            PairScale g[2][2][D / 64];             // and the scales of the lane's blocks
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -341,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                     const uint8_t* x = ks + (16 * u + 8 * y) * kRow;
                     if constexpr (D == 128) {
                         const uint32_t h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(x));
-                        g[u][y][0] = __byte_perm(h, 0, 0x1010);
-                        g[u][y][1] = __byte_perm(h, 0, 0x3232);
+                        g[u][y][0] = pair_scale<E2M1>(__byte_perm(h, 0, 0x1010));
+                        g[u][y][1] = pair_scale<E2M1>(__byte_perm(h, 0, 0x3232));
                     } else {
-                        g[u][y][0] = g[u][y][1] = __byte_perm(e4m3x2_to_f16x2(*x), 0, 0x1010);
+                        g[u][y][0] = pair_scale<E2M1>(__byte_perm(e4m3x2_to_f16x2(*x), 0, 0x1010));
                     }
                 }
 #pragma unroll
@@ -356,13 +357,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t x[4], y[4];
-                    decode_pairs<E2M1>(w[u][0][j], x);
-                    decode_pairs<E2M1>(w[u][1][j], y);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[i] = ptx::mul_f16x2(x[i], g[u][0][j / (NW / 2)]);
-                        y[i] = ptx::mul_f16x2(y[i], g[u][1][j / (NW / 2)]);
-                    }
+                    decode_pairs<E2M1>(w[u][0][j], g[u][0][j / 2], x);
+                    decode_pairs<E2M1>(w[u][1][j], g[u][1][j / 2], y);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         ptx::mma_16816(s[u][t], x[0], y[0], x[1], y[1], q[t][j][0], q[t][j][1]);
@@ -437,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint8_t* x0 = vs + 16 * u * kRow;
-                const uint32_t sab = e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[vb] << 8);
-                const uint32_t scd = e4m3x2_to_f16x2(x0[8 * kRow] | (uint32_t)x0[vb + 8 * kRow] << 8);
+                const PairScale sab = pair_scale<E2M1>(e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[vb] << 8));
+                const PairScale scd = pair_scale<E2M1>(e4m3x2_to_f16x2(x0[8 * kRow] | (uint32_t)x0[vb + 8 * kRow] << 8));
                 uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
                 load_words<NW / 2>(va + 16 * u * kRow, wa);
                 load_words<NW / 2>(va + 16 * u * kRow + vb, wb);
@@ -447,16 +443,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
                 for (int j = 0; j < NW / 2; ++j) {
                     uint32_t x[8], y[8];
-                    decode_across<E2M1>(wa[j], wb[j], x);
-                    decode_across<E2M1>(wc[j], wd[j], y);
+                    decode_across<E2M1>(wa[j], wb[j], sab, x);
+                    decode_across<E2M1>(wc[j], wd[j], scd, y);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = ptx::mul_f16x2(x[2 * i], sab), a1 = ptx::mul_f16x2(x[2 * i + 1], sab);
-                        const uint32_t a2 = ptx::mul_f16x2(y[2 * i], scd), a3 = ptx::mul_f16x2(y[2 * i + 1], scd);
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
-                            ptx::mma_16816(o[t][4 * j + i], a0, a1, a2, a3, pb[u][t][0], pb[u][t][1]);
-                    }
+                            ptx::mma_16816(o[t][4 * j + i], x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], pb[u][t][0], pb[u][t][1]);
                 }
             }
             }

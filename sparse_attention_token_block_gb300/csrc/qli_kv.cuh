@@ -82,21 +82,38 @@ __device__ __forceinline__ void decode8(uint32_t w, float (&v)[8])
     }
 }
 
-// Eight codes of one vector in a word as four fp16 pairs, exactly: E2M1 elements (2i, 2i + 1), int4
-// elements (i, i + 4).  The int4 nibbles u = code + 8 are placed as fractions of fp16 numbers (1024 + u
-// at bits 0-3; 1024 + 16 u at bits 4-7).
+// Scales of two elements as fp16, prepared for the codes they multiply.  An int4 nibble u = code + 8 is
+// placed at bits 4-7 of the fp16 number x = 1024 + 16 u, so code * s = x * (s / 16) - 72 s, one fused
+// multiply-add.  All of it is exact: s has at most four significant bits, 72 s at most eight, the result
+// at most seven, and the smallest numbers (2^-13) are normal or multiples of fp16's spacing.
+struct PairScale {
+    uint32_t mul, add;
+};
 template <bool E2M1>
-__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t (&o)[4])
+__device__ __forceinline__ PairScale pair_scale(uint32_t s)
+{
+    if (E2M1) return {s, 0u};
+    return {ptx::mul_f16x2(s, 0x2C002C00u), ptx::mul_f16x2(s, 0xD480D480u)};        // s / 16, -72 s
+}
+
+// Eight codes of one vector in a word, times their scale, as four fp16 pairs, exactly: E2M1 elements
+// (2i, 2i + 1), int4 elements (i, i + 4)
+template <bool E2M1>
+__device__ __forceinline__ void decode_pairs(uint32_t w, const PairScale& s, uint32_t (&o)[4])
 {
     if (E2M1) {
         e2m1x8_to_f16x2(w, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = ptx::mul_f16x2(o[i], s.mul);
         return;
     }
-    const uint32_t u = w ^ 0x88888888u, v = u >> 8;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[0]) : "r"((u & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[1]) : "r"((u & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2]) : "r"((v & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[3]) : "r"((v & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+    const uint32_t at[4] = {w << 4, w, w >> 4, w >> 8};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (w & 0xF0) with its top bit flipped (u = code + 8), under the exponent of 1024
+        const uint32_t x = (at[i] & 0x00F000F0u) ^ 0x64806480u;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(x), "r"(s.mul), "r"(s.add));
+    }
 }
 
 // The low nibble of every byte of a, the high nibble of every byte of b (one instruction)
@@ -107,31 +124,26 @@ __device__ __forceinline__ uint32_t select_low_nibbles(uint32_t a, uint32_t b)
     return r;
 }
 
-// Eight codes each of two vectors as eight fp16 pairs (a's element e, b's element e), exactly
+// Eight codes each of two vectors, times their scales (s: a's, b's), as eight fp16 pairs (a's element e,
+// b's element e), exactly
 template <bool E2M1>
-__device__ __forceinline__ void decode_across(uint32_t a, uint32_t b, uint32_t (&o)[8])
+__device__ __forceinline__ void decode_across(uint32_t a, uint32_t b, const PairScale& s, uint32_t (&o)[8])
 {
+    uint32_t x[4], y[4];
     if (E2M1) {
         // bytes of (a's nibble, b's nibble) for the even and the odd elements
         const uint32_t even = select_low_nibbles(a, b << 4), odd = select_low_nibbles(a >> 4, b);
-        uint32_t x[4], y[4];
-        e2m1x8_to_f16x2(even, x);
-        e2m1x8_to_f16x2(odd, y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = x[i];
-            o[2 * i + 1] = y[i];
-        }
-        return;
+        decode_pairs<true>(even, s, x);
+        decode_pairs<true>(odd, s, y);
+    } else {
+        // elements 0-3 of both in one word, 4-7 in another
+        decode_pairs<false>(__byte_perm(a, b, 0x5410), s, x);
+        decode_pairs<false>(__byte_perm(a, b, 0x7632), s, y);
     }
-    const uint32_t lo = __byte_perm(a, b, 0x5410), hi = __byte_perm(a, b, 0x7632);
-    uint32_t x[4], y[4];
-    decode_pairs<false>(lo, x);             // (a's element i, b's element i) of the low halves
-    decode_pairs<false>(hi, y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        o[i] = x[i];
-        o[4 + i] = y[i];
+        o[E2M1 ? 2 * i : i] = x[i];
+        o[E2M1 ? 2 * i + 1 : 4 + i] = y[i];
     }
 }
 

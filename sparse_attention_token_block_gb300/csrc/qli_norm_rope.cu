@@ -3,12 +3,13 @@
 // over the R leading elements (pairs (i, i + R/2) or (2i, 2i + 1)), fp32 throughout, rounded once.
 //
 // A stream over HBM: 2 bytes read and 2 written per element and a table row per token.  A CTA works
-// on one token (few tokens: several CTAs on one, by heads), so the rotation's factors and the weights
-// stay in registers; D / 8 lanes share a head vector, and each does kHeads heads at a time with all their
+// on one token (few tokens: several CTAs on one, by heads), so the rotation's factors stay in registers
+// and the weights, as fp32, in shared memory; D / 8 lanes share a head vector, and each does kHeads heads at a time with all their
 // loads under way before the first is used.  A lane has two chunks of four elements of a vector,
 // chosen so that it holds both elements of its pairs: in the half layout lane l < R/8 takes 4l.. and
 // R/2 + 4l.., in the interleaved layout (and past R) eight consecutive elements.  So the rotation
-// needs no exchange between lanes and the norm only a sum over the group.
+// needs no exchange between lanes and the norm only a sum over the group.  The arithmetic runs two
+// elements at a time in packed fp32.
 #include <cuda_runtime.h>
 
 #include "qli_kv.cuh"
@@ -17,22 +18,29 @@ namespace qli {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;
+constexpr int kManyHeads = 9;              // heads of a lane under way together, with many tokens
+
+// Four activations in two words as two packed pairs
+template <bool F16>
+__device__ __forceinline__ void unpack4(const uint2& u, uint64_t (&y)[2])
+{
+    const float2 a = act2_to_float2<F16>(u.x), b = act2_to_float2<F16>(u.y);
+    y[0] = ptx::pack2(a.x, a.y);
+    y[1] = ptx::pack2(b.x, b.y);
+}
 
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint2& u, const uint2& v, float (&y)[8])
+__device__ __forceinline__ uint2 pack4(const uint64_t (&y)[2])
 {
-    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = act2_to_float2<F16>(w[i]);
-        y[2 * i] = f.x;
-        y[2 * i + 1] = f.y;
-    }
+    float a, b, c, d;
+    ptx::unpack2(y[0], a, b);
+    ptx::unpack2(y[1], c, d);
+    return make_uint2(float2_to_act2<F16>(a, b), float2_to_act2<F16>(c, d));
 }
 
 template <bool F16, int D, bool kInterleaved, int kHeads>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(NormRopeArgs a)
+__global__ void __launch_bounds__(kNormThreads, kHeads > 1 ? 8 : 1) norm_rope_kernel(NormRopeArgs a)
 {
     constexpr int G = D / 8, kGroups = kNormThreads / G;           // lanes per vector, vectors at a time
     ptx::pdl_wait();
@@ -49,11 +57,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(NormRopeArgs a)
     const uint16_t* const in_k = static_cast<const uint16_t*>(a.in[1]) + t * a.in_stride[1] - (int64_t)a.heads[0] * D;
     uint16_t* const out_q = static_cast<uint16_t*>(a.out[0]) + t * a.out_stride[0];
     uint16_t* const out_k = static_cast<uint16_t*>(a.out[1]) + t * a.out_stride[1] - (int64_t)a.heads[0] * D;
-    uint2 w[2][2] = {};
+    __shared__ __align__(16) float weight[2][D];
+    if (a.norm) {
+        for (int i = threadIdx.x; i < D; i += kNormThreads) {
+            const int s = i >= D / 2, e = i - s * (D / 2);         // two elements of one side's weights
+            const uint32_t* w = static_cast<const uint32_t*>(a.weight[s]);
+            const float2 f = w ? act2_to_float2<F16>(w[e]) : make_float2(0.0f, 0.0f);
+            *reinterpret_cast<float2*>(&weight[s][2 * e]) = f;
+        }
+    }
     const int pos = a.positions[t];
     const bool ok = pos >= 0 && pos < a.max_positions;
     if (!ok && a.err && h_first == 0 && lane == 0) atomicOr(a.err, kErrLength);
     float cs[8] = {1, 1, 1, 1, 0, 0, 0, 0};                        // cosines, sines of the lane's pairs
+    if (ok && rot) {
+        const float* p = a.cos_sin + (int64_t)pos * R + 4 * lane;
+        const float4 c = *reinterpret_cast<const float4*>(p), s = *reinterpret_cast<const float4*>(p + R / 2);
+        cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+        cs[4] = s.x, cs[5] = s.y, cs[6] = s.z, cs[7] = s.w;
+    }
     for (int h0 = h_first; h0 - h_first < heads; h0 += kHeads * step) {        // (a whole group leaves together)
         uint2 x[kHeads][2];
 #pragma unroll
@@ -66,54 +88,55 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(NormRopeArgs a)
                 x[u][1] = *reinterpret_cast<const uint2*>(p + c1);
             }
         }
-        if (h0 == h_first) {
-            if (a.norm) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint16_t* p = static_cast<const uint16_t*>(a.weight[s]);
-                    if (p) {
-                        w[s][0] = *reinterpret_cast<const uint2*>(p + c0);
-                        w[s][1] = *reinterpret_cast<const uint2*>(p + c1);
-                    }
-                }
-            }
-            if (ok && rot) {
-                const float* p = a.cos_sin + (int64_t)pos * R + 4 * lane;
-                const float4 c = *reinterpret_cast<const float4*>(p), s = *reinterpret_cast<const float4*>(p + R / 2);
-                cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
-                cs[4] = s.x, cs[5] = s.y, cs[6] = s.z, cs[7] = s.w;
-            }
-        }
+        if (h0 == h_first) __syncthreads();                        // the weights (behind the first loads)
 #pragma unroll
         for (int u = 0; u < kHeads; ++u) {
             const int h = h0 + u * step, side = h >= a.heads[0];
-            float y[8];
-            unpack8<F16>(x[u][0], x[u][1], y);
+            if (h0 - h_first + u * step >= heads) break;           // the same for every thread
+            uint64_t y[2][2];                                      // the two chunks, in pairs
+            unpack4<F16>(x[u][0], y[0]);
+            unpack4<F16>(x[u][1], y[1]);
             if (a.norm) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+                uint64_t sq = ptx::mul2(y[0][0], y[0][0]);
+                sq = ptx::fma2(y[0][1], y[0][1], sq);
+                sq = ptx::fma2(y[1][0], y[1][0], sq);
+                sq = ptx::fma2(y[1][1], y[1][1], sq);
+                float ss, odd;
+                ptx::unpack2(sq, ss, odd);
+                ss += odd;
 #pragma unroll
                 for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-                float g[8];
-                unpack8<F16>(side ? w[1][0] : w[0][0], side ? w[1][1] : w[0][1], g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * r * g[i];
+                const uint64_t rr = ptx::pack2(r, r);
+                const float4 g0 = *reinterpret_cast<const float4*>(&weight[side][c0]);
+                const float4 g1 = *reinterpret_cast<const float4*>(&weight[side][c1]);
+                y[0][0] = ptx::mul2(ptx::mul2(y[0][0], rr), ptx::pack2(g0.x, g0.y));
+                y[0][1] = ptx::mul2(ptx::mul2(y[0][1], rr), ptx::pack2(g0.z, g0.w));
+                y[1][0] = ptx::mul2(ptx::mul2(y[1][0], rr), ptx::pack2(g1.x, g1.y));
+                y[1][1] = ptx::mul2(ptx::mul2(y[1][1], rr), ptx::pack2(g1.z, g1.w));
             }
-            if (h >= heads) continue;
-            // pairs (i, i + 4) of the lane's elements, or (2i, 2i + 1)
+            if (rot) {
+                if (kInterleaved) {
+                    // a pair of elements is a pair of the rotation
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int p = kInterleaved ? 2 * i : i, q = kInterleaved ? 2 * i + 1 : i + 4;
-                const float ya = y[p], yb = y[q];
-                if (rot) {
-                    y[p] = ya * cs[i] - yb * cs[4 + i];
-                    y[q] = yb * cs[i] + ya * cs[4 + i];
+                    for (int i = 0; i < 4; ++i) {
+                        float ya, yb;
+                        ptx::unpack2(y[i >> 1][i & 1], ya, yb);
+                        y[i >> 1][i & 1] = ptx::pack2(ya * cs[i] - yb * cs[4 + i], yb * cs[i] + ya * cs[4 + i]);
+                    }
+                } else {
+                    // the first chunk's elements turn with the second's
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint64_t c = ptx::pack2(cs[2 * i], cs[2 * i + 1]), s = ptx::pack2(cs[4 + 2 * i], cs[5 + 2 * i]);
+                        const uint64_t ns = ptx::pack2(-cs[4 + 2 * i], -cs[5 + 2 * i]), ya = y[0][i], yb = y[1][i];
+                        y[0][i] = ptx::fma2(ya, c, ptx::mul2(yb, ns));
+                        y[1][i] = ptx::fma2(yb, c, ptx::mul2(ya, s));
+                    }
                 }
             }
-            uint2 lo = make_uint2(float2_to_act2<F16>(y[0], y[1]), float2_to_act2<F16>(y[2], y[3]));
-            uint2 hi = make_uint2(float2_to_act2<F16>(y[4], y[5]), float2_to_act2<F16>(y[6], y[7]));
+            if (h >= heads) continue;
+            uint2 lo = pack4<F16>(y[0]), hi = pack4<F16>(y[1]);
             if (!ok) lo = hi = make_uint2(0u, 0u);
             uint16_t* p = (side ? out_k : out_q) + h * D;
             *reinterpret_cast<uint2*>(p + c0) = lo;
@@ -125,15 +148,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(NormRopeArgs a)
 template <bool F16, bool kInterleaved>
 cudaError_t launch_type(const NormRopeArgs& a, int head_dim, int sms, cudaStream_t st)
 {
-    // CTAs per token: as many as leave each group of lanes one head, once there are enough tokens five
-    // heads (prefill of 15360 tokens, 72 heads of 128: 143 us with one, 107 with five)
+    // CTAs per token: as many as leave each group of lanes one head; with many tokens one for every
+    // kManyHeads heads of a group (prefill of 15360 tokens, 72 heads of 128: 143 us with one head a lane,
+    // 108 with five and 256 threads, 96 with nine and 128)
     const int groups = kNormThreads / (head_dim / 8), heads = a.heads[0] + a.heads[1];
     int64_t slices = ceil_div64(heads, groups);
-    const bool many = slices > 1 && a.tokens * slices > 4 * sms;
-    if (many) slices = ceil_div64(slices, 5);
-    auto kernel = many ? (head_dim == 64 ? norm_rope_kernel<F16, 64, kInterleaved, 5>
-                                         : (head_dim == 128 ? norm_rope_kernel<F16, 128, kInterleaved, 5>
-                                                            : norm_rope_kernel<F16, 256, kInterleaved, 5>))
+    const bool many = slices > 1 && a.tokens * slices > 16 * sms;
+    if (many) slices = ceil_div64(slices, kManyHeads);
+    auto kernel = many ? (head_dim == 64 ? norm_rope_kernel<F16, 64, kInterleaved, kManyHeads>
+                                         : (head_dim == 128 ? norm_rope_kernel<F16, 128, kInterleaved, kManyHeads>
+                                                            : norm_rope_kernel<F16, 256, kInterleaved, kManyHeads>))
                        : (head_dim == 64 ? norm_rope_kernel<F16, 64, kInterleaved, 1>
                                          : (head_dim == 128 ? norm_rope_kernel<F16, 128, kInterleaved, 1>
                                                             : norm_rope_kernel<F16, 256, kInterleaved, 1>));

@@ -86,6 +86,13 @@ def test_matches_the_oracle(Q, shape, inter, f16, norm):
     assert (hq == 0 or torch.equal(q, qo)) and torch.equal(k, ko[:, :hk]) and torch.equal(x[:, hq + hk:], rest)
 
 
+# enough tokens that a lane takes several heads at a time
+@pytest.mark.parametrize("shape", [(700, 40, 3, 128, 128), (500, 90, 7, 256, 64), (2600, 20, 5, 64, 24)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_many_tokens(Q, shape, inter):
+    test_matches_the_oracle(Q, shape, inter, False, True)
+
+
 def test_zero_vectors_extreme_magnitudes_and_last_position(Q):
     import torch
     d = 128
