@@ -195,7 +195,7 @@ def _stream(stream=None):
         import torch
         torch.cuda.init()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without building a Stream object
-        device = torch.cuda.current_device
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
     return _current_stream()
 
@@ -308,31 +308,34 @@ def gather_kv(p: Problem, seq_lens_q, seq_lens_k, block_table, sparse_indices, k
 _act_dtypes = None
 
 
-def _rows(t, what, dtype, tokens, heads, dim):
-    """(address, elements between tokens) of a [tokens, heads, dim] tensor whose heads are contiguous
-    (a view of a packed projection keeps its token stride); TypeError / ValueError otherwise."""
+def _load_act_dtypes():
+    import torch
+    global _act_dtypes
+    _act_dtypes = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
+    return _act_dtypes
+
+
+def _rows(t, what, dtype, shape):
+    """(address, elements between tokens) of a tensor of `shape` = (tokens, heads, dim) whose heads are
+    contiguous (a view of a packed projection keeps its token stride); TypeError / ValueError otherwise."""
     if t is None:
         return None, 0
-    global _act_dtypes
-    if _act_dtypes is None:
-        import torch
-        _act_dtypes = (torch.bfloat16, torch.float16)
-    if t.dtype is not _act_dtypes[1 if dtype == ACT_F16 else 0]:
-        raise TypeError("%s: expected %s, got %s" % (what, _act_dtypes[1 if dtype == ACT_F16 else 0], t.dtype))
-    if t.shape != (tokens, heads, dim):
-        raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, tokens, heads, dim, tuple(t.shape)))
+    if t.dtype is not (_act_dtypes or _load_act_dtypes()).get(dtype):
+        raise TypeError("%s: expected %s, got %s" % (what, _act_dtypes.get(dtype), t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s: expected %s, got %s" % (what, list(shape), list(t.shape)))
     step, head, elem = t.stride()
-    if tokens <= 1:
-        step = 0
-    elif step < heads * dim:                     # 0 would read as contiguous
-        raise ValueError("%s: tokens overlap (stride %d)" % (what, step))
-    if (elem != 1 or (heads > 1 and head != dim)) and t.numel():
+    if (elem != 1 or (head != shape[2] and shape[1] > 1)) and t.numel():
         raise ValueError("%s: a token's heads must be contiguous" % what)
+    if shape[0] <= 1:
+        step = 0
+    elif step < shape[1] * shape[2]:             # 0 would read as contiguous
+        raise ValueError("%s: tokens overlap (stride %d)" % (what, step))
     return t.data_ptr(), step
 
 
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _workspace(t):
+    return (None, 0) if t is None else (t.data_ptr(), t.nbytes)
 
 
 def make_norm_rope(*, num_heads_q, num_heads_k, head_dim, rotary_dim, max_positions, dtype=ACT_BF16,
@@ -362,14 +365,15 @@ def norm_rope(r: Rotation, q, k, q_weight, k_weight, positions, cos_sin, q_out, 
     """qli_norm_rope: ``q`` [tokens, num_heads_q, head_dim] and ``k`` [tokens, num_heads_k, head_dim] (views
     of a packed projection are fine) normalised and rotated into ``q_out`` / ``k_out`` (which may be
     ``q`` / ``k``); ``positions`` int32 [tokens], ``cos_sin`` float32 [max_positions, rotary_dim]."""
-    n = positions.numel()
-    qa, qs = _rows(q, "q", r.dtype, n, r.num_heads_q, r.head_dim)
-    ka, ks = _rows(k, "k", r.dtype, n, r.num_heads_k, r.head_dim)
-    qo, qos = _rows(q_out, "q_out", r.dtype, n, r.num_heads_q, r.head_dim)
-    ko, kos = _rows(k_out, "k_out", r.dtype, n, r.num_heads_k, r.head_dim)
-    return _get_lib().qli_norm_rope(
-        ctypes.byref(r), n, qa, qs, ka, ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-        _ptr(cos_sin), qo, qos, ko, kos, _ptr(workspace), _bytes(workspace), _stream(stream))
+    n, d, dt = positions.numel(), r.head_dim, r.dtype
+    q_shape, k_shape = (n, r.num_heads_q, d), (n, r.num_heads_k, d)
+    qa, qs = _rows(q, "q", dt, q_shape)
+    ka, ks = _rows(k, "k", dt, k_shape)
+    qo, qos = _rows(q_out, "q_out", dt, q_shape)
+    ko, kos = _rows(k_out, "k_out", dt, k_shape)
+    ws, nbytes = _workspace(workspace)
+    return _get_lib().qli_norm_rope(r, n, qa, qs, ka, ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(cos_sin),
+                                    qo, qos, ko, kos, ws, nbytes, _stream(stream))
 
 
 def make_attention(*, num_heads_q, num_heads_kv, head_dim, dtype=ACT_BF16, kv_dtype=KV_E2M1, softmax_scale=0.0,
@@ -403,11 +407,12 @@ def kv_write(p: Problem, a: Attention, k, v, token_batch, token_pos, block_table
     """qli_kv_write: quantise ``k`` and ``v`` ([tokens, num_heads_kv, head_dim], views of a packed
     projection are fine) into the paged 4-bit cache ``kv`` at each token's (batch, compressed position)."""
     n = token_batch.numel()
-    ka, ks = _rows(k, "k", a.dtype, n, a.num_heads_kv, a.head_dim)
-    va, vs = _rows(v, "v", a.dtype, n, a.num_heads_kv, a.head_dim)
-    return _get_lib().qli_kv_write(
-        ctypes.byref(p), ctypes.byref(a), n, ka, ks, va, vs, _ptr(token_batch), _ptr(token_pos),
-        _ptr(block_table), _ptr(kv), _ptr(workspace), _bytes(workspace), _stream(stream))
+    shape, dt = (n, a.num_heads_kv, a.head_dim), a.dtype
+    ka, ks = _rows(k, "k", dt, shape)
+    va, vs = _rows(v, "v", dt, shape)
+    ws, nbytes = _workspace(workspace)
+    return _get_lib().qli_kv_write(p, a, n, ka, ks, va, vs, _ptr(token_batch), _ptr(token_pos), _ptr(block_table), _ptr(kv),
+                                   ws, nbytes, _stream(stream))
 
 
 def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k, v, workspace=None,
@@ -415,11 +420,12 @@ def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k
     """qli_kv_read: the cached keys and values of each token's (batch, compressed position) into ``k`` and
     ``v`` ([tokens, num_heads_kv, head_dim])."""
     n = token_batch.numel()
-    ka, ks = _rows(k, "k", a.dtype, n, a.num_heads_kv, a.head_dim)
-    va, vs = _rows(v, "v", a.dtype, n, a.num_heads_kv, a.head_dim)
-    return _get_lib().qli_kv_read(
-        ctypes.byref(p), ctypes.byref(a), n, _ptr(token_batch), _ptr(token_pos), _ptr(block_table),
-        _ptr(kv), ka, ks, va, vs, _ptr(workspace), _bytes(workspace), _stream(stream))
+    shape, dt = (n, a.num_heads_kv, a.head_dim), a.dtype
+    ka, ks = _rows(k, "k", dt, shape)
+    va, vs = _rows(v, "v", dt, shape)
+    ws, nbytes = _workspace(workspace)
+    return _get_lib().qli_kv_read(p, a, n, _ptr(token_batch), _ptr(token_pos), _ptr(block_table), _ptr(kv), ka, ks, va, vs,
+                                  ws, nbytes, _stream(stream))
 
 
 def sparse_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, block_table, sparse_indices, kv, out,
@@ -427,13 +433,14 @@ def sparse_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, bl
     """qli_sparse_attention: ``out`` [rows, num_heads_q, head_dim] (and ``lse`` float32 [rows, num_heads_q])
     of ``query`` over the entries of the 4-bit cache ``kv`` that ``sparse_indices`` names."""
     n = p.batch * p.max_q_tokens if p.layout_q == BSND else p.total_q_tokens
-    qa, qs = _rows(query, "query", a.dtype, n, a.num_heads_q, a.head_dim)
-    oa, os_ = _rows(out, "out", a.dtype, n, a.num_heads_q, a.head_dim)
-    if os_ not in (0, a.num_heads_q * a.head_dim):
+    shape, dt = (n, a.num_heads_q, a.head_dim), a.dtype
+    qa, qs = _rows(query, "query", dt, shape)
+    oa, os_ = _rows(out, "out", dt, shape)
+    if os_ not in (0, shape[1] * shape[2]):
         raise ValueError("out: must be contiguous")
-    return _get_lib().qli_sparse_attention(
-        ctypes.byref(p), ctypes.byref(a), qa, qs, _ptr(seq_lens_q), _ptr(seq_lens_k), _ptr(block_table),
-        _ptr(sparse_indices), _ptr(kv), oa, _ptr(lse), _ptr(workspace), _bytes(workspace), _stream(stream))
+    ws, nbytes = _workspace(workspace)
+    return _get_lib().qli_sparse_attention(p, a, qa, qs, _ptr(seq_lens_q), _ptr(seq_lens_k), _ptr(block_table),
+                                           _ptr(sparse_indices), _ptr(kv), oa, _ptr(lse), ws, nbytes, _stream(stream))
 
 
 def workspace_init(workspace, stream=None) -> int:
