@@ -388,8 +388,9 @@ size_t qli_kv_entry_bytes(const qli_attention* a);
  * qli_kv_write: token t's keys `k[t]` and values `v[t]` ([num_heads_kv, D] each, k_stride /
  * v_stride elements between tokens: 0 = contiguous, else a multiple of 8 of at least the heads'
  * size; 16-byte aligned) go to compressed position token_pos[t] of batch token_batch[t].  Nothing
- * else of the pool changes (an entry's padding included).  Positions, batches, pages and errors as
- * in qli_quantize_keys.  One kernel on `stream`; tokens = 0 enqueues nothing.
+ * else of the pool changes (an entry's padding included).  Positions must be distinct (of two tokens
+ * written to one position the entry may mix both).  Batches, pages and errors as in
+ * qli_quantize_keys.  One kernel on `stream`; tokens = 0 enqueues nothing.
  *
  * qli_kv_read: the reverse; k[t], v[t] receive k_scale * s * code, rounded once to the activations'
  * type.  A token with an invalid batch, position or page gets zeros and sets the same error bits.

@@ -29,6 +29,16 @@
 // 2^-10 to 2688); queries are scaled by a power of two of their head's largest magnitude, so that
 // bfloat16 fits fp16 too (elements below 2^-14 of the largest lose bits of 2^-25 of it).
 //
+// What bounds it: from L2 (a prefill), the SM's arithmetic.  A step of 32 entries x 8 query heads is 535
+// instructions, of which 128 conversions of code pairs, 128 scale products and 32 tensor products; a
+// probe gives 2, 2 and 7.1 cycles for these per sub-partition, products and scale products on one pipe,
+// so about 570 cycles, and a step takes about 900.  (Dropping the scale products of V alone takes 8 %
+// off; giving the keys' to the integer pipe adds 6 %: both pipes are near full.)  From HBM (a decode),
+// the gathers' latency and the start: list, entries, join.  Measured on a GB300, 64 query heads over 8 KV
+// heads of 128, E2M1, 2048 entries a row: 1 row 7.1 us, 8 rows 11.0, 32 rows (8k-32k keys) 21.4 (3.6 TB/s),
+// 64 rows 36.4 (4.2), 128 rows 65.1 (4.7); prefill of 1024 + 2048 + 4096 rows 1.76 ms (166 TFLOP/s); int4
+// 27.1 us at 32 rows: its codes take seven integer operations per eight, E2M1's four.
+//
 // Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over
 // the cluster) and are joined in a fixed order.  Every wait for a copy is bounded (0.2 s): on expiry the
 // kernel records kErrTimeout, writes NaN, lets its copies land and returns.
@@ -666,10 +676,11 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     const int k = a.p.sparse_count;
     const int64_t rows = a.p.rows;
     // CTAs per row: as many slices of the units as still run in one wave (fewer units per CTA: more warps
-    // share a unit, so each reads a shorter part of the list; long decode, 32 rows x 8 units: 8 units
-    // per CTA 80 us, 2 units 25.6, 1 unit 23.4).  The list itself is split over a cluster while each SM
-    // has at most one CTA and each warp keeps a step of its own (1 row: 14.6 us unsplit, 7.4 with 8
-    // splits; 8 rows: 15.2, 11.9 with 2, 12.3 with 4, 17.7 with 8).
+    // share a unit, so each reads a shorter part of the list.  8 units, 2048 entries; 32 rows: 8 units
+    // per CTA 73 us, 4 42, 2 24.1, 1 21.5; 64 rows: 73, 42.8, 36.4, 40.9; 128 rows: 75, 65.1, 69, 69.6).
+    // The list itself is split over a cluster while each SM has at most one CTA and each warp keeps a
+    // step of its own (1 row: 13.1 us unsplit, 7.1 with 8 splits; 8 rows: 13.8 unsplit, 11.0 with 2, 11.4
+    // with 4, 17.1 with 8).
     const int slots = ctas_per_sm(D, NT) * sms;
     L.per_cta = 1;
     while (L.per_cta < kWarps && rows * ((L.units + L.per_cta - 1) / L.per_cta) > slots) L.per_cta *= 2;
@@ -681,7 +692,7 @@ cudaError_t launch_shape(const AttentionArgs& a, int sms, cudaStream_t st)
     L.per_split = (k + L.splits - 1) / L.splits;
     // row gathers need one stride for all entries of the pool
     L.page_rows = 0;
-    if (a.page_bytes % a.entry_bytes == 0 && a.page_bytes / a.entry_bytes * a.p.num_blocks <= INT32_MAX)
+    if (a.kv && a.page_bytes % a.entry_bytes == 0 && a.page_bytes / a.entry_bytes * a.p.num_blocks <= INT32_MAX)
         L.page_rows = (int32_t)(a.page_bytes / a.entry_bytes);
     if constexpr (NT == 1) {
         if (L.page_rows && L.chunks == 1 && L.per_cta == kWarps && L.units % kWarps == 0)

@@ -11,7 +11,10 @@
 // heads, then V heads) follow one another over the threads.  A CTA looks up the entries of up to
 // kMaxTokens tokens first (batch, position, block_table, pool are four dependent loads; one lookup per
 // four tokens left the read of 65536 tokens at 89 us), then each thread streams its half-block of
-// those tokens, kUnroll at a time.
+// those tokens, kUnroll at a time.  Measured on a GB300, 8 KV heads of 128, E2M1: reading 65536 tokens
+// (344 MB) 61.7 us = 5.6 TB/s, 0.82 of a copy's rate; writing 15360 tokens (81 MB) and reading them back 36
+// us (the write is bound by its 118 instructions per eight elements at 42 % occupancy, and by its
+// length: five CTAs per SM instead of four, or two or eight tokens under way, change nothing).
 #include <cuda_runtime.h>
 
 #include <cfloat>

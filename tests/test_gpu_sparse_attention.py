@@ -227,6 +227,23 @@ def test_tnd_rows_past_the_last_prefix_sum(Q):
     _check(case, _run(Q, case, q, idx, pool, 1, True, False), q, idx, pool, 1, True, False)
 
 
+def test_rows_without_any_batch(Q):
+    """TND rows of an empty batch: no lengths, table or cache at all."""
+    import torch
+    p = Q.make_problem(batch=0, layout_q=Q.TND, total_q_tokens=5, num_blocks=1, block_size=16, max_blocks_per_seq=0,
+                       sparse_count=40, sparse_mode=0, cmp_ratio=1, max_seqlen_q=0, max_seqlen_k=0)
+    a = Q.make_attention(num_heads_q=64, num_heads_kv=8, head_dim=128)
+    out = torch.full((5, 64, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(5, 64, device="cuda")
+    ws = torch.zeros(64, dtype=torch.int32, device="cuda")
+    for last, bits in ((-1, 0), (7, 1)):
+        idx = torch.full((5, 40), -1, dtype=torch.int32, device="cuda")
+        idx[4, 39] = last
+        Q.check(Q.sparse_attention(p, a, torch.ones_like(out), None, None, None, idx, None, out, lse, ws), "sparse_attention")
+        assert Q.get_device_error(ws)[1] == bits
+        assert not out.any() and (lse == -math.inf).all()
+
+
 def test_offsets_past_32_bits(Q):
     """Entries on the last pages of a pool of over 4 GB."""
     import torch
