@@ -699,8 +699,13 @@ qli_status kv_args(const qli_problem* p, const qli_attention* a, int64_t tokens,
     A->head_dim = a->head_dim;
     A->f16 = a->dtype == QLI_ACT_F16;
     A->e2m1 = a->kv_dtype == QLI_KV_E2M1;
-    A->k_scale = a->k_scale;
-    A->v_scale = a->v_scale;
+    const float scale[2] = {a->k_scale, a->v_scale};
+    for (int i = 0; i < 2; ++i) {
+        int exp = 0;
+        const float inverse = 1.0f / scale[i];
+        A->scale[i] = scale[i];
+        A->inverse[i] = std::frexp(scale[i], &exp) == 0.5f && inverse >= FLT_MIN ? inverse : 0.0f;
+    }
     A->entry_bytes = (int64_t)entry_bytes_of(a);
     A->tokens = tokens;
     A->token_batch = token_batch;

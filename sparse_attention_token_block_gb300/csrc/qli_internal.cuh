@@ -392,7 +392,8 @@ __host__ __device__ constexpr int kv_unit_bytes(int d) { return d + 2 * (d / kKv
 struct KvArgs {
     Params p;
     int32_t heads_kv, head_dim, f16, e2m1;
-    float k_scale, v_scale;
+    float scale[2];                        // k_scale, v_scale
+    float inverse[2];                      // their reciprocals where they are powers of two, else 0
     int64_t entry_bytes, page_bytes;       // entry and page strides
     int64_t tokens;
     int64_t stride[2];                     // elements between tokens of k, v

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
         const HalfPos w = half_pos(ih, a.heads_kv, a.head_dim);
         const int64_t stride = a.stride[w.kv];
         const uint16_t* src = (w.kv ? v : k) + w.element + t0 * stride;
-        const float g = w.kv ? a.v_scale : a.k_scale;
+        const float g = w.kv ? a.scale[1] : a.scale[0], gi = w.kv ? a.inverse[1] : a.inverse[0];
         for (int l0 = 0; l0 < n; l0 += kUnroll * slots) {
             uint4 x[kUnroll];
 #pragma unroll
@@ -193,7 +193,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                if (g != 1.0f) {
+                if (gi != 0.0f) {
+                    // a power of two: the product with its reciprocal is the quotient
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] *= gi;
+                    amax *= gi;
+                } else {
                     // (the division is monotone: the largest quotient is the largest magnitude's)
                     amax = __fdiv_rn(amax, g);
                     divide8<E2M1>(y, g, amax);
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvArgs a, const uin
         const HalfPos w = half_pos(ih, a.heads_kv, a.head_dim);
         const int64_t stride = a.stride[w.kv];
         uint16_t* dst = (w.kv ? v : k) + w.element + t0 * stride;
-        const float g = w.kv ? a.v_scale : a.k_scale;
+        const float g = w.kv ? a.scale[1] : a.scale[0];
         for (int l0 = slot; l0 < n; l0 += kUnroll * slots) {
             uint32_t code[kUnroll], scale[kUnroll];
 #pragma unroll

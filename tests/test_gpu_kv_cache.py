@@ -56,7 +56,7 @@ LAYOUTS = [(1, 64), (1, 128), (3, 64), (8, 128), (5, 128), (16, 64), (64, 128)]
 @pytest.mark.parametrize("heads,dim", LAYOUTS)
 @pytest.mark.parametrize("e2m1", [True, False])
 @pytest.mark.parametrize("f16", [False, True])
-@pytest.mark.parametrize("factors", [(1.0, 1.0), (0.3, 5.0)])
+@pytest.mark.parametrize("factors", [(1.0, 1.0), (0.3, 5.0), (0.25, 2.0 ** -7)])
 def test_write_is_bit_exact_and_read_back(Q, heads, dim, e2m1, f16, factors):
     import torch
     case = cache_case(batch=3, s1=1, seq_lens_k=[70, 33, 1], block_size=16, sparse_count=1, seed=heads, extra_pages=2)
