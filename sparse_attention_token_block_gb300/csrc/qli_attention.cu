@@ -719,6 +719,7 @@ cudaError_t launch_type(const AttentionArgs& a, int head_dim, int sms, cudaStrea
 
 cudaError_t launch_attention(const AttentionArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
 {
+    if (attention_in_rows(a, head_dim, sms)) return launch_attention_rows(a, f16, e2m1, sms, st);
     if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
     return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
 }

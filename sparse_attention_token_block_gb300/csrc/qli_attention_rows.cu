@@ -1,0 +1,641 @@
+// qli_attention_rows.cu -- the sparse attention for blocks of neighbouring rows whose lists cover a large
+// part of their keys (a prefill): the same operator as qli_attention.cu, on the tcgen05 tensor cores.
+//
+// A CTA takes R consecutive rows x G query heads of one KV head after another: R * G <= 128 rows of a
+// product.  It turns the rows' lists into bit masks over the positions of their sequence, walks the
+// tiles of 128 positions in which some row has an entry, and runs per tile
+//
+//     S = Q K^T  (128 x 128 x D)     P = 2^(S f - m), zero where the row's bit is not set     O += P V
+//
+// so that a key is decoded once for R rows instead of once per row that lists it.  Roles:
+//   * 4 + 4 converter warps decode the tile's 4-bit entries into fp16 operands in shared memory: K rows
+//     as they are, V transposed (a lane takes eight entries x 16 elements and pairs the nibbles of two
+//     entries, as qli_attention.cu does); positions that no row lists are zeros and are not read;
+//   * one warp issues the products (Q and K, V from shared memory, P from tensor memory), both
+//     accumulators in tensor memory, the logits' twice;
+//   * 4 softmax warps, a row of the product per thread: masked logits, running maximum (raised only when
+//     a logit passes it by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+//
+// A position that a row lists n times counts n times: the list positions that are left over when a mask
+// is built go into the masks of further rounds.  So do the rows of a block that belong to another batch,
+// and the positions past the masks' width.
+//
+// A zero of P times a NaN would be a NaN, in rows that do not list the entry: an entry with a NaN among its
+// scales (the cache write makes none) is taken as NaN keys, which the mask hides from the other rows, and
+// finite values.
+//
+// Every wait is bounded (0.2 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+
+#include "qli_kv.cuh"
+
+namespace qli {
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kM = 128, kTileKeys2 = 128;              // rows and keys of a product
+constexpr int kSoftWarps = 4, kConvWarps = 8, kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kAtom = kM * 128;                        // 128 rows of 64 fp16 in the 128-byte swizzle
+constexpr int kOperand = 2 * kAtom;
+constexpr int kMaxRows = 32;                           // rows of a block
+constexpr int kMaskBytes = 32 * 1024;
+constexpr int kMaxTiles = kMaskBytes / 16;             // at one row a block
+constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
+constexpr float kRescale = 8.0f;
+constexpr uint64_t kWaitLimitNs = 200000000ull;
+
+struct RowsLayout {
+    int32_t rows;          // rows of a block
+    int32_t words;         // mask words per row (a multiple of 4: whole tiles)
+    int32_t heads;         // KV heads per CTA
+    int32_t slices;        // CTAs per block
+    uint32_t block_recip;
+};
+
+struct Shared {
+    uint64_t kfull[2], vfull[2], sfull[2], sfree[2], vfree[2], pfull, pvdone;
+    uint32_t tmem, abort, dup, tiles;
+    int32_t batch[kMaxRows];
+    float factor[kM];
+    alignas(16) uint32_t any[kMaxTiles * 4 / 4];       // over the rows, per word (at least four rows a block)
+    uint32_t rest[kMaxRows][kMaxSparse / 32];          // list positions left for further rounds
+    uint16_t list[kMaxTiles / 4];                      // tiles with an entry
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        const bool done = ptx::mbar_try_wait_sleep(bar, parity, 100000u);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort, err);
+}
+
+// Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand of two swizzled blocks
+__device__ __forceinline__ uint32_t operand_at(int r, int piece)
+{
+    return (piece >> 3) * kAtom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+}
+
+template <bool F16, bool E2M1>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_rows_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ RowsLayout L)
+{
+    constexpr int kUnit = kv_unit_bytes(kD);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* qs = smem;
+    uint8_t* ksm = smem + kOperand;
+    uint8_t* vsm = smem + 3 * kOperand;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + 5 * kOperand);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + 5 * kOperand + kMaskBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.heads_q / a.heads_kv, k = a.p.sparse_count;
+    const int64_t block = blockIdx.x / (uint32_t)L.slices;
+    const int slice = (int)(blockIdx.x - block * L.slices);
+    const int64_t r0 = block * L.rows;
+    const int nrows = (int)min((int64_t)L.rows, a.p.rows - r0);
+    const int head0 = slice * L.heads, head1 = min(a.heads_kv, head0 + L.heads);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.kfull[i], kConvWarps / 2);
+            ptx::mbar_init(&sh.vfull[i], kConvWarps / 2);
+            ptx::mbar_init(&sh.sfull[i], 1);
+            ptx::mbar_init(&sh.sfree[i], kSoftWarps);
+            ptx::mbar_init(&sh.vfree[i], 1);
+        }
+        ptx::mbar_init(&sh.pfull, kSoftWarps);
+        ptx::mbar_init(&sh.pvdone, 1);
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::pdl_wait();
+    if (warp == kMmaWarp) {                            // (not before: kernels that still run may need it)
+        ptx::tmem_alloc(&sh.tmem, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (tid < L.rows) sh.batch[tid] = tid < nrows ? (int32_t)row_batch(a.p, a.seq_lens_q, r0 + tid) : -1;
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // rows of no batch: any index is an error
+    for (int r = 0; r < nrows; ++r) {
+        if (sh.batch[r] >= 0) continue;
+        for (int e = tid; e < k; e += kThreads)
+            if (a.idx[(r0 + r) * k + e] != -1 && a.err) atomicOr(a.err, kErrLength);
+    }
+
+    uint32_t done = 0;                                 // tiles walked so far: every role counts the same
+    bool standing = false;                             // the masks are those of all rows and all their positions
+    for (int kvh = head0; kvh < head1; ++kvh) {
+        // ---- the head's queries as an operand: row m is query head m % group of row m / group
+        for (int m = warp; m < kM; m += kThreads / 32) {
+            const int r = m / group, h = kvh * group + m - r * group;
+            uint2 raw = make_uint2(0u, 0u);
+            // lane: 4 elements, (2 x 2 of each eight for int4: its codes come in the order 0 4 1 5 2 6 3 7)
+            const int c8 = lane >> 1, half = lane & 1;
+            if (r < nrows) {
+                const uint16_t* src = static_cast<const uint16_t*>(a.query) + (r0 + r) * a.q_stride + (int64_t)h * kD + 8 * c8;
+                if (E2M1) {
+                    raw = *reinterpret_cast<const uint2*>(src + 4 * half);
+                } else {
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 2 * half);
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(src + 4 + 2 * half);
+                    raw = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+                }
+            }
+            const float2 u = act2_to_float2<F16>(raw.x), v = act2_to_float2<F16>(raw.y);
+            float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+            const float down = __uint_as_float((254u - ex) << 23);
+            *reinterpret_cast<uint2*>(qs + operand_at(m, c8) + 8 * half) =
+                make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
+            if (lane == 0)
+                sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
+                                     3.0e38f);
+        }
+        ptx::fence_proxy_async_smem();
+        float m_run = -FLT_MAX, l_run = 0.0f;          // softmax threads
+        bool fresh = true;                             // no product has written O for this head yet
+        int first = 0;                                 // rows of the round: [first, last)
+        while (first < nrows && !sh.abort) {
+            const int b = sh.batch[first];
+            int last = first + 1;
+            while (last < nrows && sh.batch[last] == b) ++last;
+            const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : 0;
+            const int32_t* table = a.block_table + (int64_t)max(b, 0) * a.p.max_blocks_per_seq;
+            const int window = 32 * L.words;
+            int64_t from = 0;                          // first position of the masks
+            // (a list of a batch without positions is still looked at: its indices are errors)
+            for (int pass = 0; b >= 0;) {
+                if (!standing) {
+                    // ---- masks of this round
+                    __syncthreads();                   // (every thread has read dup)
+                    for (int i = tid; i < L.rows * L.words; i += kThreads) mask[i] = 0;
+                    if (pass == 0)
+                        for (int i = tid; i < kMaxRows * (kMaxSparse / 32); i += kThreads) (&sh.rest[0][0])[i] = 0;
+                    if (tid == 0) sh.dup = 0;
+                    __syncthreads();
+                    uint32_t bits = 0;
+                    constexpr int kPer = (kMaxSparse + kThreads - 1) / kThreads, kAtOnce = 4;
+                    for (int ra = first; ra < last; ra += kAtOnce) {
+                        int32_t j[kAtOnce][kPer];
+#pragma unroll
+                        for (int r = 0; r < kAtOnce; ++r)
+#pragma unroll
+                            for (int x = 0; x < kPer; ++x) {
+                                const int e = tid + x * kThreads;
+                                j[r][x] = -1;
+                                if (e < k && ra + r < last && (pass == 0 || (sh.rest[ra + r][e >> 5] >> (e & 31) & 1)))
+                                    j[r][x] = a.idx[(r0 + ra + r) * k + e];
+                            }
+#pragma unroll
+                        for (int r = 0; r < kAtOnce; ++r)
+#pragma unroll
+                            for (int x = 0; x < kPer; ++x) {
+                                if (j[r][x] == -1) continue;
+                                if (j[r][x] < 0 || j[r][x] >= limit) {
+                                    bits |= kErrLength;
+                                    continue;
+                                }
+                                const int64_t at = j[r][x] - from;
+                                if (at < 0 || at >= window) continue;
+                                const int e = tid + x * kThreads;
+                                const uint32_t bit = 1u << (at & 31);
+                                const bool again = atomicOr(&mask[(ra + r) * L.words + (int)(at >> 5)], bit) & bit;
+                                if (again) {
+                                    if (pass == 0) atomicOr(&sh.rest[ra + r][e >> 5], 1u << (e & 31));
+                                    sh.dup = 1;
+                                } else if (pass > 0) {
+                                    atomicAnd(&sh.rest[ra + r][e >> 5], ~(1u << (e & 31)));
+                                }
+                            }
+                    }
+                    __syncthreads();
+                    // what some row lists; positions on bad pages leave the masks (16 positions share a page)
+                    for (int h = tid; h < 2 * L.words; h += kThreads) {
+                        const uint16_t* m16 = reinterpret_cast<const uint16_t*>(mask) + h;
+                        uint32_t o = 0;
+                        for (int r = first; r < last; ++r) o |= m16[r * 2 * L.words];
+                        if (o) {
+                            const uint32_t at = (uint32_t)from + 16 * h;
+                            uint32_t blk = __umulhi(at, L.block_recip);
+                            if (at - blk * (uint32_t)a.p.block_size >= (uint32_t)a.p.block_size) ++blk;
+                            const int page = table[blk];
+                            if (page < 0 || page >= a.p.num_blocks) {
+                                bits |= kErrPage;
+                                o = 0;
+                                for (int r = first; r < last; ++r) reinterpret_cast<uint16_t*>(mask)[r * 2 * L.words + h] = 0;
+                            }
+                        }
+                        reinterpret_cast<uint16_t*>(sh.any)[h] = (uint16_t)o;
+                    }
+                    if (bits && a.err) atomicOr(a.err, bits);
+                    __syncthreads();
+                    if (warp == 0) {
+                        int n = 0;
+                        for (int t0 = 0; t0 < L.words / 4; t0 += 32) {
+                            const int t = t0 + lane;
+                            const uint4 w = t < L.words / 4 ? reinterpret_cast<const uint4*>(sh.any)[t] : make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t live = __ballot_sync(0xffffffffu, (w.x | w.y | w.z | w.w) != 0);
+                            if (live >> lane & 1) sh.list[n + __popc(live & ((1u << lane) - 1))] = (uint16_t)t;
+                            n += __popc(live);
+                        }
+                        if (lane == 0) sh.tiles = n;
+                    }
+                }
+                __syncthreads();
+                const int n = (int)sh.tiles;
+                if (warp < kSoftWarps) {
+                    // ------------------------------------------------------------ softmax: row `tid`
+                    const uint32_t lanes = tmem + ((uint32_t)warp << 21);
+                    const float f = sh.factor[tid];
+                    const int r = tid / group;
+                    const bool mine = r >= first && r < last;
+                    const uint32_t* row_mask = mask + (mine ? r : 0) * L.words;
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t t = done + i, buf = t & 1;
+                        if (!wait_bounded(&sh.sfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
+                        ptx::tc_fence_after();
+                        uint4 w4 = *reinterpret_cast<const uint4*>(row_mask + 4 * sh.list[i]);
+                        if (!mine) w4 = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                        bool waited = fresh && i == 0;             // nothing to wait for before the first product
+                        bool ok = true;
+                        while (true) {
+                            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                uint32_t p[32];
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    uint32_t s[32];
+                                    QLI_TMEM_LD_X32(lanes + kColS + 128 * buf + 64 * hf + 32 * q, s);
+                                    ptx::tmem_wait_ld();
+                                    const uint32_t bits = w[2 * hf + q];
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const float x = bits >> e & 1 ? __uint_as_float(s[e]) : -INFINITY;
+                                        const float y = bits >> (e + 1) & 1 ? __uint_as_float(s[e + 1]) : -INFINITY;
+                                        top = fmaxf(top, fmaxf(x, y));
+                                        const float px = ptx::ex2(fmaf(x, f, -m_run)), py = ptx::ex2(fmaf(y, f, -m_run));
+                                        sum += px + py;
+                                        p[16 * q + e / 2] = float2_to_act2<true>(px, py);
+                                    }
+                                }
+                                // P's columns are free once the product of the tile before is done
+                                if (!waited) {
+                                    ok = wait_bounded(&sh.pvdone, (t - 1) & 1, &sh.abort, a.err);
+                                    ptx::tc_fence_after();
+                                    waited = true;
+                                }
+                                QLI_TMEM_ST_X32(lanes + kColP + 32 * hf, p);
+                            }
+                            const bool over = fmaf(top, f, -m_run) > kRescale;
+                            if (!ok || !__any_sync(0xffffffffu, over)) {
+                                l_run += sum;
+                                break;
+                            }
+                            // raise the maximum of the rows that need it, rescale their sums and their rows of O
+                            const float up = over ? top * f : m_run, g = ptx::ex2(m_run - up);
+                            m_run = up;
+                            l_run *= g;
+                            if (!(fresh && i == 0)) {
+#pragma unroll 1
+                                for (int q = 0; q < 4; ++q) {
+                                    uint32_t o[32];
+                                    QLI_TMEM_LD_X32(lanes + kColO + 32 * q, o);
+                                    ptx::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                                    QLI_TMEM_ST_X32(lanes + kColO + 32 * q, o);
+                                }
+                            }
+                        }
+                        if (!ok) break;
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::mbar_arrive(&sh.sfree[buf]);
+                            ptx::mbar_arrive(&sh.pfull);
+                        }
+                    }
+                } else if (warp < kMmaWarp) {
+                    // ------------------------------------------------------------ converters
+                    const int ct = (tid - 32 * kSoftWarps) & 127;
+                    const uint32_t bs = (uint32_t)a.p.block_size;
+                    const bool stall = a.p.test_stall == 1;        // test switch: no tile is handed on, the waits run out
+                    // entry of position `at` of the masks (read only when some row lists it)
+                    auto entry = [&](uint32_t at, bool live) -> const uint8_t* {
+                        const uint32_t j = (uint32_t)from + at;
+                        uint32_t blk = __umulhi(j, L.block_recip), pos = j - blk * bs;
+                        if (pos >= bs) ++blk, pos -= bs;
+                        const int64_t page = live ? table[blk] : 0;
+                        return a.kv + kvh * kUnit + page * a.page_bytes + (int64_t)pos * a.entry_bytes;
+                    };
+                    if (warp < kSoftWarps + kConvWarps / 2) {
+                        // keys: a lane takes a quarter of positions row, row + 32, ...  The lanes of the upper half
+                        // of the elements go through their four pieces in the order 2 3 0 1: eight lanes that store
+                        // at once then meet eight different 16-byte columns.
+                        const int quarter = ct & 3, row = ct >> 2;
+                        uint4 code[4], scale[4];
+                        uint32_t word[4];
+                        auto load = [&](int i) {
+                            const uint32_t tile = sh.list[i];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                word[x] = sh.any[4 * tile + x];
+                                const bool live = word[x] >> row & 1;
+                                const uint8_t* p = entry(128 * tile + 32 * x + row, live);
+                                code[x] = scale[x] = make_uint4(0u, 0u, 0u, 0u);
+                                if (live) {
+                                    code[x] = reinterpret_cast<const uint4*>(p)[quarter];
+                                    scale[x] = *reinterpret_cast<const uint4*>(p + kD);
+                                }
+                            }
+                        };
+                        if (n > 0) load(0);
+                        for (int i = 0; i < n; ++i) {
+                            const uint32_t t = done + i, buf = t & 1;
+                            uint4 c4[4];
+                            uint32_t s4[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                c4[x] = quarter & 2 ? make_uint4(code[x].z, code[x].w, code[x].x, code[x].y) : code[x];
+                                const uint32_t half = quarter & 2 ? scale[x].y : scale[x].x;
+                                s4[x] = half >> (16 * (quarter & 1)) & 0xFFFFu;
+                                // a NaN (0x7F or 0xFF) among the values' scales
+                                const uint32_t bad = __vcmpeq4(scale[x].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(scale[x].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                if (bad) s4[x] = 0x7F7Fu;
+                            }
+                            if (i + 1 < n) load(i + 1);            // under way while this tile is decoded
+                            // the buffer of the tile before last is free once its product is done
+                            if (t >= 2 && !wait_bounded(&sh.sfull[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
+                            uint8_t* kb = ksm + buf * kOperand;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t h = e4m3x2_to_f16x2(s4[x]);
+                                // (the pieces' order swaps the lane's two blocks)
+                                const PairScale g0 = pair_scale<E2M1>(__byte_perm(h, 0, quarter & 2 ? 0x3232 : 0x1010));
+                                const PairScale g1 = pair_scale<E2M1>(__byte_perm(h, 0, quarter & 2 ? 0x1010 : 0x3232));
+                                const uint32_t w[4] = {c4[x].x, c4[x].y, c4[x].z, c4[x].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    uint32_t o[4];
+                                    decode_pairs<E2M1>(w[e], e < 2 ? g0 : g1, o);
+                                    *reinterpret_cast<uint4*>(kb + operand_at(32 * x + row, 4 * quarter + (e ^ (quarter & 2)))) =
+                                        make_uint4(o[0], o[1], o[2], o[3]);
+                                }
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.kfull[buf]);
+                        }
+                    } else {
+                        // values: a lane takes one block of 16 elements of eight positions, in odd blocks the
+                        // elements in the order 4 5 6 7 0 1 2 3 (as above)
+                        const int vb = ct & 7, vg = ct >> 3;
+                        uint2 code[8];
+                        uint32_t scale[8];
+                        auto load = [&](int i) {
+                            const uint32_t tile = sh.list[i];
+                            const uint32_t live = sh.any[4 * tile + (vg >> 2)] >> (8 * (vg & 3)) & 0xFFu;
+                            const uint8_t* p = entry(128 * tile + 8 * vg, live != 0);      // (eight positions share a page)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e, p += a.entry_bytes) {
+                                code[e] = make_uint2(0u, 0u);
+                                scale[e] = 0;
+                                if (live >> e & 1) {
+                                    code[e] = *reinterpret_cast<const uint2*>(p + kD / 2 + 8 * vb);
+                                    scale[e] = p[kD + kD / 16 + vb];
+                                }
+                            }
+                        };
+                        const uint32_t turn = vb & 1 ? 0x1032 : 0x3210;
+                        if (n > 0) load(0);
+                        for (int i = 0; i < n; ++i) {
+                            const uint32_t t = done + i, buf = t & 1;
+                            uint32_t w[2][8];
+                            PairScale g[4];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                w[0][e] = __byte_perm(code[e].x, 0, turn);
+                                w[1][e] = __byte_perm(code[e].y, 0, turn);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t h = e4m3x2_to_f16x2(scale[2 * e] | scale[2 * e + 1] << 8);
+                                asm("max.f16x2 %0, %0, %1;" : "+r"(h) : "r"(0xDF00DF00u));        // -448: NaN to a number
+                                g[e] = pair_scale<E2M1>(h);
+                            }
+                            if (i + 1 < n) load(i + 1);
+                            if (t >= 2 && !wait_bounded(&sh.vfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
+                            uint8_t* vdst = vsm + buf * kOperand;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t o[4][8];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) decode_across<E2M1>(w[y][2 * e], w[y][2 * e + 1], g[e], o[e]);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint4*>(vdst + operand_at(16 * vb + 8 * y + (e ^ (4 * (vb & 1))), vg)) =
+                                        make_uint4(o[0][e], o[1][e], o[2][e], o[3][e]);
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.vfull[buf]);
+                        }
+                    }
+                } else {
+                    // ------------------------------------------------------------ products
+                    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                    const uint32_t idesc = ptx::idesc_f16_f32(kM, kTileKeys2);
+                    const uint64_t qd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(qs));
+                    bool ok = true;
+                    for (int i = 0; ok && i <= n; ++i) {
+                        if (i < n) {
+                            const uint32_t t = done + i, buf = t & 1;
+                            ok = wait_bounded(&sh.kfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
+                                 (t < 2 || wait_bounded(&sh.sfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err));
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ksm + buf * kOperand));
+                            if (ptx::elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < kD / 16; ++kk) {
+                                    const uint64_t step = (uint64_t)(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
+                                    ptx::mma_f16_ss(tm + kColS + 128 * buf, qd + step, kd + step, idesc, kk > 0);
+                                }
+                                ptx::mma_commit(&sh.sfull[buf]);
+                            }
+                            __syncwarp();
+                        }
+                        if (i > 0) {
+                            const uint32_t t = done + i - 1, buf = t & 1;
+                            ok = wait_bounded(&sh.vfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
+                                 wait_bounded(&sh.pfull, t & 1, &sh.abort, a.err);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(vsm + buf * kOperand));
+                            const bool add = !(fresh && i == 1);
+                            if (ptx::elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < kTileKeys2 / 16; ++kk) {
+                                    const uint64_t step = (uint64_t)(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
+                                    ptx::mma_f16_ts(tm + kColO, tm + kColP + 8 * kk, vd + step, idesc, add || kk > 0);
+                                }
+                                ptx::mma_commit(&sh.vfree[buf]);
+                                ptx::mma_commit(&sh.pvdone);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    // every product is done before anything of this round is touched again
+                    if (ok && n > 0) wait_bounded(&sh.pvdone, (done + n - 1) & 1, &sh.abort, a.err);
+                }
+                done += n;
+                if (n > 0) fresh = false;
+                ptx::tc_fence_before();
+                __syncthreads();
+                ptx::tc_fence_after();
+                if (sh.abort) break;
+                standing = pass == 0 && sh.dup == 0 && first == 0 && last == nrows && limit <= window;
+                if (sh.dup) {
+                    ++pass;
+                    continue;
+                }
+                from += window;
+                pass = 0;
+                if (from >= limit) break;
+            }
+            first = last;
+        }
+        // ---- output of this head
+        const bool failed = sh.abort != 0;
+        if (warp < kSoftWarps) {
+            const int r = tid / group, h = kvh * group + tid - r * group;
+            const float sum = failed ? __int_as_float(0x7FC00000) : l_run;
+            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            const bool live = r < nrows;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + ((r0 + (live ? r : 0)) * a.heads_q + h) * kD);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                if (fresh) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                } else {
+                    QLI_TMEM_LD_X32(tmem + ((uint32_t)warp << 21) + kColO + 32 * q, o);
+                    ptx::tmem_wait_ld();
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = sum == 0.0f ? 0u : float2_to_act2<F16>(__uint_as_float(o[8 * e + 2 * x]) * inv,
+                                                                         __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                        dst[4 * q + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (live && a.lse)
+                a.lse[(r0 + r) * a.heads_q + h] = sum == 0.0f ? -INFINITY : (m_run + log2f(sum)) * 0.6931471805599453f;
+        }
+        ptx::tc_fence_before();
+        __syncthreads();
+        ptx::tc_fence_after();
+    }
+    if (warp == kMmaWarp) {
+        if (sh.abort) {                                // products that are still under way end before the memory goes
+            const uint64_t t0 = ptx::globaltimer();
+            while (ptx::globaltimer() - t0 < kWaitLimitNs) {
+            }
+        }
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <bool F16, bool E2M1>
+cudaError_t launch_rows(const AttentionArgs& a, const RowsLayout& L, int64_t grid, cudaStream_t st)
+{
+    auto kernel = attention_rows_kernel<F16, E2M1>;
+    constexpr int kSmem = 5 * kOperand + kMaskBytes + (int)sizeof(Shared);
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? UINT64_C(1) << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), kSmem, st, a, L);
+}
+
+}  // namespace
+
+namespace {
+
+// Positions that a row's list may name: the longest sequence, or what the block_table holds
+int64_t positions(const AttentionArgs& a)
+{
+    const int64_t held = (int64_t)a.p.max_blocks_per_seq * a.p.block_size;
+    return a.seq_lens_k ? std::min(held, ((int64_t)a.p.max_seqlen_k + a.p.cmp_ratio - 1) / a.p.cmp_ratio) : held;
+}
+
+}  // namespace
+
+bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
+{
+    const int group = a.heads_q / a.heads_kv;
+    if (head_dim != kD || group > 32) return false;
+    const int64_t rows = a.p.rows, per = std::min(kMaxRows, kM / group), blocks = (rows + per - 1) / per;
+    return rows >= per * a.p.batch && blocks * a.heads_kv >= sms && positions(a) <= 4 * (int64_t)a.p.sparse_count;
+}
+
+cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st)
+{
+    const int group = a.heads_q / a.heads_kv;
+    RowsLayout L;
+    L.rows = std::min(kMaxRows, kM / group);
+    const int64_t words = (positions(a) + 127) / 128 * 4;
+    L.words = (int32_t)std::max<int64_t>(4, std::min<int64_t>(words, kMaskBytes / 4 / L.rows & ~3));
+    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
+    const int64_t blocks = ((int64_t)a.p.rows + L.rows - 1) / L.rows;
+    L.slices = 1;
+    while (L.slices < a.heads_kv && blocks * L.slices < 4 * (int64_t)sms) L.slices *= 2;
+    L.heads = (a.heads_kv + L.slices - 1) / L.slices;
+    L.slices = (a.heads_kv + L.heads - 1) / L.heads;
+    const int64_t grid = blocks * L.slices;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (f16) return e2m1 ? launch_rows<true, true>(a, L, grid, st) : launch_rows<true, false>(a, L, grid, st);
+    return e2m1 ? launch_rows<false, true>(a, L, grid, st) : launch_rows<false, false>(a, L, grid, st);
+}
+
+}  // namespace qli

@@ -166,4 +166,9 @@ __device__ __forceinline__ int64_t kv_entry_offset(const Params& p, const int32_
     return page * page_bytes + (int64_t)((uint32_t)pos - block * bs) * entry_bytes;
 }
 
+// Sparse attention over blocks of neighbouring rows (qli_attention_rows.cu): whether it suits a call, and
+// its launch
+bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms);
+cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st);
+
 }  // namespace qli
