@@ -11,10 +11,11 @@
 //   * 4 + 4 converter warps decode the tile's 4-bit entries into fp16 operands in shared memory: K rows
 //     as they are, V transposed (a lane takes eight entries x 16 elements and pairs the nibbles of two
 //     entries, as qli_attention.cu does); positions that no row lists are zeros and are not read;
-//   * one warp issues the products (Q and K, V from shared memory, P from tensor memory), both
-//     accumulators in tensor memory, the logits' twice;
-//   * 4 softmax warps, a row of the product per thread: masked logits, running maximum (raised only when
-//     a logit passes it by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+//   * one warp issues the products: Q, K and V from shared memory, the logits twice in tensor memory, P in
+//     the place of the logits it came from, O once per half of a tile's keys;
+//   * 8 softmax warps, a row of the product and half of the tile's keys per thread: masked logits, running
+//     maximum (raised only when a logit passes it by more than 2^8, then the half's row of O is rescaled),
+//     sum in fp32, P to fp16.  The halves never meet before the end, where they are joined.
 //
 // A position that a row lists n times counts n times: the list positions that are left over when a mask
 // is built go into the masks of further rounds.  So do the rows of a block that belong to another batch,
@@ -39,14 +40,15 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kM = 128, kTileKeys2 = 128;              // rows and keys of a product
-constexpr int kSoftWarps = 4, kConvWarps = 8, kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kAtom = kM * 128;                        // 128 rows of 64 fp16 in the 128-byte swizzle
 constexpr int kOperand = 2 * kAtom;
 constexpr int kMaxRows = 32;                           // rows of a block
-constexpr int kMaskBytes = 32 * 1024;
-constexpr int kMaxTiles = kMaskBytes / 16;             // at one row a block
-constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
+constexpr int kMinRows = 4;                            // of a block, at 32 query heads per KV head
+constexpr int kMaskBytes = 24 * 1024;
+constexpr int kMaxWords = kMaskBytes / 4 / kMinRows;   // of a row's mask
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRescale = 8.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull;
 
@@ -59,13 +61,15 @@ struct RowsLayout {
 };
 
 struct Shared {
-    uint64_t kfull[2], vfull[2], sfull[2], sfree[2], vfree[2], pfull, pvdone;
+    uint64_t kfull[2], vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
     uint32_t tmem, abort, dup, tiles;
     int32_t batch[kMaxRows];
     float factor[kM];
-    alignas(16) uint32_t any[kMaxTiles * 4 / 4];       // over the rows, per word (at least four rows a block)
+    float2 joined[2][kM];                              // maximum and sum of a row over its half of the keys
+    alignas(16) uint32_t any[kMaxWords];               // over the rows
+    uint32_t at[2 * kMaxWords];                        // entry of every 16th position, in 16 bytes from the pool's start
     uint32_t rest[kMaxRows][kMaxSparse / 32];          // list positions left for further rounds
-    uint16_t list[kMaxTiles / 4];                      // tiles with an entry
+    uint16_t list[kMaxWords / 4];                      // tiles with an entry
 };
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
@@ -87,6 +91,15 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
 {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return wait_slow(bar, parity, abort, err);
+}
+
+// Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
+// them moves in front
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32])
+{
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand of two swizzled blocks
@@ -119,10 +132,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh.kfull[i], kConvWarps / 2);
             ptx::mbar_init(&sh.vfull[i], kConvWarps / 2);
             ptx::mbar_init(&sh.sfull[i], 1);
-            ptx::mbar_init(&sh.sfree[i], kSoftWarps);
+            ptx::mbar_init(&sh.pfull[i], kSoftWarps);
             ptx::mbar_init(&sh.vfree[i], 1);
         }
-        ptx::mbar_init(&sh.pfull, kSoftWarps);
         ptx::mbar_init(&sh.pvdone, 1);
         sh.abort = 0;
         ptx::fence_mbar_init();
@@ -148,32 +160,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
         // ---- the head's queries as an operand: row m is query head m % group of row m / group
-        for (int m = warp; m < kM; m += kThreads / 32) {
-            const int r = m / group, h = kvh * group + m - r * group;
-            uint2 raw = make_uint2(0u, 0u);
-            // lane: 4 elements, (2 x 2 of each eight for int4: its codes come in the order 0 4 1 5 2 6 3 7)
+        constexpr int kPerWarp = kM / 16;
+        if (warp < 16) {
+            // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
             const int c8 = lane >> 1, half = lane & 1;
-            if (r < nrows) {
+            uint2 raw[kPerWarp];
+#pragma unroll
+            for (int x = 0; x < kPerWarp; ++x) {
+                const int m = kPerWarp * warp + x, r = m / group, h = kvh * group + m - r * group;
+                raw[x] = make_uint2(0u, 0u);
+                if (r >= nrows) continue;
                 const uint16_t* src = static_cast<const uint16_t*>(a.query) + (r0 + r) * a.q_stride + (int64_t)h * kD + 8 * c8;
                 if (E2M1) {
-                    raw = *reinterpret_cast<const uint2*>(src + 4 * half);
+                    raw[x] = *reinterpret_cast<const uint2*>(src + 4 * half);
                 } else {
-                    const uint32_t x = *reinterpret_cast<const uint32_t*>(src + 2 * half);
-                    const uint32_t y = *reinterpret_cast<const uint32_t*>(src + 4 + 2 * half);
-                    raw = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+                    raw[x] = make_uint2(*reinterpret_cast<const uint32_t*>(src + 2 * half),
+                                        *reinterpret_cast<const uint32_t*>(src + 4 + 2 * half));
                 }
             }
-            const float2 u = act2_to_float2<F16>(raw.x), v = act2_to_float2<F16>(raw.y);
-            float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
-            const float down = __uint_as_float((254u - ex) << 23);
-            *reinterpret_cast<uint2*>(qs + operand_at(m, c8) + 8 * half) =
-                make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
-            if (lane == 0)
-                sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
-                                     3.0e38f);
+            for (int x = 0; x < kPerWarp; ++x) {
+                const int m = kPerWarp * warp + x;
+                if (!E2M1) raw[x] = make_uint2(__byte_perm(raw[x].x, raw[x].y, 0x5410), __byte_perm(raw[x].x, raw[x].y, 0x7632));
+                const float2 u = act2_to_float2<F16>(raw[x].x), v = act2_to_float2<F16>(raw[x].y);
+                float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+                const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
+                *reinterpret_cast<uint2*>(qs + operand_at(m, c8) + 8 * half) =
+                    make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
+                // (above zero: the mask's -infinity times it stays -infinity)
+                if (lane == 0)
+                    sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
+                                         3.0e38f);
+            }
         }
         ptx::fence_proxy_async_smem();
         float m_run = -FLT_MAX, l_run = 0.0f;          // softmax threads
@@ -243,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t blk = __umulhi(at, L.block_recip);
                             if (at - blk * (uint32_t)a.p.block_size >= (uint32_t)a.p.block_size) ++blk;
                             const int page = table[blk];
+                            sh.at[h] = (uint32_t)((page * a.page_bytes + (int64_t)(at - blk * a.p.block_size) * a.entry_bytes) >> 4);
                             if (page < 0 || page >= a.p.num_blocks) {
                                 bits |= kErrPage;
                                 o = 0;
@@ -268,111 +290,104 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncthreads();
                 const int n = (int)sh.tiles;
                 if (warp < kSoftWarps) {
-                    // ------------------------------------------------------------ softmax: row `tid`
-                    const uint32_t lanes = tmem + ((uint32_t)warp << 21);
-                    const float f = sh.factor[tid];
-                    const int r = tid / group;
+                    // ------------------------------------------------------------ softmax
+                    // thread: a row, half of the tile's keys, with a maximum, a sum and an accumulator for that half
+                    const int half = warp >> 2, row = tid & 127, r = row / group;
+                    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+                    const float f = sh.factor[row];
                     const bool mine = r >= first && r < last;
-                    const uint32_t* row_mask = mask + (mine ? r : 0) * L.words;
+                    const uint32_t* row_mask = mask + (mine ? r : 0) * L.words + 2 * half;
                     for (int i = 0; i < n; ++i) {
-                        const uint32_t t = done + i, buf = t & 1;
+                        const uint32_t t = done + i, buf = t & 1, cols = lanes + kColS + 128 * buf + 64 * half;
+                        uint2 w = *reinterpret_cast<const uint2*>(row_mask + 4 * sh.list[i]);
+                        if (!mine) w = make_uint2(0u, 0u);
                         if (!wait_bounded(&sh.sfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
                         ptx::tc_fence_after();
-                        uint4 w4 = *reinterpret_cast<const uint4*>(row_mask + 4 * sh.list[i]);
-                        if (!mine) w4 = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                        bool waited = fresh && i == 0;             // nothing to wait for before the first product
                         bool ok = true;
+                        uint32_t p[32];
                         while (true) {
                             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                uint32_t p[32];
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t s[32];
+                                QLI_TMEM_LD_X32(cols + 32 * q, s);
+                                wait_loaded(s);
+                                const uint32_t bits = q ? w.y : w.x;
+                                if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    uint32_t s[32];
-                                    QLI_TMEM_LD_X32(lanes + kColS + 128 * buf + 64 * hf + 32 * q, s);
-                                    ptx::tmem_wait_ld();
-                                    const uint32_t bits = w[2 * hf + q];
+                                    for (int e = 0; e < 32; ++e)
+                                        if (!(bits >> e & 1)) s[e] = 0xFF800000u;          // -infinity
+                                }
+                                float best[2] = {-INFINITY, -INFINITY}, part[2] = {0.0f, 0.0f};
 #pragma unroll
-                                    for (int e = 0; e < 32; e += 2) {
-                                        const float x = bits >> e & 1 ? __uint_as_float(s[e]) : -INFINITY;
-                                        const float y = bits >> (e + 1) & 1 ? __uint_as_float(s[e + 1]) : -INFINITY;
-                                        top = fmaxf(top, fmaxf(x, y));
-                                        const float px = ptx::ex2(fmaf(x, f, -m_run)), py = ptx::ex2(fmaf(y, f, -m_run));
-                                        sum += px + py;
-                                        p[16 * q + e / 2] = float2_to_act2<true>(px, py);
-                                    }
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
+                                    best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
+                                    const float px = ptx::ex2(fmaf(x, f, -m_run)), py = ptx::ex2(fmaf(y, f, -m_run));
+                                    part[e >> 1 & 1] += px + py;
+                                    // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
+                                    p[16 * q + e / 2] = float2_to_act2<true>(px, py);
                                 }
-                                // P's columns are free once the product of the tile before is done
-                                if (!waited) {
-                                    ok = wait_bounded(&sh.pvdone, (t - 1) & 1, &sh.abort, a.err);
-                                    ptx::tc_fence_after();
-                                    waited = true;
-                                }
-                                QLI_TMEM_ST_X32(lanes + kColP + 32 * hf, p);
+                                top = fmaxf(top, fmaxf(best[0], best[1]));
+                                sum += part[0] + part[1];
                             }
-                            const bool over = fmaf(top, f, -m_run) > kRescale;
-                            if (!ok || !__any_sync(0xffffffffu, over)) {
+                            const float up = top * f;
+                            const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
+                            if (!__any_sync(0xffffffffu, over)) {
                                 l_run += sum;
                                 break;
                             }
-                            // raise the maximum of the rows that need it, rescale their sums and their rows of O
-                            const float up = over ? top * f : m_run, g = ptx::ex2(m_run - up);
-                            m_run = up;
+                            // raise the maximum of the rows that need it, rescale their sums and accumulators
+                            const float g = over ? ptx::ex2(m_run - up) : 1.0f;
+                            if (over) m_run = up;
                             l_run *= g;
-                            if (!(fresh && i == 0)) {
+                            if (fresh && i == 0) continue;
+                            ok = wait_bounded(&sh.pvdone, (t - 1) & 1, &sh.abort, a.err);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
 #pragma unroll 1
-                                for (int q = 0; q < 4; ++q) {
-                                    uint32_t o[32];
-                                    QLI_TMEM_LD_X32(lanes + kColO + 32 * q, o);
-                                    ptx::tmem_wait_ld();
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t o[32];
+                                QLI_TMEM_LD_X32(lanes + kColO + 128 * half + 32 * q, o);
+                                wait_loaded(o);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-                                    QLI_TMEM_ST_X32(lanes + kColO + 32 * q, o);
-                                }
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                                QLI_TMEM_ST_X32(lanes + kColO + 128 * half + 32 * q, o);
                             }
                         }
                         if (!ok) break;
+                        QLI_TMEM_ST_X32(cols, p);                  // in the place of the logits
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            ptx::mbar_arrive(&sh.sfree[buf]);
-                            ptx::mbar_arrive(&sh.pfull);
-                        }
+                        if (lane == 0) ptx::mbar_arrive(&sh.pfull[buf]);
                     }
                 } else if (warp < kMmaWarp) {
                     // ------------------------------------------------------------ converters
-                    const int ct = (tid - 32 * kSoftWarps) & 127;
-                    const uint32_t bs = (uint32_t)a.p.block_size;
+                    const int ct = tid & 127;
                     const bool stall = a.p.test_stall == 1;        // test switch: no tile is handed on, the waits run out
-                    // entry of position `at` of the masks (read only when some row lists it)
-                    auto entry = [&](uint32_t at, bool live) -> const uint8_t* {
-                        const uint32_t j = (uint32_t)from + at;
-                        uint32_t blk = __umulhi(j, L.block_recip), pos = j - blk * bs;
-                        if (pos >= bs) ++blk, pos -= bs;
-                        const int64_t page = live ? table[blk] : 0;
-                        return a.kv + kvh * kUnit + page * a.page_bytes + (int64_t)pos * a.entry_bytes;
+                    // entry of position `at` of the masks
+                    auto entry = [&](uint32_t at) -> const uint8_t* {
+                        return a.kv + kvh * kUnit + (uint64_t)sh.at[at >> 4] * 16 + (at & 15) * (uint32_t)a.entry_bytes;
                     };
                     if (warp < kSoftWarps + kConvWarps / 2) {
                         // keys: a lane takes a quarter of positions row, row + 32, ...  The lanes of the upper half
                         // of the elements go through their four pieces in the order 2 3 0 1: eight lanes that store
                         // at once then meet eight different 16-byte columns.
                         const int quarter = ct & 3, row = ct >> 2;
-                        uint4 code[4], scale[4];
-                        uint32_t word[4];
+                        uint4 code[4];
+                        uint32_t scale[4], vscale[4];
                         auto load = [&](int i) {
                             const uint32_t tile = sh.list[i];
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                word[x] = sh.any[4 * tile + x];
-                                const bool live = word[x] >> row & 1;
-                                const uint8_t* p = entry(128 * tile + 32 * x + row, live);
-                                code[x] = scale[x] = make_uint4(0u, 0u, 0u, 0u);
-                                if (live) {
+                                code[x] = make_uint4(0u, 0u, 0u, 0u);
+                                scale[x] = vscale[x] = 0;
+                                if (sh.any[4 * tile + x] >> row & 1) {
+                                    const uint8_t* p = entry(128 * tile + 32 * x + row);
                                     code[x] = reinterpret_cast<const uint4*>(p)[quarter];
-                                    scale[x] = *reinterpret_cast<const uint4*>(p + kD);
+                                    scale[x] = reinterpret_cast<const uint16_t*>(p + kD)[quarter];
+                                    vscale[x] = reinterpret_cast<const uint16_t*>(p + kD + kD / 16)[quarter];
                                 }
                             }
                         };
@@ -384,11 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 c4[x] = quarter & 2 ? make_uint4(code[x].z, code[x].w, code[x].x, code[x].y) : code[x];
-                                const uint32_t half = quarter & 2 ? scale[x].y : scale[x].x;
-                                s4[x] = half >> (16 * (quarter & 1)) & 0xFFFFu;
-                                // a NaN (0x7F or 0xFF) among the values' scales
-                                const uint32_t bad = __vcmpeq4(scale[x].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(scale[x].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                                if (bad) s4[x] = 0x7F7Fu;
+                                s4[x] = scale[x];
+                                // a NaN (0x7F or 0xFF) among two of the values' scales
+                                if (__vcmpeq4(vscale[x] & 0x7F7Fu, 0x00007F7Fu) & 0xFFFFu) s4[x] = 0x7F7Fu;
                             }
                             if (i + 1 < n) load(i + 1);            // under way while this tile is decoded
                             // the buffer of the tile before last is free once its product is done
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         auto load = [&](int i) {
                             const uint32_t tile = sh.list[i];
                             const uint32_t live = sh.any[4 * tile + (vg >> 2)] >> (8 * (vg & 3)) & 0xFFu;
-                            const uint8_t* p = entry(128 * tile + 8 * vg, live != 0);      // (eight positions share a page)
+                            const uint8_t* p = entry(128 * tile + 8 * vg);         // (16 positions share a page)
 #pragma unroll
                             for (int e = 0; e < 8; ++e, p += a.entry_bytes) {
                                 code[e] = make_uint2(0u, 0u);
@@ -477,8 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; ok && i <= n; ++i) {
                         if (i < n) {
                             const uint32_t t = done + i, buf = t & 1;
+                            // P of the tile before last lies where these logits go
                             ok = wait_bounded(&sh.kfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
-                                 (t < 2 || wait_bounded(&sh.sfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err));
+                                 (i < 2 || wait_bounded(&sh.pvdone, t & 1, &sh.abort, a.err));
                             if (!ok) break;
                             ptx::tc_fence_after();
                             const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ksm + buf * kOperand));
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > 0) {
                             const uint32_t t = done + i - 1, buf = t & 1;
                             ok = wait_bounded(&sh.vfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
-                                 wait_bounded(&sh.pfull, t & 1, &sh.abort, a.err);
+                                 wait_bounded(&sh.pfull[buf], (t >> 1) & 1, &sh.abort, a.err);
                             if (!ok) break;
                             ptx::tc_fence_after();
                             const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(vsm + buf * kOperand));
@@ -504,7 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int kk = 0; kk < kTileKeys2 / 16; ++kk) {
                                     const uint64_t step = (uint64_t)(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
-                                    ptx::mma_f16_ts(tm + kColO, tm + kColP + 8 * kk, vd + step, idesc, add || kk > 0);
+                                    // the halves of the keys have accumulators of their own
+                                    ptx::mma_f16_ts(tm + kColO + 128 * (kk >> 2), tm + kColS + 128 * buf + 64 * (kk >> 2) + 8 * (kk & 3),
+                                                    vd + step, idesc, add || (kk & 3) > 0);
                                 }
                                 ptx::mma_commit(&sh.vfree[buf]);
                                 ptx::mma_commit(&sh.pvdone);
@@ -534,36 +550,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- output of this head
         const bool failed = sh.abort != 0;
+        if (warp < kSoftWarps) sh.joined[warp >> 2][tid & 127] = make_float2(m_run, l_run);
+        __syncthreads();
         if (warp < kSoftWarps) {
-            const int r = tid / group, h = kvh * group + tid - r * group;
-            const float sum = failed ? __int_as_float(0x7FC00000) : l_run;
-            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            // the two halves of the keys joined; thread: a row, half of the elements
+            const int half = warp >> 2, row = tid & 127, r = row / group, h = kvh * group + row - r * group;
+            const float2 x = sh.joined[0][row], y = sh.joined[1][row];
+            const float top = fmaxf(x.x, y.x), gx = ptx::ex2(x.x - top), gy = ptx::ex2(y.x - top);
+            const float sum = failed ? __int_as_float(0x7FC00000) : fmaf(gx, x.y, gy * y.y);
+            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum, ax = gx * inv, ay = gy * inv;
             const bool live = r < nrows;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + ((r0 + (live ? r : 0)) * a.heads_q + h) * kD);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + ((r0 + (live ? r : 0)) * a.heads_q + h) * kD + 64 * half);
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t o[32];
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t from_o = tmem + ((uint32_t)(warp & 3) << 21) + kColO + 64 * half + 32 * q;
+                uint32_t u[32], v[32];
                 if (fresh) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                    for (int e = 0; e < 32; ++e) u[e] = v[e] = 0;
                 } else {
-                    QLI_TMEM_LD_X32(tmem + ((uint32_t)warp << 21) + kColO + 32 * q, o);
-                    ptx::tmem_wait_ld();
+                    QLI_TMEM_LD_X32(from_o, u);
+                    QLI_TMEM_LD_X32(from_o + 128, v);
+                    wait_loaded(u);
+                    wait_loaded(v);
                 }
                 if (live) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = sum == 0.0f ? 0u : float2_to_act2<F16>(__uint_as_float(o[8 * e + 2 * x]) * inv,
-                                                                         __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                        for (int z = 0; z < 4; ++z) {
+                            const int at = 8 * e + 2 * z;
+                            w[z] = sum == 0.0f ? 0u
+                                               : float2_to_act2<F16>(fmaf(__uint_as_float(u[at]), ax, __uint_as_float(v[at]) * ay),
+                                                                     fmaf(__uint_as_float(u[at + 1]), ax, __uint_as_float(v[at + 1]) * ay));
+                        }
                         dst[4 * q + e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                __syncwarp();                          // the loads above take the whole warp
             }
-            if (live && a.lse)
-                a.lse[(r0 + r) * a.heads_q + h] = sum == 0.0f ? -INFINITY : (m_run + log2f(sum)) * 0.6931471805599453f;
+            if (live && a.lse && half == 0)
+                a.lse[(r0 + r) * a.heads_q + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
         ptx::tc_fence_before();
         __syncthreads();
@@ -614,7 +642,7 @@ int64_t positions(const AttentionArgs& a)
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
 {
     const int group = a.heads_q / a.heads_kv;
-    if (head_dim != kD || group > 32) return false;
+    if (head_dim != kD || group * kMinRows > kM || a.page_bytes * a.p.num_blocks >> 36) return false;
     const int64_t rows = a.p.rows, per = std::min(kMaxRows, kM / group), blocks = (rows + per - 1) / per;
     return rows >= per * a.p.batch && blocks * a.heads_kv >= sms && positions(a) <= 4 * (int64_t)a.p.sparse_count;
 }
