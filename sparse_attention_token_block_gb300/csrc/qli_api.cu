@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "qli_internal.cuh"
+#include "qli_kv.cuh"
 
 namespace qli {
 
@@ -308,6 +309,21 @@ bool encode_row_map(void* tmap, const void* pool, int64_t entry_bytes, int64_t r
     cuuint32_t box[2] = {(cuuint32_t)box_bytes / 8, 1};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(static_cast<CUtensorMap*>(tmap), CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(pool), dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_page_map(void* tmap, const void* pool, int64_t entry_bytes, int block_size, int64_t page_bytes, int num_blocks,
+                     int box_bytes, int box_entries)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)entry_bytes / 8, (cuuint64_t)block_size, (cuuint64_t)num_blocks};
+    cuuint64_t strides[2] = {(cuuint64_t)entry_bytes, (cuuint64_t)page_bytes};
+    cuuint32_t box[3] = {(cuuint32_t)box_bytes / 8, (cuuint32_t)box_entries, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(static_cast<CUtensorMap*>(tmap), CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(pool), dims,
                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;

@@ -8,9 +8,11 @@
 //     S = Q K^T  (128 x 128 x D)     P = 2^(S f - m), zero where the row's bit is not set     O += P V
 //
 // so that a key is decoded once for R rows instead of once per row that lists it.  Roles:
-//   * 4 + 4 converter warps decode the tile's 4-bit entries into fp16 operands in shared memory: K rows
-//     as they are, V transposed (a lane takes eight entries x 16 elements and pairs the nibbles of two
-//     entries, as qli_attention.cu does); positions that no row lists are zeros and are not read;
+//   * one warp copies the KV head's bytes of a tile's entries by TMA, 16 positions (of one page) a box,
+//     where any of the 16 is listed (the mask covers what else lies there, finite values);
+//   * 4 + 4 converter warps decode them into fp16 operands in shared memory: K rows as they are, V
+//     transposed (a lane takes eight entries x 16 elements and pairs the nibbles of two entries, as
+//     qli_attention.cu does);
 //   * one warp issues the products: Q, K and V from shared memory, the logits twice in tensor memory, P in
 //     the place of the logits it came from, O once per half of a tile's keys;
 //   * 8 softmax warps, a row of the product and half of the tile's keys per thread: masked logits, running
@@ -26,11 +28,13 @@
 // finite values.
 //
 // Every wait is bounded (0.2 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <cstring>
 
 #include "qli_kv.cuh"
 
@@ -40,10 +44,12 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kM = 128, kTileKeys2 = 128;              // rows and keys of a product
-constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16, kCopyWarp = 17, kWarps = 18;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kAtom = kM * 128;                        // 128 rows of 64 fp16 in the 128-byte swizzle
 constexpr int kOperand = 2 * kAtom;
+constexpr int kUnit = kv_unit_bytes(kD), kRaw = kTileKeys2 * kUnit;        // a tile's entries of one KV head
+constexpr int kSmemK = kOperand, kSmemV = 2 * kOperand, kSmemRaw = 4 * kOperand, kSmemMask = kSmemRaw + 2 * kRaw;
 constexpr int kMaxRows = 32;                           // rows of a block
 constexpr int kMinRows = 4;                            // of a block, at 32 query heads per KV head
 constexpr int kMaskBytes = 24 * 1024;
@@ -61,23 +67,24 @@ struct RowsLayout {
 };
 
 struct Shared {
-    uint64_t kfull[2], vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
+    uint64_t rawfull[2], rawfree[2], kfull, vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
     uint32_t tmem, abort, dup, tiles;
     int32_t batch[kMaxRows];
     float factor[kM];
     float2 joined[2][kM];                              // maximum and sum of a row over its half of the keys
     alignas(16) uint32_t any[kMaxWords];               // over the rows
-    uint32_t at[2 * kMaxWords];                        // entry of every 16th position, in 16 bytes from the pool's start
+    int32_t slot[2 * kMaxWords];                       // slot of the pool of every 16th position, -1: no row lists any of the 16
     uint32_t rest[kMaxRows][kMaxSparse / 32];          // list positions left for further rounds
     uint16_t list[kMaxWords / 4];                      // tiles with an entry
 };
 
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+// The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up.  (Inline: around
+// a call the registers that hold the next tile would go through local memory.)
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
 {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = ptx::globaltimer();
-    while (true) {
-        const bool done = ptx::mbar_try_wait_sleep(bar, parity, 100000u);
-        if (__all_sync(0xffffffffu, done)) return true;
+    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 100000u))) {
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
         if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
             *abort = 1;
@@ -85,12 +92,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
             return false;
         }
     }
-}
-
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
-{
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-    return wait_slow(bar, parity, abort, err);
+    return true;
 }
 
 // Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
@@ -110,15 +112,13 @@ __device__ __forceinline__ uint32_t operand_at(int r, int piece)
 
 template <bool F16, bool E2M1>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_rows_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ RowsLayout L)
+    attention_rows_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ RowsLayout L,
+                          const __grid_constant__ CUtensorMap pages)
 {
-    constexpr int kUnit = kv_unit_bytes(kD);
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qs = smem;
-    uint8_t* ksm = smem + kOperand;
-    uint8_t* vsm = smem + 3 * kOperand;
-    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + 5 * kOperand);
-    Shared& sh = *reinterpret_cast<Shared*>(smem + 5 * kOperand + kMaskBytes);
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kSmemMask);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + kSmemMask + kMaskBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.heads_q / a.heads_kv, k = a.p.sparse_count;
     const int64_t block = blockIdx.x / (uint32_t)L.slices;
@@ -129,12 +129,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&sh.kfull[i], kConvWarps / 2);
-            ptx::mbar_init(&sh.vfull[i], kConvWarps / 2);
+            ptx::mbar_init(&sh.rawfull[i], 1);
+            ptx::mbar_init(&sh.rawfree[i], kConvWarps);
+            ptx::mbar_init(&sh.vfull[i], 4);
             ptx::mbar_init(&sh.sfull[i], 1);
             ptx::mbar_init(&sh.pfull[i], kSoftWarps);
             ptx::mbar_init(&sh.vfree[i], 1);
         }
+        ptx::mbar_init(&sh.kfull, 4);
         ptx::mbar_init(&sh.pvdone, 1);
         sh.abort = 0;
         ptx::fence_mbar_init();
@@ -160,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
         // ---- the head's queries as an operand: row m is query head m % group of row m / group
-        constexpr int kPerWarp = kM / 16;
-        if (warp < 16) {
+        constexpr int kPerWarp = 8;
+        if (warp < kM / kPerWarp) {
             // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
             const int c8 = lane >> 1, half = lane & 1;
             uint2 raw[kPerWarp];
@@ -264,13 +266,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t blk = __umulhi(at, L.block_recip);
                             if (at - blk * (uint32_t)a.p.block_size >= (uint32_t)a.p.block_size) ++blk;
                             const int page = table[blk];
-                            sh.at[h] = (uint32_t)((page * a.page_bytes + (int64_t)(at - blk * a.p.block_size) * a.entry_bytes) >> 4);
+                            sh.slot[h] = page * a.p.block_size + (int)(at - blk * a.p.block_size);
                             if (page < 0 || page >= a.p.num_blocks) {
                                 bits |= kErrPage;
-                                o = 0;
+                                o = 0;                 // (what was computed of the bad page is replaced)
                                 for (int r = first; r < last; ++r) reinterpret_cast<uint16_t*>(mask)[r * 2 * L.words + h] = 0;
                             }
                         }
+                        if (!o) sh.slot[h] = -1;
                         reinterpret_cast<uint16_t*>(sh.any)[h] = (uint16_t)o;
                     }
                     if (bits && a.err) atomicOr(a.err, bits);
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
-                                        if (!(bits >> e & 1)) s[e] = 0xFF800000u;          // -infinity
+                                        s[e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[e]) : -INFINITY);
                                 }
                                 float best[2] = {-INFINITY, -INFINITY}, part[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -328,6 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
                                     p[16 * q + e / 2] = float2_to_act2<true>(px, py);
                                 }
+                                // (this half is done with before the next is loaded: both at once spill)
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(p[16 * q + e]));
                                 top = fmaxf(top, fmaxf(best[0], best[1]));
                                 sum += part[0] + part[1];
                             }
@@ -362,140 +368,122 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&sh.pfull[buf]);
                     }
-                } else if (warp < kMmaWarp) {
-                    // ------------------------------------------------------------ converters
-                    const int ct = tid & 127;
+                } else if (warp < kSoftWarps + 4) {
+                    // ------------------------------------------------------------ converters of the keys
+                    // a lane takes a quarter of four positions, eight neighbouring lanes eight positions: their
+                    // loads (144 bytes apart) and stores (swizzled rows) meet all banks once
+                    const int row = 32 * (warp - kSoftWarps) + (lane & 7), quarter = lane >> 3;
                     const bool stall = a.p.test_stall == 1;        // test switch: no tile is handed on, the waits run out
-                    // entry of position `at` of the masks
-                    auto entry = [&](uint32_t at) -> const uint8_t* {
-                        return a.kv + kvh * kUnit + (uint64_t)sh.at[at >> 4] * 16 + (at & 15) * (uint32_t)a.entry_bytes;
-                    };
-                    if (warp < kSoftWarps + kConvWarps / 2) {
-                        // keys: a lane takes a quarter of positions row, row + 32, ...  The lanes of the upper half
-                        // of the elements go through their four pieces in the order 2 3 0 1: eight lanes that store
-                        // at once then meet eight different 16-byte columns.
-                        const int quarter = ct & 3, row = ct >> 2;
-                        uint4 code[4];
-                        uint32_t scale[4], vscale[4];
-                        auto load = [&](int i) {
-                            const uint32_t tile = sh.list[i];
+                    const uint32_t off0 = kSmemK + operand_at(row, 4 * quarter);
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t t = done + i, buf = t & 1;
+                        const uint8_t* src = smem + kSmemRaw + buf * kRaw + row * kUnit;
+                        if (!wait_bounded(&sh.rawfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
+                        // the operand is free once the logits of the tile before are there
+                        if (t > 0 && !wait_bounded(&sh.sfull[buf ^ 1], ((t - 1) >> 1) & 1, &sh.abort, a.err)) break;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                code[x] = make_uint4(0u, 0u, 0u, 0u);
-                                scale[x] = vscale[x] = 0;
-                                if (sh.any[4 * tile + x] >> row & 1) {
-                                    const uint8_t* p = entry(128 * tile + 32 * x + row);
-                                    code[x] = reinterpret_cast<const uint4*>(p)[quarter];
-                                    scale[x] = reinterpret_cast<const uint16_t*>(p + kD)[quarter];
-                                    vscale[x] = reinterpret_cast<const uint16_t*>(p + kD + kD / 16)[quarter];
-                                }
-                            }
-                        };
-                        if (n > 0) load(0);
-                        for (int i = 0; i < n; ++i) {
-                            const uint32_t t = done + i, buf = t & 1;
-                            uint4 c4[4];
-                            uint32_t s4[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                c4[x] = quarter & 2 ? make_uint4(code[x].z, code[x].w, code[x].x, code[x].y) : code[x];
-                                s4[x] = scale[x];
-                                // a NaN (0x7F or 0xFF) among two of the values' scales
-                                if (__vcmpeq4(vscale[x] & 0x7F7Fu, 0x00007F7Fu) & 0xFFFFu) s4[x] = 0x7F7Fu;
-                            }
-                            if (i + 1 < n) load(i + 1);            // under way while this tile is decoded
-                            // the buffer of the tile before last is free once its product is done
-                            if (t >= 2 && !wait_bounded(&sh.sfull[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
-                            uint8_t* kb = ksm + buf * kOperand;
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint32_t h = e4m3x2_to_f16x2(s4[x]);
-                                // (the pieces' order swaps the lane's two blocks)
-                                const PairScale g0 = pair_scale<E2M1>(__byte_perm(h, 0, quarter & 2 ? 0x3232 : 0x1010));
-                                const PairScale g1 = pair_scale<E2M1>(__byte_perm(h, 0, quarter & 2 ? 0x1010 : 0x3232));
-                                const uint32_t w[4] = {c4[x].x, c4[x].y, c4[x].z, c4[x].w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    uint32_t o[4];
-                                    decode_pairs<E2M1>(w[e], e < 2 ? g0 : g1, o);
-                                    *reinterpret_cast<uint4*>(kb + operand_at(32 * x + row, 4 * quarter + (e ^ (quarter & 2)))) =
-                                        make_uint4(o[0], o[1], o[2], o[3]);
-                                }
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.kfull[buf]);
-                        }
-                    } else {
-                        // values: a lane takes one block of 16 elements of eight positions, in odd blocks the
-                        // elements in the order 4 5 6 7 0 1 2 3 (as above)
-                        const int vb = ct & 7, vg = ct >> 3;
-                        uint2 code[8];
-                        uint32_t scale[8];
-                        auto load = [&](int i) {
-                            const uint32_t tile = sh.list[i];
-                            const uint32_t live = sh.any[4 * tile + (vg >> 2)] >> (8 * (vg & 3)) & 0xFFu;
-                            const uint8_t* p = entry(128 * tile + 8 * vg);         // (16 positions share a page)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e, p += a.entry_bytes) {
-                                code[e] = make_uint2(0u, 0u);
-                                scale[e] = 0;
-                                if (live >> e & 1) {
-                                    code[e] = *reinterpret_cast<const uint2*>(p + kD / 2 + 8 * vb);
-                                    scale[e] = p[kD + kD / 16 + vb];
-                                }
-                            }
-                        };
-                        const uint32_t turn = vb & 1 ? 0x1032 : 0x3210;
-                        if (n > 0) load(0);
-                        for (int i = 0; i < n; ++i) {
-                            const uint32_t t = done + i, buf = t & 1;
-                            uint32_t w[2][8];
-                            PairScale g[4];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                w[0][e] = __byte_perm(code[e].x, 0, turn);
-                                w[1][e] = __byte_perm(code[e].y, 0, turn);
-                            }
+                        for (int x = 0; x < 4; ++x, src += 8 * kUnit) {
+                            const uint4 code = reinterpret_cast<const uint4*>(src)[quarter];
+                            uint32_t scale = reinterpret_cast<const uint16_t*>(src + kD)[quarter];
+                            const uint32_t vscale = reinterpret_cast<const uint16_t*>(src + kD + kD / 16)[quarter];
+                            // a NaN (0x7F or 0xFF) among two of the values' scales
+                            if (__vcmpeq4(vscale & 0x7F7Fu, 0x00007F7Fu) & 0xFFFFu) scale = 0x7F7Fu;
+                            const uint32_t h = e4m3x2_to_f16x2(scale), w[4] = {code.x, code.y, code.z, code.w};
+                            const PairScale g[2] = {pair_scale<E2M1>(__byte_perm(h, 0, 0x1010)), pair_scale<E2M1>(__byte_perm(h, 0, 0x3232))};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                uint32_t h = e4m3x2_to_f16x2(scale[2 * e] | scale[2 * e + 1] << 8);
-                                asm("max.f16x2 %0, %0, %1;" : "+r"(h) : "r"(0xDF00DF00u));        // -448: NaN to a number
-                                g[e] = pair_scale<E2M1>(h);
+                                uint32_t o[4];
+                                decode_pairs<E2M1>(w[e], g[e >> 1], o);
+                                *reinterpret_cast<uint4*>(smem + ((off0 ^ (e << 4)) + 8 * 128 * x)) =
+                                    make_uint4(o[0], o[1], o[2], o[3]);
                             }
-                            if (i + 1 < n) load(i + 1);
-                            if (t >= 2 && !wait_bounded(&sh.vfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
-                            uint8_t* vdst = vsm + buf * kOperand;
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                uint32_t o[4][8];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) decode_across<E2M1>(w[y][2 * e], w[y][2 * e + 1], g[e], o[e]);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    *reinterpret_cast<uint4*>(vdst + operand_at(16 * vb + 8 * y + (e ^ (4 * (vb & 1))), vg)) =
-                                        make_uint4(o[0][e], o[1][e], o[2][e], o[3][e]);
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.vfull[buf]);
                         }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && !stall) {
+                            ptx::mbar_arrive(&sh.kfull);
+                            ptx::mbar_arrive(&sh.rawfree[buf]);
+                        }
+                    }
+                } else if (warp < kMmaWarp) {
+                    // ------------------------------------------------------------ converters of the values
+                    // a lane takes one block of 16 elements of eight positions, in odd blocks the elements in the
+                    // order 4 5 6 7 0 1 2 3, so that the stores of eight neighbouring lanes meet all banks once
+                    const int ct = tid & 127, vg = (ct & 3) + 4 * (ct >> 5), vb = ct >> 2 & 7;
+                    const bool stall = a.p.test_stall == 1;
+                    const uint32_t turn = vb & 1 ? 0x1032 : 0x3210;
+                    // operand_at of its first element; of element e: 128 e further, and the column with e flipped
+                    const uint32_t off0 = operand_at(16 * vb + 4 * (vb & 1), vg);
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t t = done + i, buf = t & 1;
+                        const uint8_t* src = smem + kSmemRaw + buf * kRaw + 8 * vg * kUnit + kD / 2;
+                        if (!wait_bounded(&sh.rawfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
+                        uint32_t w[2][8], scale[8];
+                        PairScale g[4];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint2 code = reinterpret_cast<const uint2*>(src + e * kUnit)[vb];
+                            w[0][e] = __byte_perm(code.x, 0, turn);
+                            w[1][e] = __byte_perm(code.y, 0, turn);
+                            scale[e] = src[e * kUnit + kD / 2 + kD / 16 + vb];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t h = e4m3x2_to_f16x2(scale[2 * e] | scale[2 * e + 1] << 8);
+                            asm("max.f16x2 %0, %0, %1;" : "+r"(h) : "r"(0xDF00DF00u));        // -448: NaN to a number
+                            g[e] = pair_scale<E2M1>(h);
+                        }
+                        if (t >= 2 && !wait_bounded(&sh.vfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
+                        uint8_t* dst = smem + kSmemV + buf * kOperand;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t o[4][8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) decode_across<E2M1>(w[y][2 * e], w[y][2 * e + 1], g[e], o[e]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(dst + (off0 ^ (e << 7 | e << 4)) + 8 * 128 * y) =
+                                    make_uint4(o[0][e], o[1][e], o[2][e], o[3][e]);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && !stall) {
+                            ptx::mbar_arrive(&sh.vfull[buf]);
+                            ptx::mbar_arrive(&sh.rawfree[buf]);
+                        }
+                    }
+                } else if (warp == kCopyWarp) {
+                    // ------------------------------------------------------------ copies, 16 positions each
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t t = done + i, buf = t & 1;
+                        const int32_t slot = lane < 8 ? sh.slot[8 * sh.list[i] + lane] : -1;
+                        const uint32_t live = __popc(__ballot_sync(0xffffffffu, slot >= 0));
+                        if (t >= 2 && !wait_bounded(&sh.rawfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.rawfull[buf], live * 16 * kUnit);
+                        __syncwarp();
+                        if (slot >= 0) {
+                            uint32_t page = __umulhi((uint32_t)slot, L.block_recip), pos = (uint32_t)slot - page * a.p.block_size;
+                            if (pos >= (uint32_t)a.p.block_size) ++page, pos -= a.p.block_size;
+                            ptx::tma_load_3d(smem + kSmemRaw + buf * kRaw + lane * 16 * kUnit, &pages, kvh * (kUnit / 8), (int)pos, (int)page,
+                                             &sh.rawfull[buf]);
+                        }
+                        __syncwarp();
                     }
                 } else {
                     // ------------------------------------------------------------ products
-                    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                     const uint32_t idesc = ptx::idesc_f16_f32(kM, kTileKeys2);
+                    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                     const uint64_t qd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(qs));
+                    const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem + kSmemK));
                     bool ok = true;
-                    for (int i = 0; ok && i <= n; ++i) {
+                    for (int i = 0; i <= n; ++i) {
                         if (i < n) {
+                            // logits of tile i; P of the tile before last lies where they go
                             const uint32_t t = done + i, buf = t & 1;
-                            // P of the tile before last lies where these logits go
-                            ok = wait_bounded(&sh.kfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
+                            ok = wait_bounded(&sh.kfull, t & 1, &sh.abort, a.err) &&
                                  (i < 2 || wait_bounded(&sh.pvdone, t & 1, &sh.abort, a.err));
                             if (!ok) break;
                             ptx::tc_fence_after();
-                            const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ksm + buf * kOperand));
                             if (ptx::elect_one()) {
 #pragma unroll
                                 for (int kk = 0; kk < kD / 16; ++kk) {
@@ -507,12 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                         if (i > 0) {
+                            // output of tile i - 1
                             const uint32_t t = done + i - 1, buf = t & 1;
                             ok = wait_bounded(&sh.vfull[buf], (t >> 1) & 1, &sh.abort, a.err) &&
                                  wait_bounded(&sh.pfull[buf], (t >> 1) & 1, &sh.abort, a.err);
                             if (!ok) break;
                             ptx::tc_fence_after();
-                            const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(vsm + buf * kOperand));
+                            const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem + kSmemV + buf * kOperand));
                             const bool add = !(fresh && i == 1);
                             if (ptx::elect_one()) {
 #pragma unroll
@@ -611,7 +600,7 @@ template <bool F16, bool E2M1>
 cudaError_t launch_rows(const AttentionArgs& a, const RowsLayout& L, int64_t grid, cudaStream_t st)
 {
     auto kernel = attention_rows_kernel<F16, E2M1>;
-    constexpr int kSmem = 5 * kOperand + kMaskBytes + (int)sizeof(Shared);
+    constexpr int kSmem = kSmemMask + kMaskBytes + (int)sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
@@ -623,7 +612,11 @@ cudaError_t launch_rows(const AttentionArgs& a, const RowsLayout& L, int64_t gri
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), kSmem, st, a, L);
+    CUtensorMap pages;
+    std::memset(&pages, 0, sizeof(pages));
+    if (a.p.num_blocks > 0 && !encode_page_map(&pages, a.kv, a.entry_bytes, a.p.block_size, a.page_bytes, a.p.num_blocks, kUnit, 16))
+        return cudaErrorUnknown;
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), kSmem, st, a, L, pages);
 }
 
 }  // namespace
@@ -642,7 +635,7 @@ int64_t positions(const AttentionArgs& a)
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
 {
     const int group = a.heads_q / a.heads_kv;
-    if (head_dim != kD || group * kMinRows > kM || a.page_bytes * a.p.num_blocks >> 36) return false;
+    if (head_dim != kD || group * kMinRows > kM || !a.kv) return false;
     const int64_t rows = a.p.rows, per = std::min(kMaxRows, kM / group), blocks = (rows + per - 1) / per;
     return rows >= per * a.p.batch && blocks * a.heads_kv >= sms && positions(a) <= 4 * (int64_t)a.p.sparse_count;
 }

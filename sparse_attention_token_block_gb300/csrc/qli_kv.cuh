@@ -166,6 +166,11 @@ __device__ __forceinline__ int64_t kv_entry_offset(const Params& p, const int32_
     return page * page_bytes + (int64_t)((uint32_t)pos - block * bs) * entry_bytes;
 }
 
+// Tensor map (a CUtensorMap) of a paged pool: 8-byte elements, boxes of `box_entries` entries of a page, `box_bytes`
+// wide
+bool encode_page_map(void* tmap, const void* pool, int64_t entry_bytes, int block_size, int64_t page_bytes, int num_blocks,
+                     int box_bytes, int box_entries);
+
 // Sparse attention over blocks of neighbouring rows (qli_attention_rows.cu): whether it suits a call, and
 // its launch
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms);
