@@ -3,25 +3,27 @@
 //
 // A CTA takes R consecutive rows x G query heads of one KV head after another: R * G <= 128 rows of a
 // product.  It turns the rows' lists into bit masks over the positions of their sequence, walks the
-// tiles of 128 positions in which some row has an entry, and runs per tile
+// tiles of 64 positions in which some row has an entry, and runs per tile
 //
-//     S = Q K^T  (128 x 128 x D)     P = 2^(S f - m), zero where the row's bit is not set     O += P V
+//     S = Q K^T  (128 x 64 x D)     P = 2^(S f - m), zero where the row's bit is not set     O += P V
 //
 // so that a key is decoded once for R rows instead of once per row that lists it.  Roles:
 //   * one warp copies the KV head's bytes of a tile's entries by TMA, 16 positions (of one page) a box,
 //     where any of the 16 is listed (the mask covers what else lies there, finite values);
-//   * 4 + 4 converter warps decode them into fp16 operands in shared memory: K rows as they are, V
+//   * 2 + 2 converter warps decode them into fp16 operands in shared memory: K rows as they are, V
 //     transposed (a lane takes eight entries x 16 elements and pairs the nibbles of two entries, as
 //     qli_attention.cu does);
 //   * one warp issues the products: Q, K and V from shared memory, the logits twice in tensor memory, P in
-//     the place of the logits it came from, O once per half of a tile's keys;
-//   * 8 softmax warps, a row of the product and half of the tile's keys per thread: masked logits, running
-//     maximum (raised only when a logit passes it by more than 2^8, then the half's row of O is rescaled),
-//     sum in fp32, P to fp16.  The halves never meet before the end, where they are joined.
+//     the place of the logits it came from;
+//   * 4 softmax warps, a row of the product per thread: masked logits, running maximum (raised only when
+//     a logit passes it by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+// Two CTAs share an SM (half its shared and tensor memory each): what a tile costs is mostly the way from
+// role to role, and one CTA's masks, queries and outputs overlap the other's products.
 //
-// A position that a row lists n times counts n times: the list positions that are left over when a mask
-// is built go into the masks of further rounds.  So do the rows of a block that belong to another batch,
-// and the positions past the masks' width.
+// A position that a row lists n times counts n times: where the lists of a block hold duplicates (as many
+// entries as mask bits, or not), the list positions that are left over when a mask is built go into the
+// masks of further rounds.  Further rounds also take the rows of a block that belong to another batch and
+// the positions past the masks' width.
 //
 // A zero of P times a NaN would be a NaN, in rows that do not list the entry: an entry with a NaN among its
 // scales (the cache write makes none) is taken as NaN keys, which the mask hides from the other rows, and
@@ -43,24 +45,24 @@ namespace qli {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kM = 128, kTileKeys2 = 128;              // rows and keys of a product
-constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16, kCopyWarp = 17, kWarps = 18;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kAtom = kM * 128;                        // 128 rows of 64 fp16 in the 128-byte swizzle
-constexpr int kOperand = 2 * kAtom;
-constexpr int kUnit = kv_unit_bytes(kD), kRaw = kTileKeys2 * kUnit;        // a tile's entries of one KV head
-constexpr int kSmemK = kOperand, kSmemV = 2 * kOperand, kSmemRaw = 4 * kOperand, kSmemMask = kSmemRaw + 2 * kRaw;
-constexpr int kMaxRows = 32;                           // rows of a block
-constexpr int kMinRows = 4;                            // of a block, at 32 query heads per KV head
-constexpr int kMaskBytes = 24 * 1024;
-constexpr int kMaxWords = kMaskBytes / 4 / kMinRows;   // of a row's mask
-constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+constexpr int kM = 128, kTile = 64;                    // rows and keys of a product
+constexpr int kSoftWarps = 4, kKeyWarp = 4, kValueWarp = 6, kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kUnit = kv_unit_bytes(kD), kRaw = kTile * kUnit;             // a tile's entries of one KV head
+// shared memory: operands (rows of 64 fp16 in the 128-byte swizzle, 128 bytes each), the copied entries, masks
+constexpr int kAtomQ = kM * 128, kAtomK = kTile * 128, kAtomV = kD * 128;
+constexpr int kSmemK = 2 * kAtomQ, kSmemV = kSmemK + 2 * kAtomK, kSmemRaw = kSmemV + 2 * kAtomV, kSmemMask = kSmemRaw + 2 * kRaw;
+constexpr int kMaxRows = 32, kMinRows = 4;             // of a block (at most 32 query heads per KV head)
+constexpr int kMaskBytes = 12 * 1024;
+constexpr int kMaxWords = 128;                         // of a row's mask
+constexpr uint32_t kColS = 0, kColO = 2 * kTile, kTmemCols = 256;
 constexpr float kRescale = 8.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull;
 
 struct RowsLayout {
     int32_t rows;          // rows of a block
-    int32_t words;         // mask words per row (a multiple of 4: whole tiles)
+    int32_t words;         // mask words per row (whole tiles)
+    int32_t exact_words;   // the same where the masks share their space with the list positions left over
     int32_t heads;         // KV heads per CTA
     int32_t slices;        // CTAs per block
     uint32_t block_recip;
@@ -68,14 +70,11 @@ struct RowsLayout {
 
 struct Shared {
     uint64_t rawfull[2], rawfree[2], kfull, vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
-    uint32_t tmem, abort, dup, tiles;
+    uint32_t tmem, abort, dup, tiles, entries, bits;
     int32_t batch[kMaxRows];
     float factor[kM];
-    float2 joined[2][kM];                              // maximum and sum of a row over its half of the keys
-    alignas(16) uint32_t any[kMaxWords];               // over the rows
-    int32_t slot[2 * kMaxWords];                       // slot of the pool of every 16th position, -1: no row lists any of the 16
-    uint32_t rest[kMaxRows][kMaxSparse / 32];          // list positions left for further rounds
-    uint16_t list[kMaxWords / 4];                      // tiles with an entry
+    alignas(16) int32_t slot[2 * kMaxWords];                       // slot of the pool of every 16th position, -1: no row lists any of the 16
+    uint8_t list[kMaxWords / 2];                       // tiles with an entry
 };
 
 // The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up.  (Inline: around
@@ -104,14 +103,14 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[32])
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand of two swizzled blocks
-__device__ __forceinline__ uint32_t operand_at(int r, int piece)
+// Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand of swizzled blocks of `atom` bytes
+__device__ __forceinline__ uint32_t operand_at(int r, int piece, int atom)
 {
-    return (piece >> 3) * kAtom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+    return (piece >> 3) * atom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
 }
 
 template <bool F16, bool E2M1>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     attention_rows_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ RowsLayout L,
                           const __grid_constant__ CUtensorMap pages)
 {
@@ -121,8 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared& sh = *reinterpret_cast<Shared*>(smem + kSmemMask + kMaskBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.heads_q / a.heads_kv, k = a.p.sparse_count;
-    const int64_t block = blockIdx.x / (uint32_t)L.slices;
-    const int slice = (int)(blockIdx.x - block * L.slices);
+    // later rows of a sequence attend to more of it: they start first
+    const uint32_t cta = gridDim.x - 1 - blockIdx.x;
+    const int64_t block = cta / (uint32_t)L.slices;
+    const int slice = (int)(cta - block * L.slices);
     const int64_t r0 = block * L.rows;
     const int nrows = (int)min((int64_t)L.rows, a.p.rows - r0);
     const int head0 = slice * L.heads, head1 = min(a.heads_kv, head0 + L.heads);
@@ -130,13 +131,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.rawfull[i], 1);
-            ptx::mbar_init(&sh.rawfree[i], kConvWarps);
-            ptx::mbar_init(&sh.vfull[i], 4);
+            ptx::mbar_init(&sh.rawfree[i], 4);
+            ptx::mbar_init(&sh.vfull[i], 2);
             ptx::mbar_init(&sh.sfull[i], 1);
             ptx::mbar_init(&sh.pfull[i], kSoftWarps);
             ptx::mbar_init(&sh.vfree[i], 1);
         }
-        ptx::mbar_init(&sh.kfull, 4);
+        ptx::mbar_init(&sh.kfull, 2);
         ptx::mbar_init(&sh.pvdone, 1);
         sh.abort = 0;
         ptx::fence_mbar_init();
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
         // ---- the head's queries as an operand: row m is query head m % group of row m / group
-        constexpr int kPerWarp = 8;
+        constexpr int kPerWarp = 16;
         if (warp < kM / kPerWarp) {
             // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
             const int c8 = lane >> 1, half = lane & 1;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
                 const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
                 const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
-                *reinterpret_cast<uint2*>(qs + operand_at(m, c8) + 8 * half) =
+                *reinterpret_cast<uint2*>(qs + operand_at(m, c8, kAtomQ) + 8 * half) =
                     make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
                 // (above zero: the mask's -infinity times it stays -infinity)
                 if (lane == 0)
@@ -208,101 +209,128 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (last < nrows && sh.batch[last] == b) ++last;
             const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : 0;
             const int32_t* table = a.block_table + (int64_t)max(b, 0) * a.p.max_blocks_per_seq;
-            const int window = 32 * L.words;
             int64_t from = 0;                          // first position of the masks
+            bool exact = false;                        // the lists hold duplicates
             // (a list of a batch without positions is still looked at: its indices are errors)
             for (int pass = 0; b >= 0;) {
-                if (!standing) {
+                int words = exact ? L.exact_words : L.words;
+                while (!standing) {
                     // ---- masks of this round
-                    __syncthreads();                   // (every thread has read dup)
-                    for (int i = tid; i < L.rows * L.words; i += kThreads) mask[i] = 0;
-                    if (pass == 0)
-                        for (int i = tid; i < kMaxRows * (kMaxSparse / 32); i += kThreads) (&sh.rest[0][0])[i] = 0;
-                    if (tid == 0) sh.dup = 0;
+                    uint32_t* rest = mask + L.rows * L.exact_words;            // (exact) per row
+                    const int rest_words = (k + 31) >> 5;
+                    __syncthreads();                   // (every thread has read what the last round left)
+                    for (int i = tid; i < L.rows * words; i += kThreads) mask[i] = 0;
+                    if (exact && pass == 0)
+                        for (int i = tid; i < L.rows * rest_words; i += kThreads) rest[i] = 0;
+                    if (tid == 0) sh.dup = sh.entries = sh.bits = 0;
                     __syncthreads();
-                    uint32_t bits = 0;
-                    constexpr int kPer = (kMaxSparse + kThreads - 1) / kThreads, kAtOnce = 4;
-                    for (int ra = first; ra < last; ra += kAtOnce) {
-                        int32_t j[kAtOnce][kPer];
+                    uint32_t bits = 0, entries = 0, set = 0;
+                    const uint32_t width = (uint32_t)max((int64_t)0, min((int64_t)(32 * words), limit - from));
+                    if (!exact) {
+                        constexpr int kAtOnce = 16;
+                        for (int e = tid; e < k; e += kThreads) {
+#pragma unroll 1
+                            for (int ra = first; ra < last; ra += kAtOnce) {
+                                const int32_t* src = a.idx + (r0 + ra) * k + e;
+                                int32_t j[kAtOnce];
 #pragma unroll
-                        for (int r = 0; r < kAtOnce; ++r)
+                                for (int r = 0; r < kAtOnce; ++r) j[r] = ra + r < last ? src[r * k] : -1;
+                                uint32_t* m = mask + ra * words;
 #pragma unroll
-                            for (int x = 0; x < kPer; ++x) {
-                                const int e = tid + x * kThreads;
-                                j[r][x] = -1;
-                                if (e < k && ra + r < last && (pass == 0 || (sh.rest[ra + r][e >> 5] >> (e & 31) & 1)))
-                                    j[r][x] = a.idx[(r0 + ra + r) * k + e];
-                            }
-#pragma unroll
-                        for (int r = 0; r < kAtOnce; ++r)
-#pragma unroll
-                            for (int x = 0; x < kPer; ++x) {
-                                if (j[r][x] == -1) continue;
-                                if (j[r][x] < 0 || j[r][x] >= limit) {
-                                    bits |= kErrLength;
-                                    continue;
+                                for (int r = 0; r < kAtOnce; ++r) {
+                                    const uint32_t at = (uint32_t)j[r] - (uint32_t)from;
+                                    if (j[r] >= 0 && at < width) {
+                                        atomicOr(m + r * words + (at >> 5), 1u << (at & 31));
+                                        ++entries;
+                                    } else if (j[r] != -1 && (j[r] < 0 || j[r] >= limit)) {
+                                        bits |= kErrLength;
+                                    }
                                 }
-                                const int64_t at = j[r][x] - from;
-                                if (at < 0 || at >= window) continue;
-                                const int e = tid + x * kThreads;
-                                const uint32_t bit = 1u << (at & 31);
-                                const bool again = atomicOr(&mask[(ra + r) * L.words + (int)(at >> 5)], bit) & bit;
-                                if (again) {
-                                    if (pass == 0) atomicOr(&sh.rest[ra + r][e >> 5], 1u << (e & 31));
-                                    sh.dup = 1;
-                                } else if (pass > 0) {
-                                    atomicAnd(&sh.rest[ra + r][e >> 5], ~(1u << (e & 31)));
-                                }
-                            }
-                    }
-                    __syncthreads();
-                    // what some row lists; positions on bad pages leave the masks (16 positions share a page)
-                    for (int h = tid; h < 2 * L.words; h += kThreads) {
-                        const uint16_t* m16 = reinterpret_cast<const uint16_t*>(mask) + h;
-                        uint32_t o = 0;
-                        for (int r = first; r < last; ++r) o |= m16[r * 2 * L.words];
-                        if (o) {
-                            const uint32_t at = (uint32_t)from + 16 * h;
-                            uint32_t blk = __umulhi(at, L.block_recip);
-                            if (at - blk * (uint32_t)a.p.block_size >= (uint32_t)a.p.block_size) ++blk;
-                            const int page = table[blk];
-                            sh.slot[h] = page * a.p.block_size + (int)(at - blk * a.p.block_size);
-                            if (page < 0 || page >= a.p.num_blocks) {
-                                bits |= kErrPage;
-                                o = 0;                 // (what was computed of the bad page is replaced)
-                                for (int r = first; r < last; ++r) reinterpret_cast<uint16_t*>(mask)[r * 2 * L.words + h] = 0;
                             }
                         }
-                        if (!o) sh.slot[h] = -1;
-                        reinterpret_cast<uint16_t*>(sh.any)[h] = (uint16_t)o;
+                    } else {
+                        for (int r = first; r < last; ++r)
+                            for (int e = tid; e < k; e += kThreads) {
+                                uint32_t* left = rest + r * rest_words + (e >> 5);
+                                const uint32_t mine = 1u << (e & 31);
+                                const int32_t j = a.idx[(r0 + r) * k + e];
+                                const uint32_t at = (uint32_t)j - (uint32_t)from, bit = 1u << (at & 31);
+                                if (j < 0 || at >= width || (pass > 0 && !(*left & mine))) continue;
+                                if (atomicOr(mask + r * words + (at >> 5), bit) & bit) {
+                                    if (pass == 0) atomicOr(left, mine);
+                                    sh.dup = 1;
+                                } else if (pass > 0) {
+                                    atomicAnd(left, ~mine);
+                                }
+                            }
                     }
+                    entries = __reduce_add_sync(0xffffffffu, entries);
+                    if (lane == 0 && entries) atomicAdd(&sh.entries, entries);
+                    __syncthreads();
+                    // what some row lists; positions on bad pages leave the masks (16 positions share a page)
+                    for (int w = tid; w < words; w += kThreads) {
+                        uint32_t o = 0;
+                        for (int r = first; r < last; ++r) {
+                            const uint32_t x = mask[r * words + w];
+                            o |= x;
+                            set += __popc(x);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            int slot = -1;
+                            if (o >> (16 * h) & 0xFFFFu) {
+                                const uint32_t at = (uint32_t)from + 32 * w + 16 * h, bs = (uint32_t)a.p.block_size;
+                                uint32_t blk = __umulhi(at, L.block_recip);
+                                if (at - blk * bs >= bs) ++blk;
+                                const int page = table[blk];
+                                if (page < 0 || page >= a.p.num_blocks) {
+                                    bits |= kErrPage;
+                                    for (int r = first; r < last; ++r) reinterpret_cast<uint16_t*>(mask)[2 * (r * words + w) + h] = 0;
+                                } else {
+                                    slot = page * a.p.block_size + (int)(at - blk * bs);
+                                }
+                            }
+                            sh.slot[2 * w + h] = slot;
+                        }
+                    }
+                    set = __reduce_add_sync(0xffffffffu, set);
+                    if (lane == 0 && set) atomicAdd(&sh.bits, set);
                     if (bits && a.err) atomicOr(a.err, bits);
                     __syncthreads();
+                    if (!exact && sh.entries != sh.bits) {             // an entry more than bits: again, one by one
+                        exact = true;
+                        words = L.exact_words;
+                        continue;
+                    }
                     if (warp == 0) {
                         int n = 0;
-                        for (int t0 = 0; t0 < L.words / 4; t0 += 32) {
+                        for (int t0 = 0; t0 < words / 2; t0 += 32) {
                             const int t = t0 + lane;
-                            const uint4 w = t < L.words / 4 ? reinterpret_cast<const uint4*>(sh.any)[t] : make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t live = __ballot_sync(0xffffffffu, (w.x | w.y | w.z | w.w) != 0);
-                            if (live >> lane & 1) sh.list[n + __popc(live & ((1u << lane) - 1))] = (uint16_t)t;
+                            bool some = false;
+                            if (t < words / 2) {
+                                const int4 x = *reinterpret_cast<const int4*>(sh.slot + 4 * t);
+                                some = (x.x & x.y & x.z & x.w) >= 0;
+                            }
+                            const uint32_t live = __ballot_sync(0xffffffffu, some);
+                            if (some) sh.list[n + __popc(live & ((1u << lane) - 1))] = (uint8_t)t;
                             n += __popc(live);
                         }
                         if (lane == 0) sh.tiles = n;
                     }
+                    break;
                 }
                 __syncthreads();
                 const int n = (int)sh.tiles;
                 if (warp < kSoftWarps) {
                     // ------------------------------------------------------------ softmax
-                    // thread: a row, half of the tile's keys, with a maximum, a sum and an accumulator for that half
-                    const int half = warp >> 2, row = tid & 127, r = row / group;
-                    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-                    const float f = sh.factor[row];
+                    const int r = tid / group;
+                    const uint32_t lanes = tmem + ((uint32_t)warp << 21);
+                    const float f = sh.factor[tid];
                     const bool mine = r >= first && r < last;
-                    const uint32_t* row_mask = mask + (mine ? r : 0) * L.words + 2 * half;
+                    const uint32_t* row_mask = mask + (mine ? r : 0) * words;
                     for (int i = 0; i < n; ++i) {
-                        const uint32_t t = done + i, buf = t & 1, cols = lanes + kColS + 128 * buf + 64 * half;
-                        uint2 w = *reinterpret_cast<const uint2*>(row_mask + 4 * sh.list[i]);
+                        const uint32_t t = done + i, buf = t & 1, cols = lanes + kColS + kTile * buf;
+                        uint2 w = *reinterpret_cast<const uint2*>(row_mask + 2 * sh.list[i]);
                         if (!mine) w = make_uint2(0u, 0u);
                         if (!wait_bounded(&sh.sfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
                         ptx::tc_fence_after();
@@ -354,11 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
                                 uint32_t o[32];
-                                QLI_TMEM_LD_X32(lanes + kColO + 128 * half + 32 * q, o);
+                                QLI_TMEM_LD_X32(lanes + kColO + 32 * q, o);
                                 wait_loaded(o);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-                                QLI_TMEM_ST_X32(lanes + kColO + 128 * half + 32 * q, o);
+                                QLI_TMEM_ST_X32(lanes + kColO + 32 * q, o);
                             }
                         }
                         if (!ok) break;
@@ -368,13 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&sh.pfull[buf]);
                     }
-                } else if (warp < kSoftWarps + 4) {
+                } else if (warp < kValueWarp) {
                     // ------------------------------------------------------------ converters of the keys
                     // a lane takes a quarter of four positions, eight neighbouring lanes eight positions: their
                     // loads (144 bytes apart) and stores (swizzled rows) meet all banks once
-                    const int row = 32 * (warp - kSoftWarps) + (lane & 7), quarter = lane >> 3;
+                    const int row = 32 * (warp - kKeyWarp) + (lane & 7), quarter = lane >> 3;
                     const bool stall = a.p.test_stall == 1;        // test switch: no tile is handed on, the waits run out
-                    const uint32_t off0 = kSmemK + operand_at(row, 4 * quarter);
+                    const uint32_t off0 = kSmemK + operand_at(row, 4 * quarter, kAtomK);
                     for (int i = 0; i < n; ++i) {
                         const uint32_t t = done + i, buf = t & 1;
                         const uint8_t* src = smem + kSmemRaw + buf * kRaw + row * kUnit;
@@ -409,11 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // ------------------------------------------------------------ converters of the values
                     // a lane takes one block of 16 elements of eight positions, in odd blocks the elements in the
                     // order 4 5 6 7 0 1 2 3, so that the stores of eight neighbouring lanes meet all banks once
-                    const int ct = tid & 127, vg = (ct & 3) + 4 * (ct >> 5), vb = ct >> 2 & 7;
+                    const int vg = (lane & 3) + 4 * (warp - kValueWarp), vb = lane >> 2;
                     const bool stall = a.p.test_stall == 1;
                     const uint32_t turn = vb & 1 ? 0x1032 : 0x3210;
                     // operand_at of its first element; of element e: 128 e further, and the column with e flipped
-                    const uint32_t off0 = operand_at(16 * vb + 4 * (vb & 1), vg);
+                    const uint32_t off0 = operand_at(16 * vb + 4 * (vb & 1), vg, kAtomV);
                     for (int i = 0; i < n; ++i) {
                         const uint32_t t = done + i, buf = t & 1;
                         const uint8_t* src = smem + kSmemRaw + buf * kRaw + 8 * vg * kUnit + kD / 2;
@@ -434,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             g[e] = pair_scale<E2M1>(h);
                         }
                         if (t >= 2 && !wait_bounded(&sh.vfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
-                        uint8_t* dst = smem + kSmemV + buf * kOperand;
+                        uint8_t* dst = smem + kSmemV + buf * kAtomV;
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             uint32_t o[4][8];
@@ -456,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // ------------------------------------------------------------ copies, 16 positions each
                     for (int i = 0; i < n; ++i) {
                         const uint32_t t = done + i, buf = t & 1;
-                        const int32_t slot = lane < 8 ? sh.slot[8 * sh.list[i] + lane] : -1;
+                        const int32_t slot = lane < 4 ? sh.slot[4 * sh.list[i] + lane] : -1;
                         const uint32_t live = __popc(__ballot_sync(0xffffffffu, slot >= 0));
                         if (t >= 2 && !wait_bounded(&sh.rawfree[buf], ((t >> 1) - 1) & 1, &sh.abort, a.err)) break;
                         if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.rawfull[buf], live * 16 * kUnit);
@@ -471,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
                     // ------------------------------------------------------------ products
-                    const uint32_t idesc = ptx::idesc_f16_f32(kM, kTileKeys2);
+                    const uint32_t idesc_s = ptx::idesc_f16_f32(kM, kTile), idesc_o = ptx::idesc_f16_f32(kM, kD);
                     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                     const uint64_t qd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(qs));
                     const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem + kSmemK));
@@ -487,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (ptx::elect_one()) {
 #pragma unroll
                                 for (int kk = 0; kk < kD / 16; ++kk) {
-                                    const uint64_t step = (uint64_t)(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
-                                    ptx::mma_f16_ss(tm + kColS + 128 * buf, qd + step, kd + step, idesc, kk > 0);
+                                    ptx::mma_f16_ss(tm + kColS + kTile * buf, qd + (((kk >> 2) * kAtomQ + (kk & 3) * 32) >> 4),
+                                                    kd + (((kk >> 2) * kAtomK + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
                                 }
                                 ptx::mma_commit(&sh.sfull[buf]);
                             }
@@ -501,16 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  wait_bounded(&sh.pfull[buf], (t >> 1) & 1, &sh.abort, a.err);
                             if (!ok) break;
                             ptx::tc_fence_after();
-                            const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem + kSmemV + buf * kOperand));
+                            const uint64_t vd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem + kSmemV + buf * kAtomV));
                             const bool add = !(fresh && i == 1);
                             if (ptx::elect_one()) {
 #pragma unroll
-                                for (int kk = 0; kk < kTileKeys2 / 16; ++kk) {
-                                    const uint64_t step = (uint64_t)(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
-                                    // the halves of the keys have accumulators of their own
-                                    ptx::mma_f16_ts(tm + kColO + 128 * (kk >> 2), tm + kColS + 128 * buf + 64 * (kk >> 2) + 8 * (kk & 3),
-                                                    vd + step, idesc, add || (kk & 3) > 0);
-                                }
+                                for (int kk = 0; kk < kTile / 16; ++kk)
+                                    ptx::mma_f16_ts(tm + kColO, tm + kColS + kTile * buf + 8 * kk, vd + (kk * 32 >> 4), idesc_o, add || kk > 0);
                                 ptx::mma_commit(&sh.vfree[buf]);
                                 ptx::mma_commit(&sh.pvdone);
                             }
@@ -526,61 +550,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncthreads();
                 ptx::tc_fence_after();
                 if (sh.abort) break;
-                standing = pass == 0 && sh.dup == 0 && first == 0 && last == nrows && limit <= window;
+                standing = !exact && first == 0 && last == nrows && limit <= 32 * words;
                 if (sh.dup) {
                     ++pass;
                     continue;
                 }
-                from += window;
+                from += 32 * words;
                 pass = 0;
+                exact = false;
                 if (from >= limit) break;
             }
             first = last;
         }
         // ---- output of this head
         const bool failed = sh.abort != 0;
-        if (warp < kSoftWarps) sh.joined[warp >> 2][tid & 127] = make_float2(m_run, l_run);
-        __syncthreads();
         if (warp < kSoftWarps) {
-            // the two halves of the keys joined; thread: a row, half of the elements
-            const int half = warp >> 2, row = tid & 127, r = row / group, h = kvh * group + row - r * group;
-            const float2 x = sh.joined[0][row], y = sh.joined[1][row];
-            const float top = fmaxf(x.x, y.x), gx = ptx::ex2(x.x - top), gy = ptx::ex2(y.x - top);
-            const float sum = failed ? __int_as_float(0x7FC00000) : fmaf(gx, x.y, gy * y.y);
-            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum, ax = gx * inv, ay = gy * inv;
+            const int r = tid / group, h = kvh * group + tid - r * group;
+            const float sum = failed ? __int_as_float(0x7FC00000) : l_run;
+            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
             const bool live = r < nrows;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + ((r0 + (live ? r : 0)) * a.heads_q + h) * kD + 64 * half);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + ((r0 + (live ? r : 0)) * a.heads_q + h) * kD);
 #pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t from_o = tmem + ((uint32_t)(warp & 3) << 21) + kColO + 64 * half + 32 * q;
-                uint32_t u[32], v[32];
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
                 if (fresh) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = v[e] = 0;
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
                 } else {
-                    QLI_TMEM_LD_X32(from_o, u);
-                    QLI_TMEM_LD_X32(from_o + 128, v);
-                    wait_loaded(u);
-                    wait_loaded(v);
+                    QLI_TMEM_LD_X32(tmem + ((uint32_t)warp << 21) + kColO + 32 * q, o);
+                    wait_loaded(o);
                 }
                 if (live) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const int at = 8 * e + 2 * z;
-                            w[z] = sum == 0.0f ? 0u
-                                               : float2_to_act2<F16>(fmaf(__uint_as_float(u[at]), ax, __uint_as_float(v[at]) * ay),
-                                                                     fmaf(__uint_as_float(u[at + 1]), ax, __uint_as_float(v[at + 1]) * ay));
-                        }
+                        for (int z = 0; z < 4; ++z)
+                            w[z] = sum == 0.0f ? 0u : float2_to_act2<F16>(__uint_as_float(o[8 * e + 2 * z]) * inv,
+                                                                         __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
                         dst[4 * q + e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 __syncwarp();                          // the loads above take the whole warp
             }
-            if (live && a.lse && half == 0)
-                a.lse[(r0 + r) * a.heads_q + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            if (live && a.lse)
+                a.lse[(r0 + r) * a.heads_q + h] = sum == 0.0f ? -INFINITY : (m_run + log2f(sum)) * 0.6931471805599453f;
         }
         ptx::tc_fence_before();
         __syncthreads();
@@ -601,7 +615,7 @@ cudaError_t launch_rows(const AttentionArgs& a, const RowsLayout& L, int64_t gri
 {
     auto kernel = attention_rows_kernel<F16, E2M1>;
     constexpr int kSmem = kSmemMask + kMaskBytes + (int)sizeof(Shared);
-    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kSmem <= 113 * 1024, "shared memory of half an SM");
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -645,8 +659,10 @@ cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, i
     const int group = a.heads_q / a.heads_kv;
     RowsLayout L;
     L.rows = std::min(kMaxRows, kM / group);
-    const int64_t words = (positions(a) + 127) / 128 * 4;
-    L.words = (int32_t)std::max<int64_t>(4, std::min<int64_t>(words, kMaskBytes / 4 / L.rows & ~3));
+    const int64_t words = std::max<int64_t>(1, (positions(a) + kTile - 1) / kTile) * 2;
+    const int space = kMaskBytes / 4 / L.rows, rest = (a.p.sparse_count + 31) / 32;
+    L.words = (int32_t)std::min<int64_t>(words, std::min(kMaxWords, space) & ~1);
+    L.exact_words = std::min(L.words, (space - rest) & ~1);
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
     const int64_t blocks = ((int64_t)a.p.rows + L.rows - 1) / L.rows;
     L.slices = 1;
