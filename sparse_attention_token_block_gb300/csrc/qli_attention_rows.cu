@@ -52,7 +52,7 @@ constexpr int kUnit = kv_unit_bytes(kD), kRaw = kTile * kUnit;             // a 
 // shared memory: operands (rows of 64 fp16 in the 128-byte swizzle, 128 bytes each), the copied entries, masks
 constexpr int kAtomQ = kM * 128, kAtomK = kTile * 128, kAtomV = kD * 128;
 constexpr int kSmemK = 2 * kAtomQ, kSmemV = kSmemK + 2 * kAtomK, kSmemRaw = kSmemV + 2 * kAtomV, kSmemMask = kSmemRaw + 2 * kRaw;
-constexpr int kMaxRows = 32, kMinRows = 4;             // of a block (at most 32 query heads per KV head)
+constexpr int kMaxRows = 32;                           // of a block
 constexpr int kMaskBytes = 12 * 1024;
 constexpr int kMaxWords = 128;                         // of a row's mask
 constexpr uint32_t kColS = 0, kColO = 2 * kTile, kTmemCols = 256;
@@ -337,34 +337,38 @@ __global__ void __launch_bounds__(kThreads, 2)
                         bool ok = true;
                         uint32_t p[32];
                         while (true) {
-                            float top = -INFINITY, sum = 0.0f;
+                            float best[2] = {-INFINITY, -INFINITY};
+                            uint64_t part[2] = {0, 0};
+                            const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m_run, -m_run);
+                            uint32_t s[2][32];
+                            QLI_TMEM_LD_X32(cols, s[0]);
+                            QLI_TMEM_LD_X32(cols + 32, s[1]);
+                            wait_loaded(s[0]);
+                            wait_loaded(s[1]);
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                uint32_t s[32];
-                                QLI_TMEM_LD_X32(cols + 32 * q, s);
-                                wait_loaded(s);
                                 const uint32_t bits = q ? w.y : w.x;
                                 if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
-                                        s[e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[e]) : -INFINITY);
+                                        s[q][e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[q][e]) : -INFINITY);
                                 }
-                                float best[2] = {-INFINITY, -INFINITY}, part[2] = {0.0f, 0.0f};
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
+                                    const float x = __uint_as_float(s[q][e]), y = __uint_as_float(s[q][e + 1]);
                                     best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
-                                    const float px = ptx::ex2(fmaf(x, f, -m_run)), py = ptx::ex2(fmaf(y, f, -m_run));
-                                    part[e >> 1 & 1] += px + py;
+                                    float zx, zy;
+                                    ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
+                                    const float px = ptx::ex2(zx), py = ptx::ex2(zy);
+                                    part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
                                     // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
                                     p[16 * q + e / 2] = float2_to_act2<true>(px, py);
                                 }
-                                // (this half is done with before the next is loaded: both at once spill)
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(p[16 * q + e]));
-                                top = fmaxf(top, fmaxf(best[0], best[1]));
-                                sum += part[0] + part[1];
                             }
+                            float sum, other;
+                            ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
+                            sum += other;
+                            const float top = fmaxf(best[0], best[1]);
                             const float up = top * f;
                             const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
                             if (!__any_sync(0xffffffffu, over)) {
@@ -649,9 +653,10 @@ int64_t positions(const AttentionArgs& a)
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
 {
     const int group = a.heads_q / a.heads_kv;
-    if (head_dim != kD || group * kMinRows > kM || !a.kv) return false;
+    if (head_dim != kD || group > kM || !a.kv) return false;
     const int64_t rows = a.p.rows, per = std::min(kMaxRows, kM / group), blocks = (rows + per - 1) / per;
-    return rows >= per * a.p.batch && blocks * a.heads_kv >= sms && positions(a) <= 4 * (int64_t)a.p.sparse_count;
+    return rows >= 4 * per * a.p.batch && blocks * a.heads_kv >= sms && a.p.sparse_count >= 512 &&
+           positions(a) <= 4 * (int64_t)a.p.sparse_count;
 }
 
 cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st)
