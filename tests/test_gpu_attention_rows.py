@@ -1,5 +1,5 @@
 """Sparse attention of many neighbouring rows, whose lists become masks over shared tiles of keys
-(calls of at least as many blocks of rows as fill the GPU), against the 64-bit oracle (needs a GB300)."""
+(calls of lists of at least 512, at least as many blocks of rows as fill the GPU), against the 64-bit oracle (needs a GB300)."""
 import os
 import subprocess
 import sys
@@ -21,15 +21,27 @@ def _ragged(q_lens, k_lens, **kw):
     return cache_case(layout_q="TND", q_lens=q_lens, seq_lens_k=k_lens, **kw)
 
 
+def _wide(case, idx, seed=0, k=512):
+    """The lists spread over k places of which the others are -1."""
+    if idx.shape[1] >= k:
+        return idx
+    place = np.sort(np.random.default_rng(seed).permutation(k)[:idx.shape[1]])
+    wide = np.full((idx.shape[0], k), -1, np.int32)
+    wide[:, place] = idx
+    case.sparse_count = k
+    return wide
+
+
 # query heads, KV heads, rows that give at least 152 blocks of rows and KV heads
 @pytest.mark.parametrize("hq,hkv,q_lens", [(64, 8, [300, 17, 5]), (16, 16, [200, 130]), (40, 8, [333, 150]), (7, 1, [2738]),
-                                           (32, 1, [640]), (10, 5, [993, 1]), (96, 32, [95, 66])])
+                                           (32, 1, [640]), (10, 5, [993, 1]), (96, 32, [150, 118]),
+                                           (33, 1, [470]), (64, 1, [310]), (128, 1, [160])])
 @pytest.mark.parametrize("e2m1,f16", [(True, False), (False, True)])
 def test_head_layouts(Q, hq, hkv, q_lens, e2m1, f16):
     rows = sum(q_lens)
     case = _ragged(q_lens, [257, 130, 70][:len(q_lens)], block_size=48, sparse_count=90, seed=hq)
     pool = cache(case, hkv, 128, e2m1, seed=1)
-    idx = W.random_indices(case, seed=2)
+    idx = _wide(case, W.random_indices(case, seed=2))
     q = _query(rows, hq, 128, f16, 3)
     _check(case, _run(Q, case, q, idx, pool, hkv, e2m1, f16, q_pad=1), q, idx, pool, hkv, e2m1, f16)
 
@@ -38,10 +50,10 @@ def test_head_layouts(Q, hq, hkv, q_lens, e2m1, f16):
 def test_list_lengths(Q, k, keys):
     """One position, lists of all positions, an odd key past a tile, many tiles."""
     case = _ragged([330], [keys], block_size=16, sparse_count=k, seed=k)
-    pool = cache(case, 8, 128, True, seed=1)
-    idx = W.random_indices(case, seed=2, frac_pad=0.0)
+    pool = cache(case, 16, 128, True, seed=1)
+    idx = _wide(case, W.random_indices(case, seed=2, frac_pad=0.0))
     q = _query(330, 32, 128, False, 3)
-    _check(case, _run(Q, case, q, idx, pool, 8, True, False), q, idx, pool, 8, True, False)
+    _check(case, _run(Q, case, q, idx, pool, 16, True, False), q, idx, pool, 16, True, False)
 
 
 @pytest.mark.parametrize("with_k", [True, False])
@@ -52,7 +64,7 @@ def test_compressed_factors_and_page_gaps(Q, with_k):
     eb = pool.shape[2]
     gap = np.random.default_rng(4).integers(0, 256, (case.num_blocks, 32 * eb + 32), dtype=np.uint8)
     gap[:, :32 * eb] = pool.reshape(case.num_blocks, -1)
-    idx = W.random_indices(case, seed=2)
+    idx = _wide(case, W.random_indices(case, seed=2))
     q = _query(554, 64, 128, False, 3)
     got = _run(Q, case, q, idx, gap, hkv, True, False, 0.11, factors, 32 * eb + 32, with_k=with_k)
     _check(case, got, q, idx, pool, hkv, True, False, 0.11, factors, with_k=with_k)
@@ -72,6 +84,7 @@ def test_padding_duplicates_and_empty_rows(Q):
     idx[32:48] = -1                                          # a block of nothing
     idx[48:64, 1:] = -1                                      # one entry a row
     idx[64:80] = np.sort(idx[64:80], axis=1)
+    idx = _wide(case, idx)
     q = _query(320, 64, 128, False, 3)
     _check(case, _run(Q, case, q, idx, pool, 8, True, False), q, idx, pool, 8, True, False)
 
@@ -83,8 +96,8 @@ def test_unlisted_bytes_and_other_rows_nan_are_never_used(Q):
     pool = cache(case, 8, 128, True, seed=1)
     idx = W.random_indices(case, seed=2)
     idx[idx == 150] = -1                                     # listed by one row only
-    idx[:, 7][idx[:, 7] >= 120] = 5
     idx[21, 0] = 150
+    idx = _wide(case, idx)
     used = np.zeros(pool.shape[:2], bool)
     j = idx[idx >= 0]
     used[case.block_table[0, j // 32], j % 32] = True
@@ -131,14 +144,14 @@ def test_query_magnitudes(Q):
     q = _query(304, 64, 128, False, 3)
     q *= np.resize(np.array([1, 1e-6, 1e-30, 1e3, 0, 1e-3, 2.0 ** -100], np.float32), (304, 64))[..., None]
     q = (q.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)
-    idx = W.random_indices(case, seed=2)
+    idx = _wide(case, W.random_indices(case, seed=2))
     _check(case, _run(Q, case, q, idx, pool, 8, False, False, 0.05), q, idx, pool, 8, False, False, 0.05)
 
 
 def test_invalid_indices_and_pages(Q):
     case = _ragged([300, 20], [100, 40], block_size=32, sparse_count=28, seed=5)
     pool = cache(case, 8, 128, True, seed=6)
-    good = W.random_indices(case, seed=2)
+    good = _wide(case, W.random_indices(case, seed=2))
     q = _query(320, 64, 128, False, 3)
     for row, bad in ((7, 100), (7, -5), (319, 40), (0, 2147483647), (5, -2147483648)):
         idx = good.copy()
@@ -156,6 +169,7 @@ def test_rows_past_the_last_prefix_sum(Q):
     idx = np.full((310, 20), -1, np.int32)
     idx[:, 0], idx[:, 9] = 1, 60
     idx[300] = -1
+    idx = _wide(case, idx)
     q = _query(310, 64, 128, False, 3)
     _check(case, _run(Q, case, q, idx, pool, 8, True, False), q, idx, pool, 8, True, False)
 
@@ -165,8 +179,8 @@ def test_a_length_above_its_bound(Q):
     filled once per range of positions; some positions are listed twice."""
     case = _ragged([304], [600], block_size=64, sparse_count=150, seed=4)
     pool = cache(case, 8, 128, True, seed=1)
-    idx = W.random_indices(case, seed=2)
-    idx[9, 10:20] = idx[9, :10]
+    idx = _wide(case, W.random_indices(case, seed=2))
+    idx[9, 200:400] = idx[9, :200]
     q = _query(304, 64, 128, False, 3)
     kw = dict(W.problem_kwargs(case))
     p = Q.make_problem(**dict(kw, max_seqlen_k=200))
@@ -187,7 +201,7 @@ import sparse_attention_token_block_gb300 as Q
 Q.use_testing_library()
 Q.lib.qli_testing_set_stall(%d)
 rows = 304
-p = Q.make_problem(batch=1, max_q_tokens=rows, num_blocks=4, block_size=64, max_blocks_per_seq=4, sparse_count=64,
+p = Q.make_problem(batch=1, max_q_tokens=rows, num_blocks=4, block_size=64, max_blocks_per_seq=4, sparse_count=512,
                    sparse_mode=0, cmp_ratio=1, max_seqlen_q=rows, max_seqlen_k=256)
 a = Q.make_attention(num_heads_q=64, num_heads_kv=8, head_dim=128)
 dev = dict(device="cuda")
@@ -195,7 +209,8 @@ pool = torch.zeros(4, 64, Q.kv_entry_bytes(a), dtype=torch.uint8, **dev)
 q = torch.ones(rows, 64, 128, dtype=torch.bfloat16, **dev)
 out = torch.ones_like(q)
 table = torch.arange(4, dtype=torch.int32, **dev)[None]
-idx = torch.arange(64, dtype=torch.int32, **dev).repeat(rows, 1)
+idx = torch.full((rows, 512), -1, dtype=torch.int32, **dev)
+idx[:, :64] = torch.arange(64, dtype=torch.int32, **dev)
 lens = torch.full((1,), 256, dtype=torch.int32, **dev)
 ws = torch.zeros(64, dtype=torch.int32, **dev)
 Q.check(Q.sparse_attention(p, a, q, None, lens, table, idx, pool, out, None, ws), "sparse_attention")
