@@ -56,6 +56,7 @@ constexpr int kMaxRows = 32;                           // of a block
 constexpr int kMaskBytes = 12 * 1024;
 constexpr int kMaxWords = 128;                         // of a row's mask
 constexpr uint32_t kColS = 0, kColO = 2 * kTile, kTmemCols = 256;
+constexpr uint32_t kNone = 0xffffffffu;
 constexpr float kRescale = 8.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull;
 
@@ -70,7 +71,7 @@ struct RowsLayout {
 
 struct Shared {
     uint64_t rawfull[2], rawfree[2], kfull, vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
-    uint32_t tmem, abort, dup, tiles, entries, bits;
+    uint32_t tmem, abort, dup, tiles, entries, bits, next;
     int32_t batch[kMaxRows];
     float factor[kM];
     alignas(16) int32_t slot[2 * kMaxWords];                       // slot of the pool of every 16th position, -1: no row lists any of the 16
@@ -223,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int i = tid; i < L.rows * words; i += kThreads) mask[i] = 0;
                     if (exact && pass == 0)
                         for (int i = tid; i < L.rows * rest_words; i += kThreads) rest[i] = 0;
-                    if (tid == 0) sh.dup = sh.entries = sh.bits = 0;
+                    if (tid == 0) sh.dup = sh.entries = sh.bits = 0, sh.next = kNone;
                     __syncthreads();
-                    uint32_t bits = 0, entries = 0, set = 0;
+                    uint32_t bits = 0, entries = 0, set = 0, next = kNone;     // next: first valid index past the masks
                     const uint32_t width = (uint32_t)max((int64_t)0, min((int64_t)(32 * words), limit - from));
                     if (!exact) {
                         // a byte per position in the operands' space, then the bytes to bits (with an atomic OR
@@ -253,8 +254,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                                         if (j[r] >= 0 && at < width) {
                                             m[r * line + at] = 1;
                                             ++entries;
-                                        } else if (j[r] != -1 && (j[r] < 0 || j[r] >= limit)) {
-                                            bits |= kErrLength;
+                                        } else if (j[r] != -1) {
+                                            if (j[r] < 0 || j[r] >= limit) bits |= kErrLength;
+                                            else if (j[r] >= from) next = min(next, (uint32_t)j[r]);
                                         }
                                     }
                                 }
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 const uint32_t mine = 1u << (e & 31);
                                 const int32_t j = a.idx[(r0 + r) * k + e];
                                 const uint32_t at = (uint32_t)j - (uint32_t)from, bit = 1u << (at & 31);
+                                if (j >= from && j < limit && at >= width) next = min(next, (uint32_t)j);
                                 if (j < 0 || at >= width || (pass > 0 && !(*left & mine))) continue;
                                 if (atomicOr(mask + r * words + (at >> 5), bit) & bit) {
                                     if (pass == 0) atomicOr(left, mine);
@@ -286,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 }
                             }
                     }
+                    next = __reduce_min_sync(0xffffffffu, next);
+                    if (lane == 0 && next != kNone) atomicMin(&sh.next, next);
                     entries = __reduce_add_sync(0xffffffffu, entries);
                     if (lane == 0 && entries) atomicAdd(&sh.entries, entries);
                     __syncthreads();
@@ -576,15 +581,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncthreads();
                 ptx::tc_fence_after();
                 if (sh.abort) break;
-                standing = !exact && first == 0 && last == nrows && limit <= 32 * words;
+                standing = !exact && first == 0 && last == nrows && sh.next == kNone;
                 if (sh.dup) {
                     ++pass;
                     continue;
                 }
-                from += 32 * words;
+                if (sh.next == kNone) break;
+                from = sh.next & ~(uint32_t)(kTile - 1);
                 pass = 0;
                 exact = false;
-                if (from >= limit) break;
             }
             first = last;
         }
