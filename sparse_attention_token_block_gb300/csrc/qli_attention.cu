@@ -36,8 +36,9 @@
 // off; giving the keys' to the integer pipe adds 6 %: both pipes are near full.)  From HBM (a decode),
 // the gathers' latency and the start: list, entries, join.  Measured on a GB300, 64 query heads over 8 KV
 // heads of 128, E2M1, 2048 entries a row: 1 row 7.1 us, 8 rows 11.0, 32 rows (8k-32k keys) 21.4 (3.6 TB/s),
-// 64 rows 36.4 (4.2), 128 rows 65.1 (4.7); prefill of 1024 + 2048 + 4096 rows 1.76 ms (166 TFLOP/s); int4
-// 27.1 us at 32 rows: its codes take seven integer operations per eight, E2M1's four.
+// 64 rows 36.4 (4.2), 128 rows 65.1 (4.7); prefill of 1024 + 2048 + 4096 rows 1.76 ms (166 TFLOP/s; such calls
+// go to qli_attention_rows.cu, 0.62 ms); int4 27.1 us at 32 rows: its codes take seven integer operations per
+// eight, E2M1's four.
 //
 // Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over
 // the cluster) and are joined in a fixed order.  Every wait for a copy is bounded (0.2 s): on expiry the

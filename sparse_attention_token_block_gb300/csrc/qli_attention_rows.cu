@@ -29,6 +29,15 @@
 // scales (the cache write makes none) is taken as NaN keys, which the mask hides from the other rows, and
 // finite values.
 //
+// What bounds it: latency, not a pipe.  A tile takes a CTA about 4000 cycles from role to role (two CTAs:
+// 2000 an SM) of which its products take 512; the SM issues in 46 % of its cycles.  Without the arithmetic
+// of softmax and decoding at all an earlier form (one CTA, tiles of 128) still took two thirds of its time.
+// Building the masks is an eighth, staging the queries a twentieth.  Measured on a GB300, 64 query heads
+// over 8 KV heads, E2M1, causal: 1024 + 2048 + 4096 rows of up to 2048 entries 617 us (one row at a time
+// 1764), 1024 + 2048 rows of up to 1024 192 us (434), the same for one KV head 199 us (469), for groups of
+// four 137 us (432), int4 206 us (577); one CTA an SM takes 816 us for the first, the CTAs in the order of
+// the rows 737, tiles whose logits are loaded in two parts 761.
+//
 // Every wait is bounded (0.2 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t done = 0;                                 // tiles walked so far: every role counts the same
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
-        // ---- the head's queries as an operand: row m is query head m % group of row m / group
+        // ---- the head's queries as an operand (in fp16, times a power of two of their largest magnitude): row m is query head m % group of row m / group
         constexpr int kPerWarp = 16;
         if (warp < kM / kPerWarp) {
             // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
@@ -677,6 +686,12 @@ int64_t positions(const AttentionArgs& a)
 
 }  // namespace
 
+// A tile costs the same whatever the rows list of it, so the lists have to be a large part of the positions:
+// 4096 positions, lists of 1024: 435 us against 681 one row at a time; of 500: 415 against 382.  A CTA has
+// 10-20 us of latency around its tiles, so they have to be several (lists of 256, 1024 rows: 57 and 57 us; of
+// 512: 60 and 92; 32 sequences of 64 rows and positions: 77 and 47), the blocks have to fill the GPU (256 rows:
+// 18.5 and 16.2; 305 rows: 22.2 and 26.8) and mostly hold one sequence's rows (64 sequences of 17 rows: 56 and
+// 25; 8 of 64 rows with 2048 positions: 68 and 114).
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
 {
     const int group = a.heads_q / a.heads_kv;
@@ -697,6 +712,8 @@ cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, i
     L.exact_words = std::min(L.words, (space - rest) & ~1);
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
     const int64_t blocks = ((int64_t)a.p.rows + L.rows - 1) / L.rows;
+    // KV heads per CTA: more share a list's mask, fewer balance better; four waves (prefill of 7168 rows, eight
+    // heads: two 694 us, four 620, eight 624; of 1024 + 2048 rows: 222, 194, 215)
     L.slices = 1;
     while (L.slices < a.heads_kv && blocks * L.slices < 4 * (int64_t)sms) L.slices *= 2;
     L.heads = (a.heads_kv + L.slices - 1) / L.slices;
