@@ -193,6 +193,62 @@ def test_a_length_above_its_bound(Q):
     _check(case, (out.double().cpu().numpy(), lse.double().cpu().numpy(), 0), q, idx, pool, 8, True, False)
 
 
+def _make(Q, case, **kw):
+    return (Q.make_problem(**W.problem_kwargs(case)), Q.make_attention(num_heads_q=64, num_heads_kv=8, head_dim=128, **kw))
+
+
+def test_offsets_past_32_bits(Q):
+    """Entries on the last pages of a pool of over 4 GB."""
+    import torch
+    bs, nb, rows = 1024, 20, 304
+    page = bs * 1152 + (1 << 28)
+    case = _ragged([rows], [2 * bs], block_size=bs, sparse_count=512, seed=1)
+    case.num_blocks = nb
+    case.block_table = np.array([[nb - 1, nb - 2]], np.int32)
+    small = cache(case, 8, 128, True, seed=1)
+    pool = torch.zeros(nb * page, dtype=torch.uint8, device="cuda")
+    for pg in (nb - 1, nb - 2):
+        pool[pg * page:pg * page + bs * 1152] = _dev(small[pg].reshape(-1))
+    idx = W.random_indices(case, seed=2)
+    q = _query(rows, 64, 128, False, 3)
+    p, a = _make(Q, case, kv_stride=page)
+    out = torch.empty(rows, 64, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(rows, 64, device="cuda")
+    Q.check(Q.sparse_attention(p, a, _dev(q, False), _dev(case.seq_lens_q), _dev(case.seq_lens_k), _dev(case.block_table),
+                               _dev(idx), pool, out, lse), "sparse_attention")
+    _check(case, (out.double().cpu().numpy(), lse.double().cpu().numpy(), 0), q, idx, small, 8, True, False)
+
+
+def test_runs_on_its_stream_and_in_a_graph(Q):
+    """Captured on a stream of its own, twice in a row, and replayed on new queries, lists and contents."""
+    import torch
+    rows = 304
+    case = _ragged([rows], [300], block_size=16, sparse_count=512, seed=2)
+    p, a = _make(Q, case)
+    pool = torch.zeros(cache(case, 8, 128, True, seed=1).shape, dtype=torch.uint8, device="cuda")
+    q = torch.zeros(rows, 64, 128, dtype=torch.bfloat16, device="cuda")
+    idx = torch.full((rows, 512), -1, dtype=torch.int32, device="cuda")
+    out, out2 = torch.empty_like(q), torch.empty_like(q)
+    lse = torch.empty(rows, 64, device="cuda")
+    args = (_dev(case.seq_lens_q), _dev(case.seq_lens_k), _dev(case.block_table))
+    st = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        with torch.cuda.graph(g, stream=st):
+            Q.check(Q.sparse_attention(p, a, q, *args, idx, pool, out, lse), "sparse_attention")
+            Q.check(Q.sparse_attention(p, a, q, *args, idx, pool, out2), "sparse_attention")
+    for seed in (1, 2):
+        hp, hq, hi = cache(case, 8, 128, True, seed), _query(rows, 64, 128, False, seed), W.random_indices(case, seed)
+        pool.copy_(_dev(hp))
+        q.copy_(_dev(hq, False))
+        idx.copy_(_dev(hi))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), out2.view(torch.int16))
+        _check(case, (out.double().cpu().numpy(), lse.double().cpu().numpy(), 0), hq, hi, hp, 8, True, False)
+
+
 CHILD = r"""
 import sys
 sys.path.insert(0, %r)
