@@ -83,12 +83,12 @@ struct Shared {
     uint32_t tmem, abort, dup, tiles, entries, bits, next;
     int32_t batch[kMaxRows];
     float factor[kM];
-    alignas(16) int32_t slot[2 * kMaxWords];                       // slot of the pool of every 16th position, -1: no row lists any of the 16
+    alignas(16) int32_t slot[2 * kMaxWords];           // slot of the pool of every 16th position, -1: none of the 16 is listed
     uint8_t list[kMaxWords / 2];                       // tiles with an entry
 };
 
-// The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up.  (Inline: around
-// a call the registers that hold the next tile would go through local memory.)
+// The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up.  (Inline: a
+// call would send what the roles hold in registers through local memory.)
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
 {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t done = 0;                                 // tiles walked so far: every role counts the same
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
-        // ---- the head's queries as an operand (in fp16, times a power of two of their largest magnitude): row m is query head m % group of row m / group
+        // ---- the head's queries as an operand: row m is query head m % group of row m / group, in fp16, times a
+        // power of two of its largest magnitude
         constexpr int kPerWarp = 16;
         if (warp < kM / kPerWarp) {
             // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
