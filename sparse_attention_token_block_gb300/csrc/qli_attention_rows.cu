@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncthreads();
                 ptx::tc_fence_after();
                 if (sh.abort) break;
-                standing = !exact && first == 0 && last == nrows && sh.next == kNone;
+                standing = !exact && from == 0 && first == 0 && last == nrows && sh.next == kNone;
                 if (sh.dup) {
                     ++pass;
                     continue;
