@@ -20,10 +20,12 @@
 // Two CTAs share an SM (half its shared and tensor memory each): what a tile costs is mostly the way from
 // role to role, and one CTA's masks, queries and outputs overlap the other's products.
 //
-// A position that a row lists n times counts n times: where the lists of a block hold duplicates (as many
-// entries as mask bits, or not), the list positions that are left over when a mask is built go into the
-// masks of further rounds.  Further rounds also take the rows of a block that belong to another batch and
-// the positions past the masks' width.
+// A position that a row lists n times counts n times: where the lists of a block hold duplicates (more
+// entries than mask bits), the masks hold one binary digit of the counts a round, digit d's logits raised by
+// d (2^d p), so that a round is needed for each digit that occurs, at most twelve.  (2432 rows of 2048 entries,
+// 294 us: one row that names one position 2048 times 400 us, every row's second half position 0 651 us; a round
+// for each repetition took 138 ms for the former.)  Further rounds also take the rows of a block that belong to
+// another batch and the positions past the masks' width.
 //
 // A zero of P times a NaN would be a NaN, in rows that do not list the entry: an entry with a NaN among its
 // scales (the cache write makes none) is taken as NaN keys, which the mask hides from the other rows, and
@@ -72,7 +74,6 @@ constexpr uint64_t kWaitLimitNs = 200000000ull;
 struct RowsLayout {
     int32_t rows;          // rows of a block
     int32_t words;         // mask words per row (whole tiles)
-    int32_t exact_words;   // the same where the masks share their space with the list positions left over
     int32_t heads;         // KV heads per CTA
     int32_t slices;        // CTAs per block
     uint32_t block_recip;
@@ -80,7 +81,8 @@ struct RowsLayout {
 
 struct Shared {
     uint64_t rawfull[2], rawfree[2], kfull, vfull[2], sfull[2], pfull[2], vfree[2], pvdone;
-    uint32_t tmem, abort, dup, tiles, entries, bits, next;
+    uint32_t tmem, abort, tiles, entries, bits, next;
+    uint32_t digits, row_digits[kMaxRows];             // binary digits that occur among a range's counts, and each row's
     int32_t batch[kMaxRows];
     float factor[kM];
     alignas(16) int32_t slot[2 * kMaxWords];           // slot of the pool of every 16th position, -1: none of the 16 is listed
@@ -117,6 +119,43 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[32])
 __device__ __forceinline__ uint32_t operand_at(int r, int piece, int atom)
 {
     return (piece >> 3) * atom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+}
+
+// Masks of digit `digit` of how often each of `rows` lists names each position from + [0, width), and the
+// digits that occur at all (with digit 0).  The counts, 16 bits a position (a list has at most 2048), lie at
+// `space`; after digit 0 only the rows that have the digit are counted.  (A call keeps the plain masks' code
+// together: 2 % of a short prefill.)
+__device__ __noinline__ void count_rows(const int32_t* idx, int k, uint32_t from, uint32_t width, int words, int rows, int digit,
+                                        uint8_t* space, uint32_t* mask, uint32_t* row_digits, uint32_t* digits)
+{
+    const int tid = threadIdx.x, line = 32 * words;
+    uint32_t* count = reinterpret_cast<uint32_t*>(space);
+    for (int i = tid; i < rows * line / 8; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (digit == 0 && tid < rows) row_digits[tid] = 0;
+    __syncthreads();
+    for (int r = 0; r < rows; ++r, idx += k) {
+        if (digit > 0 && !(row_digits[r] >> digit & 1)) continue;
+        for (int e = tid; e < k; e += kThreads) {
+            const uint32_t at = (uint32_t)idx[e] - from;
+            if (idx[e] >= 0 && at < width) atomicAdd(count + ((r * line + at) >> 1), at & 1 ? 0x10000u : 1u);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * words; i += kThreads) {
+        uint32_t word = 0, some = 0;
+#pragma unroll 1
+        for (int z = 0; z < 16; ++z) {
+            const uint32_t c = count[16 * i + z];
+            word |= ((c >> digit & 1u) | (c >> (16 + digit) & 1u) << 1) << (2 * z);
+            some |= c;
+        }
+        mask[i] = word;
+        some = (some | some >> 16) & 0xFFFFu;
+        if (digit == 0 && some) {
+            atomicOr(row_digits + i / words, some);
+            atomicOr(digits, some);
+        }
+    }
 }
 
 template <bool F16, bool E2M1>
@@ -221,29 +260,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int64_t limit = b >= 0 ? index_limit(a.p, a.seq_lens_k, b) : 0;
             const int32_t* table = a.block_table + (int64_t)max(b, 0) * a.p.max_blocks_per_seq;
             int64_t from = 0;                          // first position of the masks
-            bool exact = false;                        // the lists hold duplicates
+            bool counted = false;                      // the lists hold duplicates: the masks hold digits of counts
+            const int words = L.words;
             // (a list of a batch without positions is still looked at: its indices are errors)
-            for (int pass = 0; b >= 0;) {
-                int words = exact ? L.exact_words : L.words;
+            for (int digit = 0; b >= 0;) {
                 while (!standing) {
                     // ---- masks of this round
-                    uint32_t* rest = mask + L.rows * L.exact_words;            // (exact) per row
-                    const int rest_words = (k + 31) >> 5;
                     __syncthreads();                   // (every thread has read what the last round left)
-                    if (exact)
-                        for (int i = tid; i < L.rows * words; i += kThreads) mask[i] = 0;
-                    if (exact && pass == 0)
-                        for (int i = tid; i < L.rows * rest_words; i += kThreads) rest[i] = 0;
-                    if (tid == 0) sh.dup = sh.entries = sh.bits = 0, sh.next = kNone;
+                    if (tid == 0) sh.entries = sh.bits = 0, sh.next = counted ? sh.next : kNone;
                     __syncthreads();
                     uint32_t bits = 0, entries = 0, set = 0, next = kNone;     // next: first valid index past the masks
                     const uint32_t width = (uint32_t)max((int64_t)0, min((int64_t)(32 * words), limit - from));
-                    if (!exact) {
+                    constexpr int kMapBytes = kSmemMask - kSmemK;
+                    const int line = 32 * words;
+                    if (!counted) {
                         // a byte per position in the operands' space, then the bytes to bits (with an atomic OR
                         // per entry into the masks a prefill takes 628 us instead of 620)
-                        constexpr int kAtOnce = 16, kMapBytes = kSmemMask - kSmemK;
+                        constexpr int kAtOnce = 16;
                         uint8_t* map = smem + kSmemK;
-                        const int line = 32 * words, fit = kMapBytes / line;
+                        const int fit = kMapBytes / line;
                         for (int ra = first; ra < last; ra += fit) {
                             const int rows = min(fit, last - ra);
                             if (ra > first) __syncthreads();
@@ -283,21 +318,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         ptx::fence_proxy_async_smem();         // before copies land in the same place
                     } else {
-                        for (int r = first; r < last; ++r)
-                            for (int e = tid; e < k; e += kThreads) {
-                                uint32_t* left = rest + r * rest_words + (e >> 5);
-                                const uint32_t mine = 1u << (e & 31);
-                                const int32_t j = a.idx[(r0 + r) * k + e];
-                                const uint32_t at = (uint32_t)j - (uint32_t)from, bit = 1u << (at & 31);
-                                if (j >= from && j < limit && at >= width) next = min(next, (uint32_t)j);
-                                if (j < 0 || at >= width || (pass > 0 && !(*left & mine))) continue;
-                                if (atomicOr(mask + r * words + (at >> 5), bit) & bit) {
-                                    if (pass == 0) atomicOr(left, mine);
-                                    sh.dup = 1;
-                                } else if (pass > 0) {
-                                    atomicAnd(left, ~mine);
-                                }
-                            }
+                        for (int ra = first; ra < last; ra += kMapBytes / (2 * line)) {
+                            if (ra > first) __syncthreads();
+                            count_rows(a.idx + (r0 + ra) * k, k, (uint32_t)from, width, words, min(kMapBytes / (2 * line), last - ra), digit,
+                                       smem + kSmemK, mask + ra * words, sh.row_digits + ra, &sh.digits);
+                        }
+                        ptx::fence_proxy_async_smem();
                     }
                     next = __reduce_min_sync(0xffffffffu, next);
                     if (lane == 0 && next != kNone) atomicMin(&sh.next, next);
@@ -334,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (lane == 0 && set) atomicAdd(&sh.bits, set);
                     if (bits && a.err) atomicOr(a.err, bits);
                     __syncthreads();
-                    if (!exact && sh.entries != sh.bits) {             // an entry more than bits: again, one by one
-                        exact = true;
-                        words = L.exact_words;
+                    if (!counted && sh.entries != sh.bits) {           // more entries than bits: again, with counts
+                        counted = true;
+                        if (tid == 0) sh.digits = 0;
                         continue;
                     }
                     if (warp == 0) {
@@ -365,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float f = sh.factor[tid];
                     const bool mine = r >= first && r < last;
                     const uint32_t* row_mask = mask + (mine ? r : 0) * words;
+                    // logits raised by the digit: the maximum lowered by it for the round
+                    m_run -= (float)digit;
                     for (int i = 0; i < n; ++i) {
                         const uint32_t t = done + i, buf = t & 1, cols = lanes + kColS + kTile * buf;
                         uint2 w = *reinterpret_cast<const uint2*>(row_mask + 2 * sh.list[i]);
@@ -437,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&sh.pfull[buf]);
                     }
+                    m_run += (float)digit;
                 } else if (warp < kValueWarp) {
                     // ------------------------------------------------------------ converters of the keys
                     // a lane takes a quarter of four positions, eight neighbouring lanes eight positions: their
@@ -591,15 +620,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncthreads();
                 ptx::tc_fence_after();
                 if (sh.abort) break;
-                standing = !exact && from == 0 && first == 0 && last == nrows && sh.next == kNone;
-                if (sh.dup) {
-                    ++pass;
+                standing = !counted && from == 0 && first == 0 && last == nrows && sh.next == kNone;
+                if (counted && sh.digits >> (digit + 1) != 0) {
+                    digit += __ffs(sh.digits >> (digit + 1));
                     continue;
                 }
                 if (sh.next == kNone) break;
                 from = sh.next & ~(uint32_t)(kTile - 1);
-                pass = 0;
-                exact = false;
+                digit = 0;
+                counted = false;
             }
             first = last;
         }
@@ -708,9 +737,8 @@ cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, i
     RowsLayout L;
     L.rows = std::min(kMaxRows, kM / group);
     const int64_t words = std::max<int64_t>(1, (positions(a) + kTile - 1) / kTile) * 2;
-    const int space = kMaskBytes / 4 / L.rows, rest = (a.p.sparse_count + 31) / 32;
+    const int space = kMaskBytes / 4 / L.rows;
     L.words = (int32_t)std::min<int64_t>(words, std::min(kMaxWords, space) & ~1);
-    L.exact_words = std::min(L.words, (space - rest) & ~1);
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
     const int64_t blocks = ((int64_t)a.p.rows + L.rows - 1) / L.rows;
     // KV heads per CTA: more share a list's mask, fewer balance better; four waves (prefill of 7168 rows, eight
