@@ -26,8 +26,8 @@
 //
 // Heads never fill the M side of a product, entries do, so groups of 8 query heads waste nothing of
 // the tensor cores.  4-bit values times e4m3 scales are exact in fp16 (at most 6 significant bits,
-// 2^-10 to 2688); queries are scaled by a power of two of their head's largest magnitude, so that
-// bfloat16 fits fp16 too (elements below 2^-14 of the largest lose bits of 2^-25 of it).
+// 2^-10 to 2688), and so are float16 queries; bfloat16 queries are scaled by a power of two of their head's
+// largest magnitude, so that they fit fp16 (elements below 2^-17 of the largest are off by up to 2^-25 of it).
 //
 // What bounds it: from L2 (a prefill), the SM's arithmetic.  A step of 32 entries x 8 query heads is 535
 // instructions, of which 128 conversions of code pairs, 128 scale products and 32 tensor products; a
@@ -274,42 +274,52 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             }
         };
         if (steps > 0) copy_step(0, 0);
-        // query fragments, scaled by a power of two
+        // query fragments: float16 as they are, bfloat16 scaled by a power of two
         uint32_t q[NT][NW][4];
         float f[NT][2];                           // base-2 logit factor of heads 2c and 2c + 1
+        const float factor = a.softmax_scale * a.k_scale * 1.4426950408889634f;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             uint32_t w[NW][4];
 #pragma unroll
             for (int j = 0; j < NW; ++j) w[j][0] = qraw[t][j].x, w[j][1] = qraw[t][j].y, w[j][2] = qraw[t][j].z, w[j][3] = qraw[t][j].w;
-            float big = 0.0f;
+            if constexpr (F16) {
 #pragma unroll
-            for (int j = 0; j < NW; ++j)
+                for (int j = 0; j < NW; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = act2_to_float2<F16>(w[j][i]);
-                    big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    for (int i = 0; i < 4; ++i)     // elements 2i, 2i + 1 or i, i + 4
+                        q[t][j][i] = E2M1 ? w[j][i] : __byte_perm(w[j][i / 2], w[j][2 + i / 2], i & 1 ? 0x7632 : 0x5410);
+                f[t][0] = f[t][1] = fminf(factor, 3.0e38f);
+            } else {
+                float big = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = act2_to_float2<F16>(w[j][i]);
+                        big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+                const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of big)
+#pragma unroll
+                for (int j = 0; j < NW; ++j) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = act2_to_float2<F16>(w[j][i]);
+                        x[2 * i] = v.x * down;
+                        x[2 * i + 1] = v.y * down;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        q[t][j][i] = E2M1 ? float2_to_act2<true>(x[2 * i], x[2 * i + 1]) : float2_to_act2<true>(x[i], x[i + 4]);
                 }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
-            const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of big)
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = act2_to_float2<F16>(w[j][i]);
-                    x[2 * i] = v.x * down;
-                    x[2 * i + 1] = v.y * down;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    q[t][j][i] = E2M1 ? float2_to_act2<true>(x[2 * i], x[2 * i + 1]) : float2_to_act2<true>(x[i], x[i + 4]);
+                const float up = __uint_as_float(ex << 23) * factor;
+                f[t][0] = fminf(__shfl_sync(0xffffffffu, up, 8 * c), 3.0e38f);
+                f[t][1] = fminf(__shfl_sync(0xffffffffu, up, 8 * c + 4), 3.0e38f);
             }
-            const float up = __uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f);
-            f[t][0] = fminf(__shfl_sync(0xffffffffu, up, 8 * c), 3.0e38f);
-            f[t][1] = fminf(__shfl_sync(0xffffffffu, up, 8 * c + 4), 3.0e38f);
 #pragma unroll
             for (int i = 0; i < MO; ++i)
 #pragma unroll

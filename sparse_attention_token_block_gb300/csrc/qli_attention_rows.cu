@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t done = 0;                                 // tiles walked so far: every role counts the same
     bool standing = false;                             // the masks are those of all rows and all their positions
     for (int kvh = head0; kvh < head1; ++kvh) {
-        // ---- the head's queries as an operand: row m is query head m % group of row m / group, in fp16, times a
-        // power of two of its largest magnitude
+        // ---- the head's queries as an operand: row m is query head m % group of row m / group, in fp16 (float16 as
+        // it is, bfloat16 times a power of two of its largest magnitude)
         constexpr int kPerWarp = 16;
         if (warp < kM / kPerWarp) {
             // lane: 4 elements (for int4 2 x 2 of each eight: its codes come in the order 0 4 1 5 2 6 3 7)
@@ -235,14 +235,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int x = 0; x < kPerWarp; ++x) {
                 const int m = kPerWarp * warp + x;
                 if (!E2M1) raw[x] = make_uint2(__byte_perm(raw[x].x, raw[x].y, 0x5410), __byte_perm(raw[x].x, raw[x].y, 0x7632));
-                const float2 u = act2_to_float2<F16>(raw[x].x), v = act2_to_float2<F16>(raw[x].y);
-                float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
+                uint32_t ex = 127;
+                if constexpr (F16) {
+                    *reinterpret_cast<uint2*>(qs + operand_at(m, c8, kAtomQ) + 8 * half) = raw[x];
+                } else {
+                    const float2 u = act2_to_float2<F16>(raw[x].x), v = act2_to_float2<F16>(raw[x].y);
+                    float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
-                const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
-                *reinterpret_cast<uint2*>(qs + operand_at(m, c8, kAtomQ) + 8 * half) =
-                    make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
+                    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+                    const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
+                    *reinterpret_cast<uint2*>(qs + operand_at(m, c8, kAtomQ) + 8 * half) =
+                        make_uint2(float2_to_act2<true>(u.x * down, u.y * down), float2_to_act2<true>(v.x * down, v.y * down));
+                }
                 // (above zero: the mask's -infinity times it stays -infinity)
                 if (lane == 0)
                     sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
