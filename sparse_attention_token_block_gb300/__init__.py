@@ -305,33 +305,73 @@ def gather_kv(p: Problem, seq_lens_q, seq_lens_k, block_table, sparse_indices, k
 
 
 # ------------------------------------------------------------------------------ the attention side
-_act_dtypes = None
+_act_dtypes = _int32 = _float32 = None
 
 
 def _load_act_dtypes():
     import torch
-    global _act_dtypes
+    global _act_dtypes, _int32, _float32
     _act_dtypes = {ACT_BF16: torch.bfloat16, ACT_F16: torch.float16}
+    _int32, _float32 = torch.int32, torch.float32
     return _act_dtypes
 
 
-def _rows(t, what, dtype, shape):
-    """(address, elements between tokens) of a tensor of `shape` = (tokens, heads, dim) whose heads are
-    contiguous (a view of a packed projection keeps its token stride); TypeError / ValueError otherwise."""
+def _rows(t, what, act, shape):
+    """(address, elements between tokens, 0 if contiguous) of a tensor of type `act` and `shape` = (tokens,
+    heads, dim) whose heads are contiguous (a view of a packed projection keeps its token stride); TypeError /
+    ValueError otherwise."""
     if t is None:
         return None, 0
-    if t.dtype is not (_act_dtypes or _load_act_dtypes()).get(dtype):
-        raise TypeError("%s: expected %s, got %s" % (what, _act_dtypes.get(dtype), t.dtype))
+    if t.dtype is not act:
+        raise TypeError("%s: expected %s, got %s" % (what, act, t.dtype))
     if t.shape != shape:
         raise ValueError("%s: expected %s, got %s" % (what, list(shape), list(t.shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     step, head, elem = t.stride()
-    if (elem != 1 or (head != shape[2] and shape[1] > 1)) and t.numel():
+    if elem != 1 or (head != shape[2] and shape[1] > 1):
         raise ValueError("%s: a token's heads must be contiguous" % what)
-    if shape[0] <= 1:
+    if shape[0] == 1:
         step = 0
     elif step < shape[1] * shape[2]:             # 0 would read as contiguous
         raise ValueError("%s: tokens overlap (stride %d)" % (what, step))
     return t.data_ptr(), step
+
+
+def _array(t, what, dtype, nbytes):
+    """Address of a contiguous tensor of at least `nbytes` bytes (None and plain addresses pass); TypeError /
+    ValueError otherwise."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
+    if t.dtype is not dtype:
+        raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    raise ValueError("%s: expected at least %d contiguous bytes, got %s of strides %s" % (
+        what, nbytes, list(t.shape), list(t.stride())))
+
+
+def _pool(t, p, a):
+    """Address of the cache `t`, of any type: contiguous bytes that hold all pages, or one page per step of the
+    first dimension, a page stride apart."""
+    if t is None or isinstance(t, int):
+        return t
+    d, blocks = a.head_dim, p.num_blocks
+    page = p.block_size * (a.num_heads_kv * (d + (d >> 3)) + 15 & -16)
+    step = a.kv_stride or page
+    if t.is_contiguous():
+        if t.nbytes >= (blocks - 1) * step + page:
+            return t.data_ptr()
+    elif (t.shape[0] >= blocks and t.stride(0) * t.element_size() == step and t[0].is_contiguous()
+          and t[0].nbytes >= page):
+        return t.data_ptr()
+    raise ValueError("kv: expected %d pages of %d bytes, %d apart, got %s of strides %s" % (
+        blocks, page, step, list(t.shape), list(t.stride())))
 
 
 def _workspace(t):
@@ -365,15 +405,19 @@ def norm_rope(r: Rotation, q, k, q_weight, k_weight, positions, cos_sin, q_out, 
     """qli_norm_rope: ``q`` [tokens, num_heads_q, head_dim] and ``k`` [tokens, num_heads_k, head_dim] (views
     of a packed projection are fine) normalised and rotated into ``q_out`` / ``k_out`` (which may be
     ``q`` / ``k``); ``positions`` int32 [tokens], ``cos_sin`` float32 [max_positions, rotary_dim]."""
-    n, d, dt = positions.numel(), r.head_dim, r.dtype
+    n, d, dt = positions.numel(), r.head_dim, (_act_dtypes or _load_act_dtypes()).get(r.dtype)
     q_shape, k_shape = (n, r.num_heads_q, d), (n, r.num_heads_k, d)
     qa, qs = _rows(q, "q", dt, q_shape)
     ka, ks = _rows(k, "k", dt, k_shape)
     qo, qos = _rows(q_out, "q_out", dt, q_shape)
     ko, kos = _rows(k_out, "k_out", dt, k_shape)
+    norm = r.norm
+    qw = _array(q_weight, "q_weight", dt, 2 * d) if norm and q_shape[1] else None
+    kw = _array(k_weight, "k_weight", dt, 2 * d) if norm and k_shape[1] else None
+    pos = _array(positions, "positions", _int32, 4 * n)
+    cs = _array(cos_sin, "cos_sin", _float32, 4 * r.max_positions * r.rotary_dim)
     ws, nbytes = _workspace(workspace)
-    return _get_lib().qli_norm_rope(r, n, qa, qs, ka, ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(cos_sin),
-                                    qo, qos, ko, kos, ws, nbytes, _stream(stream))
+    return _get_lib().qli_norm_rope(r, n, qa, qs, ka, ks, qw, kw, pos, cs, qo, qos, ko, kos, ws, nbytes, _stream(stream))
 
 
 def make_attention(*, num_heads_q, num_heads_kv, head_dim, dtype=ACT_BF16, kv_dtype=KV_E2M1, softmax_scale=0.0,
@@ -407,12 +451,14 @@ def kv_write(p: Problem, a: Attention, k, v, token_batch, token_pos, block_table
     """qli_kv_write: quantise ``k`` and ``v`` ([tokens, num_heads_kv, head_dim], views of a packed
     projection are fine) into the paged 4-bit cache ``kv`` at each token's (batch, compressed position)."""
     n = token_batch.numel()
-    shape, dt = (n, a.num_heads_kv, a.head_dim), a.dtype
+    shape, dt = (n, a.num_heads_kv, a.head_dim), (_act_dtypes or _load_act_dtypes()).get(a.dtype)
     ka, ks = _rows(k, "k", dt, shape)
     va, vs = _rows(v, "v", dt, shape)
+    tb, tp = _array(token_batch, "token_batch", _int32, 4 * n), _array(token_pos, "token_pos", _int32, 4 * n)
+    bt = _array(block_table, "block_table", _int32, 4 * p.batch * p.max_blocks_per_seq)
+    pool = _pool(kv, p, a) if n else _ptr(kv)
     ws, nbytes = _workspace(workspace)
-    return _get_lib().qli_kv_write(p, a, n, ka, ks, va, vs, _ptr(token_batch), _ptr(token_pos), _ptr(block_table), _ptr(kv),
-                                   ws, nbytes, _stream(stream))
+    return _get_lib().qli_kv_write(p, a, n, ka, ks, va, vs, tb, tp, bt, pool, ws, nbytes, _stream(stream))
 
 
 def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k, v, workspace=None,
@@ -420,27 +466,35 @@ def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k
     """qli_kv_read: the cached keys and values of each token's (batch, compressed position) into ``k`` and
     ``v`` ([tokens, num_heads_kv, head_dim])."""
     n = token_batch.numel()
-    shape, dt = (n, a.num_heads_kv, a.head_dim), a.dtype
+    shape, dt = (n, a.num_heads_kv, a.head_dim), (_act_dtypes or _load_act_dtypes()).get(a.dtype)
     ka, ks = _rows(k, "k", dt, shape)
     va, vs = _rows(v, "v", dt, shape)
+    tb, tp = _array(token_batch, "token_batch", _int32, 4 * n), _array(token_pos, "token_pos", _int32, 4 * n)
+    bt = _array(block_table, "block_table", _int32, 4 * p.batch * p.max_blocks_per_seq)
+    pool = _pool(kv, p, a) if n else _ptr(kv)
     ws, nbytes = _workspace(workspace)
-    return _get_lib().qli_kv_read(p, a, n, _ptr(token_batch), _ptr(token_pos), _ptr(block_table), _ptr(kv), ka, ks, va, vs,
-                                  ws, nbytes, _stream(stream))
+    return _get_lib().qli_kv_read(p, a, n, tb, tp, bt, pool, ka, ks, va, vs, ws, nbytes, _stream(stream))
 
 
 def sparse_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, block_table, sparse_indices, kv, out,
                      lse=None, workspace=None, stream=None) -> int:
     """qli_sparse_attention: ``out`` [rows, num_heads_q, head_dim] (and ``lse`` float32 [rows, num_heads_q])
     of ``query`` over the entries of the 4-bit cache ``kv`` that ``sparse_indices`` names."""
-    n = p.batch * p.max_q_tokens if p.layout_q == BSND else p.total_q_tokens
-    shape, dt = (n, a.num_heads_q, a.head_dim), a.dtype
+    bsnd = p.layout_q == BSND
+    n = p.batch * p.max_q_tokens if bsnd else p.total_q_tokens
+    shape, dt = (n, a.num_heads_q, a.head_dim), (_act_dtypes or _load_act_dtypes()).get(a.dtype)
     qa, qs = _rows(query, "query", dt, shape)
     oa, os_ = _rows(out, "out", dt, shape)
     if os_ not in (0, shape[1] * shape[2]):
         raise ValueError("out: must be contiguous")
+    b = 4 * p.batch
+    sq = None if bsnd else _array(seq_lens_q, "seq_lens_q", _int32, b)
+    sk = _array(seq_lens_k, "seq_lens_k", _int32, b)
+    bt = _array(block_table, "block_table", _int32, b * p.max_blocks_per_seq)
+    idx = _array(sparse_indices, "sparse_indices", _int32, 4 * n * p.sparse_count)
+    pool, la = _pool(kv, p, a) if n and b else _ptr(kv), _array(lse, "lse", _float32, 4 * n * shape[1])
     ws, nbytes = _workspace(workspace)
-    return _get_lib().qli_sparse_attention(p, a, qa, qs, _ptr(seq_lens_q), _ptr(seq_lens_k), _ptr(block_table),
-                                           _ptr(sparse_indices), _ptr(kv), oa, _ptr(lse), ws, nbytes, _stream(stream))
+    return _get_lib().qli_sparse_attention(p, a, qa, qs, sq, sk, bt, idx, pool, oa, la, ws, nbytes, _stream(stream))
 
 
 def workspace_init(workspace, stream=None) -> int:
