@@ -23,8 +23,8 @@ extern "C" {
  * Either stall ends the launch with QLI_ERR_DEVICE_TIMEOUT in the workspace's device error word
  * (qli_get_device_error); the kernel lets its in-flight copies land and releases its tensor
  * memory before it exits, so the CUDA context stays usable.  Other values select 0.
- * Mode 1 also holds for qli_sparse_attention's kernels: no row gather is issued, the waits run out
- * (0.2 s) and the outputs are NaN.
+ * Mode 1 also holds for qli_sparse_attention's kernels: no entry is copied or handed on, the waits run
+ * out (0.2 s) and the outputs are NaN.
  */
 void qli_testing_set_stall(int mode);
 

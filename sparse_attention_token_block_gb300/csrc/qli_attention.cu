@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                     }
                 }
                 __syncwarp();
-            } else {
+            } else if (!stall) {
                 // a lane per entry, 16 bytes at a time
                 if (go) {
                     const int slot = list[32 * ch + lane], pg = slot / a.p.block_size;
