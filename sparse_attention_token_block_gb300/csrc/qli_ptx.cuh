@@ -244,15 +244,6 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src)
                  : "memory");
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// Wait until at most N of this thread's latest committed groups of copies are under way
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Arrive on `bar` once this thread's earlier cp.async copies have landed (the barrier's expected
 // arrival count includes this arrival)
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar)
