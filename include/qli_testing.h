@@ -10,6 +10,8 @@
 #ifndef QLI_TESTING_H
 #define QLI_TESTING_H
 
+#include "qli.h"
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -36,6 +38,14 @@ void qli_testing_set_stall(int mode);
  * The results are the same whatever the cap.
  */
 void qli_testing_set_topk_ctas(int ctas);
+
+/*
+ * Whether qli_sparse_attention would take a call of these attributes, on a GPU of `sms` SMs, in blocks of
+ * neighbouring rows (1) or a row at a time (0); -1 for invalid attributes.  If in blocks, `shape` receives
+ * the rows of a block, the KV heads that a CTA takes one after another, and the positions of a mask.
+ * Host code only: the tests assert with it that their calls reach the kernel that they are meant for.
+ */
+int qli_testing_attention_rows(const qli_problem* p, const qli_attention* a, int with_seq_lens_k, int sms, int32_t* shape);
 
 #ifdef __cplusplus
 }

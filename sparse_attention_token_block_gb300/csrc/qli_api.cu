@@ -846,6 +846,24 @@ int qli_version(void) { return 100; }
 #ifdef QLI_TESTING
 void qli_testing_set_stall(int mode) { g_test_stall.store(mode == 1 || mode == 2 ? mode : 0); }
 void qli_testing_set_topk_ctas(int ctas) { g_test_topk_ctas.store(ctas > 0 ? ctas : 0); }
+int qli_testing_attention_rows(const qli_problem* p, const qli_attention* a, int with_seq_lens_k, int sms, int32_t* shape)
+{
+    if (check(p, nullptr) != QLI_OK || check_attention(a, nullptr) != QLI_OK || sms < 1) return -1;
+    // (the rule looks at sizes and at which arrays are given, never into them)
+    AttentionArgs A;
+    std::memset(&A, 0, sizeof(A));
+    A.p = params_of(p);
+    A.heads_q = a->num_heads_q;
+    A.heads_kv = a->num_heads_kv;
+    A.kv = reinterpret_cast<const uint8_t*>(p);
+    A.seq_lens_k = with_seq_lens_k ? reinterpret_cast<const int32_t*>(p) : nullptr;
+    if (A.p.rows == 0 || !attention_in_rows(A, a->head_dim, sms)) return 0;
+    const RowsShape s = attention_rows_shape(A, sms);
+    shape[0] = s.rows;
+    shape[1] = s.heads;
+    shape[2] = s.positions;
+    return 1;
+}
 #endif
 
 }  // extern "C"

@@ -736,7 +736,9 @@ bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms)
            positions(a) <= 4 * (int64_t)a.p.sparse_count;
 }
 
-cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st)
+namespace {
+
+RowsLayout rows_layout(const AttentionArgs& a, int sms)
 {
     const int group = a.heads_q / a.heads_kv;
     RowsLayout L;
@@ -752,7 +754,21 @@ cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, i
     while (L.slices < a.heads_kv && blocks * L.slices < 4 * (int64_t)sms) L.slices *= 2;
     L.heads = (a.heads_kv + L.slices - 1) / L.slices;
     L.slices = (a.heads_kv + L.heads - 1) / L.heads;
-    const int64_t grid = blocks * L.slices;
+    return L;
+}
+
+}  // namespace
+
+RowsShape attention_rows_shape(const AttentionArgs& a, int sms)
+{
+    const RowsLayout L = rows_layout(a, sms);
+    return {L.rows, L.heads, 32 * L.words};
+}
+
+cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st)
+{
+    const RowsLayout L = rows_layout(a, sms);
+    const int64_t grid = ((int64_t)a.p.rows + L.rows - 1) / L.rows * L.slices;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (f16) return e2m1 ? launch_rows<true, true>(a, L, grid, st) : launch_rows<true, false>(a, L, grid, st);
     return e2m1 ? launch_rows<false, true>(a, L, grid, st) : launch_rows<false, false>(a, L, grid, st);

@@ -175,5 +175,10 @@ bool encode_page_map(void* tmap, const void* pool, int64_t entry_bytes, int bloc
 // its launch
 bool attention_in_rows(const AttentionArgs& a, int head_dim, int sms);
 cudaError_t launch_attention_rows(const AttentionArgs& a, bool f16, bool e2m1, int sms, cudaStream_t st);
+// How that launch is laid out: rows of a block, KV heads of a CTA, positions of a mask
+struct RowsShape {
+    int32_t rows, heads, positions;
+};
+RowsShape attention_rows_shape(const AttentionArgs& a, int sms);
 
 }  // namespace qli
