@@ -20,7 +20,7 @@ namespace qli {
 namespace {
 
 constexpr int kNormThreads = 128;
-constexpr int kManyHeads = 9;              // heads of a lane under way together, with many tokens
+constexpr int kMostHeads = 9;              // heads of a lane under way together, with many tokens
 
 // Four activations in two words as two packed pairs
 template <bool F16>
@@ -146,22 +146,38 @@ __global__ void __launch_bounds__(kNormThreads, kHeads > 1 ? 8 : 1) norm_rope_ke
     }
 }
 
+using Kernel = void (*)(NormRopeArgs);
+
+// The build whose lanes take `heads` heads at a time, 1 ... kMostHeads (of 6 and 8: 7 and 9)
+template <bool F16, int D, bool kInterleaved>
+Kernel kernel_of(int heads)
+{
+    if (heads == 1) return norm_rope_kernel<F16, D, kInterleaved, 1>;
+    if (heads == 2) return norm_rope_kernel<F16, D, kInterleaved, 2>;
+    if (heads == 3) return norm_rope_kernel<F16, D, kInterleaved, 3>;
+    if (heads == 4) return norm_rope_kernel<F16, D, kInterleaved, 4>;
+    if (heads == 5) return norm_rope_kernel<F16, D, kInterleaved, 5>;
+    return heads <= 7 ? norm_rope_kernel<F16, D, kInterleaved, 7> : norm_rope_kernel<F16, D, kInterleaved, kMostHeads>;
+}
+
 template <bool F16, bool kInterleaved>
 cudaError_t launch_type(const NormRopeArgs& a, int head_dim, int sms, cudaStream_t st)
 {
-    // CTAs per token: as many as leave each group of lanes one head; with many tokens one for every
-    // kManyHeads heads of a group (prefill of 15360 tokens, 72 heads of 128: 143 us with one head a lane,
-    // 108 with five and 256 threads, 96 with nine and 128)
+    // CTAs per token: as many as leave each group of lanes one head; with many tokens as few as take at most
+    // kMostHeads heads a lane, in the build that holds no more.  us for 8000 tokens, one head a lane / 3 / 4 / 5 /
+    // 6 / 7 / 9: 72 heads of 128 83 / 62 / 62 / 60 / 62 / 63 / 53, 40 of 128 48 / 40 / 40 / 33 / 34 / 35 / 37, 32 of
+    // 128 39 / 34 / 27 / 30 / 30 / 31 / 33, 24 of 256 62 / 46 / 46 / 51 / 39 / 40 / 42; 4000 tokens, 104 of 128
+    // 60 / 46 / 43 / 44 / 45 / 41 / 44.
     const int groups = kNormThreads / (head_dim / 8), heads = a.heads[0] + a.heads[1];
     int64_t slices = ceil_div64(heads, groups);
-    const bool many = slices > 1 && a.tokens * slices > 16 * sms;
-    if (many) slices = ceil_div64(slices, kManyHeads);
-    auto kernel = many ? (head_dim == 64 ? norm_rope_kernel<F16, 64, kInterleaved, kManyHeads>
-                                         : (head_dim == 128 ? norm_rope_kernel<F16, 128, kInterleaved, kManyHeads>
-                                                            : norm_rope_kernel<F16, 256, kInterleaved, kManyHeads>))
-                       : (head_dim == 64 ? norm_rope_kernel<F16, 64, kInterleaved, 1>
-                                         : (head_dim == 128 ? norm_rope_kernel<F16, 128, kInterleaved, 1>
-                                                            : norm_rope_kernel<F16, 256, kInterleaved, 1>));
+    int each = 1;
+    if (slices > 1 && a.tokens * slices > 16 * sms) {
+        const int64_t all = slices;
+        slices = ceil_div64(all, kMostHeads);
+        each = (int)ceil_div64(all, slices);
+    }
+    const Kernel kernel = head_dim == 64 ? kernel_of<F16, 64, kInterleaved>(each)
+                                         : (head_dim == 128 ? kernel_of<F16, 128, kInterleaved>(each) : kernel_of<F16, 256, kInterleaved>(each));
     return launch_pdl(kernel, dim3((unsigned)a.tokens, (unsigned)slices), dim3(kNormThreads), 0, st, a);
 }
 
