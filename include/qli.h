@@ -419,10 +419,10 @@ qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tok
  * (optional) float32 [rows, num_heads_q].  query, kv and out 16-byte aligned.  Logits, softmax
  * statistics and accumulators are fp32; float16 queries, keys and values enter the products exactly,
  * bfloat16 queries in fp16, scaled by a power of two of their head's largest magnitude (off by at most
- * 2^-25 of it), probabilities in fp16.  A scale byte of NaN (qli_kv_write writes none) in a listed entry
- * gives NaN in that row and head, in some or all of its elements, and nowhere else.  One kernel on
- * `stream`, chosen by the sizes and by whether seq_lens_k is given, never by contents; the result does
- * not depend on scheduling.
+ * 2^-25 of it), probabilities rounded to fp16, for float16 outputs with what that rounding dropped (2^-22
+ * of them).  A scale byte of NaN (qli_kv_write writes none) in a listed entry gives NaN in that row and
+ * head, in some or all of its elements, and nowhere else.  One kernel on `stream`, chosen by the sizes and
+ * by whether seq_lens_k is given, never by contents; the result does not depend on scheduling.
  */
 qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, const void* query, int64_t q_stride,
                                 const int32_t* seq_lens_q, const int32_t* seq_lens_k, const int32_t* block_table,

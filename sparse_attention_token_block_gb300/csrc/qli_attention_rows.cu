@@ -16,7 +16,10 @@
 //   * one warp issues the products: Q, K and V from shared memory, the logits twice in tensor memory, P in
 //     the place of the logits it came from;
 //   * 4 softmax warps, a row of the product per thread: masked logits, running maximum (raised only when
-//     a logit passes it by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+//     a logit passes it by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16; with float16
+//     activations what that rounding dropped follows P as a second operand, where the other half of the
+//     logits was (1024 + 2048 rows of up to 1024 entries 212 us instead of 184; the errors as in
+//     qli_attention.cu).
 // Two CTAs share an SM (half its shared and tensor memory each): what a tile costs is mostly the way from
 // role to role, and one CTA's masks, queries and outputs overlap the other's products.
 //
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (!wait_bounded(&sh.sfull[buf], (t >> 1) & 1, &sh.abort, a.err)) break;
                         ptx::tc_fence_after();
                         bool ok = true;
-                        uint32_t p[32];
+                        uint32_t p[32], rest[F16 ? 32 : 1];
                         while (true) {
                             float best[2] = {-INFINITY, -INFINITY};
                             uint64_t part[2] = {0, 0};
@@ -431,8 +434,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                                     ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
                                     const float px = ptx::ex2(zx), py = ptx::ex2(zy);
                                     part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
-                                    // one rounding to fp16 of each probability (the sum keeps the unrounded ones)
-                                    p[16 * q + e / 2] = float2_to_act2<true>(px, py);
+                                    const int at = 16 * q + e / 2;
+                                    p[at] = float2_to_act2<true>(px, py);
+                                    if constexpr (F16) rest[at] = remainder_f16x2(px, py, p[at]);
                                 }
                             }
                             float sum, other;
@@ -464,7 +468,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                             }
                         }
                         if (!ok) break;
-                        QLI_TMEM_ST_X32(cols, p);                  // in the place of the logits
+                        // in the place of the logits (in parts of 16 columns where the registers of p and rest are
+                        // those that the logits leave)
+                        if constexpr (F16) {
+                            QLI_TMEM_ST_X16(cols, p);
+                            QLI_TMEM_ST_X16(cols + 16, (p + 16));
+                            QLI_TMEM_ST_X16(cols + 32, rest);
+                            QLI_TMEM_ST_X16(cols + 48, (rest + 16));
+                        } else {
+                            QLI_TMEM_ST_X32(cols, p);
+                        }
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
                         __syncwarp();
@@ -608,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                             const bool add = !(fresh && i == 1);
                             if (ptx::elect_one()) {
 #pragma unroll
-                                for (int kk = 0; kk < kTile / 16; ++kk)
-                                    ptx::mma_f16_ts(tm + kColO, tm + kColS + kTile * buf + 8 * kk, vd + (kk * 32 >> 4), idesc_o, add || kk > 0);
+                                for (int kk = 0; kk < (F16 ? 2 : 1) * kTile / 16; ++kk)
+                                    ptx::mma_f16_ts(tm + kColO, tm + kColS + kTile * buf + 8 * kk, vd + (kk % 4 * 32 >> 4), idesc_o, add || kk > 0);
                                 ptx::mma_commit(&sh.vfree[buf]);
                                 ptx::mma_commit(&sh.pvdone);
                             }

@@ -29,6 +29,15 @@ __device__ __forceinline__ uint32_t float2_to_act2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What the rounding of lo and hi to the fp16 pair p left, rounded to fp16
+__device__ __forceinline__ uint32_t remainder_f16x2(float lo, float hi, uint32_t p)
+{
+    const float2 r = act2_to_float2<true>(p);
+    float x, y;
+    ptx::unpack2(ptx::fma2(ptx::pack2(r.x, r.y), ptx::pack2(-1.0f, -1.0f), ptx::pack2(lo, hi)), x, y);
+    return float2_to_act2<true>(x, y);
+}
+
 // Two scale bytes as fp16 (exact), the low byte in the low half
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t bytes)
 {

@@ -388,6 +388,15 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t m, uint32_t n)
         "r"(r[29]), "r"(r[30]), "r"(r[31])                                                         \
         : "memory")
 
+#define QLI_TMEM_ST_X16(taddr, r)                                                                  \
+    asm volatile(                                                                                  \
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"   \
+        "%13,%14,%15,%16};" ::"r"(taddr),                                                          \
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),    \
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),          \
+        "r"(r[15])                                                                                 \
+        : "memory")
+
 // ------------------------------------------------------------------------------------ conversions
 // Four int8 in a word -> two f16x2 words, exactly: bias each byte to u = x + 128, place it as the
 // fraction of the fp16 number 1024 + u (exponent field 25), then subtract 1152.
