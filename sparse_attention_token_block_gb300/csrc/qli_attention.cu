@@ -28,9 +28,10 @@
 //     interleaved before they are decoded.
 //
 // Heads never fill the M side of a product, entries do, so groups of 8 query heads waste nothing of
-// the tensor cores.  4-bit values times e4m3 scales are exact in fp16 (at most 6 significant bits,
-// 2^-10 to 2688), and so are float16 queries; bfloat16 queries are scaled by a power of two of their head's
-// largest magnitude, so that they fit fp16 (elements below 2^-17 of the largest are off by up to 2^-25 of it).
+// the tensor cores.  4-bit values times e4m3 scales are exact in fp16 (E2M1: at most 6 significant bits, 2^-10
+// to 2688; int4: 7, 2^-9 to 3136), and so are float16 queries; bfloat16 queries are scaled by a power of two of
+// their head's largest magnitude, so that they fit fp16 (elements below 2^-17 of the largest are off by up to
+// 2^-25 of it).
 //
 // What bounds it: from L2 (a prefill), the SM's arithmetic.  A step of 32 entries x 8 query heads is 535
 // instructions, of which 128 conversions of code pairs, 128 scale products and 32 tensor products; a
@@ -40,7 +41,7 @@
 // the gathers' latency and the start: list, entries, join.  Measured on a GB300, 64 query heads over 8 KV
 // heads of 128, E2M1, 2048 entries a row: 1 row 7.1 us, 8 rows 11.0, 32 rows (8k-32k keys) 21.4 (3.6 TB/s),
 // 64 rows 36.4 (4.2), 128 rows 65.1 (4.7); prefill of 1024 + 2048 + 4096 rows 1.76 ms (166 TFLOP/s; such calls
-// go to qli_attention_rows.cu, 0.62 ms); int4 27.1 us at 32 rows: its codes take seven integer operations per
+// go to qli_attention_rows.cu, 0.61 ms); int4 27.1 us at 32 rows: its codes take seven integer operations per
 // eight, E2M1's four.
 //
 // Partial results of the warps and CTAs that share a unit meet in shared memory (distributed over

@@ -38,10 +38,10 @@
 // 2000 an SM) of which its products take 512; the SM issues in 46 % of its cycles.  Without the arithmetic
 // of softmax and decoding at all an earlier form (one CTA, tiles of 128) still took two thirds of its time.
 // Building the masks is an eighth, staging the queries a twentieth.  Measured on a GB300, 64 query heads
-// over 8 KV heads, E2M1, causal: 1024 + 2048 + 4096 rows of up to 2048 entries 617 us (one row at a time
-// 1764), 1024 + 2048 rows of up to 1024 192 us (434), the same for one KV head 199 us (469), for groups of
-// four 137 us (432), int4 206 us (577); one CTA an SM takes 816 us for the first, the CTAs in the order of
-// the rows 737, tiles whose logits are loaded in two parts 761.
+// over 8 KV heads, E2M1, causal: 1024 + 2048 + 4096 rows of up to 2048 entries 612 us (one row at a time
+// 1764), with 8192 more, which take two masks, 2311 us (4327); 1024 + 2048 rows of up to 1024 190 us (434), the
+// same for one KV head 199 us (469), for groups of four 137 us (432), int4 204 us (577); one CTA an SM takes 816
+// us for the first, the CTAs in the order of the rows 737, tiles whose logits are loaded in two parts 761.
 //
 // Every wait is bounded (0.2 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
 #include <cuda.h>

@@ -4,8 +4,8 @@
 //
 // A stream over HBM: 2 bytes read and 2 written per element and a table row per token.  A CTA works
 // on one token (few tokens: several CTAs on one, by heads), so the rotation's factors stay in registers
-// and the weights, as fp32, in shared memory; D / 8 lanes share a head vector, and each does kHeads heads at a time with all their
-// loads under way before the first is used.  A lane has two chunks of four elements of a vector,
+// and the weights, as fp32, in shared memory; D / 8 lanes share a head vector, and each does kHeads heads
+// at a time with all their loads under way before the first is used.  A lane has two chunks of four elements of a vector,
 // chosen so that it holds both elements of its pairs: in the half layout lane l < R/8 takes 4l.. and
 // R/2 + 4l.., in the interleaved layout (and past R) eight consecutive elements.  So the rotation
 // needs no exchange between lanes and the norm only a sum over the group.  The arithmetic runs two
@@ -20,7 +20,7 @@ namespace qli {
 namespace {
 
 constexpr int kNormThreads = 128;
-constexpr int kMostHeads = 9;              // heads of a lane under way together, with many tokens
+constexpr int kMostHeads = 9;              // heads of a lane under way together: 64 registers, eight CTAs an SM
 
 // Four activations in two words as two packed pairs
 template <bool F16>
