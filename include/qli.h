@@ -393,7 +393,8 @@ size_t qli_kv_entry_bytes(const qli_attention* a);
  * qli_quantize_keys.  One kernel on `stream`; tokens = 0 enqueues nothing.
  *
  * qli_kv_read: the reverse; k[t], v[t] receive k_scale * s * code, computed in fp32 (one rounding, none
- * for factors that are powers of two) and rounded to the activations' type.  A token with an invalid batch, position or page gets zeros and sets the same error bits.
+ * for factors that are powers of two) and rounded to the activations' type.  A token with an invalid
+ * batch, position or page gets zeros and sets the same error bits.
  */
 qli_status qli_kv_write(const qli_problem* p, const qli_attention* a, int64_t tokens, const void* k, int64_t k_stride,
                         const void* v, int64_t v_stride, const int32_t* token_batch, const int32_t* token_pos,
