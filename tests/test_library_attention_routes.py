@@ -44,12 +44,12 @@ def test_the_rule(route):
     assert route(**dict(good, held=4096, with_k=False, k=1024)) == (16, 1, 4096)
 
 
-@pytest.mark.parametrize("hq,hkv,block,mask", [(64, 8, 16, 4096), (32, 8, 32, 3072), (40, 8, 25, 3904), (8, 8, 32, 3072),
-                                               (128, 1, 1, 4096), (48, 8, 21, 4096)])
-def test_layouts(route, hq, hkv, block, mask):
-    """Rows of a block and positions of a mask by the size of the group; heads of a CTA by the waves."""
+@pytest.mark.parametrize("hq,hkv,block,tiles", [(64, 8, 16, 64), (32, 8, 32, 48), (40, 8, 25, 61), (8, 8, 32, 48),
+                                                (128, 1, 1, 64), (48, 8, 21, 64)])
+def test_layouts(route, hq, hkv, block, tiles):
+    """Rows of a block and tiles of 64 positions of a mask by the size of the group; heads of a CTA by the waves."""
     got = route(rows=SMS * block, hq=hq, hkv=hkv, positions=8000, k=2000)
-    assert got == (block, max(1, hkv // 4), mask)
+    assert got == (block, max(1, hkv // 4), 64 * tiles)
     assert route(rows=8 * SMS * block, hq=hq, hkv=hkv, positions=8000, k=2000)[1] == hkv
 
 
