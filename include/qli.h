@@ -405,6 +405,23 @@ qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tok
                        void* stream);
 
 /*
+ * A step's new tokens in one pass: qli_norm_rope of their query and key heads, the keys and the values
+ * written to the cache as by qli_kv_write.  Token t's queries q[t] and keys k[t] are normalised and turned by
+ * the table's row positions[t]; the queries go to q_out[t], the keys, in fp32 and without a rounding in
+ * between, and the values v[t] are quantised to compressed position token_pos[t] of batch token_batch[t].  `r`
+ * and `a` must agree: r->num_heads_k = a->num_heads_kv, the same head_dim (64 or 128) and dtype; the query heads
+ * are r's (none: q and q_out may be NULL).  Layouts, strides and alignment as in the two calls; q_out may be q.
+ * A token with an invalid batch, position in the cache or page is not written, its queries are; one whose
+ * positions[t] lies outside the table gets zero queries and is not written.  Both set the error bits of the two
+ * calls.  One kernel on `stream`; tokens = 0 enqueues nothing.
+ */
+qli_status qli_kv_append(const qli_problem* p, const qli_attention* a, const qli_rotation* r, int64_t tokens, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const void* q_weight, const void* k_weight, const int32_t* positions, const float* cos_sin,
+                         const int32_t* token_batch, const int32_t* token_pos, const int32_t* block_table, void* q_out,
+                         int64_t q_out_stride, void* kv, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Attention over the selected entries.  For row r (batch b as in qli_gather_kv), query head h and
  * its KV head g, over the entries i < sparse_count whose index j = sparse_indices[r][i] is valid,
  * K_i and V_i the cached vectors of position j of batch b:
@@ -429,6 +446,35 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
                                 const int32_t* seq_lens_q, const int32_t* seq_lens_k, const int32_t* block_table,
                                 const int32_t* sparse_indices, const void* kv, void* out, float* lse,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over what it has cached (dense layers, sliding-window layers, short
+ * sequences; one token or a chunk of a prompt).  Row r of sequence b sees the compressed positions that the
+ * indexer's mask gives it: with Sq new tokens (max_q_tokens or seq_lens_q[b], for TND the prefix sums'
+ * difference) and Sk = seq_lens_k[b] tokens in all, the new ones included and already cached,
+ *
+ *     j < n,  n = clamp(ceil((Sk - Sq + r + 1) / cmp_ratio), 0, Lc)     (sparse_mode 3; floor with
+ *                                                      mask_complete_blocks),  n = Lc (sparse_mode 0)
+ *     and, if window > 0:  j >= n - window  or  j < sinks
+ *
+ * (`window` the last positions that a row sees, 0 = all; `sinks` the first positions, which stay visible).  Per
+ * query head h, over the visible positions of its KV head:
+ *
+ *     z_j = softmax_scale * (query[r][h] . K_j),   out[r][h] = sum_j softmax(z)_j V_j,   lse[r][h] = ln sum_j exp(z_j)
+ *
+ * A row that sees nothing gets zeros and lse = -infinity; so do rows of no sequence (BSND rows from seq_lens_q[b]
+ * on, TND rows behind the last prefix sum) and, with error bit 1, the rows of a sequence whose lengths are
+ * invalid (as for qli_metadata; all rows, for bad TND prefix sums).  Positions on a page outside the pool are left
+ * out, with error bit 2; pages of positions that no row sees are not looked at.  sparse_count is not used.
+ * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention (float16 outputs too have their
+ * probabilities rounded to fp16 once).  A scale byte of NaN gives NaN in the rows and heads that see the position,
+ * in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
+ * does not depend on scheduling.
+ */
+qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks, const void* query,
+                               int64_t q_stride, const int32_t* seq_lens_q, const int32_t* seq_lens_k,
+                               const int32_t* block_table, const void* kv, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Zero the workspace's device error word (enqueued on `stream`).  Call once after allocating a
  * workspace, before its first qli_score_topk. */

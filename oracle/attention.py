@@ -182,3 +182,93 @@ def sparse_attention(case, query, idx, pool, heads_kv, e2m1, scale, k_scale=1.0,
             spread["qk"][r, h] = (np.abs(kk) @ np.abs(q)).max() * scale
             spread["kq"][r, h] = np.abs(kk).sum(-1).max() * np.abs(q).max() * scale
     return out, lse, err, spread
+
+
+def append(case, pool, q, k, v, q_weight, k_weight, positions, cos_sin, rotary, interleaved, eps, token_batch, token_pos,
+           e2m1, k_scale=1.0, v_scale=1.0, norm=True):
+    """Queries turned, keys turned and written with the values into ``pool`` in place; returns (q float64, turned
+    keys float64, error bits).  Tokens at positions outside the table are not written."""
+    turned = [norm_rope(x, w, positions, cos_sin, rotary, interleaved, eps, norm) for x, w in ((q, q_weight), (k, k_weight))]
+    err = 0
+    known = [0 <= p < cos_sin.shape[0] for p in positions]
+    for t, ok in enumerate(known):
+        where, e = entry_of(case, int(token_batch[t]), int(token_pos[t]), case.max_blocks_per_seq * case.block_size)
+        err |= e if ok else e | ERR_LENGTH
+        if where and ok:
+            y = turned[1][t:t + 1].astype(np.float32)
+            pool[where] = encode(y, v[t:t + 1], e2m1, k_scale, v_scale, into=pool[where][None])[0]
+    return turned[0], turned[1], err
+
+
+def sequence_rows(case, b):
+    """(first row, new tokens, rows) of sequence b; new tokens None when its lengths are invalid."""
+    if case.layout_q == "BSND":
+        sq = case.s1 if case.seq_lens_q is None else int(case.seq_lens_q[b])
+        return b * case.s1, sq if 0 <= sq <= case.s1 else None, case.s1
+    first = int(case.seq_lens_q[b - 1]) if b else 0
+    n = int(case.seq_lens_q[b]) - first
+    return first, n, n
+
+
+def visible(case, sq, sk, r, window=0, sinks=0, complete=False):
+    """Compressed positions that new token r sees, in order."""
+    lc = -(-sk // case.cmp_ratio)
+    n = lc
+    if case.sparse_mode == 3:
+        p = sk - sq + r
+        started = 0 if p < 0 else (p + 1) // case.cmp_ratio if complete else p // case.cmp_ratio + 1
+        n = min(lc, started)
+    return [j for j in range(n) if window == 0 or j >= n - window or j < sinks]
+
+
+def paged_attention(case, query, pool, heads_kv, e2m1, scale, k_scale=1.0, v_scale=1.0, window=0, sinks=0, complete=False,
+                    max_seqlen_k=None):
+    """(out, lse, error bits, spread) as sparse_attention, each row over the positions that it sees."""
+    rows, hq, d = query.shape
+    g = hq // heads_kv
+    out = np.zeros((rows, hq, d))
+    lse = np.full((rows, hq), -np.inf)
+    spread = dict(wv=np.zeros((rows, hq, d)), vmax=np.zeros((rows, hq)), qk=np.zeros((rows, hq)), kq=np.zeros((rows, hq)),
+                  n=np.zeros(rows, int))
+    err = 0
+    longest = case.max_seqlen_k if max_seqlen_k is None else max_seqlen_k
+    if case.layout_q != "BSND":
+        cum = np.concatenate([[0], case.seq_lens_q])
+        if (np.diff(cum) < 0).any() or (cum < 0).any() or (cum > rows).any():
+            return out, lse, ERR_LENGTH, spread
+    for b in range(case.batch):
+        first, sq, _ = sequence_rows(case, b)
+        sk = int(case.seq_lens_k[b])
+        if sq is None or not 0 <= sk <= longest or -(-sk // case.cmp_ratio) > case.max_blocks_per_seq * case.block_size:
+            err |= ERR_LENGTH
+            continue
+        seen = [visible(case, sq, sk, r, window, sinks, complete) for r in range(sq)]
+        needed = sorted(set().union(*map(set, seen))) if seen else []
+        found = {}
+        for j in needed:
+            where, e = entry_of(case, b, j, case.max_blocks_per_seq * case.block_size)
+            err |= e
+            if where:
+                found[j] = len(found)
+        if not found:
+            continue
+        k, v = decode(np.stack([pool[entry_of(case, b, j, 1 << 40)[0]] for j in found]), heads_kv, d, e2m1, k_scale, v_scale)
+        for r in range(sq):
+            at = [found[j] for j in seen[r] if j in found]
+            if not at:
+                continue
+            i = first + r
+            spread["n"][i] = len(at)
+            for h in range(hq):
+                kk, vv, q = k[at, h // g], v[at, h // g], query[i, h].astype(np.float64)
+                z = kk @ q * scale
+                top = z.max()
+                w = np.exp(z - top)
+                lse[i, h] = top + np.log(w.sum())
+                w = w / w.sum()
+                out[i, h] = w @ vv
+                spread["wv"][i, h] = w @ np.abs(vv)
+                spread["vmax"][i, h] = np.abs(vv).max()
+                spread["qk"][i, h] = (np.abs(kk) @ np.abs(q)).max() * scale
+                spread["kq"][i, h] = np.abs(kk).sum(-1).max() * np.abs(q).max() * scale
+    return out, lse, err, spread

@@ -37,8 +37,8 @@ EXPORTS = ("qli_problem_init", "qli_validate", "qli_metadata_words", "qli_worksp
            "qli_plan_create", "qli_plan_launch", "qli_plan_destroy",
            "qli_quantize", "qli_quantize_keys", "qli_gather_kv",
            "qli_rotation_init", "qli_rotation_validate", "qli_norm_rope",
-           "qli_attention_init", "qli_attention_validate", "qli_kv_entry_bytes", "qli_kv_write", "qli_kv_read",
-           "qli_sparse_attention",
+           "qli_attention_init", "qli_attention_validate", "qli_kv_entry_bytes", "qli_kv_write", "qli_kv_read", "qli_kv_append",
+           "qli_sparse_attention", "qli_paged_attention",
            "qli_status_string", "qli_version")
 
 
@@ -148,6 +148,11 @@ def _load():
     L.qli_kv_write.restype = ctypes.c_int
     L.qli_kv_read.argtypes = [P, A, i64, i32p, i32p, i32p, vp, vp, i64, vp, i64, vp, sz, vp]
     L.qli_kv_read.restype = ctypes.c_int
+    L.qli_kv_append.argtypes = [P, A, R, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32p, vp, i32p, i32p, i32p, vp, i64, vp, vp,
+                                sz, vp]
+    L.qli_kv_append.restype = ctypes.c_int
+    L.qli_paged_attention.argtypes = [P, A, ctypes.c_int32, ctypes.c_int32, vp, i64, i32p, i32p, i32p, vp, vp, vp, vp, sz, vp]
+    L.qli_paged_attention.restype = ctypes.c_int
     L.qli_sparse_attention.argtypes = [P, A, vp, i64, i32p, i32p, i32p, i32p, vp, vp, vp, vp, sz, vp]
     L.qli_sparse_attention.restype = ctypes.c_int
     return L
@@ -377,6 +382,19 @@ def _pool(t, p, a):
         blocks, page, step, list(t.shape), list(t.stride())))
 
 
+def _here(*tensors):
+    """ValueError unless every tensor given lies on the current CUDA device (the one that the call runs on)."""
+    at = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if at is None:
+            import torch
+            at = torch.cuda.current_device()
+        if t.get_device() != at:
+            raise ValueError("expected tensors on the current device cuda:%d, got %s" % (at, t.device))
+
+
 def _workspace(t):
     return (None, 0) if t is None else (t.data_ptr(), t.nbytes)
 
@@ -464,6 +482,31 @@ def kv_write(p: Problem, a: Attention, k, v, token_batch, token_pos, block_table
     return _get_lib().qli_kv_write(p, a, n, ka, ks, va, vs, tb, tp, bt, pool, ws, nbytes, _stream(stream))
 
 
+def kv_append(p: Problem, a: Attention, r: Rotation, q, k, v, q_weight, k_weight, positions, cos_sin, token_batch,
+              token_pos, block_table, q_out, kv, workspace=None, stream=None) -> int:
+    """qli_kv_append: ``q``, ``k``, ``v`` ([tokens, heads, head_dim], views of a packed projection are fine) of new
+    tokens: queries normalised and rotated into ``q_out`` (which may be ``q``), keys the same and quantised with
+    the values into the paged 4-bit cache ``kv`` at each token's (batch, compressed position)."""
+    n, d, dt = token_batch.numel(), r.head_dim, (_act_dtypes or _load_act_dtypes()).get(r.dtype)
+    q_shape, shape = (n, r.num_heads_q, d), (n, a.num_heads_kv, d)
+    qa, qs = _rows(q, "q", dt, q_shape)
+    ka, ks = _rows(k, "k", dt, shape)
+    va, vs = _rows(v, "v", dt, shape)
+    qo, qos = _rows(q_out, "q_out", dt, q_shape)
+    qw = _array(q_weight, "q_weight", dt, 2 * d) if r.norm and q_shape[1] else None
+    kw = _array(k_weight, "k_weight", dt, 2 * d) if r.norm else None
+    pos = _array(positions, "positions", _int32, 4 * n)
+    cs = _array(cos_sin, "cos_sin", _float32, 4 * r.max_positions * r.rotary_dim)
+    tb, tp = _array(token_batch, "token_batch", _int32, 4 * n), _array(token_pos, "token_pos", _int32, 4 * n)
+    bt = _array(block_table, "block_table", _int32, 4 * p.batch * p.max_blocks_per_seq)
+    pool = _pool(kv, p, a) if n else _ptr(kv)
+    ws, nbytes = _workspace(workspace)
+    if n:
+        _here(q, k, v, q_out, q_weight, k_weight, positions, cos_sin, token_batch, token_pos, block_table, kv, workspace)
+    return _get_lib().qli_kv_append(p, a, r, n, qa, qs, ka, ks, va, vs, qw, kw, pos, cs, tb, tp, bt, qo, qos, pool, ws, nbytes,
+                                    _stream(stream))
+
+
 def kv_read(p: Problem, a: Attention, token_batch, token_pos, block_table, kv, k, v, workspace=None,
             stream=None) -> int:
     """qli_kv_read: the cached keys and values of each token's (batch, compressed position) into ``k`` and
@@ -498,6 +541,29 @@ def sparse_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, bl
     pool, la = _pool(kv, p, a) if n and b else _ptr(kv), _array(lse, "lse", _float32, 4 * n * shape[1])
     ws, nbytes = _workspace(workspace)
     return _get_lib().qli_sparse_attention(p, a, qa, qs, sq, sk, bt, idx, pool, oa, la, ws, nbytes, _stream(stream))
+
+
+def paged_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, block_table, kv, out, lse=None,
+                    workspace=None, window=0, sinks=0, stream=None) -> int:
+    """qli_paged_attention: ``out`` [rows, num_heads_q, head_dim] (and ``lse`` float32 [rows, num_heads_q]) of
+    ``query`` over the positions of the 4-bit cache ``kv`` that each row sees: all up to its own, or the last
+    ``window`` of them and the first ``sinks``."""
+    bsnd = p.layout_q == BSND
+    n = p.batch * p.max_q_tokens if bsnd else p.total_q_tokens
+    shape, dt = (n, a.num_heads_q, a.head_dim), (_act_dtypes or _load_act_dtypes()).get(a.dtype)
+    qa, qs = _rows(query, "query", dt, shape)
+    oa, os_ = _rows(out, "out", dt, shape)
+    if os_ not in (0, shape[1] * shape[2]):
+        raise ValueError("out: must be contiguous")
+    b = 4 * p.batch
+    sq = _array(seq_lens_q, "seq_lens_q", _int32, b)
+    sk = _array(seq_lens_k, "seq_lens_k", _int32, b)
+    bt = _array(block_table, "block_table", _int32, b * p.max_blocks_per_seq)
+    pool, la = _pool(kv, p, a) if n and b else _ptr(kv), _array(lse, "lse", _float32, 4 * n * shape[1])
+    ws, nbytes = _workspace(workspace)
+    if n:
+        _here(query, out, seq_lens_q, seq_lens_k, block_table, kv, lse, workspace)
+    return _get_lib().qli_paged_attention(p, a, window, sinks, qa, qs, sq, sk, bt, pool, oa, la, ws, nbytes, _stream(stream))
 
 
 def workspace_init(workspace, stream=None) -> int:

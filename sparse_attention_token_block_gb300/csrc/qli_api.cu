@@ -12,6 +12,7 @@
 
 #include "qli_internal.cuh"
 #include "qli_kv.cuh"
+#include "qli_paged.cuh"
 
 namespace qli {
 
@@ -619,6 +620,53 @@ void qli_rotation_init(qli_rotation* r)
 
 qli_status qli_rotation_validate(const qli_rotation* r, const char** why) { return check_rotation(r, why); }
 
+namespace {
+
+// Argument checks of the norm and rotation; fills `a` (nothing to do when tokens = 0 or there are no heads).  With
+// `keys_out` false the keys have no output of their own (they go to the cache).
+qli_status rotation_args(const qli_rotation* r, int64_t tokens, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* q_weight, const void* k_weight, const int32_t* positions, const float* cos_sin, void* q_out,
+                         int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* workspace, NormRopeArgs* A,
+                         bool keys_out = true)
+{
+    NormRopeArgs& a = *A;
+    std::memset(&a, 0, sizeof(a));
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const void* weight[2] = {q_weight, k_weight};
+    const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
+    const int32_t heads[2] = {r->num_heads_q, r->num_heads_k};
+    for (int i = 0; i < 2; ++i) {
+        a.heads[i] = heads[i];
+        if (heads[i] == 0) continue;
+        const bool writes = i == 0 || keys_out;
+        a.in[i] = in[i];
+        a.out[i] = out[i];
+        a.weight[i] = r->norm ? weight[i] : nullptr;
+        a.in_stride[i] = token_stride(is[i], heads[i], r->head_dim);
+        a.out_stride[i] = token_stride(os[i], heads[i], r->head_dim);
+        if (a.in_stride[i] < 0 || a.out_stride[i] < 0) return QLI_ERR_INVALID_ARG;
+        if (tokens == 0) continue;
+        if (!in[i] || !aligned(in[i], 16) || (writes && (!out[i] || !aligned(out[i], 16)))) return QLI_ERR_INVALID_ARG;
+        if (r->norm && (!weight[i] || !aligned(weight[i], 16))) return QLI_ERR_INVALID_ARG;
+    }
+    if (tokens == 0 || heads[0] + heads[1] == 0) return QLI_OK;
+    if (!positions || !aligned(positions, 4)) return QLI_ERR_INVALID_ARG;
+    if (r->rotary_dim > 0 && (!cos_sin || !aligned(cos_sin, 16))) return QLI_ERR_INVALID_ARG;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.err = static_cast<uint32_t*>(workspace);
+    a.tokens = tokens;
+    a.rotary = r->rotary_dim;
+    a.max_positions = r->max_positions;
+    a.interleaved = r->interleaved;
+    a.norm = r->norm;
+    a.eps = r->eps;
+    return QLI_OK;
+}
+
+}  // namespace
+
 qli_status qli_norm_rope(const qli_rotation* r, int64_t tokens, const void* q, int64_t q_stride, const void* k,
                          int64_t k_stride, const void* q_weight, const void* k_weight, const int32_t* positions,
                          const float* cos_sin, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
@@ -629,40 +677,12 @@ qli_status qli_norm_rope(const qli_rotation* r, int64_t tokens, const void* q, i
     if (tokens < 0 || tokens > kMaxTokens) return QLI_ERR_INVALID_ARG;
     if (workspace && (workspace_bytes < kWsHeaderBytes || !aligned(workspace, 256))) return QLI_ERR_INVALID_ARG;
     NormRopeArgs a;
-    std::memset(&a, 0, sizeof(a));
-    const void* in[2] = {q, k};
-    void* out[2] = {q_out, k_out};
-    const void* weight[2] = {q_weight, k_weight};
-    const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
-    const int32_t heads[2] = {r->num_heads_q, r->num_heads_k};
-    for (int i = 0; i < 2; ++i) {
-        a.heads[i] = heads[i];
-        if (heads[i] == 0) continue;
-        a.in[i] = in[i];
-        a.out[i] = out[i];
-        a.weight[i] = r->norm ? weight[i] : nullptr;
-        a.in_stride[i] = token_stride(is[i], heads[i], r->head_dim);
-        a.out_stride[i] = token_stride(os[i], heads[i], r->head_dim);
-        if (a.in_stride[i] < 0 || a.out_stride[i] < 0) return QLI_ERR_INVALID_ARG;
-        if (tokens == 0) continue;
-        if (!in[i] || !out[i] || !aligned(in[i], 16) || !aligned(out[i], 16)) return QLI_ERR_INVALID_ARG;
-        if (r->norm && (!weight[i] || !aligned(weight[i], 16))) return QLI_ERR_INVALID_ARG;
-    }
-    if (tokens == 0 || heads[0] + heads[1] == 0) return QLI_OK;
-    if (!positions || !aligned(positions, 4)) return QLI_ERR_INVALID_ARG;
-    if (r->rotary_dim > 0 && (!cos_sin || !aligned(cos_sin, 16))) return QLI_ERR_INVALID_ARG;
+    s = rotation_args(r, tokens, q, q_stride, k, k_stride, q_weight, k_weight, positions, cos_sin, q_out, q_out_stride, k_out,
+                      k_out_stride, workspace, &a);
+    if (s != QLI_OK || tokens == 0 || r->num_heads_q + r->num_heads_k == 0) return s;
     int sms = device_sms(nullptr);
     if (sms < 0) return QLI_ERR_CUDA;
     if (sms == 0) return QLI_ERR_NO_DEVICE;
-    a.positions = positions;
-    a.cos_sin = cos_sin;
-    a.err = static_cast<uint32_t*>(workspace);
-    a.tokens = tokens;
-    a.rotary = r->rotary_dim;
-    a.max_positions = r->max_positions;
-    a.interleaved = r->interleaved;
-    a.norm = r->norm;
-    a.eps = r->eps;
     cudaError_t e = launch_norm_rope(a, r->head_dim, r->dtype == QLI_ACT_F16, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
@@ -746,6 +766,31 @@ qli_status qli_kv_write(const qli_problem* p, const qli_attention* a, int64_t to
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 
+qli_status qli_kv_append(const qli_problem* p, const qli_attention* a, const qli_rotation* r, int64_t tokens, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const void* q_weight, const void* k_weight, const int32_t* positions, const float* cos_sin,
+                         const int32_t* token_batch, const int32_t* token_pos, const int32_t* block_table, void* q_out,
+                         int64_t q_out_stride, void* kv, void* workspace, size_t workspace_bytes, void* stream)
+{
+    qli_status s = check_rotation(r, nullptr);
+    if (s != QLI_OK) return s;
+    if (tokens < 0 || tokens > kMaxTokens) return QLI_ERR_INVALID_ARG;
+    s = check_attention(a, nullptr);
+    if (s != QLI_OK) return s;
+    if (r->num_heads_k != a->num_heads_kv || r->head_dim != a->head_dim || r->dtype != a->dtype) return QLI_ERR_INVALID_ARG;
+    KvArgs c;
+    NormRopeArgs n;
+    int sms = 0;
+    s = rotation_args(r, tokens, q, q_stride, k, k_stride, q_weight, k_weight, positions, cos_sin, q_out, q_out_stride, nullptr,
+                      0, workspace, &n, false);
+    if (s != QLI_OK) return s;
+    s = kv_args(p, a, tokens, k, k_stride, v, v_stride, token_batch, token_pos, block_table, kv, workspace, workspace_bytes, &c,
+                &sms);
+    if (s != QLI_OK || tokens == 0) return s;
+    cudaError_t e = launch_kv_append(n, c, v, kv, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
 qli_status qli_kv_read(const qli_problem* p, const qli_attention* a, int64_t tokens, const int32_t* token_batch,
                        const int32_t* token_pos, const int32_t* block_table, const void* kv, void* k,
                        int64_t k_stride, void* v, int64_t v_stride, void* workspace, size_t workspace_bytes,
@@ -801,6 +846,52 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
     A.v_scale = a->v_scale;
     cudaError_t e = launch_attention(A, a->head_dim, a->dtype == QLI_ACT_F16, a->kv_dtype == QLI_KV_E2M1, sms,
                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
+}
+
+qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks, const void* query,
+                               int64_t q_stride, const int32_t* seq_lens_q, const int32_t* seq_lens_k,
+                               const int32_t* block_table, const void* kv, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    qli_status s = check(p, nullptr);
+    if (s != QLI_OK) return s;
+    s = check_attention(a, nullptr);
+    if (s != QLI_OK) return s;
+    if (window < 0 || sinks < 0) return QLI_ERR_INVALID_ARG;
+    if (workspace && (workspace_bytes < kWsHeaderBytes || !aligned(workspace, 256))) return QLI_ERR_INVALID_ARG;
+    PagedArgs A;
+    std::memset(&A, 0, sizeof(A));
+    A.p = params_of(p);
+    A.q_stride = token_stride(q_stride, a->num_heads_q, a->head_dim);
+    A.page_bytes = kv_page_bytes(p, a);
+    if (A.q_stride < 0 || A.page_bytes < 0) return QLI_ERR_INVALID_ARG;
+    if (A.p.rows == 0) return QLI_OK;
+    if (!query || !out || !aligned(query, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return QLI_ERR_INVALID_ARG;
+    if (A.p.batch > 0 && (!seq_lens_k || !block_table || !kv || !aligned(kv, 16))) return QLI_ERR_INVALID_ARG;
+    if (A.p.layout_tnd && A.p.batch > 0 && !seq_lens_q) return QLI_ERR_INVALID_ARG;
+    if ((int64_t)A.p.rows * a->num_heads_q >= (INT64_C(1) << 28)) return QLI_ERR_UNSUPPORTED;    // grid limit
+    int sms = device_sms(nullptr);
+    if (sms < 0) return QLI_ERR_CUDA;
+    if (sms == 0) return QLI_ERR_NO_DEVICE;
+    A.query = query;
+    A.seq_lens_q = seq_lens_q;
+    A.seq_lens_k = seq_lens_k;
+    A.block_table = block_table;
+    A.kv = static_cast<const uint8_t*>(kv);
+    A.out = out;
+    A.lse = lse;
+    A.err = static_cast<uint32_t*>(workspace);
+    A.entry_bytes = (int32_t)entry_bytes_of(a);
+    A.heads_q = a->num_heads_q;
+    A.heads_kv = a->num_heads_kv;
+    A.window = window;
+    A.sinks = sinks;
+    A.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : 1.0f / sqrtf((float)a->head_dim);
+    A.k_scale = a->k_scale;
+    A.v_scale = a->v_scale;
+    cudaError_t e = launch_paged_attention(A, a->head_dim, a->dtype == QLI_ACT_F16, a->kv_dtype == QLI_KV_E2M1, sms,
+                                           static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
 }
 

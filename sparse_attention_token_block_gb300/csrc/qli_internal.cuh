@@ -404,6 +404,9 @@ struct KvArgs {
 };
 cudaError_t launch_kv_write(const KvArgs& a, int sms, const void* k, const void* v, void* kv, cudaStream_t st);
 cudaError_t launch_kv_read(const KvArgs& a, int sms, const void* kv, void* k, void* v, cudaStream_t st);
+// Norm, rotation and cache write in one pass (qli_kv_append.cu): `a`'s key side has no output, `c` takes the
+// values' token stride in stride[1]
+cudaError_t launch_kv_append(const NormRopeArgs& a, const KvArgs& c, const void* v, void* kv, int sms, cudaStream_t st);
 
 // Tensor map (a CUtensorMap) of a pool of `rows` entries of `entry_bytes` bytes in a row: 8-byte elements,
 // boxes one entry high and `box_bytes` wide (at most 2048; past the entry's end they are filled with zeros)

@@ -17,8 +17,6 @@
 // length: five CTAs per SM instead of four, or two or eight tokens under way, change nothing).
 #include <cuda_runtime.h>
 
-#include <cfloat>
-
 #include "qli_kv.cuh"
 
 namespace qli {
@@ -59,92 +57,6 @@ __device__ __forceinline__ void find_entries(const KvArgs& a, int64_t t0, int n,
                                              a.entry_bytes, &bits);
         if (bits && a.err) atomicOr(a.err, bits);
     }
-}
-
-// y <- y / d for eight elements whose largest quotient is `top`: a reciprocal and remainder corrections
-// where they give the correctly rounded quotient, else divisions.  The corrections can lose the sign
-// of a zero quotient; kSign keeps it.
-template <bool kSign>
-__device__ __forceinline__ void divide8(float (&y)[8], float d, float top)
-{
-    if (top <= FLT_MAX && ptx::reciprocal_ok(d)) {
-        const float r = __frcp_rn(d);
-        const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-d, -d);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float lo, hi;
-            ptx::unpack2(ptx::quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), lo, hi);
-            y[i] = kSign ? copysignf(lo, y[i]) : lo;
-            y[i + 1] = kSign ? copysignf(hi, y[i + 1]) : hi;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], d);
-    }
-}
-
-// The correctly rounded quotients y / d of a finite y and a d of at most four significant bits (a scale,
-// 6 or 7), from r within an ulp of 1 / d: q = RN(y r) is within two ulps of y / d, its remainder
-// y - q d is exact in a fused multiply-add, and q + (y - q d) r lies within 2^-21 ulp of y / d.
-// Rounded, that is the quotient rounded: y / d is no midpoint of two fp32 numbers (a 25-bit number
-// times d has more bits than y) and no nearer to one than 2^-5 ulp.  Quotients below 2^-126 may
-// differ, but give code 0 and scale 0 either way.
-__device__ __forceinline__ uint64_t short_quotient2(uint64_t Y, uint64_t R, uint64_t ND)
-{
-    const uint64_t Q = ptx::mul2(Y, R);
-    return ptx::fma2(ptx::fma2(Q, ND, Y), R, Q);
-}
-
-// Codes of eight elements y and the scale byte of their block, whose largest magnitude is amax
-template <bool E2M1>
-__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float amax, uint32_t& scale)
-{
-    constexpr float kTop = E2M1 ? 6.0f : 7.0f, kTopInv = 1.0f / kTop;
-    if (!(amax <= FLT_MAX)) {                          // y = x / g overflowed: the largest scale, codes +-Q or 0
-        scale = 0x7E;
-        uint32_t code = 0;
-        for (int i = 0; i < 8; ++i) {
-            const float q = fminf(fmaxf(__fdiv_rn(y[i], 448.0f), -kTop), kTop);
-            uint32_t c = (uint32_t)__float2int_rn(q) & 15u;
-            if (E2M1) {
-                asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
-                    : "=r"(c)
-                    : "f"(0.0f), "f"(q));
-                c &= 15u;
-            }
-            code |= c << (4 * i);
-        }
-        return code;
-    }
-    float s, dummy;
-    ptx::unpack2(short_quotient2(ptx::pack2(amax, 0.0f), ptx::pack2(kTopInv, kTopInv), ptx::pack2(-kTop, -kTop)), s, dummy);
-    scale = float_to_e4m3(fminf(s, 448.0f));
-    s = e4m3_to_float(scale);
-    if (s == 0.0f) return 0u;
-    const float r = ptx::rcp_approx(s);
-    const uint64_t R = ptx::pack2(r, r), NS = ptx::pack2(-s, -s);
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) ptx::unpack2(short_quotient2(ptx::pack2(y[i], y[i + 1]), R, NS), q[i], q[i + 1]);
-    uint32_t code = 0;
-    if (E2M1) {
-        uint32_t byte[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (the correction can lose the sign of a zero quotient, which the code keeps)
-            const float lo = copysignf(q[2 * i], y[2 * i]), hi = copysignf(q[2 * i + 1], y[2 * i + 1]);
-            asm("{\n\t.reg .b8 d;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\n\tmov.b32 %0, {d, 0, 0, 0};\n\t}"
-                : "=r"(byte[i])
-                : "f"(hi), "f"(lo));
-        }
-        code = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
-    } else {
-        // q + 1.5 * 2^23 rounds q to an integer (ties to even), whose two's complement ends the sum's bits
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            code |= (__float_as_uint(fminf(fmaxf(q[i], -7.0f), 7.0f) + 12582912.0f) & 15u) << (4 * i);
-    }
-    return code;
 }
 
 template <bool F16, bool E2M1>
@@ -193,16 +105,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(KvArgs a, const ui
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                if (gi != 0.0f) {
-                    // a power of two: the product with its reciprocal is the quotient
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] *= gi;
-                    amax *= gi;
-                } else {
-                    // (the division is monotone: the largest quotient is the largest magnitude's)
-                    amax = __fdiv_rn(amax, g);
-                    divide8<E2M1>(y, g, amax);
-                }
+                divide_by_factor<E2M1>(y, amax, g, gi);
                 uint32_t scale;
                 const uint32_t code = quantize8<E2M1>(y, amax, scale);
                 const int64_t at = live && l < n ? entry[l] : -1;

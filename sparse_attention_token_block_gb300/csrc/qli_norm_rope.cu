@@ -13,7 +13,7 @@
 // 96 us = 6.0 TB/s, 0.88 of a copy's rate; one token 1.9 us.
 #include <cuda_runtime.h>
 
-#include "qli_kv.cuh"
+#include "qli_norm_rope.cuh"
 
 namespace qli {
 
@@ -21,24 +21,6 @@ namespace {
 
 constexpr int kNormThreads = 128;
 constexpr int kMostHeads = 9;              // heads of a lane under way together: 64 registers, eight CTAs an SM
-
-// Four activations in two words as two packed pairs
-template <bool F16>
-__device__ __forceinline__ void unpack4(const uint2& u, uint64_t (&y)[2])
-{
-    const float2 a = act2_to_float2<F16>(u.x), b = act2_to_float2<F16>(u.y);
-    y[0] = ptx::pack2(a.x, a.y);
-    y[1] = ptx::pack2(b.x, b.y);
-}
-
-template <bool F16>
-__device__ __forceinline__ uint2 pack4(const uint64_t (&y)[2])
-{
-    float a, b, c, d;
-    ptx::unpack2(y[0], a, b);
-    ptx::unpack2(y[1], c, d);
-    return make_uint2(float2_to_act2<F16>(a, b), float2_to_act2<F16>(c, d));
-}
 
 template <bool F16, int D, bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(kNormThreads, kHeads > 1 ? 8 : 1) norm_rope_kernel(NormRopeArgs a)
@@ -97,45 +79,7 @@ __global__ void __launch_bounds__(kNormThreads, kHeads > 1 ? 8 : 1) norm_rope_ke
             uint64_t y[2][2];                                      // the two chunks, in pairs
             unpack4<F16>(x[u][0], y[0]);
             unpack4<F16>(x[u][1], y[1]);
-            if (a.norm) {
-                uint64_t sq = ptx::mul2(y[0][0], y[0][0]);
-                sq = ptx::fma2(y[0][1], y[0][1], sq);
-                sq = ptx::fma2(y[1][0], y[1][0], sq);
-                sq = ptx::fma2(y[1][1], y[1][1], sq);
-                float ss, odd;
-                ptx::unpack2(sq, ss, odd);
-                ss += odd;
-#pragma unroll
-                for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-                const uint64_t rr = ptx::pack2(r, r);
-                const float4 g0 = *reinterpret_cast<const float4*>(&weight[side][c0]);
-                const float4 g1 = *reinterpret_cast<const float4*>(&weight[side][c1]);
-                y[0][0] = ptx::mul2(ptx::mul2(y[0][0], rr), ptx::pack2(g0.x, g0.y));
-                y[0][1] = ptx::mul2(ptx::mul2(y[0][1], rr), ptx::pack2(g0.z, g0.w));
-                y[1][0] = ptx::mul2(ptx::mul2(y[1][0], rr), ptx::pack2(g1.x, g1.y));
-                y[1][1] = ptx::mul2(ptx::mul2(y[1][1], rr), ptx::pack2(g1.z, g1.w));
-            }
-            if (rot) {
-                if (kInterleaved) {
-                    // a pair of elements is a pair of the rotation
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float ya, yb;
-                        ptx::unpack2(y[i >> 1][i & 1], ya, yb);
-                        y[i >> 1][i & 1] = ptx::pack2(ya * cs[i] - yb * cs[4 + i], yb * cs[i] + ya * cs[4 + i]);
-                    }
-                } else {
-                    // the first chunk's elements turn with the second's
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint64_t c = ptx::pack2(cs[2 * i], cs[2 * i + 1]), s = ptx::pack2(cs[4 + 2 * i], cs[5 + 2 * i]);
-                        const uint64_t ns = ptx::pack2(-cs[4 + 2 * i], -cs[5 + 2 * i]), ya = y[0][i], yb = y[1][i];
-                        y[0][i] = ptx::fma2(ya, c, ptx::mul2(yb, ns));
-                        y[1][i] = ptx::fma2(yb, c, ptx::mul2(ya, s));
-                    }
-                }
-            }
+            norm_and_turn<D, kInterleaved>(y, a.norm, a.eps, &weight[side][c0], &weight[side][c1], rot, cs);
             if (h >= heads) continue;
             uint2 lo = pack4<F16>(y[0]), hi = pack4<F16>(y[1]);
             if (!ok) lo = hi = make_uint2(0u, 0u);

@@ -1,0 +1,672 @@
+// qli_paged_attention.cu -- attention of each sequence's new tokens over the cached positions that they see: all
+// of them up to the row's own (causal), or a sliding window of them and the first few (sinks); the entries are
+// held in 4 bits:
+//     z_j = scale * q_h . K_j,   out_h = sum_j softmax(z)_j V_j,   lse_h = ln sum_j exp(z_j)
+//
+// A unit is a KV head with up to 8 * NT of the (token, query head) rows that read it; a warp carries it over its
+// share of the positions, 32 a step:
+//   * logits:  S^T (16 positions x 8 rows) = K Q^T, keys decoded from shared memory straight into the fragment;
+//   * softmax: running maximum and sum per row in fp32 (base 2); the accumulators are rescaled only when a logit
+//     exceeds the maximum in use by more than 8;
+//   * output:  O^T (D x 8 rows) += V^T P^T, P rounded to fp16 (values of codes times scales are exact in fp16).
+// The units of `per_cta` KV heads of the same rows share a CTA, and a copy warp brings their bytes of 16 positions
+// of a page by one TMA box; warps that are left over (`parts`) and the CTAs of a cluster (`splits`) share the
+// steps in turn, and their partial results are joined in shared memory in a fixed order.
+//
+// Positions that a step holds beyond what a row sees are masked, and so are those on pages outside the pool (of
+// which nothing is copied).  What lies there is arbitrary: scales of NaN among the values are taken as numbers
+// and their positions' keys as NaN instead, which the mask hides from the rows that do not see them.
+//
+// Every wait is bounded (0.2 s): on expiry the kernel records kErrTimeout, writes NaN, lets its copies land and
+// returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <cstring>
+
+#include "qli_paged.cuh"
+
+namespace qli {
+
+namespace {
+
+constexpr int kWarps = 8;                         // with a unit each, and one that copies
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kStep = 32;                         // positions
+constexpr int kMaxSplits = 8;                     // a portable cluster
+constexpr int kMaxStages = 4;
+constexpr int kHalfSmem = 112 * 1024;             // dynamic, of one of two CTAs on an SM
+constexpr uint64_t kWaitLimitNs = 200000000ull;
+constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
+
+// How a launch is laid out (host)
+struct Layout {
+    int32_t blocks;        // BSND: row blocks per sequence
+    int32_t per_cta;       // KV heads of a CTA
+    int32_t slices;        // CTAs a block's heads take
+    int32_t parts;         // warps that share a unit: kWarps / per_cta
+    int32_t splits;        // CTAs of a cluster
+    int32_t stages;        // of a ring
+    int32_t row_bytes;     // from one position to the next in a ring
+    uint32_t block_recip;
+};
+
+constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 128 ? 2 : 1; }
+
+// The whole warp waits for the phase of a barrier; false (for every lane) when a wait gave up
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        const bool done = ptx::mbar_try_wait_sleep(bar, parity, 100000u);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort, err);
+}
+
+// Position (of a group of eight) that row r of an 8-row fragment holds.  With a stride of 32 or 96 modulo 128
+// bytes between positions, the two that a quarter-warp reads of K and the four that it reads of V then lie in
+// different banks.
+__device__ __forceinline__ int entry_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
+{
+    static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+template <bool F16, bool E2M1, int D, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
+    paged_attention_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Layout L,
+                           const __grid_constant__ CUtensorMap pages)
+{
+    constexpr int kUnit = kv_unit_bytes(D);
+    constexpr int M = 8 * NT;                     // rows of a unit
+    constexpr int NW = D / 32;                    // words of key codes per lane and position
+    constexpr int MO = D / 16;                    // 16-row tiles of the output
+    constexpr int kHeadStride = D + 4;            // of partial outputs, in floats
+    __shared__ uint64_t full[kWarps][kMaxStages], freed[kWarps][kMaxStages];
+    __shared__ uint32_t live[kWarps][kMaxStages];         // which 16 of a step's positions lie in the pool
+    __shared__ uint32_t abort;
+    __shared__ RowBlock blk;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
+    const int group = a.heads_q / a.heads_kv;
+    if (tid == 0) abort = 0;
+    if (tid < kWarps) {
+        for (int x = 0; x < L.stages; ++x) {
+            ptx::mbar_init(&full[tid][x], 1);
+            ptx::mbar_init(&freed[tid][x], L.per_cta);
+        }
+        ptx::fence_mbar_init();
+    }
+    ptx::pdl_wait();
+    const uint32_t task = blockIdx.x / (uint32_t)L.splits, slot = task / (uint32_t)L.slices;
+    const int u0 = (int)(task - slot * L.slices) * L.per_cta, nu = min(L.per_cta, a.heads_kv - u0);
+    if (!find_rows(a, slot, L.blocks, M, group, &blk)) {
+        // prefix sums that are not: every row is zero
+        clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
+        return;
+    }
+    if (blk.rows == 0) return;                    // (the whole cluster)
+    const KeyRange<kStep> range = key_range<kStep>(a, blk, group);
+    // the steps of this CTA and part: numbers part + parts * (rank + splits * i)
+    const int lanes_of = L.parts * L.splits;
+    auto steps_of = [&](int part) { return max(0, (range.steps - (rank * L.parts + part) + lanes_of - 1) / lanes_of); };
+
+    const int unit = wid / L.parts, part = wid - unit * L.parts;
+    const int r = lane >> 2, c = lane & 3;
+    const bool works = wid < kWarps && unit < nu;
+    float o[NT][MO][4], m[NT][2], l[NT][2];
+    if (wid == kWarps) {
+        // ---------------------------------------------------------------- copies: a lane per part
+        if (lane < L.parts) {
+            const int n = steps_of(lane), lo = u0 * kUnit & ~15;
+            const bool stall = a.p.test_stall == 1;            // test switch: nothing arrives, the waits run out
+            const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
+            const uint32_t bs = (uint32_t)a.p.block_size, bytes = 16 * L.row_bytes;
+            uint8_t* ring = smem + lane * L.stages * 2 * bytes;
+            // pages and positions in them of a step's two boxes; -1: nothing to copy
+            int page[2], at[2];
+            auto resolve = [&](int i) {
+                const int pos = range.position((i * L.splits + rank) * L.parts + lane), end = range.limit(pos);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t j = pos + 16 * x;
+                    uint32_t b = __umulhi(j, L.block_recip);
+                    if (j - b * bs >= bs) ++b;
+                    at[x] = (int)(j - b * bs);
+                    page[x] = (int)j < end ? table[b] : INT32_MIN;
+                }
+            };
+            if (n > 0) resolve(0);
+            int stage = 0, parity = 1;
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                uint32_t mask = 0;
+                int pg[2], ps[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    pg[x] = page[x], ps[x] = at[x];
+                    if (pg[x] >= 0 && pg[x] < a.p.num_blocks) mask |= 1u << x;
+                    else if (pg[x] != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
+                }
+                if (i + 1 < n) resolve(i + 1);
+                if (!ptx::mbar_try_wait(&freed[lane][stage], parity)) {
+                    const uint64_t t0 = ptx::globaltimer();
+                    while (ok && !ptx::mbar_try_wait_sleep(&freed[lane][stage], parity, 100000u)) {
+                        if (*(volatile uint32_t*)&abort) ok = false;
+                        else if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+                            abort = 1;
+                            if (a.err) atomicOr(a.err, kErrTimeout);
+                            ok = false;
+                        }
+                    }
+                    if (!ok) break;
+                }
+                live[lane][stage] = mask;
+                ptx::mbar_arrive_expect_tx(&full[lane][stage], stall ? bytes : __popc(mask) * bytes);
+                if (!stall) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (mask >> x & 1)
+                            ptx::tma_load_3d(ring + (2 * stage + x) * bytes, &pages, lo / 8, ps[x], pg[x], &full[lane][stage]);
+                }
+                if (++stage == L.stages) stage = 0, parity ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (works) {
+        const int kvh = u0 + unit;
+        // query fragments: row r of each block of eight, this lane's quarter of D; float16 as they are, bfloat16
+        // in fp16, scaled by a power of two of the row's largest magnitude
+        uint32_t q[NT][NW][4];
+        float f[NT][2];                           // base-2 logit factor of rows 2c and 2c + 1
+        int hi[NT][2];                            // positions that they see
+        const float factor = a.softmax_scale * a.k_scale * 1.4426950408889634f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int i = blk.first + 8 * t + r, tok = i / group;
+            uint4 raw[NW];
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                raw[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * t + r < blk.rows)
+                    raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.query) + (blk.row0 + tok) * a.q_stride +
+                                                             (int64_t)(kvh * group + i - tok * group) * D + c * (D / 4) + 8 * j);
+            }
+            uint32_t w[NW][4];
+#pragma unroll
+            for (int j = 0; j < NW; ++j) w[j][0] = raw[j].x, w[j][1] = raw[j].y, w[j][2] = raw[j].z, w[j][3] = raw[j].w;
+            if constexpr (F16) {
+#pragma unroll
+                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)     // elements 2e, 2e + 1 or e, e + 4
+                        q[t][j][e] = E2M1 ? w[j][e] : __byte_perm(w[j][e / 2], w[j][2 + e / 2], e & 1 ? 0x7632 : 0x5410);
+                f[t][0] = f[t][1] = fminf(factor, 3.0e38f);
+            } else {
+                float big = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = act2_to_float2<F16>(w[j][e]);
+                        big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+                const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of big)
+#pragma unroll
+                for (int j = 0; j < NW; ++j) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = act2_to_float2<F16>(w[j][e]);
+                        x[2 * e] = v.x * down;
+                        x[2 * e + 1] = v.y * down;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        q[t][j][e] = E2M1 ? float2_to_act2<true>(x[2 * e], x[2 * e + 1]) : float2_to_act2<true>(x[e], x[e + 4]);
+                }
+                const float up = __uint_as_float(ex << 23) * factor;
+                f[t][0] = fminf(__shfl_sync(0xffffffffu, up, 8 * c), 3.0e38f);
+                f[t][1] = fminf(__shfl_sync(0xffffffffu, up, 8 * c + 4), 3.0e38f);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) hi[t][e] = seen_end(a, blk, (blk.first + 8 * t + 2 * c + e) / group);
+#pragma unroll
+            for (int i2 = 0; i2 < MO; ++i2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i2][e] = 0.0f;
+            m[t][0] = m[t][1] = -FLT_MAX;
+            l[t][0] = l[t][1] = 0.0f;
+        }
+        const int steps = steps_of(part), step_bytes = kStep * L.row_bytes, row = L.row_bytes;
+        const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
+        const uint8_t* head = smem + part * L.stages * step_bytes + kvh * kUnit - (u0 * kUnit & ~15);
+        const uint8_t* kc0 = head + tk * row + (D / 8) * c;                        // the lane's key codes and scales,
+        const uint8_t* ks0 = head + tk * row + D + (D == 128 ? 2 * c : c);
+        const uint8_t* vc0 = head + ta * row + D / 2 + (D / 16) * r;               // value codes and scales
+        const uint8_t* vs0 = head + ta * row + D + D / 16 + (D == 128 ? r : r >> 1);
+        const int vb = (tb - ta) * row;
+        int stage = 0, parity = 0;
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st) {
+            const int pos = range.position((st * L.splits + rank) * L.parts + part);
+            if (!wait_bounded(&full[part][stage], parity, &abort, a.err)) break;
+            const uint32_t mask = live[part][stage];
+            const uint8_t* kc = kc0 + stage * step_bytes;
+            const uint8_t* ks = ks0 + stage * step_bytes;
+            const uint8_t* va = vc0 + stage * step_bytes;
+            const uint8_t* vs = vs0 + stage * step_bytes;
+            // ---- logits of two tiles of 16 positions
+            float s[2][NT][4];
+            uint32_t w[2][2][NW];                  // tile, row r or r + 8: codes
+            PairScale g[2][2][D / 64];             // and the scales of the lane's blocks
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    load_words<NW>(kc + (16 * u + 8 * y) * row, w[u][y]);
+                    const uint8_t* x = ks + (16 * u + 8 * y) * row;
+                    // a NaN (0x7F or 0xFF) among the values' scales becomes one of the keys'
+                    if constexpr (D == 128) {
+                        uint32_t b = *reinterpret_cast<const uint16_t*>(x);
+                        const uint32_t v = *reinterpret_cast<const uint16_t*>(x + D / 16);
+                        if (__vcmpeq4(v & 0x7F7Fu, 0x00007F7Fu) & 0xFFFFu) b = 0x7F7Fu;
+                        const uint32_t h = e4m3x2_to_f16x2(b);
+                        g[u][y][0] = pair_scale<E2M1>(__byte_perm(h, 0, 0x1010));
+                        g[u][y][1] = pair_scale<E2M1>(__byte_perm(h, 0, 0x3232));
+                    } else {
+                        uint32_t b = *x;
+                        if ((x[D / 16] & 0x7F) == 0x7F) b = 0x7F;
+                        g[u][y][0] = pair_scale<E2M1>(__byte_perm(e4m3x2_to_f16x2(b), 0, 0x1010));
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t x[4], y[4];
+                    decode_pairs<E2M1>(w[u][0][j], g[u][0][j / 2], x);
+                    decode_pairs<E2M1>(w[u][1][j], g[u][1][j / 2], y);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        ptx::mma_16816(s[u][t], x[0], y[0], x[1], y[1], q[t][j][0], q[t][j][1]);
+                        ptx::mma_16816(s[u][t], x[2], y[2], x[3], y[3], q[t][j][2], q[t][j][3]);
+                    }
+                }
+            // ---- softmax: masked positions get -infinity
+            float z[2][NT][4], over = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[u][t][e] = fmaf(s[u][t][e], f[t][e & 1], -m[t][e & 1]);
+            if (mask != 3u || !range.all_see(pos)) {
+                const int limit = range.limit(pos);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = pos + 16 * u + 8 * (e >> 1) + tk;
+                            if (!(mask >> u & 1) || j >= limit || !sees(a, hi[t][e & 1], j)) z[u][t][e] = -INFINITY;
+                        }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    over = fmaxf(over, fmaxf(fmaxf(z[u][t][0], z[u][t][1]), fmaxf(z[u][t][2], z[u][t][3])));
+            if (__any_sync(0xffffffffu, over > kRescale)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = m[t][e];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int y = e; y < 4; y += 2)
+                                if (z[u][t][y] > -INFINITY) top = fmaxf(top, s[u][t][y] * f[t][e]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float down = ptx::ex2(m[t][e] - top);
+                        m[t][e] = top;
+                        l[t][e] *= down;
+#pragma unroll
+                        for (int i = 0; i < MO; ++i) {
+                            o[t][i][e] *= down;
+                            o[t][i][e + 2] *= down;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int y = e; y < 4; y += 2)
+                                if (z[u][t][y] > -INFINITY) z[u][t][y] = fmaf(s[u][t][y], f[t][e], -top);
+                    }
+            }
+            // each probability rounded to fp16 (the sum keeps the unrounded ones)
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[u][t][e] = ptx::ex2(z[u][t][e]);
+                    l[t][0] += z[u][t][0] + z[u][t][2];
+                    l[t][1] += z[u][t][1] + z[u][t][3];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        pb[u][t][y] = ptx::transpose_8x8(float2_to_act2<true>(z[u][t][2 * y], z[u][t][2 * y + 1]));
+                }
+            // ---- output
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t* x0 = vs + 16 * u * row;
+                const PairScale sab = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[vb] << 8)));
+                const PairScale scd = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[8 * row] | (uint32_t)x0[vb + 8 * row] << 8)));
+                uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
+                load_words<NW / 2>(va + 16 * u * row, wa);
+                load_words<NW / 2>(va + 16 * u * row + vb, wb);
+                load_words<NW / 2>(va + (16 * u + 8) * row, wc);
+                load_words<NW / 2>(va + (16 * u + 8) * row + vb, wd);
+#pragma unroll
+                for (int j = 0; j < NW / 2; ++j) {
+                    uint32_t x[8], y[8];
+                    decode_across<E2M1>(wa[j], wb[j], sab, x);
+                    decode_across<E2M1>(wc[j], wd[j], scd, y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            ptx::mma_16816(o[t][4 * j + i], x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], pb[u][t][0], pb[u][t][1]);
+                }
+            }
+            __syncwarp();                          // every lane is done with the stage
+            if (lane == 0) ptx::mbar_arrive(&freed[part][stage]);
+            if (++stage == L.stages) stage = 0, parity ^= 1;
+        }
+        // the sums over the lanes that share a row's column
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+            }
+    } else {
+        // a warp without a unit hands its stages straight back (the barriers count per_cta warps)
+        const int steps = unit < L.per_cta ? steps_of(part) : 0;
+        int stage = 0, parity = 0;
+        for (int st = 0; st < steps; ++st) {
+            if (!wait_bounded(&full[part][stage], parity, &abort, a.err)) break;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&freed[part][stage]);
+            if (++stage == L.stages) stage = 0, parity ^= 1;
+        }
+    }
+
+    // ---- join and write.  Lane (r, c) holds elements r * D / 8 ... of rows 2c and 2c + 1 of each block.
+    __syncthreads();                               // the rings are free
+    const bool failed = abort != 0;
+    if (failed) {                                  // copies that are still under way land before the CTA ends
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kWaitLimitNs) {
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = __int_as_float(0x7FC00000);
+    }
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+    // element 0 of row `i` of unit `un` in the output, in heads of D
+    auto out_head = [&](int un, int i) {
+        const int at = blk.first + i, tok = at / group;
+        return (blk.row0 + tok) * a.heads_q + (u0 + un) * group + at - tok * group;
+    };
+    if (L.parts * L.splits == 1) {
+        if (!works) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 8 * t + 2 * c + e;
+                if (i >= blk.rows) continue;
+                const float sum = l[t][e];
+                const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+                uint32_t w[MO];
+#pragma unroll
+                for (int x = 0; x < MO; ++x) w[x] = float2_to_act2<F16>(o[t][x][e] * inv, o[t][x][e + 2] * inv);
+                const int64_t at = out_head(unit, i);
+                uint4* dst = reinterpret_cast<uint4*>(out + at * D + r * (D / 8));
+#pragma unroll
+                for (int x = 0; x < MO / 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                if (a.lse && r == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (m[t][e] + log2f(sum)) * 0.6931471805599453f;
+            }
+        return;
+    }
+    // partial outputs [warp][M rows][kHeadStride], (maximum, sum) [warp][M rows], and the same pairs of the CTA's
+    // units once its warps are joined
+    float* part_o = reinterpret_cast<float*>(smem);
+    float2* part_ml = reinterpret_cast<float2*>(part_o + kWarps * M * kHeadStride);
+    float2* unit_ml = part_ml + kWarps * M;
+    if (works) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = wid * M + 8 * t + 2 * c + e;
+                float4* dst = reinterpret_cast<float4*>(part_o + h * kHeadStride + r * (D / 8));
+#pragma unroll
+                for (int i = 0; i < MO / 2; ++i)
+                    dst[i] = make_float4(o[t][2 * i][e], o[t][2 * i][e + 2], o[t][2 * i + 1][e], o[t][2 * i + 1][e + 2]);
+                if (r == 0) (L.parts > 1 ? part_ml : unit_ml)[h] = make_float2(m[t][e], l[t][e]);
+            }
+    }
+    const int pieces = nu * M * (D / 4);           // 4 elements of a row
+    auto finish = [&](int hh, int d4, const float4& v, float top, float sum) {
+        const int un = hh / M, i = hh - un * M;
+        if (i >= blk.rows) return;
+        const int64_t at = out_head(un, i);
+        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        *reinterpret_cast<uint2*>(out + at * D + 4 * d4) =
+            make_uint2(float2_to_act2<F16>(v.x * inv, v.y * inv), float2_to_act2<F16>(v.z * inv, v.w * inv));
+        if (a.lse && d4 == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    };
+    if (L.parts > 1) {
+        // the warps of each unit; the joined result replaces the first warp's
+        __syncthreads();
+        for (int i = tid; i < pieces; i += kThreads) {
+            const int hh = i / (D / 4), d4 = i % (D / 4), un = hh / M;
+            const int at = hh + un * (L.parts - 1) * M;            // of the unit's first warp
+            float2 ml[kWarps];
+            float4 v[kWarps];
+            float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                ml[x] = make_float2(-FLT_MAX, 0.0f);
+                v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x < L.parts) {
+                    ml[x] = part_ml[at + x * M];
+                    v[x] = *reinterpret_cast<const float4*>(part_o + (at + x * M) * kHeadStride + 4 * d4);
+                }
+                top = fmaxf(top, ml[x].x);
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float g = ptx::ex2(ml[x].x - top);
+                sum = fmaf(g, ml[x].y, sum);
+                acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
+                acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
+            }
+            if (L.splits == 1) {
+                finish(hh, d4, acc, top, sum);
+            } else {
+                *reinterpret_cast<float4*>(part_o + at * kHeadStride + 4 * d4) = acc;
+                if (d4 == 0) unit_ml[at] = make_float2(top, sum);
+            }
+        }
+        if (L.splits == 1) return;
+        __syncwarp();
+    }
+    ptx::cluster_sync();
+    for (int i = rank * kThreads + tid; i < pieces; i += L.splits * kThreads) {
+        const int hh = i / (D / 4), d4 = i % (D / 4), un = hh / M;
+        const int at = hh + un * (L.parts - 1) * M;
+        const uint32_t from_ml = ptx::smem_addr(unit_ml + at), from_o = ptx::smem_addr(part_o + at * kHeadStride + 4 * d4);
+        float2 ml[kMaxSplits];
+        float4 v[kMaxSplits];
+        float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) {
+            ml[x] = make_float2(-FLT_MAX, 0.0f);
+            v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (x < L.splits) {
+                ml[x] = ptx::ld_cluster2(ptx::cluster_addr(from_ml, x));
+                v[x] = ptx::ld_cluster4(ptx::cluster_addr(from_o, x));
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) top = fmaxf(top, ml[x].x);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int x = 0; x < kMaxSplits; ++x) {
+            const float g = ptx::ex2(ml[x].x - top);
+            sum = fmaf(g, ml[x].y, sum);
+            acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
+            acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
+        }
+        finish(hh, d4, acc, top, sum);
+    }
+    __syncwarp();
+    ptx::cluster_sync();                           // no CTA leaves while another reads its partial results
+}
+
+// Row stride in a ring of `heads` KV heads' bytes: 32 or 96 beyond a multiple of 128, with room for a start that
+// is no multiple of 16
+int ring_row(int heads, int unit)
+{
+    const int need = (heads * unit + 15 & ~15) + (heads * unit % 16 ? 16 : 0);
+    int row = need;
+    while (row % 128 != 32 && row % 128 != 96) row += 16;
+    return row;
+}
+
+template <bool F16, bool E2M1, int D, int NT>
+cudaError_t launch_shape(const PagedArgs& a, int sms, cudaStream_t st)
+{
+    constexpr int M = 8 * NT;
+    const int group = a.heads_q / a.heads_kv;
+    Layout L;
+    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
+    const int64_t slots = row_slots(a, M, group, &L.blocks);
+    const int64_t most = most_positions(a, M, group);        // of a row block
+    const int room = ctas_per_sm(D, NT) * sms;
+    L.per_cta = 1;
+    while (L.per_cta < kWarps && slots * ceil_div64(a.heads_kv, L.per_cta) > room) L.per_cta *= 2;
+    L.per_cta = std::min<int>(L.per_cta, a.heads_kv);
+    L.slices = (int)ceil_div64(a.heads_kv, L.per_cta);
+    L.per_cta = (int)ceil_div64(a.heads_kv, L.slices);
+    L.parts = kWarps / L.per_cta;
+    L.splits = 1;
+    while (L.splits < kMaxSplits && slots * L.slices * L.splits * 2 <= room && most >= kStep * L.parts * L.splits * 2) L.splits *= 2;
+    L.row_bytes = ring_row(L.per_cta, kv_unit_bytes(D));
+    const int step = L.parts * kStep * L.row_bytes;
+    L.stages = std::max(2, std::min(kMaxStages, kHalfSmem * (ctas_per_sm(D, NT) == 1 ? 2 : 1) / step));
+    const int join = L.parts * L.splits > 1 ? kWarps * M * ((D + 4) + 2 + 2) * 4 : 0;       // partial outputs, pairs twice
+    const int smem = std::max(L.stages * step, join);
+    const int64_t grid = slots * L.slices * L.splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    CUtensorMap pages;
+    std::memset(&pages, 0, sizeof(pages));
+    if (a.p.batch > 0 && !encode_page_map(&pages, a.kv, a.entry_bytes, a.p.block_size, a.page_bytes, a.p.num_blocks, L.row_bytes, 16))
+        return cudaErrorUnknown;
+    auto kernel = paged_attention_kernel<F16, E2M1, D, NT>;
+    constexpr int kMaxSmem = ctas_per_sm(D, NT) == 1 ? 220 * 1024 : kHalfSmem;
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? UINT64_C(1) << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, L, pages);
+}
+
+template <bool F16, bool E2M1>
+cudaError_t launch_type(const PagedArgs& a, int head_dim, int sms, cudaStream_t st)
+{
+    // rows per unit: as few blocks of eight as hold a sequence's, within the registers (an accumulator of D x 8 NT
+    // fp32 per warp)
+    const int64_t rows = (int64_t)(a.p.layout_tnd ? std::max(1, std::min(a.p.max_seqlen_q, a.p.total_q)) : a.p.s1) * (a.heads_q / a.heads_kv);
+    if (head_dim == 64) {
+        if (rows <= 8) return launch_shape<F16, E2M1, 64, 1>(a, sms, st);
+        if (rows <= 16) return launch_shape<F16, E2M1, 64, 2>(a, sms, st);
+        return launch_shape<F16, E2M1, 64, 4>(a, sms, st);
+    }
+    return rows <= 8 ? launch_shape<F16, E2M1, 128, 1>(a, sms, st) : launch_shape<F16, E2M1, 128, 2>(a, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
+{
+    if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
+    return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
+}
+
+}  // namespace qli
