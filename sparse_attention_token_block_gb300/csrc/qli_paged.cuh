@@ -108,43 +108,53 @@ __device__ __forceinline__ bool sees(const PagedArgs& a, int end, int j)
     return j < end && (a.window == 0 || j >= end - a.window || j < a.sinks);
 }
 
-// The positions that some row of a block sees, in steps of kStep: first those of the sinks that lie before the
-// windows, then from the first window's start (rounded down to 16 positions, which share a page) on
-template <int kStep>
+// The positions that some row of a block sees, in chunks of 16 (which share a page): first those of the sinks that
+// lie before the windows, then from the first window's start (rounded down to 16) on
+constexpr int kChunk = 16;
 struct KeyRange {
-    int base, end, steps;
-    int sink_end, sink_steps;
+    int base, end, chunks;
+    int sink_end, sink_chunks;
     int low, high;                         // positions [high, low) are seen by every row
-    int sinks;
 
-    __device__ __forceinline__ int position(int step) const
+    __device__ __forceinline__ int position(int chunk) const
     {
-        return step < sink_steps ? kStep * step : base + kStep * (step - sink_steps);
+        return chunk < sink_chunks ? kChunk * chunk : base + kChunk * (chunk - sink_chunks);
     }
-    // end of what the step at `pos` may count (a position is not counted as sink and as part of the window)
-    __device__ __forceinline__ int limit(int pos) const { return pos < sink_end ? sink_end : end; }
-    // whether every row sees all of the step at `pos`
-    __device__ __forceinline__ bool all_see(int pos) const
+    // end of what a chunk may count (a position is not counted as a sink and as part of the window)
+    __device__ __forceinline__ int limit(int chunk) const { return chunk < sink_chunks ? sink_end : end; }
+    // whether every row sees all of chunks [chunk, chunk + n)
+    __device__ __forceinline__ bool all_see(int chunk, int n) const
     {
-        return pos + kStep <= low && (pos >= high || pos + kStep <= sinks) && (pos >= base || pos + kStep <= sink_end);
+        const int pos = position(chunk), last = pos + kChunk * n;
+        return last <= low && (chunk >= sink_chunks ? pos >= high : last <= sink_end);
     }
 };
 
-template <int kStep>
-__device__ __forceinline__ KeyRange<kStep> key_range(const PagedArgs& a, const RowBlock& b, int group)
+__device__ __forceinline__ KeyRange key_range(const PagedArgs& a, const RowBlock& b, int group)
 {
-    KeyRange<kStep> r;
+    KeyRange r;
     const int t0 = b.first / group, t1 = min((b.first + b.rows - 1) / group, b.sq - 1);
-    r.sinks = a.sinks;
+    const int first = t0 < b.sq ? seen_end(a, b, t0) : 0;
     // (rows of a block behind the live ones see nothing)
-    r.low = (b.first + b.rows - 1) / group < b.sq ? seen_end(a, b, t0) : 0;
+    r.low = (b.first + b.rows - 1) / group < b.sq ? first : 0;
     r.end = t0 < b.sq ? seen_end(a, b, t1) : 0;
     r.high = a.window > 0 ? max(0, r.end - a.window) : 0;
-    r.base = a.window > 0 && t0 < b.sq ? max(0, seen_end(a, b, t0) - a.window) & ~15 : 0;
+    r.base = a.window > 0 ? max(0, first - a.window) & ~(kChunk - 1) : 0;
     r.sink_end = min(a.sinks, r.base);
-    r.sink_steps = (r.sink_end + kStep - 1) / kStep;
-    r.steps = r.end > 0 ? r.sink_steps + (r.end - r.base + kStep - 1) / kStep : 0;
+    r.sink_chunks = (r.sink_end + kChunk - 1) / kChunk;
+    r.chunks = r.end > 0 ? r.sink_chunks + (r.end - r.base + kChunk - 1) / kChunk : 0;
     return r;
+}
+
+// Page of a chunk and its position there; INT32_MIN: no row sees any of the chunk
+__device__ __forceinline__ int chunk_page(const PagedArgs& a, const KeyRange& r, const int32_t* table, uint32_t block_recip, int chunk,
+                                          int* at)
+{
+    const uint32_t bs = (uint32_t)a.p.block_size, j = (uint32_t)r.position(chunk);
+    uint32_t b = __umulhi(j, block_recip);         // the reciprocal rounded down gives the quotient or one less
+    if (j - b * bs >= bs) ++b;
+    *at = (int)(j - b * bs);
+    return chunk < r.chunks && (int)j < r.limit(chunk) ? table[b] : INT32_MIN;
 }
 
 // Most positions that a block of M rows goes over
@@ -172,6 +182,15 @@ __device__ __forceinline__ uint32_t finite_f16x2(uint32_t h)
     return h;
 }
 
+// Rows that read a KV head of one sequence, at most
+inline int64_t most_rows(const PagedArgs& a)
+{
+    const int64_t tokens = a.p.layout_tnd ? (a.p.max_seqlen_q < a.p.total_q ? a.p.max_seqlen_q : a.p.total_q) : a.p.s1;
+    return (tokens > 1 ? tokens : 1) * (a.heads_q / a.heads_kv);
+}
+
+// For many such rows (qli_paged_chunk.cu)
+cudaError_t launch_paged_chunk(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int64_t most_rows, int sms, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st);
 
 }  // namespace qli

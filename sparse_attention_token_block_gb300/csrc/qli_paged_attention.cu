@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kWarps = 8;                         // with a unit each, and one that copies
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStep = 32;                         // positions
+constexpr int kStep = 2 * kChunk;                 // positions
 constexpr int kMaxSplits = 8;                     // a portable cluster
 constexpr int kMaxStages = 4;
 constexpr int kHalfSmem = 112 * 1024;             // dynamic, of one of two CTAs on an SM
@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         return;
     }
     if (blk.rows == 0) return;                    // (the whole cluster)
-    const KeyRange<kStep> range = key_range<kStep>(a, blk, group);
+    const KeyRange range = key_range(a, blk, group);
     // the steps of this CTA and part: numbers part + parts * (rank + splits * i)
-    const int lanes_of = L.parts * L.splits;
-    auto steps_of = [&](int part) { return max(0, (range.steps - (rank * L.parts + part) + lanes_of - 1) / lanes_of); };
+    const int lanes_of = L.parts * L.splits, all_steps = (range.chunks + 1) / 2;
+    auto steps_of = [&](int part) { return max(0, (all_steps - (rank * L.parts + part) + lanes_of - 1) / lanes_of); };
 
     const int unit = wid / L.parts, part = wid - unit * L.parts;
     const int r = lane >> 2, c = lane & 3;
@@ -148,20 +148,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             const int n = steps_of(lane), lo = u0 * kUnit & ~15;
             const bool stall = a.p.test_stall == 1;            // test switch: nothing arrives, the waits run out
             const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
-            const uint32_t bs = (uint32_t)a.p.block_size, bytes = 16 * L.row_bytes;
+            const uint32_t bytes = kChunk * L.row_bytes;
             uint8_t* ring = smem + lane * L.stages * 2 * bytes;
-            // pages and positions in them of a step's two boxes; -1: nothing to copy
+            // pages and positions in them of a step's two chunks
             int page[2], at[2];
             auto resolve = [&](int i) {
-                const int pos = range.position((i * L.splits + rank) * L.parts + lane), end = range.limit(pos);
+                const int ch = 2 * ((i * L.splits + rank) * L.parts + lane);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t j = pos + 16 * x;
-                    uint32_t b = __umulhi(j, L.block_recip);
-                    if (j - b * bs >= bs) ++b;
-                    at[x] = (int)(j - b * bs);
-                    page[x] = (int)j < end ? table[b] : INT32_MIN;
-                }
+                for (int x = 0; x < 2; ++x) page[x] = chunk_page(a, range, table, L.block_recip, ch + x, &at[x]);
             };
             if (n > 0) resolve(0);
             int stage = 0, parity = 1;
@@ -279,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         int stage = 0, parity = 0;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
-            const int pos = range.position((st * L.splits + rank) * L.parts + part);
+            const int ch = 2 * ((st * L.splits + rank) * L.parts + part);
             if (!wait_bounded(&full[part][stage], parity, &abort, a.err)) break;
             const uint32_t mask = live[part][stage];
             const uint8_t* kc = kc0 + stage * step_bytes;
@@ -335,17 +329,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[u][t][e] = fmaf(s[u][t][e], f[t][e & 1], -m[t][e & 1]);
-            if (mask != 3u || !range.all_see(pos)) {
-                const int limit = range.limit(pos);
+            if (mask != 3u || !range.all_see(ch, 2)) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
+                    const int pos = range.position(ch + u), limit = mask >> u & 1 ? range.limit(ch + u) : 0;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = pos + 16 * u + 8 * (e >> 1) + tk;
-                            if (!(mask >> u & 1) || j >= limit || !sees(a, hi[t][e & 1], j)) z[u][t][e] = -INFINITY;
+                            const int j = pos + 8 * (e >> 1) + tk;
+                            if (j >= limit || !sees(a, hi[t][e & 1], j)) z[u][t][e] = -INFINITY;
                         }
+                }
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -652,7 +647,7 @@ cudaError_t launch_type(const PagedArgs& a, int head_dim, int sms, cudaStream_t 
 {
     // rows per unit: as few blocks of eight as hold a sequence's, within the registers (an accumulator of D x 8 NT
     // fp32 per warp)
-    const int64_t rows = (int64_t)(a.p.layout_tnd ? std::max(1, std::min(a.p.max_seqlen_q, a.p.total_q)) : a.p.s1) * (a.heads_q / a.heads_kv);
+    const int64_t rows = most_rows(a);
     if (head_dim == 64) {
         if (rows <= 8) return launch_shape<F16, E2M1, 64, 1>(a, sms, st);
         if (rows <= 16) return launch_shape<F16, E2M1, 64, 2>(a, sms, st);
@@ -665,6 +660,7 @@ cudaError_t launch_type(const PagedArgs& a, int head_dim, int sms, cudaStream_t 
 
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
 {
+    if (most_rows(a) > 16) return launch_paged_chunk(a, head_dim, f16, e2m1, most_rows(a), sms, st);
     if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
     return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
 }

@@ -1,0 +1,635 @@
+// qli_paged_chunk.cu -- the paged attention of qli_paged_attention.cu for many rows that read the same KV head (chunks
+// of prompts, several new tokens, wide groups of query heads), on the tcgen05 tensor cores.
+//
+// A CTA takes up to 256 consecutive (token, query head) rows of a sequence and one KV head, and walks the cached
+// positions that some of them see in tiles of 128:
+//
+//     S = Q K^T  (128 x 128 x D)     P = 2^(S f - m), zero where the row does not see the position     O += P V
+//
+// with the rows of a product on its M side.  Two streams of products keep the tensor cores busy while the other's
+// softmax runs: with more than 128 rows each stream has its own 128 and both walk all tiles; with fewer both share
+// the rows, each takes every other tile, and their results are joined at the end.  Roles:
+//   * one warp copies the KV head's bytes of a tile's positions by TMA, 16 positions of a page a box;
+//   * 4 converter warps, a position per thread, decode them into fp16 operands in shared memory: rows of positions
+//     for K and for V (V enters the product with its positions as the K dimension, "MN-major");
+//   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
+//     place of the logits it came from;
+//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when a logit passes it
+//     by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+// Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
+// through distributed shared memory in a fixed order.
+//
+// Masks, pages outside the pool and NaN scales as in qli_paged_attention.cu.  Every wait is bounded (0.2 s); on
+// expiry the kernel records kErrTimeout, writes NaN and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <cstring>
+
+#include "qli_paged.cuh"
+
+namespace qli {
+
+namespace {
+
+constexpr int kM = 128, kTile = 128;                   // rows and positions of a product
+constexpr int kTileChunks = kTile / kChunk;
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kCopyWarp = 13;
+constexpr int kThreads = 32 * 14;
+constexpr int kRawStages = 3, kMaxRing = 4;
+constexpr int kMaxSplits = 8;
+constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
+constexpr float kRescale = 8.0f;
+constexpr uint64_t kWaitLimitNs = 200000000ull;
+
+struct Layout {
+    int32_t rows;          // of a block: 128 or 256
+    int32_t blocks;        // BSND: blocks per sequence
+    int32_t splits;        // CTAs of a cluster
+    uint32_t block_recip;
+};
+
+struct Shared {
+    uint64_t rawfull[kRawStages], rawfree[kRawStages], opfull[kMaxRing], opfree[kMaxRing], sfull[2], pfull[2], odone;
+    uint32_t tmem, abort;
+    uint8_t valid[8];                                  // chunks of a tile that lie in the pool
+    RowBlock blk;
+    float factor[2 * kM];
+};
+
+template <int D>
+struct Sizes {
+    static constexpr int atom = kM * 128;              // 128 rows of 64 fp16 in the 128-byte swizzle
+    static constexpr int operand = D / 64 * atom;      // 128 rows of D
+    // the KV head's bytes of a position, from a multiple of 16 on (heads of 72 bytes start on a multiple of 8)
+    static constexpr int raw_row = D == 128 ? 144 : 80;
+    static constexpr int raw = kTile * raw_row;
+    // Q and a ring of operands: two blocks of rows and a ring of 3, or one and 4
+    static constexpr int operands = 5 * operand;
+    static constexpr int raw_at = operands, shared_at = raw_at + kRawStages * raw;
+    static constexpr int smem = shared_at + (int)sizeof(Shared);
+};
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 100000u))) {
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
+// them moves in front
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32])
+{
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand
+template <int D>
+__device__ __forceinline__ uint32_t operand_at(int r, int piece)
+{
+    return (piece >> 3) * Sizes<D>::atom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+}
+
+// Stage and phase of the ring's fill number n
+struct Fill {
+    int stage;
+    uint32_t phase;
+};
+__device__ __forceinline__ Fill fill_of(int n, bool four)
+{
+    const int lap = four ? n >> 2 : n / 3;
+    return {n - lap * (four ? 4 : 3), (uint32_t)lap & 1};
+}
+
+// The low n bits, n clamped to [0, 16]
+__device__ __forceinline__ uint32_t low16(int n) { return (1u << min(max(n, 0), 16)) - 1; }
+
+// Bits of the chunk's positions that a row with end `hi` sees
+__device__ __forceinline__ uint32_t chunk_bits(const PagedArgs& a, const KeyRange& range, int chunk, int hi)
+{
+    const int pos = range.position(chunk);
+    uint32_t bits = low16(min(hi, range.limit(chunk)) - pos);
+    if (a.window > 0) bits &= ~low16(hi - a.window - pos) | low16(a.sinks - pos);
+    return bits;
+}
+
+// Eight scale bytes times 16-element blocks: prepared pairs
+template <bool E2M1, int N>
+__device__ __forceinline__ void scale_pairs(const uint32_t (&w)[N], bool finite, PairScale (&g)[4 * N])
+{
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+        uint32_t h = e4m3x2_to_f16x2(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+        if (finite) h = finite_f16x2(h);
+        g[2 * i] = pair_scale<E2M1>(__byte_perm(h, 0, 0x1010));
+        g[2 * i + 1] = pair_scale<E2M1>(__byte_perm(h, 0, 0x3232));
+    }
+}
+
+// One position's codes of K or V: for D = 128 16 bytes at a time (eight lanes' rows, 144 bytes apart, lie in
+// different banks), heads of 72 bytes 8 at a time
+template <int D>
+__device__ __forceinline__ void load_codes(const uint8_t* src, uint32_t (&w)[D / 8])
+{
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 x = reinterpret_cast<const uint4*>(src)[i];
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint2 x = reinterpret_cast<const uint2*>(src)[i];
+            w[2 * i] = x.x, w[2 * i + 1] = x.y;
+        }
+    }
+}
+
+// One position's codes (D / 8 words) times their scales into row `row` of an operand
+template <bool E2M1, int D>
+__device__ __forceinline__ void store_row(uint8_t* operand, int row, const uint32_t (&code)[D / 8], const PairScale (&g)[D / 16])
+{
+    uint8_t* dst = operand + row * 128;
+    const int flip = (row & 7) << 4;
+#pragma unroll
+    for (int p = 0; p < D / 8; ++p) {
+        uint32_t o[4];
+        decode_pairs<E2M1>(code[p], g[p / 2], o);
+        *reinterpret_cast<uint4*>(dst + (p >> 3) * Sizes<D>::atom + (((p & 7) << 4) ^ flip)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <bool F16, bool E2M1, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Layout L,
+                       const __grid_constant__ CUtensorMap pages)
+{
+    using Z = Sizes<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem + Z::shared_at);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.heads_q / a.heads_kv;
+    const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
+    // later rows of a sequence see more of it: they start first
+    const uint32_t tasks = gridDim.x / (uint32_t)L.splits, task = tasks - 1 - blockIdx.x / (uint32_t)L.splits;
+    const uint32_t slot = task / (uint32_t)a.heads_kv;
+    const int kvh = (int)(task - slot * a.heads_kv);
+
+    if (tid == 0) {
+        for (int i = 0; i < kRawStages; ++i) {
+            ptx::mbar_init(&sh.rawfull[i], 1);
+            ptx::mbar_init(&sh.rawfree[i], kConvWarps);
+        }
+        for (int i = 0; i < kMaxRing; ++i) {
+            ptx::mbar_init(&sh.opfull[i], kConvWarps);
+            ptx::mbar_init(&sh.opfree[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.sfull[i], 1);
+            ptx::mbar_init(&sh.pfull[i], 4);
+        }
+        ptx::mbar_init(&sh.odone, 1);
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::pdl_wait();
+    if (!find_rows(a, slot, L.blocks, L.rows, group, &sh.blk)) {
+        clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
+        return;
+    }
+    const RowBlock blk = sh.blk;
+    if (blk.rows == 0) return;                             // (the whole cluster)
+    if (warp == kMmaWarp) {                                // (not before: kernels that still run may need it)
+        ptx::tmem_alloc(&sh.tmem, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    const bool shared = blk.rows <= kM;                    // both streams on the same rows
+    const KeyRange range = key_range(a, blk, group);
+    const int all_tiles = (range.chunks + kTileChunks - 1) / kTileChunks;
+    const int n = max(0, (all_tiles - rank + L.splits - 1) / L.splits);        // tiles of this CTA
+    auto steps_of = [&](int q) { return shared ? (n - q + 1) / 2 : n; };
+    auto tile_of = [&](int q, int j) { return shared ? 2 * j + q : j; };
+    uint8_t* ring = smem + (shared ? 1 : 2) * Z::operand;
+
+    // ---- the queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
+    // times a power of two of its largest magnitude)
+    {
+        constexpr int kPerWarp = 4, kLaneBytes = D / 16;   // bytes of a lane: four or two elements
+        // for int4 the elements of each eight in the order 0 4 1 5 2 6 3 7, as its codes come
+        const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
+        const int x0 = E2M1 ? el : (el & ~7) + e8 / 2, x1 = E2M1 ? el + 2 : (el & ~7) + e8 / 2 + 1;
+        const int total = shared ? kM : 2 * kM;
+        for (int m0 = warp * kPerWarp; m0 < total; m0 += kThreads / 32 * kPerWarp) {
+            uint32_t raw[kPerWarp][2];
+#pragma unroll
+            for (int x = 0; x < kPerWarp; ++x) {
+                const int m = m0 + x, i = blk.first + m, tok = i / group;
+                raw[x][0] = raw[x][1] = 0;
+                if (m >= blk.rows) continue;
+                const uint16_t* src = static_cast<const uint16_t*>(a.query) + (blk.row0 + tok) * a.q_stride +
+                                      (int64_t)(kvh * group + i - tok * group) * D;
+                if (E2M1) {
+                    raw[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
+                    if (D == 128) raw[x][1] = *reinterpret_cast<const uint32_t*>(src + x1);
+                } else {
+                    raw[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
+                    if (D == 128) raw[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kPerWarp; ++x) {
+                const int m = m0 + x;
+                uint32_t ex = 127;
+                if constexpr (!F16) {
+                    const float2 u = act2_to_float2<F16>(raw[x][0]), v = act2_to_float2<F16>(raw[x][1]);
+                    float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+                    const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
+                    raw[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
+                    raw[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
+                }
+                uint8_t* dst = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
+                if constexpr (kLaneBytes == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(raw[x][0], raw[x][1]);
+                else *reinterpret_cast<uint32_t*>(dst) = raw[x][0];
+                // (above zero: the mask's -infinity times it stays -infinity)
+                if (lane == 0)
+                    sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
+                                         3.0e38f);
+            }
+        }
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    float m_run = -FLT_MAX, l_run = 0.0f;                  // softmax threads
+    if (warp < kSoftWarps) {
+        // ---------------------------------------------------------------- softmax
+        const int q = warp >> 2, m = (shared ? 0 : q * kM) + (tid & 127), steps = steps_of(q);
+        const int hi = seen_end(a, blk, (blk.first + m) / group);
+        const float f = sh.factor[m];
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), cols = lanes + kTile * q, out = lanes + kColO + D * q;
+        for (int j = 0; j < steps; ++j) {
+            const int t = tile_of(q, j), ch = kTileChunks * (t * L.splits + rank);
+            if (!wait_bounded(&sh.sfull[q], j & 1, &sh.abort, a.err)) break;
+            ptx::tc_fence_after();
+            const uint32_t valid = sh.valid[t & 7];
+            const bool whole = valid == 0xFFu && range.all_see(ch, kTileChunks);
+            uint32_t p[64];
+            while (true) {
+                float best[2] = {-INFINITY, -INFINITY};
+                uint64_t part[2] = {0, 0};
+                const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m_run, -m_run);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32];
+                    QLI_TMEM_LD_X32(cols + 32 * c, s);
+                    wait_loaded(s);
+                    if (!whole) {
+                        uint32_t bits = chunk_bits(a, range, ch + 2 * c, hi) | chunk_bits(a, range, ch + 2 * c + 1, hi) << 16;
+                        if (!(valid >> (2 * c) & 1)) bits &= 0xFFFF0000u;
+                        if (!(valid >> (2 * c + 1) & 1)) bits &= 0x0000FFFFu;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[e]) : -INFINITY);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
+                        best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
+                        float zx, zy;
+                        ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
+                        const float px = ptx::ex2(zx), py = ptx::ex2(zy);
+                        part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
+                        p[16 * c + e / 2] = float2_to_act2<true>(px, py);
+                    }
+                }
+                float sum, other;
+                ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
+                sum += other;
+                const float top = fmaxf(best[0], best[1]), up = top * f;
+                const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
+                if (!__any_sync(0xffffffffu, over)) {
+                    l_run += sum;
+                    break;
+                }
+                // raise the maximum of the rows that need it, rescale their sums and accumulators.  (The stream's last
+                // product was issued before these logits, and has ended.)
+                const float g = over ? ptx::ex2(m_run - up) : 1.0f;
+                if (over) m_run = up;
+                l_run *= g;
+                if (j == 0) continue;
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    QLI_TMEM_LD_X32(out + 32 * x, o);
+                    wait_loaded(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                    QLI_TMEM_ST_X32(out + 32 * x, o);
+                }
+            }
+            // in the place of the logits
+            QLI_TMEM_ST_X32(cols, p);
+            QLI_TMEM_ST_X32(cols + 32, (p + 32));
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.pfull[q]);
+        }
+    } else if (warp < kMmaWarp) {
+        // ---------------------------------------------------------------- converters, a position per thread
+        const int row = tid - 32 * kConvWarp, lo = kvh * kv_unit_bytes(D) & 8;       // (heads of 72 bytes)
+        const bool stall = a.p.test_stall == 1;            // test switch: no tile is handed on, the waits run out
+        int rs = 0;
+        uint32_t rp = 0;
+        for (int t = 0; t < n; ++t) {
+            const uint8_t* src = smem + Z::raw_at + rs * Z::raw + row * Z::raw_row + lo;
+            if (!wait_bounded(&sh.rawfull[rs], rp, &sh.abort, a.err)) break;
+            uint32_t kc[D / 8], ks[D / 64], vs[D / 64];
+            load_codes<D>(src, kc);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                ks[i] = reinterpret_cast<const uint32_t*>(src + D)[i];
+                vs[i] = reinterpret_cast<const uint32_t*>(src + D + D / 16)[i];
+                // a NaN (0x7F or 0xFF) among the values' scales becomes one of the keys'
+                ks[i] |= __vcmpeq4(vs[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            }
+            PairScale g[D / 16];
+            const Fill fk = fill_of(2 * t, shared), fv = fill_of(2 * t + 1, shared);
+            scale_pairs<E2M1>(ks, false, g);
+            if (!wait_bounded(&sh.opfree[fk.stage], fk.phase ^ 1, &sh.abort, a.err)) break;
+            store_row<E2M1, D>(ring + fk.stage * Z::operand, row, kc, g);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[fk.stage]);
+            load_codes<D>(src + D / 2, kc);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.rawfree[rs]);
+            scale_pairs<E2M1>(vs, true, g);
+            if (!wait_bounded(&sh.opfree[fv.stage], fv.phase ^ 1, &sh.abort, a.err)) break;
+            store_row<E2M1, D>(ring + fv.stage * Z::operand, row, kc, g);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[fv.stage]);
+            if (++rs == kRawStages) rs = 0, rp ^= 1;
+        }
+    } else if (warp == kCopyWarp) {
+        // ---------------------------------------------------------------- copies, a chunk per lane
+        const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
+        const int x = (kvh * kv_unit_bytes(D) & ~15) / 8;
+        int rs = 0, at = 0, page = INT32_MIN;
+        uint32_t rp = 1;
+        if (n > 0 && lane < kTileChunks) page = chunk_page(a, range, table, L.block_recip, kTileChunks * rank + lane, &at);
+        for (int t = 0; t < n; ++t) {
+            const int pg = page, ps = at;
+            const bool ok = pg >= 0 && pg < a.p.num_blocks;
+            if (!ok && pg != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
+            const uint32_t live = __ballot_sync(0xffffffffu, ok);
+            if (t + 1 < n && lane < kTileChunks)
+                page = chunk_page(a, range, table, L.block_recip, kTileChunks * ((t + 1) * L.splits + rank) + lane, &at);
+            if (!wait_bounded(&sh.rawfree[rs], rp, &sh.abort, a.err)) break;
+            if (lane == 0) {
+                sh.valid[t & 7] = (uint8_t)live;
+                ptx::mbar_arrive_expect_tx(&sh.rawfull[rs], __popc(live) * kChunk * Z::raw_row);
+            }
+            __syncwarp();
+            if (ok) ptx::tma_load_3d(smem + Z::raw_at + rs * Z::raw + lane * kChunk * Z::raw_row, &pages, x, ps, pg, &sh.rawfull[rs]);
+            __syncwarp();
+            if (++rs == kRawStages) rs = 0, rp ^= 1;
+        }
+    } else {
+        // ---------------------------------------------------------------- products
+        const uint32_t idesc_s = ptx::idesc_f16_f32(kM, kTile), idesc_o = ptx::idesc_f16_f32(kM, D) | ptx::kIdescMajorB;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t qd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem));
+        const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ring));
+        const uint64_t vd = ptx::sdesc_mnmajor_sw128(ptx::smem_addr(ring), Z::atom);
+        auto logits = [&](int q, int t) {
+            const Fill f = fill_of(2 * t, shared);
+            if (!wait_bounded(&sh.opfull[f.stage], f.phase, &sh.abort, a.err)) return false;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint64_t qo = qd + ((shared ? 0 : q * Z::operand) >> 4), ko = kd + (f.stage * Z::operand >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int off = (kk >> 2) * Z::atom + (kk & 3) * 32;
+                    ptx::mma_f16_ss(tm + kTile * q, qo + (off >> 4), ko + (off >> 4), idesc_s, kk > 0);
+                }
+                ptx::mma_commit(&sh.sfull[q]);
+                if (shared || q == 1) ptx::mma_commit(&sh.opfree[f.stage]);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto output = [&](int q, int t, int j) {
+            const Fill f = fill_of(2 * t + 1, shared);
+            if (!wait_bounded(&sh.opfull[f.stage], f.phase, &sh.abort, a.err) || !wait_bounded(&sh.pfull[q], j & 1, &sh.abort, a.err))
+                return false;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint64_t vo = vd + (f.stage * Z::operand >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + 8 * kk, vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0);
+                if (shared || q == 1) ptx::mma_commit(&sh.opfree[f.stage]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // a stream's next logits follow its output, so that the other's products run beside its softmax
+        const int s0 = steps_of(0), s1 = steps_of(1);
+        bool ok = true;
+        if (s0 > 0) ok = logits(0, tile_of(0, 0));
+        if (ok && s1 > 0) ok = logits(1, tile_of(1, 0));
+        for (int j = 0; ok && j < s0; ++j) {
+            ok = output(0, tile_of(0, j), j);
+            if (ok && j + 1 < s0) ok = logits(0, tile_of(0, j + 1));
+            if (ok && j < s1) ok = output(1, tile_of(1, j), j);
+            if (ok && j + 1 < s1) ok = logits(1, tile_of(1, j + 1));
+        }
+        if (ok && n > 0) {
+            if (ptx::elect_one()) ptx::mma_commit(&sh.odone);
+            __syncwarp();
+        }
+    }
+
+    // ---- join and write
+    __syncwarp();
+    if (n > 0) wait_bounded(&sh.odone, 0, &sh.abort, a.err);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const bool failed = sh.abort != 0;
+    if (failed && warp == kMmaWarp) {                      // products and copies that are still under way end first
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kWaitLimitNs) {
+        }
+    }
+    if (failed) __syncthreads();
+    // global head row of the block's row i
+    auto head_of = [&](int i) {
+        const int at = blk.first + i, tok = at / group;
+        return (blk.row0 + tok) * a.heads_q + kvh * group + at - tok * group;
+    };
+    uint16_t* const dst = static_cast<uint16_t*>(a.out);
+    const bool joins = shared || L.splits > 1;
+    constexpr int kStride = D + 4;                         // of partial rows, in floats
+    float* const part_o = reinterpret_cast<float*>(smem);  // [2 * kM][kStride], then the rows' (maximum, sum)
+    float2* const part_ml = reinterpret_cast<float2*>(part_o + 2 * kM * kStride);
+    static_assert(2 * kM * (kStride * 4 + 8) <= Z::shared_at, "partial results in the operands' place");
+    if (warp < kSoftWarps) {
+        const int q = warp >> 2, m = tid & 127, i = (shared ? 0 : q * kM) + m;
+        const bool live = i < blk.rows, some = steps_of(q) > 0;
+        const uint32_t cols = tmem + ((uint32_t)(warp & 3) << 21) + kColO + D * q;
+        const float sum = failed ? __int_as_float(0x7FC00000) : l_run;
+        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        const int64_t head = live ? head_of(i) : 0;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            if (some) {
+                QLI_TMEM_LD_X32(cols + 32 * x, o);
+                wait_loaded(o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+            // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
+            auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
+            if (live && joins) {
+                float4* to = reinterpret_cast<float4*>(part_o + (q * kM + m) * kStride + 32 * x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) to[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
+            } else if (live) {
+                uint4* to = reinterpret_cast<uint4*>(dst + head * D + 32 * x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        w[z] = sum == 0.0f ? 0u : float2_to_act2<F16>(el(8 * e + 2 * z) * inv, el(8 * e + 2 * z + 1) * inv);
+                    to[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();                                  // (the loads take the whole warp)
+        }
+        if (joins) part_ml[q * kM + m] = make_float2(m_run, sum);
+        else if (live && a.lse) a.lse[head] = sum == 0.0f ? -INFINITY : (m_run + log2f(sum)) * 0.6931471805599453f;
+    }
+    if (joins) {
+        if (L.splits > 1) ptx::cluster_sync();
+        else __syncthreads();
+        const int pieces = blk.rows * (D / 4), streams = shared ? 2 : 1;
+        for (int z = rank * kThreads + tid; z < pieces; z += L.splits * kThreads) {
+            const int i = z / (D / 4), d4 = z % (D / 4);
+            float top = -FLT_MAX, sum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int parts = streams * L.splits;
+            // part x: stream x % streams of CTA x / streams
+            auto ml_of = [&](int x) {
+                return ptx::ld_cluster2(ptx::cluster_addr(ptx::smem_addr(part_ml + i + (shared ? kM * (x & 1) : 0)), shared ? x >> 1 : x));
+            };
+            for (int x = 0; x < parts; ++x) top = fmaxf(top, ml_of(x).x);
+            for (int x = 0; x < parts; ++x) {
+                const float2 ml = ml_of(x);
+                const float4 v = ptx::ld_cluster4(ptx::cluster_addr(
+                    ptx::smem_addr(part_o + (i + (shared ? kM * (x & 1) : 0)) * kStride + 4 * d4), shared ? x >> 1 : x));
+                const float g = ptx::ex2(ml.x - top);
+                sum = fmaf(g, ml.y, sum);
+                acc.x = fmaf(g, v.x, acc.x), acc.y = fmaf(g, v.y, acc.y);
+                acc.z = fmaf(g, v.z, acc.z), acc.w = fmaf(g, v.w, acc.w);
+            }
+            const int64_t head = head_of(i);
+            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            *reinterpret_cast<uint2*>(dst + head * D + 4 * d4) =
+                make_uint2(float2_to_act2<F16>(acc.x * inv, acc.y * inv), float2_to_act2<F16>(acc.z * inv, acc.w * inv));
+            if (a.lse && d4 == 0) a.lse[head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        __syncwarp();
+        if (L.splits > 1) ptx::cluster_sync();             // no CTA leaves while another reads its partial results
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool F16, bool E2M1, int D>
+cudaError_t launch_shape(const PagedArgs& a, int64_t most_rows, int sms, cudaStream_t st)
+{
+    using Z = Sizes<D>;
+    static_assert(Z::smem <= 227 * 1024, "shared memory of an SM");
+    const int group = a.heads_q / a.heads_kv;
+    Layout L;
+    L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
+    L.rows = most_rows <= kM ? kM : 2 * kM;
+    const int64_t slots = row_slots(a, L.rows, group, &L.blocks);
+    const int64_t tiles = ceil_div64(most_positions(a, L.rows, group), kTile);
+    L.splits = 1;
+    while (L.splits < kMaxSplits && slots * a.heads_kv * L.splits * 2 <= sms && tiles >= 4 * L.splits) L.splits *= 2;
+    const int64_t grid = slots * a.heads_kv * L.splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    CUtensorMap pages;
+    std::memset(&pages, 0, sizeof(pages));
+    if (a.p.batch > 0 && !encode_page_map(&pages, a.kv, a.entry_bytes, a.p.block_size, a.page_bytes, a.p.num_blocks, Z::raw_row, kChunk))
+        return cudaErrorUnknown;
+    auto kernel = paged_chunk_kernel<F16, E2M1, D>;
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? UINT64_C(1) << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::smem);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Z::smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, L, pages);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int64_t most_rows, int sms, cudaStream_t st)
+{
+    if (head_dim == 64) {
+        if (f16) return e2m1 ? launch_shape<true, true, 64>(a, most_rows, sms, st) : launch_shape<true, false, 64>(a, most_rows, sms, st);
+        return e2m1 ? launch_shape<false, true, 64>(a, most_rows, sms, st) : launch_shape<false, false, 64>(a, most_rows, sms, st);
+    }
+    if (f16) return e2m1 ? launch_shape<true, true, 128>(a, most_rows, sms, st) : launch_shape<true, false, 128>(a, most_rows, sms, st);
+    return e2m1 ? launch_shape<false, true, 128>(a, most_rows, sms, st) : launch_shape<false, false, 128>(a, most_rows, sms, st);
+}
+
+}  // namespace qli

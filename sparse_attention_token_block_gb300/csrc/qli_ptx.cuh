@@ -334,6 +334,20 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr)
     return d;
 }
 
+// The same for an operand whose M or N side is contiguous: rows of one K index, 64 elements (128 B) wide, 8-row groups
+// 1024 B apart, the next 64 elements `next` bytes on
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t next)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+    d |= static_cast<uint64_t>(next >> 4) << 16;           // leading byte offset: the next 64 elements
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;           // stride byte offset: 8 rows x 128 B
+    d |= static_cast<uint64_t>(1) << 46;                   // descriptor version
+    d |= static_cast<uint64_t>(2) << 61;                   // SWIZZLE_128B
+    return d;
+}
+constexpr uint32_t kIdescMajorB = 1u << 16;               // B's N side is contiguous
+
 // Instruction descriptor, kind::f16: fp16 A and B (K-major), fp32 D, shape M x N
 __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t m, uint32_t n)
 {

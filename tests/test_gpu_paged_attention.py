@@ -111,6 +111,16 @@ def test_long_and_many(Q, batch, lens, hq, hkv, dim):
     _both(Q, case, hq, hkv, dim)
 
 
+@pytest.mark.parametrize("q_lens,lens", [([300], [2000]), ([33, 129, 1], [1300, 129, 700]), ([64], [4001])])
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 1, 128), (4, 2, 64), (3, 3, 128), (32, 1, 64), (12, 1, 128)])
+@pytest.mark.parametrize("e2m1,f16", [(True, False), (False, False), (True, True)])
+def test_chunks_over_many_tiles(Q, q_lens, lens, hq, hkv, dim, e2m1, f16):
+    case = cache_case(layout_q="TND", q_lens=q_lens, seq_lens_k=lens, block_size=64, sparse_count=1, sparse_mode=3, seed=dim)
+    _both(Q, case, hq, hkv, dim, e2m1, f16)
+    if e2m1:
+        _both(Q, case, hq, hkv, dim, e2m1, f16, window=333, sinks=20)
+
+
 def test_growing_logits(Q):
     """Each position's logit above the last one's: the maximum rises at every step."""
     case = cache_case(batch=1, s1=1, seq_lens_k=[1500], block_size=64, sparse_count=1, sparse_mode=3, seed=6, permute=False)
@@ -121,9 +131,12 @@ def test_growing_logits(Q):
     k = base * np.linspace(0.05, 6, n)[:, None, None]
     pool = A.encode(k.astype(np.float32), rng.normal(size=(n, hkv, dim)).astype(np.float32), True).reshape(case.num_blocks, 64, -1)
     q = np.repeat(base, 4, 1).astype(np.float32)
-    q = queries(1, 8, dim, False, 1) * 0 + (q.view(np.uint32) & 0xFFFF0000).view(np.float32)
-    for sign in (1, -1):
-        check(case, attend(Q, case, sign * q, pool, hkv, True, False), sign * q, pool, hkv, True, False)
+    q = (np.ascontiguousarray(q).view(np.uint32) & 0xFFFF0000).view(np.float32)
+    for tokens in (1, 20):
+        case.s1 = tokens
+        many = np.repeat(q, tokens, 0)
+        for sign in (1, -1):
+            check(case, attend(Q, case, sign * many, pool, hkv, True, False), sign * many, pool, hkv, True, False)
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (64, 5)])
