@@ -39,7 +39,7 @@ constexpr int kM = 128, kTile = 128;                   // rows and positions of 
 constexpr int kTileChunks = kTile / kChunk;
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kCopyWarp = 13;
 constexpr int kThreads = 32 * 14;
-constexpr int kRawStages = 3, kMaxRing = 4;
+constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
 constexpr float kRescale = 8.0f;
@@ -53,7 +53,7 @@ struct Layout {
 };
 
 struct Shared {
-    uint64_t rawfull[kRawStages], rawfree[kRawStages], opfull[kMaxRing], opfree[kMaxRing], sfull[2], pfull[2], odone;
+    uint64_t rawfull[kMaxRaw], rawfree[kMaxRaw], opfull[kRing], opfree[kRing], sfull[2], pfull[2], qfull, odone;
     uint32_t tmem, abort;
     uint8_t valid[8];                                  // chunks of a tile that lie in the pool
     RowBlock blk;
@@ -67,10 +67,11 @@ struct Sizes {
     // the KV head's bytes of a position, from a multiple of 16 on (heads of 72 bytes start on a multiple of 8)
     static constexpr int raw_row = D == 128 ? 144 : 80;
     static constexpr int raw = kTile * raw_row;
-    // Q and a ring of operands: two blocks of rows and a ring of 3, or one and 4
-    static constexpr int operands = 5 * operand;
-    static constexpr int raw_at = operands, shared_at = raw_at + kRawStages * raw;
+    // Q (one or two blocks of rows), a ring of operands, and copied bytes: one stage, or two in place of the second
+    // block of rows
+    static constexpr int shared_at = (2 + kRing) * operand + raw;
     static constexpr int smem = shared_at + (int)sizeof(Shared);
+    static_assert(kMaxRaw * raw <= operand + raw, "copied bytes");
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
@@ -102,17 +103,6 @@ template <int D>
 __device__ __forceinline__ uint32_t operand_at(int r, int piece)
 {
     return (piece >> 3) * Sizes<D>::atom + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-}
-
-// Stage and phase of the ring's fill number n
-struct Fill {
-    int stage;
-    uint32_t phase;
-};
-__device__ __forceinline__ Fill fill_of(int n, bool four)
-{
-    const int lap = four ? n >> 2 : n / 3;
-    return {n - lap * (four ? 4 : 3), (uint32_t)lap & 1};
 }
 
 // The low n bits, n clamped to [0, 16]
@@ -191,11 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kvh = (int)(task - slot * a.heads_kv);
 
     if (tid == 0) {
-        for (int i = 0; i < kRawStages; ++i) {
+        for (int i = 0; i < kMaxRaw; ++i) {
             ptx::mbar_init(&sh.rawfull[i], 1);
             ptx::mbar_init(&sh.rawfree[i], kConvWarps);
         }
-        for (int i = 0; i < kMaxRing; ++i) {
+        for (int i = 0; i < kRing; ++i) {
             ptx::mbar_init(&sh.opfull[i], kConvWarps);
             ptx::mbar_init(&sh.opfree[i], 1);
         }
@@ -203,86 +193,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh.sfull[i], 1);
             ptx::mbar_init(&sh.pfull[i], 4);
         }
+        ptx::mbar_init(&sh.qfull, kSoftWarps);
         ptx::mbar_init(&sh.odone, 1);
         sh.abort = 0;
         ptx::fence_mbar_init();
     }
     ptx::pdl_wait();
-    if (!find_rows(a, slot, L.blocks, L.rows, group, &sh.blk)) {
-        clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
-        return;
-    }
-    const RowBlock blk = sh.blk;
-    if (blk.rows == 0) return;                             // (the whole cluster)
     if (warp == kMmaWarp) {                                // (not before: kernels that still run may need it)
         ptx::tmem_alloc(&sh.tmem, kTmemCols);
         ptx::tmem_relinquish();
     }
+    ptx::tc_fence_before();
+    const bool found = find_rows(a, slot, L.blocks, L.rows, group, &sh.blk);        // (every thread meets)
+    if (!found) __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    if (!found || sh.blk.rows == 0) {                      // (the whole cluster)
+        if (!found) clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
+        if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
+    const RowBlock blk = sh.blk;
     const bool shared = blk.rows <= kM;                    // both streams on the same rows
     const KeyRange range = key_range(a, blk, group);
     const int all_tiles = (range.chunks + kTileChunks - 1) / kTileChunks;
     const int n = max(0, (all_tiles - rank + L.splits - 1) / L.splits);        // tiles of this CTA
     auto steps_of = [&](int q) { return shared ? (n - q + 1) / 2 : n; };
     auto tile_of = [&](int q, int j) { return shared ? 2 * j + q : j; };
-    uint8_t* ring = smem + (shared ? 1 : 2) * Z::operand;
-
-    // ---- the queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
-    // times a power of two of its largest magnitude)
-    {
-        constexpr int kPerWarp = 4, kLaneBytes = D / 16;   // bytes of a lane: four or two elements
-        // for int4 the elements of each eight in the order 0 4 1 5 2 6 3 7, as its codes come
-        const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
-        const int x0 = E2M1 ? el : (el & ~7) + e8 / 2, x1 = E2M1 ? el + 2 : (el & ~7) + e8 / 2 + 1;
-        const int total = shared ? kM : 2 * kM;
-        for (int m0 = warp * kPerWarp; m0 < total; m0 += kThreads / 32 * kPerWarp) {
-            uint32_t raw[kPerWarp][2];
-#pragma unroll
-            for (int x = 0; x < kPerWarp; ++x) {
-                const int m = m0 + x, i = blk.first + m, tok = i / group;
-                raw[x][0] = raw[x][1] = 0;
-                if (m >= blk.rows) continue;
-                const uint16_t* src = static_cast<const uint16_t*>(a.query) + (blk.row0 + tok) * a.q_stride +
-                                      (int64_t)(kvh * group + i - tok * group) * D;
-                if (E2M1) {
-                    raw[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
-                    if (D == 128) raw[x][1] = *reinterpret_cast<const uint32_t*>(src + x1);
-                } else {
-                    raw[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
-                    if (D == 128) raw[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < kPerWarp; ++x) {
-                const int m = m0 + x;
-                uint32_t ex = 127;
-                if constexpr (!F16) {
-                    const float2 u = act2_to_float2<F16>(raw[x][0]), v = act2_to_float2<F16>(raw[x][1]);
-                    float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
-                    const float down = __uint_as_float((254u - ex) << 23);              // 2^-(exponent of big)
-                    raw[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
-                    raw[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
-                }
-                uint8_t* dst = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
-                if constexpr (kLaneBytes == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(raw[x][0], raw[x][1]);
-                else *reinterpret_cast<uint32_t*>(dst) = raw[x][0];
-                // (above zero: the mask's -infinity times it stays -infinity)
-                if (lane == 0)
-                    sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f),
-                                         3.0e38f);
-            }
-        }
-    }
-    ptx::fence_proxy_async_smem();
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    uint8_t* const ring = smem + (shared ? 1 : 2) * Z::operand;
+    uint8_t* const raw = ring + kRing * Z::operand;
+    const int raw_stages = shared ? kMaxRaw : 1;
 
     float m_run = -FLT_MAX, l_run = 0.0f;                  // softmax threads
     if (warp < kSoftWarps) {
+        // ---- the queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
+        // times a power of two of its largest magnitude)
+        {
+            constexpr int kPerWarp = 16;
+            // a lane's four (D = 64: two) elements; for int4 those of each eight in the order 0 4 1 5 2 6 3 7, as its
+            // codes come
+            const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
+            const int x0 = E2M1 ? el : (el & ~7) + e8 / 2, x1 = E2M1 ? el + 2 : (el & ~7) + e8 / 2 + 1;
+            const int tok0 = blk.first / group, rest0 = blk.first - tok0 * group;
+            const uint32_t recip = 65536 / group + 1;      // exact quotients of numbers below 512 by up to 256
+            for (int m0 = warp * kPerWarp; m0 < (shared ? kM : 2 * kM); m0 += kSoftWarps * kPerWarp) {
+                uint32_t raw2[kPerWarp][2];
+#pragma unroll
+                for (int x = 0; x < kPerWarp; ++x) {
+                    const uint32_t i = rest0 + m0 + x, tok = i * recip >> 16;
+                    raw2[x][0] = raw2[x][1] = 0;
+                    if (m0 + x < blk.rows) {
+                        const uint16_t* src = static_cast<const uint16_t*>(a.query) + (blk.row0 + tok0 + tok) * a.q_stride +
+                                              (kvh * group + (int)(i - tok * group)) * D;
+                        if (E2M1) {
+                            if constexpr (D == 128) {
+                                const uint2 w = *reinterpret_cast<const uint2*>(src + x0);
+                                raw2[x][0] = w.x, raw2[x][1] = w.y;
+                            } else {
+                                raw2[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
+                            }
+                        } else {
+                            raw2[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
+                            if (D == 128) raw2[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kPerWarp; ++x) {
+                    const int m = m0 + x;
+                    uint32_t ex = 127;
+                    if constexpr (!F16) {
+                        const float2 u = act2_to_float2<F16>(raw2[x][0]), v = act2_to_float2<F16>(raw2[x][1]);
+                        // the largest magnitude's bits: non-negative floats order like integers
+                        const float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+                        ex = min(max(top >> 23, 1u), 253u);
+                        const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of the largest)
+                        raw2[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
+                        raw2[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
+                    }
+                    uint8_t* dst = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
+                    if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(raw2[x][0], raw2[x][1]);
+                    else *reinterpret_cast<uint32_t*>(dst) = raw2[x][0];
+                    // (above zero: the mask's -infinity times it stays -infinity)
+                    if (lane == 0)
+                        sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f),
+                                                   1.0e-30f), 3.0e38f);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.qfull);
+            wait_bounded(&sh.qfull, 0, &sh.abort, a.err);
+        }
         // ---------------------------------------------------------------- softmax
         const int q = warp >> 2, m = (shared ? 0 : q * kM) + (tid & 127), steps = steps_of(q);
         const int hi = seen_end(a, blk, (blk.first + m) / group);
@@ -294,62 +297,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t valid = sh.valid[t & 7];
             const bool whole = valid == 0xFFu && range.all_see(ch, kTileChunks);
-            uint32_t p[64];
-            while (true) {
-                float best[2] = {-INFINITY, -INFINITY};
-                uint64_t part[2] = {0, 0};
-                const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m_run, -m_run);
+            // half a tile at a time, in two pieces of 32 columns: the next piece is on its way while one is worked on
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
-                    QLI_TMEM_LD_X32(cols + 32 * c, s);
-                    wait_loaded(s);
-                    if (!whole) {
-                        uint32_t bits = chunk_bits(a, range, ch + 2 * c, hi) | chunk_bits(a, range, ch + 2 * c + 1, hi) << 16;
-                        if (!(valid >> (2 * c) & 1)) bits &= 0xFFFF0000u;
-                        if (!(valid >> (2 * c + 1) & 1)) bits &= 0x0000FFFFu;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+                while (true) {
+                    float best[2] = {-INFINITY, -INFINITY};
+                    uint64_t part[2] = {0, 0};
+                    const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m_run, -m_run);
+                    uint32_t s[2][32];
+                    QLI_TMEM_LD_X32(cols + 64 * h, s[0]);
+                    wait_loaded(s[0]);
+                    QLI_TMEM_LD_X32(cols + 64 * h + 32, s[1]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[e]) : -INFINITY);
+                    for (int c = 0; c < 2; ++c) {
+                        if (c == 1) wait_loaded(s[1]);
+                        if (!whole) {
+                            const int x = 4 * h + 2 * c;
+                            uint32_t bits = chunk_bits(a, range, ch + x, hi) | chunk_bits(a, range, ch + x + 1, hi) << 16;
+                            if (!(valid >> x & 1)) bits &= 0xFFFF0000u;
+                            if (!(valid >> (x + 1) & 1)) bits &= 0x0000FFFFu;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[c][e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[c][e]) : -INFINITY);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
+                            best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
+                            float zx, zy;
+                            ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
+                            const float px = ptx::ex2(zx), py = ptx::ex2(zy);
+                            part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
+                            p[16 * c + e / 2] = float2_to_act2<true>(px, py);
+                        }
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
-                        best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
-                        float zx, zy;
-                        ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
-                        const float px = ptx::ex2(zx), py = ptx::ex2(zy);
-                        part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
-                        p[16 * c + e / 2] = float2_to_act2<true>(px, py);
+                    float sum, other;
+                    ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
+                    sum += other;
+                    const float top = fmaxf(best[0], best[1]), up = top * f;
+                    const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
+                    if (!__any_sync(0xffffffffu, over)) {
+                        l_run += sum;
+                        break;
                     }
-                }
-                float sum, other;
-                ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
-                sum += other;
-                const float top = fmaxf(best[0], best[1]), up = top * f;
-                const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
-                if (!__any_sync(0xffffffffu, over)) {
-                    l_run += sum;
-                    break;
-                }
-                // raise the maximum of the rows that need it, rescale their sums and accumulators.  (The stream's last
-                // product was issued before these logits, and has ended.)
-                const float g = over ? ptx::ex2(m_run - up) : 1.0f;
-                if (over) m_run = up;
-                l_run *= g;
-                if (j == 0) continue;
+                    // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's first
+                    // half of P.  (The stream's last product was issued before these logits, and has ended.)
+                    const float g = over ? ptx::ex2(m_run - up) : 1.0f;
+                    if (over) m_run = up;
+                    l_run *= g;
+                    if (h == 1) {
+                        uint32_t o[32];
+                        ptx::tmem_wait_st();
+                        QLI_TMEM_LD_X32(cols, o);
+                        wait_loaded(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 v = act2_to_float2<true>(o[e]);
+                            o[e] = float2_to_act2<true>(v.x * g, v.y * g);
+                        }
+                        QLI_TMEM_ST_X32(cols, o);
+                    }
+                    if (j == 0) continue;
 #pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t o[32];
-                    QLI_TMEM_LD_X32(out + 32 * x, o);
-                    wait_loaded(o);
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
+                        QLI_TMEM_LD_X32(out + 32 * x, o);
+                        wait_loaded(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-                    QLI_TMEM_ST_X32(out + 32 * x, o);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                        QLI_TMEM_ST_X32(out + 32 * x, o);
+                    }
                 }
+                // in the place of the logits that are through
+                QLI_TMEM_ST_X32(cols + 32 * h, p);
             }
-            // in the place of the logits
-            QLI_TMEM_ST_X32(cols, p);
-            QLI_TMEM_ST_X32(cols + 32, (p + 32));
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
@@ -362,10 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int rs = 0;
         uint32_t rp = 0;
         for (int t = 0; t < n; ++t) {
-            const uint8_t* src = smem + Z::raw_at + rs * Z::raw + row * Z::raw_row + lo;
+            // the position's bytes into registers: the next tile's may land
+            const uint8_t* src = raw + rs * Z::raw + row * Z::raw_row + lo;
             if (!wait_bounded(&sh.rawfull[rs], rp, &sh.abort, a.err)) break;
-            uint32_t kc[D / 8], ks[D / 64], vs[D / 64];
+            uint32_t kc[D / 8], vc[D / 8], ks[D / 64], vs[D / 64];
             load_codes<D>(src, kc);
+            load_codes<D>(src + D / 2, vc);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 ks[i] = reinterpret_cast<const uint32_t*>(src + D)[i];
@@ -373,24 +397,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a NaN (0x7F or 0xFF) among the values' scales becomes one of the keys'
                 ks[i] |= __vcmpeq4(vs[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             }
-            PairScale g[D / 16];
-            const Fill fk = fill_of(2 * t, shared), fv = fill_of(2 * t + 1, shared);
-            scale_pairs<E2M1>(ks, false, g);
-            if (!wait_bounded(&sh.opfree[fk.stage], fk.phase ^ 1, &sh.abort, a.err)) break;
-            store_row<E2M1, D>(ring + fk.stage * Z::operand, row, kc, g);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[fk.stage]);
-            load_codes<D>(src + D / 2, kc);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sh.rawfree[rs]);
-            scale_pairs<E2M1>(vs, true, g);
-            if (!wait_bounded(&sh.opfree[fv.stage], fv.phase ^ 1, &sh.abort, a.err)) break;
-            store_row<E2M1, D>(ring + fv.stage * Z::operand, row, kc, g);
+            if (++rs == raw_stages) rs = 0, rp ^= 1;
+            // fills 2 t and 2 t + 1 of the ring
+            const int sk = 2 * t & 3, sv = sk + 1;
+            const uint32_t free_phase = (t >> 1 & 1) ^ 1;
+            PairScale g[D / 16];
+            scale_pairs<E2M1>(ks, false, g);
+            if (!wait_bounded(&sh.opfree[sk], free_phase, &sh.abort, a.err)) break;
+            store_row<E2M1, D>(ring + sk * Z::operand, row, kc, g);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[fv.stage]);
-            if (++rs == kRawStages) rs = 0, rp ^= 1;
+            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sk]);
+            scale_pairs<E2M1>(vs, true, g);
+            if (!wait_bounded(&sh.opfree[sv], free_phase, &sh.abort, a.err)) break;
+            store_row<E2M1, D>(ring + sv * Z::operand, row, vc, g);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sv]);
         }
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------------- copies, a chunk per lane
@@ -412,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_arrive_expect_tx(&sh.rawfull[rs], __popc(live) * kChunk * Z::raw_row);
             }
             __syncwarp();
-            if (ok) ptx::tma_load_3d(smem + Z::raw_at + rs * Z::raw + lane * kChunk * Z::raw_row, &pages, x, ps, pg, &sh.rawfull[rs]);
+            if (ok) ptx::tma_load_3d(raw + rs * Z::raw + lane * kChunk * Z::raw_row, &pages, x, ps, pg, &sh.rawfull[rs]);
             __syncwarp();
-            if (++rs == kRawStages) rs = 0, rp ^= 1;
+            if (++rs == raw_stages) rs = 0, rp ^= 1;
         }
     } else {
         // ---------------------------------------------------------------- products
@@ -424,41 +449,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ring));
         const uint64_t vd = ptx::sdesc_mnmajor_sw128(ptx::smem_addr(ring), Z::atom);
         auto logits = [&](int q, int t) {
-            const Fill f = fill_of(2 * t, shared);
-            if (!wait_bounded(&sh.opfull[f.stage], f.phase, &sh.abort, a.err)) return false;
+            const int stage = 2 * t & 3;
+            if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err)) return false;
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
-                const uint64_t qo = qd + ((shared ? 0 : q * Z::operand) >> 4), ko = kd + (f.stage * Z::operand >> 4);
+                const uint64_t qo = qd + ((shared ? 0 : q * Z::operand) >> 4), ko = kd + (stage * Z::operand >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int off = (kk >> 2) * Z::atom + (kk & 3) * 32;
                     ptx::mma_f16_ss(tm + kTile * q, qo + (off >> 4), ko + (off >> 4), idesc_s, kk > 0);
                 }
                 ptx::mma_commit(&sh.sfull[q]);
-                if (shared || q == 1) ptx::mma_commit(&sh.opfree[f.stage]);
+                if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
             }
             __syncwarp();
             return true;
         };
         auto output = [&](int q, int t, int j) {
-            const Fill f = fill_of(2 * t + 1, shared);
-            if (!wait_bounded(&sh.opfull[f.stage], f.phase, &sh.abort, a.err) || !wait_bounded(&sh.pfull[q], j & 1, &sh.abort, a.err))
+            const int stage = (2 * t & 3) + 1;
+            if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err) || !wait_bounded(&sh.pfull[q], j & 1, &sh.abort, a.err))
                 return false;
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
-                const uint64_t vo = vd + (f.stage * Z::operand >> 4);
+                const uint64_t vo = vd + (stage * Z::operand >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + 8 * kk, vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0);
-                if (shared || q == 1) ptx::mma_commit(&sh.opfree[f.stage]);
+                if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
             }
             __syncwarp();
             return true;
         };
         // a stream's next logits follow its output, so that the other's products run beside its softmax
         const int s0 = steps_of(0), s1 = steps_of(1);
-        bool ok = true;
-        if (s0 > 0) ok = logits(0, tile_of(0, 0));
+        bool ok = wait_bounded(&sh.qfull, 0, &sh.abort, a.err);
+        if (ok && s0 > 0) ok = logits(0, tile_of(0, 0));
         if (ok && s1 > 0) ok = logits(1, tile_of(1, 0));
         for (int j = 0; ok && j < s0; ++j) {
             ok = output(0, tile_of(0, j), j);
