@@ -164,6 +164,43 @@ __device__ __forceinline__ void store_row(uint8_t* operand, int row, const uint3
     }
 }
 
+// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, their sum and the largest
+// logit; kMasked: where `bits` is not set the logit counts as -infinity
+template <bool kMasked>
+__device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, const uint32_t* bits, uint32_t (&p)[32], float& best,
+                                          float& sum)
+{
+    uint32_t s[2][32];
+    QLI_TMEM_LD_X32(cols, s[0]);
+    QLI_TMEM_LD_X32(cols + 32, s[1]);
+    wait_loaded(s[0]);
+    wait_loaded(s[1]);
+    float top[2] = {-INFINITY, -INFINITY};
+    uint64_t part[2] = {0, 0};
+    const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m, -m);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            if constexpr (kMasked) {
+                s[c][e] = __float_as_uint(bits[c] & (1u << e) ? __uint_as_float(s[c][e]) : -INFINITY);
+                s[c][e + 1] = __float_as_uint(bits[c] & (2u << e) ? __uint_as_float(s[c][e + 1]) : -INFINITY);
+            }
+            const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
+            top[e >> 1 & 1] = ptx::max3(top[e >> 1 & 1], x, y);
+            float zx, zy;
+            ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
+            const float px = ptx::ex2(zx), py = ptx::ex2(zy);
+            part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
+            p[16 * c + e / 2] = float2_to_act2<true>(px, py);
+        }
+    }
+    float other;
+    ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
+    sum += other;
+    best = fmaxf(top[0], top[1]);
+}
+
 template <bool F16, bool E2M1, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Layout L,
@@ -297,46 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t valid = sh.valid[t & 7];
             const bool whole = valid == 0xFFu && range.all_see(ch, kTileChunks);
-            // half a tile at a time, in two pieces of 32 columns: the next piece is on its way while one is worked on
+            // half a tile at a time
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t p[32];
                 while (true) {
-                    float best[2] = {-INFINITY, -INFINITY};
-                    uint64_t part[2] = {0, 0};
-                    const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m_run, -m_run);
-                    uint32_t s[2][32];
-                    QLI_TMEM_LD_X32(cols + 64 * h, s[0]);
-                    wait_loaded(s[0]);
-                    QLI_TMEM_LD_X32(cols + 64 * h + 32, s[1]);
+                    float best = -INFINITY, sum;
+                    if (whole) {
+                        soft_half<false>(cols + 64 * h, f, m_run, nullptr, p, best, sum);
+                    } else {
+                        uint32_t bits[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (c == 1) wait_loaded(s[1]);
-                        if (!whole) {
+                        for (int c = 0; c < 2; ++c) {
                             const int x = 4 * h + 2 * c;
-                            uint32_t bits = chunk_bits(a, range, ch + x, hi) | chunk_bits(a, range, ch + x + 1, hi) << 16;
-                            if (!(valid >> x & 1)) bits &= 0xFFFF0000u;
-                            if (!(valid >> (x + 1) & 1)) bits &= 0x0000FFFFu;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[c][e] = __float_as_uint(bits & (1u << e) ? __uint_as_float(s[c][e]) : -INFINITY);
+                            bits[c] = chunk_bits(a, range, ch + x, hi) | chunk_bits(a, range, ch + x + 1, hi) << 16;
+                            if (!(valid >> x & 1)) bits[c] &= 0xFFFF0000u;
+                            if (!(valid >> (x + 1) & 1)) bits[c] &= 0x0000FFFFu;
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
-                            best[e >> 1 & 1] = fmaxf(best[e >> 1 & 1], fmaxf(x, y));
-                            float zx, zy;
-                            ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
-                            const float px = ptx::ex2(zx), py = ptx::ex2(zy);
-                            part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
-                            p[16 * c + e / 2] = float2_to_act2<true>(px, py);
-                        }
+                        soft_half<true>(cols + 64 * h, f, m_run, bits, p, best, sum);
                     }
-                    float sum, other;
-                    ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
-                    sum += other;
-                    const float top = fmaxf(best[0], best[1]), up = top * f;
-                    const bool over = fmaf(top, f, -m_run) > kRescale && up > m_run;
+                    const float up = best * f;
+                    const bool over = fmaf(best, f, -m_run) > kRescale && up > m_run;
                     if (!__any_sync(0xffffffffu, over)) {
                         l_run += sum;
                         break;

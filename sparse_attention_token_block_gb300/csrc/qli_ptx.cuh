@@ -469,6 +469,14 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
+// The largest of three (NaN: the others)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // 2^x (about 2 ulp; 2^-infinity = 0)
 __device__ __forceinline__ float ex2(float x)
 {
