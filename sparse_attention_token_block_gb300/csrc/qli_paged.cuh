@@ -46,6 +46,28 @@ inline int64_t row_slots(const PagedArgs& a, int M, int group, int32_t* blocks)
     return (int64_t)a.p.total_q * group / M + a.p.batch + 1;
 }
 
+// Block `block` of sequence b (p.batch: of the rows behind the last); `reports`: sets the error bit of an invalid one
+__device__ __forceinline__ void rows_of_block(const PagedArgs& a, int b, int block, int M, int group, bool reports, RowBlock& r)
+{
+    const Params& p = a.p;
+    r.batch = b;
+    r.sq = r.sk = r.lc = 0;
+    int64_t tokens = p.s1;
+    if (b >= p.batch) {
+        r.row0 = p.batch > 0 ? a.seq_lens_q[p.batch - 1] : 0;
+        tokens = p.total_q - r.row0;
+    } else {
+        const BatchExtent e = batch_extent(p, a.seq_lens_q, a.seq_lens_k, b);
+        r.row0 = e.first;
+        if (p.layout_tnd) tokens = e.sq;
+        if (e.ok) r.sq = e.sq, r.sk = e.sk, r.lc = e.lc;
+        else if (reports && a.err) atomicOr(a.err, kErrLength);
+    }
+    const int64_t first = (int64_t)block * M, left = tokens * group - first;
+    r.first = (int32_t)min(first, (int64_t)INT32_MAX);
+    r.rows = (int32_t)max((int64_t)0, min((int64_t)M, left));
+}
+
 // Block number `slot`, found by the whole CTA; rows = 0 for a number that no block has.  False: the prefix sums
 // are invalid.
 __device__ __forceinline__ bool find_rows(const PagedArgs& a, uint32_t slot, int blocks, int M, int group, RowBlock* out)
@@ -73,26 +95,7 @@ __device__ __forceinline__ bool find_rows(const PagedArgs& a, uint32_t slot, int
         const int64_t done = b > 0 ? a.seq_lens_q[b - 1] : 0;
         block = (int)((int64_t)slot - (done * group / M + b));
     }
-    if (threadIdx.x == 0) {
-        RowBlock r;
-        r.batch = b;
-        r.sq = r.sk = r.lc = 0;
-        int64_t tokens = p.s1;
-        if (b >= p.batch) {                                        // behind the last sequence
-            r.row0 = p.batch > 0 ? a.seq_lens_q[p.batch - 1] : 0;
-            tokens = p.total_q - r.row0;
-        } else {
-            const BatchExtent e = batch_extent(p, a.seq_lens_q, a.seq_lens_k, b);
-            r.row0 = e.first;
-            if (p.layout_tnd) tokens = e.sq;
-            if (e.ok) r.sq = e.sq, r.sk = e.sk, r.lc = e.lc;
-            else if (a.err) atomicOr(a.err, kErrLength);
-        }
-        const int64_t first = (int64_t)block * M, left = tokens * group - first;
-        r.first = (int32_t)min(first, (int64_t)INT32_MAX);
-        r.rows = (int32_t)max((int64_t)0, min((int64_t)M, left));
-        *out = r;
-    }
+    if (threadIdx.x == 0) rows_of_block(a, b, block, M, group, true, *out);
     __syncthreads();
     return true;
 }

@@ -11,11 +11,14 @@
 // the rows, each takes every other tile, and their results are joined at the end.  Roles:
 //   * one warp copies the KV head's bytes of a tile's positions by TMA, 16 positions of a page a box;
 //   * 4 converter warps, a position per thread, decode them into fp16 operands in shared memory: rows of positions
-//     for K and for V (V enters the product with its positions as the K dimension, "MN-major");
+//     for K and for V (V enters the product with its positions as the K dimension, "MN-major"); they also bring the
+//     queries in;
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
 //   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when a logit passes it
 //     by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+//   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
+//     come first), and the next block's positions and queries are under way while the last one's rows are written.
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
 // through distributed shared memory in a fixed order.
 //
@@ -37,13 +40,13 @@ namespace {
 
 constexpr int kM = 128, kTile = 128;                   // rows and positions of a product
 constexpr int kTileChunks = kTile / kChunk;
-constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kCopyWarp = 13;
-constexpr int kThreads = 32 * 14;
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kCopyWarp = 13;      // and one for work
+constexpr int kThreads = 32 * 15;
 constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
 constexpr float kRescale = 8.0f;
-constexpr uint64_t kWaitLimitNs = 200000000ull;
+constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 20000000000ull;      // (the length of a task: 2^31 positions)
 
 struct Layout {
     int32_t rows;          // of a block: 128 or 256
@@ -52,12 +55,25 @@ struct Layout {
     uint32_t block_recip;
 };
 
+// A block of rows and a KV head
+struct Task {
+    RowBlock blk;
+    KeyRange range;
+    int32_t kvh;
+    int32_t n;                                         // tiles of this CTA, or one of these
+};
+constexpr int32_t kNoMore = -1, kBadSums = -2;
+
 struct Shared {
-    uint64_t rawfull[kMaxRaw], rawfree[kMaxRaw], opfull[kRing], opfree[kRing], sfull[2], pfull[2], qfull, odone;
+    uint4 taken;                                       // the answer to a request for a pending CTA
+    uint64_t rawfull[kMaxRaw], rawfree[kMaxRaw], opfull[kRing], opfree[kRing], sfull[2], pfull[2];
+    uint64_t taskfull[2], taskfree[2], qfull, qfree, odone, oread, joined, copied, answer;
     uint32_t tmem, abort;
     uint8_t valid[8];                                  // chunks of a tile that lie in the pool
-    RowBlock blk;
-    float factor[2 * kM];
+    Task task[2];
+    uint32_t held, asking;                             // 1 + the CTA whose work is not in a task yet; a request is out
+    float factor[2][2 * kM];
+    float2 ml[2][2][kM];                               // maximum and sum of the streams' shared rows
 };
 
 template <int D>
@@ -74,13 +90,14 @@ struct Sizes {
     static_assert(kMaxRaw * raw <= operand + raw, "copied bytes");
 };
 
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err)
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, uint32_t* err,
+                                             uint64_t limit = kWaitLimitNs)
 {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 100000u))) {
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > kWaitLimitNs)) {
+        if (__any_sync(0xffffffffu, ptx::globaltimer() - t0 > limit)) {
             *abort = 1;
             if (err) atomicOr(err, kErrTimeout);
             return false;
@@ -201,6 +218,58 @@ __device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, const
     best = fmaxf(top[0], top[1]);
 }
 
+// The block number `slot`, found by a warp (as find_rows); false: the prefix sums are invalid
+__device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot, int blocks, int M, int group, RowBlock& r)
+{
+    const Params& p = a.p;
+    const int lane = threadIdx.x & 31;
+    int b, block;
+    if (!p.layout_tnd) {
+        b = (int)(slot / (uint32_t)blocks);
+        block = (int)(slot - (uint32_t)b * blocks);
+    } else {
+        bool bad = false;
+        b = 0;
+        for (int i0 = 0; i0 < p.batch; i0 += 32) {
+            const int i = i0 + lane;
+            bool before = false;
+            if (i < p.batch) {
+                const int64_t lo = i > 0 ? a.seq_lens_q[i - 1] : 0, hi = a.seq_lens_q[i];
+                if (lo < 0 || hi < lo || hi > p.total_q) bad = true;
+                else before = hi * group / M + i + 1 <= (int64_t)slot;
+            }
+            b += __popc(__ballot_sync(0xffffffffu, before));
+        }
+        if (__any_sync(0xffffffffu, bad)) return false;
+        const int64_t done = b > 0 ? a.seq_lens_q[b - 1] : 0;
+        block = (int)((int64_t)slot - (done * group / M + b));
+    }
+    rows_of_block(a, b, block, M, group, lane == 0, r);
+    return true;
+}
+
+// Four rows' worth of 64 bytes: lane k of each four holds four 16-byte pieces of row k and gets piece k of the four rows
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool odd = lane & bit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // piece i of the odd lane against piece i + bit of the even one
+                const uint32_t out = odd ? w[4 * i + e] : w[4 * (i + bit) + e];
+                const uint32_t in = __shfl_xor_sync(0xffffffffu, out, bit);
+                if (odd) w[4 * i + e] = in;
+                else w[4 * (i + bit) + e] = in;
+            }
+        }
+    }
+}
+
 template <bool F16, bool E2M1, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Layout L,
@@ -212,10 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.heads_q / a.heads_kv;
     const int rank = L.splits > 1 ? (int)ptx::cluster_rank() : 0;
-    // later rows of a sequence see more of it: they start first
-    const uint32_t tasks = gridDim.x / (uint32_t)L.splits, task = tasks - 1 - blockIdx.x / (uint32_t)L.splits;
-    const uint32_t slot = task / (uint32_t)a.heads_kv;
-    const int kvh = (int)(task - slot * a.heads_kv);
+    uint8_t* const ring = smem + (L.rows == kM ? 1 : 2) * Z::operand;
+    uint8_t* const raw = ring + kRing * Z::operand;
+    const int raw_stages = L.rows == kM ? kMaxRaw : 1;
 
     if (tid == 0) {
         for (int i = 0; i < kMaxRaw; ++i) {
@@ -229,9 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.sfull[i], 1);
             ptx::mbar_init(&sh.pfull[i], 4);
+            ptx::mbar_init(&sh.taskfull[i], 1);
+            ptx::mbar_init(&sh.taskfree[i], kSoftWarps + kConvWarps + 2);
+            sh.task[i].blk.rows = 0;
         }
-        ptx::mbar_init(&sh.qfull, kSoftWarps);
+        ptx::mbar_init(&sh.qfull, kConvWarps);
+        ptx::mbar_init(&sh.qfree, 1);
         ptx::mbar_init(&sh.odone, 1);
+        ptx::mbar_init(&sh.oread, kSoftWarps);
+        ptx::mbar_init(&sh.joined, kSoftWarps);
+        ptx::mbar_init(&sh.copied, 1);
+        ptx::mbar_init(&sh.answer, 1);
+        sh.held = blockIdx.x / (uint32_t)L.splits + 1;
+        sh.asking = 0;
         sh.abort = 0;
         ptx::fence_mbar_init();
     }
@@ -241,57 +319,243 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    const bool found = find_rows(a, slot, L.blocks, L.rows, group, &sh.blk);        // (every thread meets)
-    if (!found) __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    if (!found || sh.blk.rows == 0) {                      // (the whole cluster)
-        if (!found) clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
-        if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
-        return;
-    }
-    const RowBlock blk = sh.blk;
-    const bool shared = blk.rows <= kM;                    // both streams on the same rows
-    const KeyRange range = key_range(a, blk, group);
-    const int all_tiles = (range.chunks + kTileChunks - 1) / kTileChunks;
-    const int n = max(0, (all_tiles - rank + L.splits - 1) / L.splits);        // tiles of this CTA
-    auto steps_of = [&](int q) { return shared ? (n - q + 1) / 2 : n; };
-    auto tile_of = [&](int q, int j) { return shared ? 2 * j + q : j; };
-    uint8_t* const ring = smem + (shared ? 1 : 2) * Z::operand;
-    uint8_t* const raw = ring + kRing * Z::operand;
-    const int raw_stages = shared ? kMaxRaw : 1;
 
-    float m_run = -FLT_MAX, l_run = 0.0f;                  // softmax threads
+    // whether the streams share a task's rows, and a stream's steps and tiles
+    auto shares = [](const Task& k) { return k.blk.rows <= kM; };
+    auto steps_of = [&](const Task& k, int q) { return shares(k) ? (k.n - q + 1) / 2 : k.n; };
+    auto tile_of = [&](const Task& k, int q, int j) { return shares(k) ? 2 * j + q : j; };
+    // global head row of a task's row i: `base` + i + (tokens before it) (heads_q - group)
+    const uint32_t recip = 65536 / group + 1;              // exact quotients of numbers below 512 by up to 256
+    struct Heads {
+        int64_t base;
+        uint32_t rest;
+    };
+    auto heads_of = [&](const Task& k) {
+        const int tok0 = k.blk.first / group;
+        Heads h;
+        h.rest = (uint32_t)(k.blk.first - tok0 * group);
+        h.base = (k.blk.row0 + tok0) * a.heads_q + k.kvh * group + h.rest;
+        return h;
+    };
+    auto head_of = [&](const Heads& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 16) * (a.heads_q - group); };
+    // the next task; false when a wait gave up.  A role that keeps nothing of the entry hands it back at once.
+    auto next_task = [&](int it, Task& k, bool keep) {
+        if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err)) return false;
+        k = sh.task[it & 1];
+        __syncwarp();
+        if (!keep && lane == 0) ptx::mbar_arrive(&sh.taskfree[it & 1]);
+        return true;
+    };
+    uint16_t* const dst = static_cast<uint16_t*>(a.out);
+    constexpr int kStride = D + 4;                         // of partial rows (splits), in floats
+    float* const part_o = reinterpret_cast<float*>(smem);  // [2 * kM][kStride], then the rows' (maximum, sum)
+    float2* const part_ml = reinterpret_cast<float2*>(part_o + 2 * kM * kStride);
+    static_assert(2 * kM * (kStride * 4 + 8) <= Z::shared_at, "partial results in the operands' place");
+    Task task;
+
     if (warp < kSoftWarps) {
-        // ---- the queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
+        // ---------------------------------------------------------------- softmax
+        const int q = warp >> 2, lane_row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), cols = lanes + kTile * q, out = lanes + kColO;
+        uint32_t step = 0, tiles = 0, turn = 0;            // steps, tiles and tasks with tiles so far
+        uint32_t joins = 0;
+        for (int it = 0;; ++it) {
+            if (!next_task(it, task, true) || task.n < 0) break;
+            const bool shared = shares(task);
+            const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
+            float m_run = -FLT_MAX, l_run = 0.0f;
+            bool ok = true;
+            if (task.n > 0) {
+                const int hi = seen_end(a, task.blk, (task.blk.first + row) / group);
+                if (!wait_bounded(&sh.qfull, turn & 1, &sh.abort, a.err)) break;
+                const float f = sh.factor[turn & 1][row];
+                for (int j = 0; j < steps; ++j, ++step) {
+                    const int t = tile_of(task, q, j), ch = kTileChunks * (t * L.splits + rank);
+                    ok = wait_bounded(&sh.sfull[q], step & 1, &sh.abort, a.err);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t valid = sh.valid[(tiles + t) & 7];
+                    const bool whole = valid == 0xFFu && task.range.all_see(ch, kTileChunks);
+                    // half a tile at a time
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+                        while (true) {
+                            float best = -INFINITY, sum;
+                            if (whole) {
+                                soft_half<false>(cols + 64 * h, f, m_run, nullptr, p, best, sum);
+                            } else {
+                                uint32_t bits[2];
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const int x = 4 * h + 2 * c;
+                                    bits[c] = chunk_bits(a, task.range, ch + x, hi) | chunk_bits(a, task.range, ch + x + 1, hi) << 16;
+                                    if (!(valid >> x & 1)) bits[c] &= 0xFFFF0000u;
+                                    if (!(valid >> (x + 1) & 1)) bits[c] &= 0x0000FFFFu;
+                                }
+                                soft_half<true>(cols + 64 * h, f, m_run, bits, p, best, sum);
+                            }
+                            const float up = best * f;
+                            const bool over = fmaf(best, f, -m_run) > kRescale && up > m_run;
+                            if (!__any_sync(0xffffffffu, over)) {
+                                l_run += sum;
+                                break;
+                            }
+                            // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's
+                            // first half of P.  (The stream's last product was issued before these logits, and has ended.)
+                            const float g = over ? ptx::ex2(m_run - up) : 1.0f;
+                            if (over) m_run = up;
+                            l_run *= g;
+                            if (h == 1) {
+                                uint32_t o[32];
+                                ptx::tmem_wait_st();
+                                QLI_TMEM_LD_X32(cols, o);
+                                wait_loaded(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float2 v = act2_to_float2<true>(o[e]);
+                                    o[e] = float2_to_act2<true>(v.x * g, v.y * g);
+                                }
+                                QLI_TMEM_ST_X32(cols, o);
+                            }
+                            if (j == 0) continue;
+#pragma unroll 1
+                            for (int x = 0; x < D / 32; ++x) {
+                                uint32_t o[32];
+                                QLI_TMEM_LD_X32(out + D * q + 32 * x, o);
+                                wait_loaded(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                                QLI_TMEM_ST_X32(out + D * q + 32 * x, o);
+                            }
+                        }
+                        // in the place of the logits that are through
+                        QLI_TMEM_ST_X32(cols + 32 * h, p);
+                    }
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sh.pfull[q]);
+                }
+                if (!ok || !wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
+                ptx::tc_fence_after();
+            }
+            // ---- the rows' outputs.  Shared rows: each stream's warps join half of the elements of both accumulators.
+            float g[2] = {1.0f, 0.0f};
+            float top = m_run, sum = l_run;
+            const bool both = shared && steps_of(task, 1) > 0;
+            if (both) {
+                sh.ml[joins & 1][q][lane_row] = make_float2(m_run, l_run);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.joined);
+                if (!wait_bounded(&sh.joined, joins & 1, &sh.abort, a.err)) break;
+                const float2 u = sh.ml[joins & 1][0][lane_row], v = sh.ml[joins & 1][1][lane_row];
+                ++joins;
+                top = fmaxf(u.x, v.x);
+                g[0] = ptx::ex2(u.x - top);
+                g[1] = ptx::ex2(v.x - top);
+                sum = fmaf(g[0], u.y, g[1] * v.y);
+            }
+            // (a stream without steps of its own leaves shared rows to the other)
+            const bool writes = !shared || both || q == 0;
+            const int from = both ? q * (D / 64) : 0, to = both ? from + D / 64 : D / 32;
+            const uint32_t acc = out + (shared ? 0 : D * q);
+            const Heads heads = heads_of(task);
+            int64_t at[4];                                 // of the rows that these four lanes write
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[i] = (row & ~3) + i < task.blk.rows ? head_of(heads, (row & ~3) + i) * D + 8 * (lane & 3) : -1;
+            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            if (writes) {
+#pragma unroll 1
+                for (int x = from; x < to; ++x) {
+                    uint32_t o[32];
+                    if (task.n > 0) {
+                        QLI_TMEM_LD_X32(acc + 32 * x, o);
+                        wait_loaded(o);
+                        if (both) {
+                            uint32_t o2[32];
+                            QLI_TMEM_LD_X32(acc + D + 32 * x, o2);
+                            wait_loaded(o2);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(fmaf(g[0], __uint_as_float(o[e]), g[1] * __uint_as_float(o2[e])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
+                    auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
+                    if (L.splits > 1) {
+                        float4* to4 = reinterpret_cast<float4*>(part_o + row * kStride + 32 * x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) to4[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
+                        __syncwarp();
+                        continue;
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = sum == 0.0f ? 0u : float2_to_act2<F16>(el(2 * e) * inv, el(2 * e + 1) * inv);
+                    // 64 bytes of a row by four lanes
+                    transpose_pieces(w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (at[i] >= 0)
+                            *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    }
+                }
+            }
+            if (task.n > 0) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.oread);
+            }
+            if (L.splits > 1) {
+                if (writes && from == 0) part_ml[row] = make_float2(top, sum);
+            } else if (writes && from == 0 && row < task.blk.rows && a.lse) {
+                a.lse[head_of(heads, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            }
+            tiles += task.n;
+            turn += task.n > 0;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.taskfree[it & 1]);
+        }
+    } else if (warp < kMmaWarp) {
+        // ---------------------------------------------------------------- converters, a position per thread
+        const int row = tid - 32 * kConvWarp;
+        const bool stall = a.p.test_stall == 1;            // test switch: no tile is handed on, the waits run out
+        int rs = 0;
+        uint32_t rp = 0, tiles = 0, turn = 0;
+        // the task's queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
         // times a power of two of its largest magnitude)
-        {
+        auto queries = [&]() {
+            if (turn > 0 && !wait_bounded(&sh.qfree, turn - 1 & 1, &sh.abort, a.err)) return false;
             constexpr int kPerWarp = 16;
             // a lane's four (D = 64: two) elements; for int4 those of each eight in the order 0 4 1 5 2 6 3 7, as its
             // codes come
             const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
             const int x0 = E2M1 ? el : (el & ~7) + e8 / 2, x1 = E2M1 ? el + 2 : (el & ~7) + e8 / 2 + 1;
-            const int tok0 = blk.first / group, rest0 = blk.first - tok0 * group;
-            const uint32_t recip = 65536 / group + 1;      // exact quotients of numbers below 512 by up to 256
-            for (int m0 = warp * kPerWarp; m0 < (shared ? kM : 2 * kM); m0 += kSoftWarps * kPerWarp) {
-                uint32_t raw2[kPerWarp][2];
+            const int tok0 = task.blk.first / group, rest0 = task.blk.first - tok0 * group;
+            for (int m0 = (warp - kConvWarp) * kPerWarp; m0 < (shares(task) ? kM : 2 * kM); m0 += kConvWarps * kPerWarp) {
+                uint32_t w[kPerWarp][2];
 #pragma unroll
                 for (int x = 0; x < kPerWarp; ++x) {
                     const uint32_t i = rest0 + m0 + x, tok = i * recip >> 16;
-                    raw2[x][0] = raw2[x][1] = 0;
-                    if (m0 + x < blk.rows) {
-                        const uint16_t* src = static_cast<const uint16_t*>(a.query) + (blk.row0 + tok0 + tok) * a.q_stride +
-                                              (kvh * group + (int)(i - tok * group)) * D;
-                        if (E2M1) {
-                            if constexpr (D == 128) {
-                                const uint2 w = *reinterpret_cast<const uint2*>(src + x0);
-                                raw2[x][0] = w.x, raw2[x][1] = w.y;
-                            } else {
-                                raw2[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
-                            }
+                    w[x][0] = w[x][1] = 0;
+                    if (m0 + x < task.blk.rows) {
+                        const uint16_t* src = static_cast<const uint16_t*>(a.query) + (task.blk.row0 + tok0 + tok) * a.q_stride +
+                                              (task.kvh * group + (int)(i - tok * group)) * D;
+                        if (!E2M1) {
+                            w[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
+                            if (D == 128) w[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
+                        } else if (D == 128) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(src + x0);
+                            w[x][0] = v.x, w[x][1] = v.y;
                         } else {
-                            raw2[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
-                            if (D == 128) raw2[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
+                            w[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
                         }
                     }
                 }
@@ -300,319 +564,318 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int m = m0 + x;
                     uint32_t ex = 127;
                     if constexpr (!F16) {
-                        const float2 u = act2_to_float2<F16>(raw2[x][0]), v = act2_to_float2<F16>(raw2[x][1]);
+                        const float2 u = act2_to_float2<F16>(w[x][0]), v = act2_to_float2<F16>(w[x][1]);
                         // the largest magnitude's bits: non-negative floats order like integers
                         const float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-                        ex = min(max(top >> 23, 1u), 253u);
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+                        ex = min(max(most >> 23, 1u), 253u);
                         const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of the largest)
-                        raw2[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
-                        raw2[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
+                        w[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
+                        w[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
                     }
-                    uint8_t* dst = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
-                    if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(raw2[x][0], raw2[x][1]);
-                    else *reinterpret_cast<uint32_t*>(dst) = raw2[x][0];
+                    uint8_t* to = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
+                    if constexpr (D == 128) *reinterpret_cast<uint2*>(to) = make_uint2(w[x][0], w[x][1]);
+                    else *reinterpret_cast<uint32_t*>(to) = w[x][0];
                     // (above zero: the mask's -infinity times it stays -infinity)
                     if (lane == 0)
-                        sh.factor[m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f),
-                                                   1.0e-30f), 3.0e38f);
+                        sh.factor[turn & 1][m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f),
+                                                             1.0e-30f), 3.0e38f);
                 }
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sh.qfull);
-            wait_bounded(&sh.qfull, 0, &sh.abort, a.err);
-        }
-        // ---------------------------------------------------------------- softmax
-        const int q = warp >> 2, m = (shared ? 0 : q * kM) + (tid & 127), steps = steps_of(q);
-        const int hi = seen_end(a, blk, (blk.first + m) / group);
-        const float f = sh.factor[m];
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), cols = lanes + kTile * q, out = lanes + kColO + D * q;
-        for (int j = 0; j < steps; ++j) {
-            const int t = tile_of(q, j), ch = kTileChunks * (t * L.splits + rank);
-            if (!wait_bounded(&sh.sfull[q], j & 1, &sh.abort, a.err)) break;
-            ptx::tc_fence_after();
-            const uint32_t valid = sh.valid[t & 7];
-            const bool whole = valid == 0xFFu && range.all_see(ch, kTileChunks);
-            // half a tile at a time
+            return true;
+        };
+        for (int it = 0;; ++it) {
+            if (!next_task(it, task, false) || task.n < 0) break;
+            if (task.n == 0) continue;
+            const int lo = task.kvh * kv_unit_bytes(D) & 8;                    // (heads of 72 bytes)
+            bool ok = turn > 0 || queries();
+            for (int t = 0; ok && t < task.n; ++t, ++tiles) {
+                // the position's bytes into registers: the next tile's may land
+                const uint8_t* src = raw + rs * Z::raw + row * Z::raw_row + lo;
+                ok = wait_bounded(&sh.rawfull[rs], rp, &sh.abort, a.err);
+                if (!ok) break;
+                uint32_t kc[D / 8], vc[D / 8], ks[D / 64], vs[D / 64];
+                load_codes<D>(src, kc);
+                load_codes<D>(src + D / 2, vc);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-                while (true) {
-                    float best = -INFINITY, sum;
-                    if (whole) {
-                        soft_half<false>(cols + 64 * h, f, m_run, nullptr, p, best, sum);
-                    } else {
-                        uint32_t bits[2];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int x = 4 * h + 2 * c;
-                            bits[c] = chunk_bits(a, range, ch + x, hi) | chunk_bits(a, range, ch + x + 1, hi) << 16;
-                            if (!(valid >> x & 1)) bits[c] &= 0xFFFF0000u;
-                            if (!(valid >> (x + 1) & 1)) bits[c] &= 0x0000FFFFu;
-                        }
-                        soft_half<true>(cols + 64 * h, f, m_run, bits, p, best, sum);
-                    }
-                    const float up = best * f;
-                    const bool over = fmaf(best, f, -m_run) > kRescale && up > m_run;
-                    if (!__any_sync(0xffffffffu, over)) {
-                        l_run += sum;
-                        break;
-                    }
-                    // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's first
-                    // half of P.  (The stream's last product was issued before these logits, and has ended.)
-                    const float g = over ? ptx::ex2(m_run - up) : 1.0f;
-                    if (over) m_run = up;
-                    l_run *= g;
-                    if (h == 1) {
-                        uint32_t o[32];
-                        ptx::tmem_wait_st();
-                        QLI_TMEM_LD_X32(cols, o);
-                        wait_loaded(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float2 v = act2_to_float2<true>(o[e]);
-                            o[e] = float2_to_act2<true>(v.x * g, v.y * g);
-                        }
-                        QLI_TMEM_ST_X32(cols, o);
-                    }
-                    if (j == 0) continue;
-#pragma unroll 1
-                    for (int x = 0; x < D / 32; ++x) {
-                        uint32_t o[32];
-                        QLI_TMEM_LD_X32(out + 32 * x, o);
-                        wait_loaded(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-                        QLI_TMEM_ST_X32(out + 32 * x, o);
-                    }
+                for (int i = 0; i < D / 64; ++i) {
+                    ks[i] = reinterpret_cast<const uint32_t*>(src + D)[i];
+                    vs[i] = reinterpret_cast<const uint32_t*>(src + D + D / 16)[i];
+                    // a NaN (0x7F or 0xFF) among the values' scales becomes one of the keys'
+                    ks[i] |= __vcmpeq4(vs[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                 }
-                // in the place of the logits that are through
-                QLI_TMEM_ST_X32(cols + 32 * h, p);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.rawfree[rs]);
+                if (++rs == raw_stages) rs = 0, rp ^= 1;
+                // fills 2 tiles and 2 tiles + 1 of the ring
+                const int sk = 2 * tiles & 3, sv = sk + 1;
+                const uint32_t free_phase = (tiles >> 1 & 1) ^ 1;
+                PairScale g[D / 16];
+                scale_pairs<E2M1>(ks, false, g);
+                ok = wait_bounded(&sh.opfree[sk], free_phase, &sh.abort, a.err);
+                if (!ok) break;
+                store_row<E2M1, D>(ring + sk * Z::operand, row, kc, g);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sk]);
+                scale_pairs<E2M1>(vs, true, g);
+                ok = wait_bounded(&sh.opfree[sv], free_phase, &sh.abort, a.err);
+                if (!ok) break;
+                store_row<E2M1, D>(ring + sv * Z::operand, row, vc, g);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sv]);
+                // (behind the first tile: the queries of the task before are needed until its last logits are there)
+                if (t == 0 && turn > 0) ok = queries();
             }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.pfull[q]);
-        }
-    } else if (warp < kMmaWarp) {
-        // ---------------------------------------------------------------- converters, a position per thread
-        const int row = tid - 32 * kConvWarp, lo = kvh * kv_unit_bytes(D) & 8;       // (heads of 72 bytes)
-        const bool stall = a.p.test_stall == 1;            // test switch: no tile is handed on, the waits run out
-        int rs = 0;
-        uint32_t rp = 0;
-        for (int t = 0; t < n; ++t) {
-            // the position's bytes into registers: the next tile's may land
-            const uint8_t* src = raw + rs * Z::raw + row * Z::raw_row + lo;
-            if (!wait_bounded(&sh.rawfull[rs], rp, &sh.abort, a.err)) break;
-            uint32_t kc[D / 8], vc[D / 8], ks[D / 64], vs[D / 64];
-            load_codes<D>(src, kc);
-            load_codes<D>(src + D / 2, vc);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                ks[i] = reinterpret_cast<const uint32_t*>(src + D)[i];
-                vs[i] = reinterpret_cast<const uint32_t*>(src + D + D / 16)[i];
-                // a NaN (0x7F or 0xFF) among the values' scales becomes one of the keys'
-                ks[i] |= __vcmpeq4(vs[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.rawfree[rs]);
-            if (++rs == raw_stages) rs = 0, rp ^= 1;
-            // fills 2 t and 2 t + 1 of the ring
-            const int sk = 2 * t & 3, sv = sk + 1;
-            const uint32_t free_phase = (t >> 1 & 1) ^ 1;
-            PairScale g[D / 16];
-            scale_pairs<E2M1>(ks, false, g);
-            if (!wait_bounded(&sh.opfree[sk], free_phase, &sh.abort, a.err)) break;
-            store_row<E2M1, D>(ring + sk * Z::operand, row, kc, g);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sk]);
-            scale_pairs<E2M1>(vs, true, g);
-            if (!wait_bounded(&sh.opfree[sv], free_phase, &sh.abort, a.err)) break;
-            store_row<E2M1, D>(ring + sv * Z::operand, row, vc, g);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sv]);
+            if (!ok) break;
+            ++turn;
         }
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------------- copies, a chunk per lane
-        const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
-        const int x = (kvh * kv_unit_bytes(D) & ~15) / 8;
-        int rs = 0, at = 0, page = INT32_MIN;
-        uint32_t rp = 1;
-        if (n > 0 && lane < kTileChunks) page = chunk_page(a, range, table, L.block_recip, kTileChunks * rank + lane, &at);
-        for (int t = 0; t < n; ++t) {
-            const int pg = page, ps = at;
-            const bool ok = pg >= 0 && pg < a.p.num_blocks;
-            if (!ok && pg != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
-            const uint32_t live = __ballot_sync(0xffffffffu, ok);
-            if (t + 1 < n && lane < kTileChunks)
-                page = chunk_page(a, range, table, L.block_recip, kTileChunks * ((t + 1) * L.splits + rank) + lane, &at);
-            if (!wait_bounded(&sh.rawfree[rs], rp, &sh.abort, a.err)) break;
-            if (lane == 0) {
-                sh.valid[t & 7] = (uint8_t)live;
-                ptx::mbar_arrive_expect_tx(&sh.rawfull[rs], __popc(live) * kChunk * Z::raw_row);
+        int rs = 0;
+        uint32_t rp = 1, tiles = 0;
+        for (int it = 0;; ++it) {
+            if (!next_task(it, task, false) || task.n < 0) break;
+            const int32_t* table = a.block_table + (int64_t)task.blk.batch * a.p.max_blocks_per_seq;
+            const int x = (task.kvh * kv_unit_bytes(D) & ~15) / 8;
+            int at = 0, page = INT32_MIN;
+            if (task.n > 0 && lane < kTileChunks) page = chunk_page(a, task.range, table, L.block_recip, kTileChunks * rank + lane, &at);
+            bool ok = true;
+            for (int t = 0; t < task.n; ++t, ++tiles) {
+                const int pg = page, ps = at;
+                const bool here = pg >= 0 && pg < a.p.num_blocks;
+                if (!here && pg != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
+                const uint32_t live = __ballot_sync(0xffffffffu, here);
+                if (t + 1 < task.n && lane < kTileChunks)
+                    page = chunk_page(a, task.range, table, L.block_recip, kTileChunks * ((t + 1) * L.splits + rank) + lane, &at);
+                ok = wait_bounded(&sh.rawfree[rs], rp, &sh.abort, a.err);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.valid[tiles & 7] = (uint8_t)live;
+                    ptx::mbar_arrive_expect_tx(&sh.rawfull[rs], __popc(live) * kChunk * Z::raw_row);
+                }
+                __syncwarp();
+                if (here) ptx::tma_load_3d(raw + rs * Z::raw + lane * kChunk * Z::raw_row, &pages, x, ps, pg, &sh.rawfull[rs]);
+                __syncwarp();
+                if (++rs == raw_stages) rs = 0, rp ^= 1;
             }
-            __syncwarp();
-            if (ok) ptx::tma_load_3d(raw + rs * Z::raw + lane * kChunk * Z::raw_row, &pages, x, ps, pg, &sh.rawfull[rs]);
-            __syncwarp();
-            if (++rs == raw_stages) rs = 0, rp ^= 1;
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive(&sh.copied);
         }
-    } else {
+    } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- products
         const uint32_t idesc_s = ptx::idesc_f16_f32(kM, kTile), idesc_o = ptx::idesc_f16_f32(kM, D) | ptx::kIdescMajorB;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t qd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(smem));
         const uint64_t kd = ptx::sdesc_kmajor_sw128(ptx::smem_addr(ring));
         const uint64_t vd = ptx::sdesc_mnmajor_sw128(ptx::smem_addr(ring), Z::atom);
-        auto logits = [&](int q, int t) {
-            const int stage = 2 * t & 3;
-            if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err)) return false;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint64_t qo = qd + ((shared ? 0 : q * Z::operand) >> 4), ko = kd + (stage * Z::operand >> 4);
+        uint32_t tiles = 0, turn = 0, step0 = 0, step1 = 0;
+        for (int it = 0;; ++it) {
+            if (!next_task(it, task, false) || task.n < 0) break;
+            if (task.n == 0) continue;
+            const bool shared = shares(task);
+            const int s0 = steps_of(task, 0), s1 = steps_of(task, 1);
+            int left = s0 + s1;                            // logits to issue
+            auto logits = [&](int q, int j) {
+                const uint32_t t = tiles + tile_of(task, q, j);
+                const int stage = 2 * t & 3;
+                if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err)) return false;
+                ptx::tc_fence_after();
+                --left;
+                if (ptx::elect_one()) {
+                    const uint64_t qo = qd + ((shared ? 0 : q * Z::operand) >> 4), ko = kd + (stage * Z::operand >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int off = (kk >> 2) * Z::atom + (kk & 3) * 32;
-                    ptx::mma_f16_ss(tm + kTile * q, qo + (off >> 4), ko + (off >> 4), idesc_s, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int off = (kk >> 2) * Z::atom + (kk & 3) * 32;
+                        ptx::mma_f16_ss(tm + kTile * q, qo + (off >> 4), ko + (off >> 4), idesc_s, kk > 0);
+                    }
+                    ptx::mma_commit(&sh.sfull[q]);
+                    if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
+                    if (left == 0) ptx::mma_commit(&sh.qfree);
                 }
-                ptx::mma_commit(&sh.sfull[q]);
-                if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto output = [&](int q, int t, int j) {
-            const int stage = (2 * t & 3) + 1;
-            if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err) || !wait_bounded(&sh.pfull[q], j & 1, &sh.abort, a.err))
-                return false;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint64_t vo = vd + (stage * Z::operand >> 4);
+                __syncwarp();
+                return true;
+            };
+            auto output = [&](int q, int j) {
+                const uint32_t t = tiles + tile_of(task, q, j);
+                const int stage = (2 * t & 3) + 1;
+                if (!wait_bounded(&sh.opfull[stage], t >> 1 & 1, &sh.abort, a.err) ||
+                    !wait_bounded(&sh.pfull[q], (q ? step1 : step0) + j & 1, &sh.abort, a.err))
+                    return false;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    const uint64_t vo = vd + (stage * Z::operand >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + 8 * kk, vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0);
-                if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + 8 * kk, vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0);
+                    if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = wait_bounded(&sh.qfull, turn & 1, &sh.abort, a.err) && logits(0, 0);
+            if (ok && s1 > 0) ok = logits(1, 0);
+            // (the accumulators of the task before have been read)
+            if (ok && turn > 0) ok = wait_bounded(&sh.oread, turn - 1 & 1, &sh.abort, a.err);
+            // a stream's next logits follow its output, so that the other's products run beside its softmax
+            for (int j = 0; ok && j < s0; ++j) {
+                ok = output(0, j);
+                if (ok && j + 1 < s0) ok = logits(0, j + 1);
+                if (ok && j < s1) ok = output(1, j);
+                if (ok && j + 1 < s1) ok = logits(1, j + 1);
             }
-            __syncwarp();
-            return true;
-        };
-        // a stream's next logits follow its output, so that the other's products run beside its softmax
-        const int s0 = steps_of(0), s1 = steps_of(1);
-        bool ok = wait_bounded(&sh.qfull, 0, &sh.abort, a.err);
-        if (ok && s0 > 0) ok = logits(0, tile_of(0, 0));
-        if (ok && s1 > 0) ok = logits(1, tile_of(1, 0));
-        for (int j = 0; ok && j < s0; ++j) {
-            ok = output(0, tile_of(0, j), j);
-            if (ok && j + 1 < s0) ok = logits(0, tile_of(0, j + 1));
-            if (ok && j < s1) ok = output(1, tile_of(1, j), j);
-            if (ok && j + 1 < s1) ok = logits(1, tile_of(1, j + 1));
-        }
-        if (ok && n > 0) {
+            if (!ok) break;
             if (ptx::elect_one()) ptx::mma_commit(&sh.odone);
             __syncwarp();
+            tiles += task.n, step0 += s0, step1 += s1, ++turn;
+        }
+    } else {
+        // ---------------------------------------------------------------- work.  Later rows of a sequence see more of it:
+        // they start first.
+        const uint32_t tasks = gridDim.x / (uint32_t)L.splits;
+        uint32_t id = blockIdx.x / (uint32_t)L.splits, asked = 0;
+        bool more = true, ok = true;
+        for (int it = 0; more; ++it) {
+            Task k;
+            k.n = k.blk.rows = 0;
+            const uint32_t at = tasks - 1 - id, slot = at / (uint32_t)a.heads_kv;
+            k.kvh = (int)(at - slot * a.heads_kv);
+            if (!find_rows_warp(a, slot, L.blocks, L.rows, group, k.blk)) {
+                k.n = kBadSums;
+                more = false;
+            } else if (k.blk.rows > 0) {
+                k.range = key_range(a, k.blk, group);
+                const int all = (k.range.chunks + kTileChunks - 1) / kTileChunks;
+                k.n = max(0, (all - rank + L.splits - 1) / L.splits);
+            }
+            if (k.n < 0 || k.blk.rows > 0) {
+                ok = wait_bounded(&sh.taskfree[it & 1], (it >> 1 & 1) ^ 1, &sh.abort, a.err, kTaskLimitNs);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.task[it & 1] = k;
+                    sh.held = 0;
+                    ptx::mbar_arrive(&sh.taskfull[it & 1]);
+                }
+                __syncwarp();
+            } else {
+                --it;                                      // (a number that no block has)
+                if (lane == 0) sh.held = 0;
+            }
+            if (!more) break;
+            more = false;
+            if (L.splits == 1) {
+                // (not before the task's last copy, a few tiles ahead of its end: 472 blocks of 100 to 400 us 1099 us when
+                // the next one is taken at once)
+                if (it >= 0) ok = wait_bounded(&sh.copied, it & 1, &sh.abort, a.err, kTaskLimitNs);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.asking = 1;
+                    ptx::mbar_arrive_expect_tx(&sh.answer, 16);
+                    ptx::take_pending_cta(&sh.taken, &sh.answer);
+                }
+                __syncwarp();
+                ok = wait_bounded(&sh.answer, asked & 1, &sh.abort, a.err);
+                if (!ok) break;
+                ++asked;
+                more = ptx::taken_cta(&sh.taken, id);
+                if (lane == 0) sh.asking = 0, sh.held = more ? id + 1 : 0;
+                ptx::fence_proxy_async_smem();             // (the next answer lands in the same place)
+                __syncwarp();
+            }
+            if (!more) {
+                const int end = it + 1;
+                ok = wait_bounded(&sh.taskfree[end & 1], (end >> 1 & 1) ^ 1, &sh.abort, a.err, kTaskLimitNs);
+                if (ok && lane == 0) {
+                    sh.task[end & 1].n = kNoMore;
+                    sh.task[end & 1].blk.rows = 0;
+                    ptx::mbar_arrive(&sh.taskfull[end & 1]);
+                }
+                __syncwarp();
+            }
         }
     }
 
-    // ---- join and write
+    // ---- the end
     __syncwarp();
-    if (n > 0) wait_bounded(&sh.odone, 0, &sh.abort, a.err);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const bool failed = sh.abort != 0;
-    if (failed && warp == kMmaWarp) {                      // products and copies that are still under way end first
-        const uint64_t t0 = ptx::globaltimer();
-        while (ptx::globaltimer() - t0 < kWaitLimitNs) {
-        }
-    }
-    if (failed) __syncthreads();
-    // global head row of the block's row i
-    auto head_of = [&](int i) {
-        const int at = blk.first + i, tok = at / group;
-        return (blk.row0 + tok) * a.heads_q + kvh * group + at - tok * group;
-    };
-    uint16_t* const dst = static_cast<uint16_t*>(a.out);
-    const bool joins = shared || L.splits > 1;
-    constexpr int kStride = D + 4;                         // of partial rows, in floats
-    float* const part_o = reinterpret_cast<float*>(smem);  // [2 * kM][kStride], then the rows' (maximum, sum)
-    float2* const part_ml = reinterpret_cast<float2*>(part_o + 2 * kM * kStride);
-    static_assert(2 * kM * (kStride * 4 + 8) <= Z::shared_at, "partial results in the operands' place");
-    if (warp < kSoftWarps) {
-        const int q = warp >> 2, m = tid & 127, i = (shared ? 0 : q * kM) + m;
-        const bool live = i < blk.rows, some = steps_of(q) > 0;
-        const uint32_t cols = tmem + ((uint32_t)(warp & 3) << 21) + kColO + D * q;
-        const float sum = failed ? __int_as_float(0x7FC00000) : l_run;
-        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-        const int64_t head = live ? head_of(i) : 0;
-#pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            if (some) {
-                QLI_TMEM_LD_X32(cols + 32 * x, o);
-                wait_loaded(o);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0;
+    if (sh.abort != 0) {
+        if (warp == kMmaWarp) {                            // products and copies that are still under way end first
+            const uint64_t t0 = ptx::globaltimer();
+            while (ptx::globaltimer() - t0 < kWaitLimitNs) {
             }
-            // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
-            auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
-            if (live && joins) {
-                float4* to = reinterpret_cast<float4*>(part_o + (q * kM + m) * kStride + 32 * x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
-            } else if (live) {
-                uint4* to = reinterpret_cast<uint4*>(dst + head * D + 32 * x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        w[z] = sum == 0.0f ? 0u : float2_to_act2<F16>(el(8 * e + 2 * z) * inv, el(8 * e + 2 * z + 1) * inv);
-                    to[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            __syncwarp();                                  // (the loads take the whole warp)
         }
-        if (joins) part_ml[q * kM + m] = make_float2(m_run, sum);
-        else if (live && a.lse) a.lse[head] = sum == 0.0f ? -INFINITY : (m_run + log2f(sum)) * 0.6931471805599453f;
+        __syncthreads();
+        // NaN for the rows of every task that this CTA may have left
+        auto fail_rows = [&](const Task& k) {
+            const Heads heads = heads_of(k);
+            for (int i = tid; i < k.blk.rows * (D / 8); i += kThreads)
+                reinterpret_cast<uint4*>(dst + head_of(heads, i / (D / 8)) * D)[i % (D / 8)] =
+                    make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            if (a.lse)
+                for (int i = tid; i < k.blk.rows; i += kThreads) a.lse[head_of(heads, i)] = __int_as_float(0x7FC00000);
+        };
+        if (rank == 0) {
+            fail_rows(sh.task[0]);
+            fail_rows(sh.task[1]);
+            uint32_t held = sh.held, id;
+            if (sh.asking && ptx::taken_cta(&sh.taken, id)) held = id + 1;
+            if (held > 0) {
+                const uint32_t at = gridDim.x / (uint32_t)L.splits - held, slot = at / (uint32_t)a.heads_kv;
+                task.kvh = (int)(at - slot * a.heads_kv);
+                if (find_rows_warp(a, slot, L.blocks, L.rows, group, task.blk)) fail_rows(task);
+            }
+        }
+    } else if (sh.task[0].n == kBadSums) {
+        clear_rows(a, D, (int64_t)blockIdx.x * kThreads + tid, (int64_t)gridDim.x * kThreads);
     }
-    if (joins) {
-        if (L.splits > 1) ptx::cluster_sync();
-        else __syncthreads();
-        const int pieces = blk.rows * (D / 4), streams = shared ? 2 : 1;
+    if (L.splits > 1) {
+        // join the cluster's partial results (of its only task)
+        const bool failed = sh.abort != 0;
+        const Task& k = sh.task[0];
+        const Heads heads = heads_of(k);
+        if (failed) {
+            for (int i = tid; i < 2 * kM; i += kThreads) part_ml[i] = make_float2(0.0f, __int_as_float(0x7FC00000));
+        }
+        ptx::cluster_sync();
+        const int pieces = (k.n >= 0 ? k.blk.rows : 0) * (D / 4);
         for (int z = rank * kThreads + tid; z < pieces; z += L.splits * kThreads) {
             const int i = z / (D / 4), d4 = z % (D / 4);
             float top = -FLT_MAX, sum = 0.0f;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int parts = streams * L.splits;
-            // part x: stream x % streams of CTA x / streams
-            auto ml_of = [&](int x) {
-                return ptx::ld_cluster2(ptx::cluster_addr(ptx::smem_addr(part_ml + i + (shared ? kM * (x & 1) : 0)), shared ? x >> 1 : x));
-            };
-            for (int x = 0; x < parts; ++x) top = fmaxf(top, ml_of(x).x);
-            for (int x = 0; x < parts; ++x) {
-                const float2 ml = ml_of(x);
-                const float4 v = ptx::ld_cluster4(ptx::cluster_addr(
-                    ptx::smem_addr(part_o + (i + (shared ? kM * (x & 1) : 0)) * kStride + 4 * d4), shared ? x >> 1 : x));
-                const float g = ptx::ex2(ml.x - top);
-                sum = fmaf(g, ml.y, sum);
-                acc.x = fmaf(g, v.x, acc.x), acc.y = fmaf(g, v.y, acc.y);
-                acc.z = fmaf(g, v.z, acc.z), acc.w = fmaf(g, v.w, acc.w);
+            float2 ml[kMaxSplits];
+            float4 v[kMaxSplits];
+#pragma unroll
+            for (int x = 0; x < kMaxSplits; ++x) {
+                ml[x] = make_float2(-FLT_MAX, 0.0f);
+                v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x < L.splits) {
+                    ml[x] = ptx::ld_cluster2(ptx::cluster_addr(ptx::smem_addr(part_ml + i), x));
+                    v[x] = ptx::ld_cluster4(ptx::cluster_addr(ptx::smem_addr(part_o + i * kStride + 4 * d4), x));
+                }
+                top = fmaxf(top, ml[x].x);
             }
-            const int64_t head = head_of(i);
+#pragma unroll
+            for (int x = 0; x < kMaxSplits; ++x) {
+                const float g = ptx::ex2(ml[x].x - top);
+                sum = fmaf(g, ml[x].y, sum);
+                acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
+                acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
+            }
+            const int64_t head = head_of(heads, i);
             const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
             *reinterpret_cast<uint2*>(dst + head * D + 4 * d4) =
                 make_uint2(float2_to_act2<F16>(acc.x * inv, acc.y * inv), float2_to_act2<F16>(acc.z * inv, acc.w * inv));
             if (a.lse && d4 == 0) a.lse[head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
         __syncwarp();
-        if (L.splits > 1) ptx::cluster_sync();             // no CTA leaves while another reads its partial results
+        ptx::cluster_sync();                               // no CTA leaves while another reads its partial results
     }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 

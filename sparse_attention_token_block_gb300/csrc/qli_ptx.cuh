@@ -154,6 +154,34 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // ... and allow the next grid in the stream to begin launching before this one exits.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ------------------------------------------------------------------------------------ pending CTAs
+// Ask for a CTA of this grid that has not begun yet: 16 bytes at `response` (16-byte aligned) say which one this CTA
+// takes over, if any; their arrival counts on `bar`.  After an answer of none no further request may follow.
+__device__ __forceinline__ void take_pending_cta(void* response, uint64_t* bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_addr(response)),
+                 "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// The answer: whether a CTA was taken over, and its blockIdx.x
+__device__ __forceinline__ bool taken_cta(const void* response, uint32_t& x)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_addr(response))
+        : "memory");
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_proxy_async_smem()
 {
