@@ -181,11 +181,8 @@ __device__ __forceinline__ void store_row(uint8_t* operand, int row, const uint3
     }
 }
 
-// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, their sum and the largest
-// logit; kMasked: where `bits` is not set the logit counts as -infinity
-template <bool kMasked>
-__device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, const uint32_t* bits, uint32_t (&p)[32], float& best,
-                                          float& sum)
+// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, their sum and the largest logit
+__device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, uint32_t (&p)[32], float& best, float& sum)
 {
     uint32_t s[2][32];
     QLI_TMEM_LD_X32(cols, s[0]);
@@ -199,10 +196,6 @@ __device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, const
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-            if constexpr (kMasked) {
-                s[c][e] = __float_as_uint(bits[c] & (1u << e) ? __uint_as_float(s[c][e]) : -INFINITY);
-                s[c][e + 1] = __float_as_uint(bits[c] & (2u << e) ? __uint_as_float(s[c][e + 1]) : -INFINITY);
-            }
             const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
             top[e >> 1 & 1] = ptx::max3(top[e >> 1 & 1], x, y);
             float zx, zy;
@@ -216,6 +209,119 @@ __device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, const
     ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
     sum += other;
     best = fmaxf(top[0], top[1]);
+}
+
+// The rarer steps are calls, so that they take no registers from the ones above.
+
+// -infinity for those of a row's 64 logits whose bit is not set
+__device__ __noinline__ void mask_half(uint32_t cols, uint32_t bits0, uint32_t bits1)
+{
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t bits = c ? bits1 : bits0;
+        uint32_t s[32];
+        QLI_TMEM_LD_X32(cols + 32 * c, s);
+        wait_loaded(s);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = bits & (1u << e) ? s[e] : 0xFF800000u;
+        QLI_TMEM_ST_X32(cols + 32 * c, s);
+    }
+    ptx::tmem_wait_st();
+}
+
+// A row's accumulators (32 n columns) times g
+__device__ __noinline__ void scale_row(uint32_t cols, int n, float g)
+{
+#pragma unroll 1
+    for (int x = 0; x < n; ++x) {
+        uint32_t o[32];
+        QLI_TMEM_LD_X32(cols + 32 * x, o);
+        wait_loaded(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+        QLI_TMEM_ST_X32(cols + 32 * x, o);
+    }
+}
+
+// A row's 64 probabilities times g
+__device__ __noinline__ void scale_half(uint32_t cols, float g)
+{
+    uint32_t o[32];
+    ptx::tmem_wait_st();
+    QLI_TMEM_LD_X32(cols, o);
+    wait_loaded(o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        const float2 v = act2_to_float2<true>(o[e]);
+        o[e] = float2_to_act2<true>(v.x * g, v.y * g);
+    }
+    QLI_TMEM_ST_X32(cols, o);
+}
+
+// Four rows' worth of 64 bytes: lane k of each four holds four 16-byte pieces of row k and gets piece k of the four rows
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool odd = lane & bit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // piece i of the odd lane against piece i + bit of the even one
+                const uint32_t out = odd ? w[4 * i + e] : w[4 * (i + bit) + e];
+                const uint32_t in = __shfl_xor_sync(0xffffffffu, out, bit);
+                if (odd) w[4 * i + e] = in;
+                else w[4 * (i + bit) + e] = in;
+            }
+        }
+    }
+}
+
+// Columns [32 from, 32 to) of a row's accumulators from `acc` on (with `both`, joined with those D further, weighted g0 and
+// g1; without `some`, zeros) into the output, times inv, or as they are into `partial`.  Four neighbouring lanes write 64
+// bytes of each other's rows, which begin at elements at0 ... at3 (-1: none).
+template <bool F16, bool E2M1, int D>
+__device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool both, bool some, float g0, float g1, float inv, uint16_t* dst,
+                                        int64_t at0, int64_t at1, int64_t at2, int64_t at3, float* partial)
+{
+#pragma unroll 1
+    for (int x = from; x < to; ++x) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+        if (some) {
+            QLI_TMEM_LD_X32(acc + 32 * x, o);
+            wait_loaded(o);
+        }
+        if (both) {
+            uint32_t o2[32];
+            QLI_TMEM_LD_X32(acc + D + 32 * x, o2);
+            wait_loaded(o2);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(g0, __uint_as_float(o[e]), g1 * __uint_as_float(o2[e])));
+        }
+        // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
+        auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
+        if (partial) {
+            float4* to4 = reinterpret_cast<float4*>(partial + 32 * x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to4[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
+            __syncwarp();
+            continue;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = inv == 0.0f ? 0u : float2_to_act2<F16>(el(2 * e) * inv, el(2 * e + 1) * inv);
+        transpose_pieces(w);
+        const int64_t at[4] = {at0, at1, at2, at3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at[i] >= 0)
+                *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
 }
 
 // The block number `slot`, found by a warp (as find_rows); false: the prefix sums are invalid
@@ -246,28 +352,6 @@ __device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot
     }
     rows_of_block(a, b, block, M, group, lane == 0, r);
     return true;
-}
-
-// Four rows' worth of 64 bytes: lane k of each four holds four 16-byte pieces of row k and gets piece k of the four rows
-__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16])
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int bit = 1; bit <= 2; bit <<= 1) {
-        const bool odd = lane & bit;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & bit) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // piece i of the odd lane against piece i + bit of the even one
-                const uint32_t out = odd ? w[4 * i + e] : w[4 * (i + bit) + e];
-                const uint32_t in = __shfl_xor_sync(0xffffffffu, out, bit);
-                if (odd) w[4 * i + e] = in;
-                else w[4 * (i + bit) + e] = in;
-            }
-        }
-    }
 }
 
 template <bool F16, bool E2M1, int D>
@@ -383,21 +467,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t p[32];
-                        while (true) {
-                            float best = -INFINITY, sum;
-                            if (whole) {
-                                soft_half<false>(cols + 64 * h, f, m_run, nullptr, p, best, sum);
-                            } else {
-                                uint32_t bits[2];
+                        if (!whole) {
+                            uint32_t bits[2];
 #pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    const int x = 4 * h + 2 * c;
-                                    bits[c] = chunk_bits(a, task.range, ch + x, hi) | chunk_bits(a, task.range, ch + x + 1, hi) << 16;
-                                    if (!(valid >> x & 1)) bits[c] &= 0xFFFF0000u;
-                                    if (!(valid >> (x + 1) & 1)) bits[c] &= 0x0000FFFFu;
-                                }
-                                soft_half<true>(cols + 64 * h, f, m_run, bits, p, best, sum);
+                            for (int c = 0; c < 2; ++c) {
+                                const int x = 4 * h + 2 * c;
+                                bits[c] = chunk_bits(a, task.range, ch + x, hi) | chunk_bits(a, task.range, ch + x + 1, hi) << 16;
+                                if (!(valid >> x & 1)) bits[c] &= 0xFFFF0000u;
+                                if (!(valid >> (x + 1) & 1)) bits[c] &= 0x0000FFFFu;
                             }
+                            mask_half(cols + 64 * h, bits[0], bits[1]);
+                        }
+                        while (true) {
+                            float best, sum;
+                            soft_half(cols + 64 * h, f, m_run, p, best, sum);
                             const float up = best * f;
                             const bool over = fmaf(best, f, -m_run) > kRescale && up > m_run;
                             if (!__any_sync(0xffffffffu, over)) {
@@ -409,28 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float g = over ? ptx::ex2(m_run - up) : 1.0f;
                             if (over) m_run = up;
                             l_run *= g;
-                            if (h == 1) {
-                                uint32_t o[32];
-                                ptx::tmem_wait_st();
-                                QLI_TMEM_LD_X32(cols, o);
-                                wait_loaded(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float2 v = act2_to_float2<true>(o[e]);
-                                    o[e] = float2_to_act2<true>(v.x * g, v.y * g);
-                                }
-                                QLI_TMEM_ST_X32(cols, o);
-                            }
-                            if (j == 0) continue;
-#pragma unroll 1
-                            for (int x = 0; x < D / 32; ++x) {
-                                uint32_t o[32];
-                                QLI_TMEM_LD_X32(out + D * q + 32 * x, o);
-                                wait_loaded(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-                                QLI_TMEM_ST_X32(out + D * q + 32 * x, o);
-                            }
+                            if (h == 1) scale_half(cols, g);
+                            if (j > 0) scale_row(out + D * q, D / 32, g);
                         }
                         // in the place of the logits that are through
                         QLI_TMEM_ST_X32(cols + 32 * h, p);
@@ -468,46 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) at[i] = (row & ~3) + i < task.blk.rows ? head_of(heads, (row & ~3) + i) * D + 8 * (lane & 3) : -1;
             const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-            if (writes) {
-#pragma unroll 1
-                for (int x = from; x < to; ++x) {
-                    uint32_t o[32];
-                    if (task.n > 0) {
-                        QLI_TMEM_LD_X32(acc + 32 * x, o);
-                        wait_loaded(o);
-                        if (both) {
-                            uint32_t o2[32];
-                            QLI_TMEM_LD_X32(acc + D + 32 * x, o2);
-                            wait_loaded(o2);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(fmaf(g[0], __uint_as_float(o[e]), g[1] * __uint_as_float(o2[e])));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0;
-                    }
-                    // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
-                    auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
-                    if (L.splits > 1) {
-                        float4* to4 = reinterpret_cast<float4*>(part_o + row * kStride + 32 * x);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) to4[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
-                        __syncwarp();
-                        continue;
-                    }
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = sum == 0.0f ? 0u : float2_to_act2<F16>(el(2 * e) * inv, el(2 * e + 1) * inv);
-                    // 64 bytes of a row by four lanes
-                    transpose_pieces(w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (at[i] >= 0)
-                            *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    }
-                }
-            }
+            if (writes)
+                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0], g[1], sum == 0.0f ? 0.0f : inv, dst, at[0], at[1], at[2], at[3],
+                                         L.splits > 1 ? part_o + row * kStride : nullptr);
             if (task.n > 0) {
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -533,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // times a power of two of its largest magnitude)
         auto queries = [&]() {
             if (turn > 0 && !wait_bounded(&sh.qfree, turn - 1 & 1, &sh.abort, a.err)) return false;
-            constexpr int kPerWarp = 16;
+            constexpr int kPerWarp = 32;
             // a lane's four (D = 64: two) elements; for int4 those of each eight in the order 0 4 1 5 2 6 3 7, as its
             // codes come
             const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
@@ -753,6 +779,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 k.n = max(0, (all - rank + L.splits - 1) / L.splits);
             }
             if (k.n < 0 || k.blk.rows > 0) {
+                if (k.n > 0 && it > 0) {
+                    // the queries on their way to L2
+                    const Heads heads = heads_of(k);
+                    const int64_t first = k.blk.first / group;
+                    for (int i = lane; i < k.blk.rows; i += 32) {
+                        const uint32_t tok = (heads.rest + i) * recip >> 16;
+                        const uint16_t* src = static_cast<const uint16_t*>(a.query) + (k.blk.row0 + first + tok) * a.q_stride +
+                                              (k.kvh * group + (int)(heads.rest + i - tok * group)) * D;
+#pragma unroll
+                        for (int x = 0; x < D; x += 64) ptx::prefetch_l2(src + x);
+                    }
+                }
                 ok = wait_bounded(&sh.taskfree[it & 1], (it >> 1 & 1) ^ 1, &sh.abort, a.err, kTaskLimitNs);
                 if (!ok) break;
                 if (lane == 0) {

@@ -240,6 +240,9 @@ __device__ __forceinline__ void prefetch_tensormap(const void* tmap)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
+// Ask for the line of `p` to come to L2
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Four rows y0 ... y3 of a 2-D tensor (a box one row high), from element x on, into consecutive rows of
 // shared memory (128-byte aligned); x * element size must be a multiple of 16 bytes
 __device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int32_t x, int32_t y0, int32_t y1, int32_t y2,
