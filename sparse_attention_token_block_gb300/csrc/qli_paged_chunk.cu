@@ -45,7 +45,7 @@ constexpr int kThreads = 32 * 15;
 constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
-constexpr float kRescale = 8.0f;
+constexpr float kMostSum = 32768.0f;                   // of 64 probabilities, which then fit fp16
 constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 20000000000ull;      // (the length of a task: 2^31 positions)
 
 struct Layout {
@@ -181,15 +181,14 @@ __device__ __forceinline__ void store_row(uint8_t* operand, int row, const uint3
     }
 }
 
-// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, their sum and the largest logit
-__device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, uint32_t (&p)[32], float& best, float& sum)
+// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, and their sum
+__device__ __forceinline__ float soft_half(uint32_t cols, float f, float m, uint32_t (&p)[32])
 {
     uint32_t s[2][32];
     QLI_TMEM_LD_X32(cols, s[0]);
     QLI_TMEM_LD_X32(cols + 32, s[1]);
     wait_loaded(s[0]);
     wait_loaded(s[1]);
-    float top[2] = {-INFINITY, -INFINITY};
     uint64_t part[2] = {0, 0};
     const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m, -m);
 #pragma unroll
@@ -197,7 +196,6 @@ __device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, uint3
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
-            top[e >> 1 & 1] = ptx::max3(top[e >> 1 & 1], x, y);
             float zx, zy;
             ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
             const float px = ptx::ex2(zx), py = ptx::ex2(zy);
@@ -205,13 +203,26 @@ __device__ __forceinline__ void soft_half(uint32_t cols, float f, float m, uint3
             p[16 * c + e / 2] = float2_to_act2<true>(px, py);
         }
     }
-    float other;
+    float sum, other;
     ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
-    sum += other;
-    best = fmaxf(top[0], top[1]);
+    return sum + other;
 }
 
 // The rarer steps are calls, so that they take no registers from the ones above.
+
+// The largest of a row's 64 logits (NaN: of the others)
+__device__ __noinline__ float max_half(uint32_t cols)
+{
+    uint32_t s[2][32];
+    QLI_TMEM_LD_X32(cols, s[0]);
+    QLI_TMEM_LD_X32(cols + 32, s[1]);
+    wait_loaded(s[0]);
+    wait_loaded(s[1]);
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top = ptx::max3(top, __uint_as_float(s[0][e]), __uint_as_float(s[1][e]));
+    return top;
+}
 
 // -infinity for those of a row's 64 logits whose bit is not set
 __device__ __noinline__ void mask_half(uint32_t cols, uint32_t bits0, uint32_t bits1)
@@ -479,16 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mask_half(cols + 64 * h, bits[0], bits[1]);
                         }
                         while (true) {
-                            float best, sum;
-                            soft_half(cols + 64 * h, f, m_run, p, best, sum);
-                            const float up = best * f;
-                            const bool over = fmaf(best, f, -m_run) > kRescale && up > m_run;
-                            if (!__any_sync(0xffffffffu, over)) {
+                            const float sum = soft_half(cols + 64 * h, f, m_run, p);
+                            if (!__any_sync(0xffffffffu, sum > kMostSum)) {
                                 l_run += sum;
                                 break;
                             }
                             // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's
                             // first half of P.  (The stream's last product was issued before these logits, and has ended.)
+                            const float up = max_half(cols + 64 * h) * f;
+                            const bool over = sum > kMostSum && up > m_run;
+                            if (!__any_sync(0xffffffffu, over)) {
+                                l_run += sum;
+                                break;
+                            }
                             const float g = over ? ptx::ex2(m_run - up) : 1.0f;
                             if (over) m_run = up;
                             l_run *= g;
