@@ -186,13 +186,13 @@ __device__ __forceinline__ float soft_half(uint32_t cols, float f, float m, uint
 {
     uint32_t s[2][32];
     QLI_TMEM_LD_X32(cols, s[0]);
-    QLI_TMEM_LD_X32(cols + 32, s[1]);
     wait_loaded(s[0]);
-    wait_loaded(s[1]);
+    QLI_TMEM_LD_X32(cols + 32, s[1]);
     uint64_t part[2] = {0, 0};
     const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m, -m);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+        if (c == 1) wait_loaded(s[1]);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
@@ -436,12 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return h;
     };
     auto head_of = [&](const Heads& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 16) * (a.heads_q - group); };
-    // the next task; false when a wait gave up.  A role that keeps nothing of the entry hands it back at once.
-    auto next_task = [&](int it, Task& k, bool keep) {
+    // the next task; false when a wait gave up.  (The softmax warps read theirs in place and hand it back at its end.)
+    auto next_task = [&](int it, Task& k) {
         if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err)) return false;
         k = sh.task[it & 1];
         __syncwarp();
-        if (!keep && lane == 0) ptx::mbar_arrive(&sh.taskfree[it & 1]);
+        if (lane == 0) ptx::mbar_arrive(&sh.taskfree[it & 1]);
         return true;
     };
     uint16_t* const dst = static_cast<uint16_t*>(a.out);
@@ -458,7 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t step = 0, tiles = 0, turn = 0;            // steps, tiles and tasks with tiles so far
         uint32_t joins = 0;
         for (int it = 0;; ++it) {
-            if (!next_task(it, task, true) || task.n < 0) break;
+            const Task& task = sh.task[it & 1];
+            if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err) || task.n < 0) break;
+
             const bool shared = shares(task);
             const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
             float m_run = -FLT_MAX, l_run = 0.0f;
@@ -517,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&sh.pfull[q]);
                 }
-                if (!ok || !wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
-                ptx::tc_fence_after();
+                if (!ok) break;
             }
             // ---- the rows' outputs.  Shared rows: each stream's warps join half of the elements of both accumulators.
+            // (What there is to know before the last products end.)
             float g[2] = {1.0f, 0.0f};
             float top = m_run, sum = l_run;
             const bool both = shared && steps_of(task, 1) > 0;
@@ -545,18 +547,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) at[i] = (row & ~3) + i < task.blk.rows ? head_of(heads, (row & ~3) + i) * D + 8 * (lane & 3) : -1;
             const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            if (L.splits == 1 && writes && from == 0 && row < task.blk.rows && a.lse)
+                a.lse[head_of(heads, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            if (task.n > 0) {
+                if (!wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
+                ptx::tc_fence_after();
+            }
+            // (the operands' place is free now)
+            if (L.splits > 1 && writes && from == 0) part_ml[row] = make_float2(top, sum);
             if (writes)
-                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0], g[1], sum == 0.0f ? 0.0f : inv, dst, at[0], at[1], at[2], at[3],
+                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0], g[1], inv, dst, at[0], at[1], at[2], at[3],
                                          L.splits > 1 ? part_o + row * kStride : nullptr);
             if (task.n > 0) {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sh.oread);
-            }
-            if (L.splits > 1) {
-                if (writes && from == 0) part_ml[row] = make_float2(top, sum);
-            } else if (writes && from == 0 && row < task.blk.rows && a.lse) {
-                a.lse[head_of(heads, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             }
             tiles += task.n;
             turn += task.n > 0;
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         for (int it = 0;; ++it) {
-            if (!next_task(it, task, false) || task.n < 0) break;
+            if (!next_task(it, task) || task.n < 0) break;
             if (task.n == 0) continue;
             const int lo = task.kvh * kv_unit_bytes(D) & 8;                    // (heads of 72 bytes)
             bool ok = turn > 0 || queries();
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int rs = 0;
         uint32_t rp = 1, tiles = 0;
         for (int it = 0;; ++it) {
-            if (!next_task(it, task, false) || task.n < 0) break;
+            if (!next_task(it, task) || task.n < 0) break;
             const int32_t* table = a.block_table + (int64_t)task.blk.batch * a.p.max_blocks_per_seq;
             const int x = (task.kvh * kv_unit_bytes(D) & ~15) / 8;
             int at = 0, page = INT32_MIN;
@@ -715,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = ptx::sdesc_mnmajor_sw128(ptx::smem_addr(ring), Z::atom);
         uint32_t tiles = 0, turn = 0, step0 = 0, step1 = 0;
         for (int it = 0;; ++it) {
-            if (!next_task(it, task, false) || task.n < 0) break;
+            if (!next_task(it, task) || task.n < 0) break;
             if (task.n == 0) continue;
             const bool shared = shares(task);
             const int s0 = steps_of(task, 0), s1 = steps_of(task, 1);
