@@ -192,7 +192,8 @@ inline int64_t most_rows(const PagedArgs& a)
     return (tokens > 1 ? tokens : 1) * (a.heads_q / a.heads_kv);
 }
 
-// For many such rows (qli_paged_chunk.cu)
+// For many such rows (qli_paged_chunk.cu), and whether a call goes there
+bool paged_in_chunks(const PagedArgs& a);
 cudaError_t launch_paged_chunk(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int64_t most_rows, int sms, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st);
 

@@ -36,9 +36,10 @@ namespace {
 constexpr int kWarps = 8;                         // with a unit each, and one that copies
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStep = 2 * kChunk;                 // positions
-constexpr int kMaxSplits = 8;                     // a portable cluster
-constexpr int kMaxStages = 4;
+constexpr int kMaxSplits = 16;                    // the largest cluster
+constexpr int kMaxStages = 6;
 constexpr int kHalfSmem = 112 * 1024;             // dynamic, of one of two CTAs on an SM
+constexpr int kMostSmem = 220 * 1024;
 constexpr uint64_t kWaitLimitNs = 200000000ull;
 constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
 
@@ -77,11 +78,6 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return wait_slow(bar, parity, abort, err);
 }
-
-// Position (of a group of eight) that row r of an 8-row fragment holds.  With a stride of 32 or 96 modulo 128
-// bytes between positions, the two that a quarter-warp reads of K and the four that it reads of V then lie in
-// different banks.
-__device__ __forceinline__ int entry_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N])
@@ -143,55 +139,52 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     const bool works = wid < kWarps && unit < nu;
     float o[NT][MO][4], m[NT][2], l[NT][2];
     if (wid == kWarps) {
-        // ---------------------------------------------------------------- copies: a lane per part
-        if (lane < L.parts) {
-            const int n = steps_of(lane), lo = u0 * kUnit & ~15;
-            const bool stall = a.p.test_stall == 1;            // test switch: nothing arrives, the waits run out
-            const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
-            const uint32_t bytes = kChunk * L.row_bytes;
-            uint8_t* ring = smem + lane * L.stages * 2 * bytes;
-            // pages and positions in them of a step's two chunks
-            int page[2], at[2];
-            auto resolve = [&](int i) {
-                const int ch = 2 * ((i * L.splits + rank) * L.parts + lane);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) page[x] = chunk_page(a, range, table, L.block_recip, ch + x, &at[x]);
-            };
-            if (n > 0) resolve(0);
-            int stage = 0, parity = 1;
-            bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
-                uint32_t mask = 0;
-                int pg[2], ps[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    pg[x] = page[x], ps[x] = at[x];
-                    if (pg[x] >= 0 && pg[x] < a.p.num_blocks) mask |= 1u << x;
-                    else if (pg[x] != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
+        // ---------------------------------------------------------------- copies: a lane per part and chunk of its steps
+        const int p = min(lane >> 1, L.parts - 1), x = lane & 1, n = lane < 2 * L.parts ? steps_of(p) : 0, lo = u0 * kUnit & ~15;
+        const bool stall = a.p.test_stall == 1;                // test switch: nothing arrives, the waits run out
+        const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
+        const uint32_t bytes = kChunk * L.row_bytes;
+        uint8_t* const ring = smem + p * L.stages * 2 * bytes + x * bytes;
+        // pages, and positions in them, of the next step's chunk and of the one after it
+        int page[2], at[2];
+        auto resolve = [&](int i, int& pg, int& ps) {
+            pg = INT32_MIN;
+            if (i < n) pg = chunk_page(a, range, table, L.block_recip, 2 * ((i * L.splits + rank) * L.parts + p) + x, &ps);
+        };
+        resolve(0, page[0], at[0]);
+        resolve(1, page[1], at[1]);
+        int i = 0, stage = 0;
+        uint32_t parity = 1;
+        uint64_t since = ptx::globaltimer();
+        while (__any_sync(0xffffffffu, i < n)) {
+            // those parts whose next stage is free go on
+            const bool ready = i < n && ptx::mbar_test_wait(&freed[p][stage], parity);
+            if (!__any_sync(0xffffffffu, ready)) {
+                if (__any_sync(0xffffffffu, *(volatile uint32_t*)&abort != 0)) break;
+                if (__any_sync(0xffffffffu, ptx::globaltimer() - since > kWaitLimitNs)) {
+                    abort = 1;
+                    if (a.err) atomicOr(a.err, kErrTimeout);
+                    break;
                 }
-                if (i + 1 < n) resolve(i + 1);
-                if (!ptx::mbar_try_wait(&freed[lane][stage], parity)) {
-                    const uint64_t t0 = ptx::globaltimer();
-                    while (ok && !ptx::mbar_try_wait_sleep(&freed[lane][stage], parity, 100000u)) {
-                        if (*(volatile uint32_t*)&abort) ok = false;
-                        else if (ptx::globaltimer() - t0 > kWaitLimitNs) {
-                            abort = 1;
-                            if (a.err) atomicOr(a.err, kErrTimeout);
-                            ok = false;
-                        }
-                    }
-                    if (!ok) break;
-                }
-                live[lane][stage] = mask;
-                ptx::mbar_arrive_expect_tx(&full[lane][stage], stall ? bytes : __popc(mask) * bytes);
-                if (!stall) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if (mask >> x & 1)
-                            ptx::tma_load_3d(ring + (2 * stage + x) * bytes, &pages, lo / 8, ps[x], pg[x], &full[lane][stage]);
-                }
-                if (++stage == L.stages) stage = 0, parity ^= 1;
+                __nanosleep(50);
+                continue;
             }
+            const bool here = ready && page[0] >= 0 && page[0] < a.p.num_blocks;
+            if (ready && !here && page[0] != INT32_MIN && a.err) atomicOr(a.err, kErrPage);
+            const uint32_t mask = __ballot_sync(0xffffffffu, here) >> (lane & ~1) & 3;
+            if (ready && x == 0) {
+                live[p][stage] = mask;
+                ptx::mbar_arrive_expect_tx(&full[p][stage], stall ? bytes : __popc(mask) * bytes);
+            }
+            __syncwarp();
+            if (here && !stall) ptx::tma_load_3d(ring + 2 * stage * bytes, &pages, lo / 8, at[0], page[0], &full[p][stage]);
+            if (ready) {
+                if (++stage == L.stages) stage = 0, parity ^= 1;
+                ++i;
+                page[0] = page[1], at[0] = at[1];
+                resolve(i + 1, page[1], at[1]);
+            }
+            since = ptx::globaltimer();
         }
         __syncwarp();
     } else if (works) {
@@ -263,13 +256,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             l[t][0] = l[t][1] = 0.0f;
         }
         const int steps = steps_of(part), step_bytes = kStep * L.row_bytes, row = L.row_bytes;
-        const int tk = entry_of_row(r), ta = c, tb = 4 + ((c + 2) & 3);
+        // rows r of a fragment are positions r of each eight, columns 2c and 2c + 1 of the values' too
         const uint8_t* head = smem + part * L.stages * step_bytes + kvh * kUnit - (u0 * kUnit & ~15);
-        const uint8_t* kc0 = head + tk * row + (D / 8) * c;                        // the lane's key codes and scales,
-        const uint8_t* ks0 = head + tk * row + D + (D == 128 ? 2 * c : c);
-        const uint8_t* vc0 = head + ta * row + D / 2 + (D / 16) * r;               // value codes and scales
-        const uint8_t* vs0 = head + ta * row + D + D / 16 + (D == 128 ? r : r >> 1);
-        const int vb = (tb - ta) * row;
+        const uint8_t* kc0 = head + r * row + (D / 8) * c;                         // the lane's key codes and scales,
+        const uint8_t* ks0 = head + r * row + D + (D == 128 ? 2 * c : c);
+        const uint8_t* vc0 = head + 2 * c * row + D / 2 + (D / 16) * r;               // value codes and scales
+        const uint8_t* vs0 = head + 2 * c * row + D + D / 16 + (D == 128 ? r : r >> 1);
         int stage = 0, parity = 0;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
@@ -337,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = pos + 8 * (e >> 1) + tk;
+                            const int j = pos + 8 * (e >> 1) + r;
                             if (j >= limit || !sees(a, hi[t][e & 1], j)) z[u][t][e] = -INFINITY;
                         }
                 }
@@ -394,13 +386,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint8_t* x0 = vs + 16 * u * row;
-                const PairScale sab = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[vb] << 8)));
-                const PairScale scd = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[8 * row] | (uint32_t)x0[vb + 8 * row] << 8)));
+                const PairScale sab = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[0] | (uint32_t)x0[row] << 8)));
+                const PairScale scd = pair_scale<E2M1>(finite_f16x2(e4m3x2_to_f16x2(x0[8 * row] | (uint32_t)x0[9 * row] << 8)));
                 uint32_t wa[NW / 2], wb[NW / 2], wc[NW / 2], wd[NW / 2];
                 load_words<NW / 2>(va + 16 * u * row, wa);
-                load_words<NW / 2>(va + 16 * u * row + vb, wb);
+                load_words<NW / 2>(va + (16 * u + 1) * row, wb);
                 load_words<NW / 2>(va + (16 * u + 8) * row, wc);
-                load_words<NW / 2>(va + (16 * u + 8) * row + vb, wd);
+                load_words<NW / 2>(va + (16 * u + 9) * row, wd);
 #pragma unroll
                 for (int j = 0; j < NW / 2; ++j) {
                     uint32_t x[8], y[8];
@@ -574,14 +566,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     ptx::cluster_sync();                           // no CTA leaves while another reads its partial results
 }
 
-// Row stride in a ring of `heads` KV heads' bytes: 32 or 96 beyond a multiple of 128, with room for a start that
-// is no multiple of 16
+// Row stride in a ring of `heads` KV heads' bytes, with room for a start that is no multiple of 16: an odd multiple of 16,
+// so that the four positions that a half-warp reads of V lie in different banks (of K two share them; strides for both
+// would take a quarter of the ring)
 int ring_row(int heads, int unit)
 {
-    const int need = (heads * unit + 15 & ~15) + (heads * unit % 16 ? 16 : 0);
-    int row = need;
-    while (row % 128 != 32 && row % 128 != 96) row += 16;
-    return row;
+    return ((heads * unit + 15 & ~15) + (heads * unit % 16 ? 16 : 0)) | 16;
 }
 
 template <bool F16, bool E2M1, int D, int NT>
@@ -592,19 +582,31 @@ cudaError_t launch_shape(const PagedArgs& a, int sms, cudaStream_t st)
     Layout L;
     L.block_recip = (uint32_t)((UINT64_C(1) << 32) / (uint32_t)a.p.block_size);
     const int64_t slots = row_slots(a, M, group, &L.blocks);
-    const int64_t most = most_positions(a, M, group);        // of a row block
+    const int64_t steps = ceil_div64(most_positions(a, M, group), kStep);         // of a row block
+    // row blocks that hold rows (TND: most of the numbers past these have none)
+    const int64_t full = a.p.layout_tnd ? std::min<int64_t>(slots, a.p.batch * ceil_div64(most_rows(a), M) + 1) : slots;
     const int room = ctas_per_sm(D, NT) * sms;
     L.per_cta = 1;
-    while (L.per_cta < kWarps && slots * ceil_div64(a.heads_kv, L.per_cta) > room) L.per_cta *= 2;
+    while (L.per_cta < kWarps && full * ceil_div64(a.heads_kv, L.per_cta) > room) L.per_cta *= 2;
     L.per_cta = std::min<int>(L.per_cta, a.heads_kv);
     L.slices = (int)ceil_div64(a.heads_kv, L.per_cta);
     L.per_cta = (int)ceil_div64(a.heads_kv, L.slices);
     L.parts = kWarps / L.per_cta;
+    // a cluster shares the steps while its CTAs fit the GPU together, and further (so that sequences of different lengths
+    // balance) while a warp keeps 16 steps.  us, 64 / 8 heads, splits 1 / 2 / 4 / 8: 32 sequences of 8k-32k 210 / 183 / 175 /
+    // 195, 32 windows of 4096 41 / 49 / 58 / 86, 64 of 1k-4k 63 / 68 / 90 / 144, 8 of 8k-32k 151 / 81 / 66 / 66.
     L.splits = 1;
-    while (L.splits < kMaxSplits && slots * L.slices * L.splits * 2 <= room && most >= kStep * L.parts * L.splits * 2) L.splits *= 2;
+    while (L.splits < kMaxSplits) {
+        const int64_t ctas = full * L.slices * L.splits * 2, each = steps / (L.parts * L.splits * 2);
+        if (!(ctas <= room && L.splits < 8 ? each >= 1 : each >= 16 && ctas <= 4 * room)) break;
+        L.splits *= 2;
+    }
     L.row_bytes = ring_row(L.per_cta, kv_unit_bytes(D));
     const int step = L.parts * kStep * L.row_bytes;
-    L.stages = std::max(2, std::min(kMaxStages, kHalfSmem * (ctas_per_sm(D, NT) == 1 ? 2 : 1) / step));
+    // (a CTA that has its SM to itself takes all of it; clusters do not: fewer of them would fit the GPU at a time, 16 CTAs
+    // of one 131072-position sequence's 8 heads 101 us instead of 71)
+    const bool alone = ctas_per_sm(D, NT) == 1 || (L.splits == 1 && full * L.slices <= sms);
+    L.stages = std::max(2, std::min(kMaxStages, (alone ? kMostSmem : kHalfSmem) / step));
     const int join = L.parts * L.splits > 1 ? kWarps * M * ((D + 4) + 2 + 2) * 4 : 0;       // partial outputs, pairs twice
     const int smem = std::max(L.stages * step, join);
     const int64_t grid = slots * L.slices * L.splits;
@@ -614,14 +616,14 @@ cudaError_t launch_shape(const PagedArgs& a, int sms, cudaStream_t st)
     if (a.p.batch > 0 && !encode_page_map(&pages, a.kv, a.entry_bytes, a.p.block_size, a.page_bytes, a.p.num_blocks, L.row_bytes, 16))
         return cudaErrorUnknown;
     auto kernel = paged_attention_kernel<F16, E2M1, D, NT>;
-    constexpr int kMaxSmem = ctas_per_sm(D, NT) == 1 ? 220 * 1024 : kHalfSmem;
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? UINT64_C(1) << dev : 0;
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -658,9 +660,23 @@ cudaError_t launch_type(const PagedArgs& a, int head_dim, int sms, cudaStream_t 
 
 }  // namespace
 
+// The tensor cores' rows cost what 24 of this kernel's do, and their kernel about 6 us more.  us for this kernel and for
+// that one, 8 KV heads of 128: 32 sequences of 16384 positions, 16 rows each 191 and 277, 32 rows 370 and 278; 4 sequences of
+// 16384, 16 rows 33 and 47, 32 rows 56 and 48; 24 of 512, 32 rows 21 and 27, 64 rows 29 and 27; 4 of 512, 128 rows 14 and 18;
+// 4 heads of 64, 16 sequences of 12000, 28 rows 45 and 49, 56 rows 76 and 49.
+bool paged_in_chunks(const PagedArgs& a)
+{
+    if (most_rows(a) <= 16) return false;
+    const int group = a.heads_q / a.heads_kv;
+    int32_t blocks;
+    const int64_t few = row_slots(a, 16, group, &blocks) * most_positions(a, 16, group);
+    const int64_t many = row_slots(a, 128, group, &blocks) * most_positions(a, 128, group);
+    return a.heads_kv * (2 * few - 3 * many) > 2 * 140000;
+}
+
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
 {
-    if (most_rows(a) > 16) return launch_paged_chunk(a, head_dim, f16, e2m1, most_rows(a), sms, st);
+    if (paged_in_chunks(a)) return launch_paged_chunk(a, head_dim, f16, e2m1, most_rows(a), sms, st);
     if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
     return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
 }

@@ -463,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             const bool shared = shares(task);
             const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
+            const bool idle = (row & ~31) >= task.blk.rows;
             float m_run = -FLT_MAX, l_run = 0.0f;
             bool ok = true;
             if (task.n > 0) {
@@ -474,6 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_bounded(&sh.sfull[q], step & 1, &sh.abort, a.err);
                     if (!ok) break;
                     ptx::tc_fence_after();
+                    // (a warp without rows hands its part of P on as it is: it weighs in no row that counts)
+                    if (idle) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&sh.pfull[q]);
+                        continue;
+                    }
                     const uint32_t valid = sh.valid[(tiles + t) & 7];
                     const bool whole = valid == 0xFFu && task.range.all_see(ch, kTileChunks);
                     // half a tile at a time
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (the operands' place is free now)
             if (L.splits > 1 && writes && from == 0) part_ml[row] = make_float2(top, sum);
-            if (writes)
+            if (writes && !idle)
                 write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0], g[1], inv, dst, at[0], at[1], at[2], at[3],
                                          L.splits > 1 ? part_o + row * kStride : nullptr);
             if (task.n > 0) {
