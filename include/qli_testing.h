@@ -25,8 +25,8 @@ extern "C" {
  * Either stall ends the launch with QLI_ERR_DEVICE_TIMEOUT in the workspace's device error word
  * (qli_get_device_error); the kernel lets its in-flight copies land and releases its tensor
  * memory before it exits, so the CUDA context stays usable.  Other values select 0.
- * Mode 1 also holds for qli_sparse_attention's kernels: no entry is copied or handed on, the waits run
- * out (0.2 s) and the outputs are NaN.
+ * Mode 1 also holds for qli_sparse_attention's and qli_paged_attention's kernels: no entry is copied or
+ * handed on, the waits run out (0.2 s) and the outputs are NaN.
  */
 void qli_testing_set_stall(int mode);
 
@@ -46,6 +46,18 @@ void qli_testing_set_topk_ctas(int ctas);
  * Host code only: the tests assert with it that their calls reach the kernel that they are meant for.
  */
 int qli_testing_attention_rows(const qli_problem* p, const qli_attention* a, int with_seq_lens_k, int sms, int32_t* shape);
+
+/*
+ * Take the qli_paged_attention calls after this one (process-wide, host memory) with the kernel of few
+ * rows (1) or of many (2) whatever their sizes, so that small tests reach both; else the rule decides.
+ */
+void qli_testing_set_paged(int kernel);
+
+/*
+ * Whether the rule sends a qli_paged_attention call of these attributes to the kernel of many rows (1) or
+ * of few (0); -1 for invalid attributes.  Host code only.
+ */
+int qli_testing_paged_chunks(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks);
 
 #ifdef __cplusplus
 }

@@ -86,6 +86,10 @@ def _load():
         L.qli_testing_attention_rows.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(Attention), ctypes.c_int, ctypes.c_int,
                                                  ctypes.POINTER(ctypes.c_int32)]
         L.qli_testing_attention_rows.restype = ctypes.c_int
+        L.qli_testing_set_paged.argtypes = [ctypes.c_int]
+        L.qli_testing_set_paged.restype = None
+        L.qli_testing_paged_chunks.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(Attention), ctypes.c_int32, ctypes.c_int32]
+        L.qli_testing_paged_chunks.restype = ctypes.c_int
     vp, sz, i32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p
     P = ctypes.POINTER(Problem)
     L.qli_problem_init.argtypes = [P]

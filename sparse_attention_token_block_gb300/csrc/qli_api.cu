@@ -33,6 +33,7 @@ namespace {
 #ifdef QLI_TESTING
 std::atomic<int> g_test_stall{0};
 std::atomic<int> g_test_topk_ctas{0};
+std::atomic<int> g_test_paged{0};
 #endif
 
 constexpr int64_t kMaxTokens = INT64_C(1) << 30;      // of one call that takes a token list (grid limit)
@@ -890,6 +891,9 @@ qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int
     A.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : 1.0f / sqrtf((float)a->head_dim);
     A.k_scale = a->k_scale;
     A.v_scale = a->v_scale;
+#ifdef QLI_TESTING
+    A.route = g_test_paged.load();
+#endif
     cudaError_t e = launch_paged_attention(A, a->head_dim, a->dtype == QLI_ACT_F16, a->kv_dtype == QLI_KV_E2M1, sms,
                                            static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QLI_OK : QLI_ERR_CUDA;
@@ -937,6 +941,19 @@ int qli_version(void) { return 100; }
 #ifdef QLI_TESTING
 void qli_testing_set_stall(int mode) { g_test_stall.store(mode == 1 || mode == 2 ? mode : 0); }
 void qli_testing_set_topk_ctas(int ctas) { g_test_topk_ctas.store(ctas > 0 ? ctas : 0); }
+void qli_testing_set_paged(int kernel) { g_test_paged.store(kernel == 1 || kernel == 2 ? kernel : 0); }
+int qli_testing_paged_chunks(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks)
+{
+    if (check(p, nullptr) != QLI_OK || check_attention(a, nullptr) != QLI_OK || window < 0 || sinks < 0) return -1;
+    PagedArgs A;
+    std::memset(&A, 0, sizeof(A));
+    A.p = params_of(p);
+    A.heads_q = a->num_heads_q;
+    A.heads_kv = a->num_heads_kv;
+    A.window = window;
+    A.sinks = sinks;
+    return A.p.rows > 0 && paged_in_chunks(A) ? 1 : 0;
+}
 int qli_testing_attention_rows(const qli_problem* p, const qli_attention* a, int with_seq_lens_k, int sms, int32_t* shape)
 {
     if (check(p, nullptr) != QLI_OK || check_attention(a, nullptr) != QLI_OK || sms < 1) return -1;

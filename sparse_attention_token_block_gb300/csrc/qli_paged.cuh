@@ -21,6 +21,7 @@ struct PagedArgs {
     int32_t entry_bytes;
     int32_t heads_q, heads_kv;
     int32_t window, sinks;                 // window 0: everything up to the row's own position
+    int32_t route;                         // test switch: 1 the kernel of few rows, 2 that of many
     float softmax_scale, k_scale, v_scale;
 };
 

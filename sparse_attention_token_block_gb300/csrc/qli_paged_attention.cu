@@ -676,7 +676,7 @@ bool paged_in_chunks(const PagedArgs& a)
 
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)
 {
-    if (paged_in_chunks(a)) return launch_paged_chunk(a, head_dim, f16, e2m1, most_rows(a), sms, st);
+    if (a.route ? a.route == 2 : paged_in_chunks(a)) return launch_paged_chunk(a, head_dim, f16, e2m1, most_rows(a), sms, st);
     if (f16) return e2m1 ? launch_type<true, true>(a, head_dim, sms, st) : launch_type<true, false>(a, head_dim, sms, st);
     return e2m1 ? launch_type<false, true>(a, head_dim, sms, st) : launch_type<false, false>(a, head_dim, sms, st);
 }

@@ -15,8 +15,8 @@
 //     queries in;
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
-//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when a logit passes it
-//     by more than 2^8, then the row of O is rescaled), sum in fp32, P to fp16.
+//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64
+//     probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16.
 //   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
 //     come first), and the next block's positions and queries are under way while the last one's rows are written.
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto steps_of = [&](const Task& k, int q) { return shares(k) ? (k.n - q + 1) / 2 : k.n; };
     auto tile_of = [&](const Task& k, int q, int j) { return shares(k) ? 2 * j + q : j; };
     // global head row of a task's row i: `base` + i + (tokens before it) (heads_q - group)
-    const uint32_t recip = 65536 / group + 1;              // exact quotients of numbers below 512 by up to 256
+    const uint32_t recip = (1u << 22) / group + 1;         // exact quotients of numbers below 512 by up to 256
     struct Heads {
         int64_t base;
         uint32_t rest;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         h.base = (k.blk.row0 + tok0) * a.heads_q + k.kvh * group + h.rest;
         return h;
     };
-    auto head_of = [&](const Heads& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 16) * (a.heads_q - group); };
+    auto head_of = [&](const Heads& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 22) * (a.heads_q - group); };
     // the next task; false when a wait gave up.  (The softmax warps read theirs in place and hand it back at its end.)
     auto next_task = [&](int it, Task& k) {
         if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err)) return false;
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t w[kPerWarp][2];
 #pragma unroll
                 for (int x = 0; x < kPerWarp; ++x) {
-                    const uint32_t i = rest0 + m0 + x, tok = i * recip >> 16;
+                    const uint32_t i = rest0 + m0 + x, tok = i * recip >> 22;
                     w[x][0] = w[x][1] = 0;
                     if (m0 + x < task.blk.rows) {
                         const uint16_t* src = static_cast<const uint16_t*>(a.query) + (task.blk.row0 + tok0 + tok) * a.q_stride +
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Heads heads = heads_of(k);
                     const int64_t first = k.blk.first / group;
                     for (int i = lane; i < k.blk.rows; i += 32) {
-                        const uint32_t tok = (heads.rest + i) * recip >> 16;
+                        const uint32_t tok = (heads.rest + i) * recip >> 22;
                         const uint16_t* src = static_cast<const uint16_t*>(a.query) + (k.blk.row0 + first + tok) * a.q_stride +
                                               (k.kvh * group + (int)(heads.rest + i - tok * group)) * D;
 #pragma unroll
@@ -955,7 +955,9 @@ cudaError_t launch_shape(const PagedArgs& a, int64_t most_rows, int sms, cudaStr
     const int64_t slots = row_slots(a, L.rows, group, &L.blocks);
     const int64_t tiles = ceil_div64(most_positions(a, L.rows, group), kTile);
     L.splits = 1;
-    while (L.splits < kMaxSplits && slots * a.heads_kv * L.splits * 2 <= sms && tiles >= 4 * L.splits) L.splits *= 2;
+    // (clusters of more than two leave some SMs of each group of 18 to 20 out)
+    while (L.splits < kMaxSplits && slots * a.heads_kv * L.splits * 2 <= (L.splits == 1 ? sms : sms * 5 / 6) && tiles >= 4 * L.splits)
+        L.splits *= 2;
     const int64_t grid = slots * a.heads_kv * L.splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     CUtensorMap pages;
