@@ -552,6 +552,8 @@ def paged_attention(p: Problem, a: Attention, query, seq_lens_q, seq_lens_k, blo
     """qli_paged_attention: ``out`` [rows, num_heads_q, head_dim] (and ``lse`` float32 [rows, num_heads_q]) of
     ``query`` over the positions of the 4-bit cache ``kv`` that each row sees: all up to its own, or the last
     ``window`` of them and the first ``sinks``."""
+    if not (-2 ** 31 <= window < 2 ** 31 and -2 ** 31 <= sinks < 2 ** 31):         # (ctypes would drop the high bits)
+        raise ValueError("window, sinks: expected 32-bit numbers, got %r, %r" % (window, sinks))
     bsnd = p.layout_q == BSND
     n = p.batch * p.max_q_tokens if bsnd else p.total_q_tokens
     shape, dt = (n, a.num_heads_q, a.head_dim), (_act_dtypes or _load_act_dtypes()).get(a.dtype)

@@ -872,6 +872,8 @@ qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int
     if (A.p.batch > 0 && (!seq_lens_k || !block_table || !kv || !aligned(kv, 16))) return QLI_ERR_INVALID_ARG;
     if (A.p.layout_tnd && A.p.batch > 0 && !seq_lens_q) return QLI_ERR_INVALID_ARG;
     if ((int64_t)A.p.rows * a->num_heads_q >= (INT64_C(1) << 28)) return QLI_ERR_UNSUPPORTED;    // grid limit
+    // (a tile's end is an int)
+    if (compressed_keys(p->max_seqlen_k, p->cmp_ratio) > INT32_MAX - 1024) return QLI_ERR_UNSUPPORTED;
     int sms = device_sms(nullptr);
     if (sms < 0) return QLI_ERR_CUDA;
     if (sms == 0) return QLI_ERR_NO_DEVICE;

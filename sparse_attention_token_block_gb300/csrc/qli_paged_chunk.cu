@@ -22,8 +22,8 @@
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
 // through distributed shared memory in a fixed order.
 //
-// Masks, pages outside the pool and NaN scales as in qli_paged_attention.cu.  Every wait is bounded (0.2 s); on
-// expiry the kernel records kErrTimeout, writes NaN and returns.
+// Masks, pages outside the pool and NaN scales as in qli_paged_attention.cu.  Every wait is bounded (0.2 s, those for
+// the end of a whole task 100 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +46,7 @@ constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
 constexpr float kMostSum = 32768.0f;                   // of 64 probabilities, which then fit fp16
-constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 20000000000ull;      // (the length of a task: 2^31 positions)
+constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 100000000000ull;     // (the length of a task: 2^31 positions)
 
 struct Layout {
     int32_t rows;          // of a block: 128 or 256
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t rp = 0, tiles = 0, turn = 0;
         // the task's queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
         // times a power of two of its largest magnitude)
-        auto queries = [&]() {
+        auto queries = [&](const Task& task) {
             if (turn > 0 && !wait_bounded(&sh.qfree, turn - 1 & 1, &sh.abort, a.err)) return false;
             constexpr int kPerWarp = 32;
             // a lane's four (D = 64: two) elements; for int4 those of each eight in the order 0 4 1 5 2 6 3 7, as its
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!next_task(it, task) || task.n < 0) break;
             if (task.n == 0) continue;
             const int lo = task.kvh * kv_unit_bytes(D) & 8;                    // (heads of 72 bytes)
-            bool ok = turn > 0 || queries();
+            bool ok = turn > 0 || queries(task);
             for (int t = 0; ok && t < task.n; ++t, ++tiles) {
                 // the position's bytes into registers: the next tile's may land
                 const uint8_t* src = raw + rs * Z::raw + row * Z::raw_row + lo;
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sv]);
                 // (behind the first tile: the queries of the task before are needed until its last logits are there)
-                if (t == 0 && turn > 0) ok = queries();
+                if (t == 0 && turn > 0) ok = queries(task);
             }
             if (!ok) break;
             ++turn;

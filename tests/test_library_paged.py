@@ -80,6 +80,10 @@ def test_paged_attention_attributes(Q):
     assert _paged(Q, p=_problem(Q, batch=0), query=None, out=None) == 0
     many = _problem(Q, layout_q=Q.TND, total_q_tokens=1 << 25, max_seqlen_k=1)
     assert _paged(Q, p=many, seq_lens_q=X) == 2
+    # positions that tiles would count past 2^31
+    far = dict(block_size=1024, max_blocks_per_seq=1 << 21)
+    assert _paged(Q, p=_problem(Q, max_seqlen_k=(1 << 31) - 1, **far)) == 2
+    assert _paged(Q, p=_problem(Q, max_seqlen_k=(1 << 31) - 1023, **far)) == 2
 
 
 @pytest.mark.parametrize("kw", [
@@ -123,6 +127,14 @@ def test_binding_of_paged_attention(Q):
         ("seq_lens_q", torch.zeros(1, dtype=I32), ValueError), ("seq_lens_k", torch.zeros(1, dtype=I32), ValueError),
         ("seq_lens_k", torch.zeros(2, dtype=torch.int64), TypeError), ("block_table", torch.zeros(2, 3, dtype=I32), ValueError),
         ("kv", good["kv"][:-1], ValueError), ("lse", torch.zeros(4, 16).half(), TypeError), ("lse", torch.zeros(4, 15), ValueError)])
+
+
+@pytest.mark.parametrize("window, sinks", [(1 << 32, 0), ((1 << 31), 4), (16, 1 << 32), (-(1 << 31) - 1, 0)])
+def test_binding_keeps_the_whole_window(Q, window, sinks):
+    q = torch.zeros(4, 16, 128, dtype=BF16)
+    with pytest.raises(ValueError, match="32-bit"):
+        Q.paged_attention(_problem(Q), _attention(Q), q, None, torch.zeros(2, dtype=I32), torch.zeros(2, 4, dtype=I32),
+                          torch.zeros(8 * 64 * 288, dtype=torch.uint8), q.clone(), window=window, sinks=sinks, stream=0)
 
 
 def test_binding_of_append(Q):
