@@ -1,11 +1,13 @@
-"""One decode step of a sparse-attention layer, from the packed projections to the attention's output.
+"""One decode step of an attention layer, from the packed projections to the attention's output.
 
-    python examples/sparse_layer_step.py [--batch 32] [--kv-dtype e2m1|int4] [--check]
+    python examples/sparse_layer_step.py [--batch 32] [--kv-dtype e2m1|int4] [--window N [--sinks N]] [--check]
 
-Per step: norm and rotate the new token's queries and keys, write its key and value into the 4-bit
-cache, quantise the indexer's query and key, select 2048 cached positions per sequence, attend to
-them.  Every call only enqueues, so the step is captured once into a CUDA graph and replayed.
-``--check`` compares the last step with the 64-bit oracle (on the host).
+Per step: norm and rotate the new token's queries and keys, its key and value going straight into the
+4-bit cache (one pass), quantise the indexer's query and key, select 2048 cached positions per sequence,
+attend to them.  With ``--window`` the layer is one without an indexer: its tokens attend to the last N
+cached positions and the first few (``--sinks``), with 0 to all of them.  Every call only enqueues, so the
+step is captured once into a CUDA graph and replayed.  ``--check`` compares the last step with the 64-bit
+oracle (on the host).
 """
 import argparse
 import math
@@ -23,9 +25,11 @@ HQ, HKV, DIM, INDEX_HEADS, BLOCK, TOP = 64, 8, 128, 64, 64, 2048
 
 
 class LayerStep:
-    """Buffers of one layer for `lens` cached tokens per sequence (the new token included)."""
+    """Buffers of one layer for `lens` cached tokens per sequence (the new token included); `window` None: the
+    indexer selects `top` positions."""
 
-    def __init__(self, lens, kv_dtype=Q.KV_E2M1, seed=0, top=TOP):
+    def __init__(self, lens, kv_dtype=Q.KV_E2M1, seed=0, top=TOP, window=None, sinks=0):
+        self.window, self.sinks = window, sinks
         gen = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda")  # noqa: E731
         i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()  # noqa: E731
@@ -64,7 +68,6 @@ class LayerStep:
                     "kv_write")
         # what the step writes
         self.q = torch.empty(b, HQ, DIM, dtype=torch.bfloat16, device="cuda")
-        self.k = torch.empty(b, HKV, DIM, dtype=torch.bfloat16, device="cuda")
         self.index_q8 = torch.empty(b, INDEX_HEADS, DIM, dtype=torch.int8, device="cuda")
         self.index_q_scale = torch.empty(b, INDEX_HEADS, dtype=torch.float16, device="cuda")
         self.out = torch.empty_like(self.q)
@@ -72,10 +75,13 @@ class LayerStep:
 
     def __call__(self):
         p, a, ws = self.p, self.a, self.indexer.workspace
-        Q.check(Q.norm_rope(self.r, self.qkv[:, :HQ], self.qkv[:, HQ:HQ + HKV], self.q_weight, self.k_weight, self.token_pos,
-                            self.cos_sin, self.q, self.k, ws), "norm_rope")
-        Q.check(Q.kv_write(p, a, self.k, self.qkv[:, HQ + HKV:], self.token_batch, self.token_pos, self.table, self.kv_pool,
-                           ws), "kv_write")
+        Q.check(Q.kv_append(p, a, self.r, self.qkv[:, :HQ], self.qkv[:, HQ:HQ + HKV], self.qkv[:, HQ + HKV:], self.q_weight,
+                            self.k_weight, self.token_pos, self.cos_sin, self.token_batch, self.token_pos, self.table, self.q,
+                            self.kv_pool, ws), "kv_append")
+        if self.window is not None:
+            Q.check(Q.paged_attention(p, a, self.q, None, self.seq_lens_k, self.table, self.kv_pool, self.out, self.lse, ws,
+                                      window=self.window, sinks=self.sinks), "paged_attention")
+            return self.out
         Q.check(Q.quantize(Q.INT8, Q.F16, self.index_q, self.index_q8, self.index_q_scale), "quantize")
         Q.check(Q.quantize_keys(p, self.index_k, self.token_batch, self.token_pos, self.table, self.index_pool,
                                 self.index_scale, ws), "quantize_keys")
@@ -95,10 +101,14 @@ class LayerStep:
         from oracle import attention as A
         case = SimpleNamespace(layout_q="BSND", s1=1, batch=len(self.lens), cmp_ratio=1, block_size=BLOCK,
                                num_blocks=self.p.num_blocks, max_blocks_per_seq=self.p.max_blocks_per_seq,
-                               block_table=self.table.cpu().numpy(), seq_lens_k=self.lens)
-        ref, lse, err, _ = A.sparse_attention(case, self.q.float().cpu().numpy(), self.indices.cpu().numpy(),
-                                              self.kv_pool.cpu().numpy(), HKV, self.a.kv_dtype == Q.KV_E2M1,
-                                              1 / math.sqrt(DIM))
+                               block_table=self.table.cpu().numpy(), seq_lens_q=None, seq_lens_k=self.lens, sparse_mode=3,
+                               max_seqlen_k=self.p.max_seqlen_k)
+        q, pool, e2m1 = self.q.float().cpu().numpy(), self.kv_pool.cpu().numpy(), self.a.kv_dtype == Q.KV_E2M1
+        if self.window is None:
+            ref, lse, err, _ = A.sparse_attention(case, q, self.indices.cpu().numpy(), pool, HKV, e2m1, 1 / math.sqrt(DIM))
+        else:
+            ref, lse, err, _ = A.paged_attention(case, q, pool, HKV, e2m1, 1 / math.sqrt(DIM), window=self.window,
+                                                 sinks=self.sinks)
         assert err == 0
         off = np.abs(self.out.double().cpu().numpy() - ref).max() / np.abs(ref).max()
         off_lse = np.abs(self.lse.double().cpu().numpy() - lse).max()
@@ -109,10 +119,12 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--batch", type=int, default=32)
     ap.add_argument("--kv-dtype", default="e2m1", choices=["e2m1", "int4"])
+    ap.add_argument("--window", type=int, default=None, help="no indexer: attend to the last N positions (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="and to the first N")
     ap.add_argument("--check", action="store_true")
     args = ap.parse_args()
     lens = np.random.default_rng(3).integers(8192, 32768, size=args.batch, endpoint=True)
-    step = LayerStep(lens, Q.KV_E2M1 if args.kv_dtype == "e2m1" else Q.KV_INT4)
+    step = LayerStep(lens, Q.KV_E2M1 if args.kv_dtype == "e2m1" else Q.KV_INT4, window=args.window, sinks=args.sinks)
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
     graph = torch.cuda.CUDAGraph()
