@@ -660,10 +660,10 @@ cudaError_t launch_type(const PagedArgs& a, int head_dim, int sms, cudaStream_t 
 
 }  // namespace
 
-// The tensor cores' rows cost what 24 of this kernel's do, and their kernel about 6 us more.  us for this kernel and for
-// that one, 8 KV heads of 128: 32 sequences of 16384 positions, 16 rows each 191 and 277, 32 rows 370 and 278; 4 sequences of
-// 16384, 16 rows 33 and 47, 32 rows 56 and 48; 24 of 512, 32 rows 21 and 27, 64 rows 29 and 27; 4 of 512, 128 rows 14 and 18;
-// 4 heads of 64, 16 sequences of 12000, 28 rows 45 and 49, 56 rows 76 and 49.
+// A block of 128 rows of the tensor cores costs what 19 rows of this kernel do, and their kernel a few us more.  us for this
+// kernel and for that one, 8 KV heads of 128: 32 sequences of 16384 positions, 16 rows each 218 and 246, 24 rows 404 and 247; 4
+// sequences of 16384, 16 rows 33 and 43, 24 rows 63 and 43; 24 of 512, 32 rows 21 and 22, 64 rows 29 and 22; 4 of 512, 64 rows
+// 10 and 14, 128 rows 14 and 16; 4 heads of 64, 16 sequences of 12000, 28 rows 47 and 45, 42 rows 91 and 45.
 bool paged_in_chunks(const PagedArgs& a)
 {
     if (most_rows(a) <= 16) return false;
@@ -671,7 +671,7 @@ bool paged_in_chunks(const PagedArgs& a)
     int32_t blocks;
     const int64_t few = row_slots(a, 16, group, &blocks) * most_positions(a, 16, group);
     const int64_t many = row_slots(a, 128, group, &blocks) * most_positions(a, 128, group);
-    return a.heads_kv * (2 * few - 3 * many) > 2 * 140000;
+    return a.heads_kv * (5 * few - 6 * many) > 900000;
 }
 
 cudaError_t launch_paged_attention(const PagedArgs& a, int head_dim, bool f16, bool e2m1, int sms, cudaStream_t st)

@@ -61,6 +61,9 @@ struct Task {
     KeyRange range;
     int32_t kvh;
     int32_t n;                                         // tiles of this CTA, or one of these
+    int32_t tok0;
+    uint32_t rest;                                     // global head row of row i: `base` + i + (tokens before it) (heads_q - group)
+    int64_t base;
 };
 constexpr int32_t kNoMore = -1, kBadSums = -2;
 
@@ -108,11 +111,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
 
 // Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
 // them moves in front
-__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32])
+template <int N>
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[N])
 {
     ptx::tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Byte offset of 16-byte piece `piece` (eight fp16) of row r in an operand
@@ -181,28 +185,40 @@ __device__ __forceinline__ void store_row(uint8_t* operand, int row, const uint3
     }
 }
 
-// Probabilities 2^(s f - m) of a row's 64 logits from column `cols` on, in fp16 pairs, and their sum
-__device__ __forceinline__ float soft_half(uint32_t cols, float f, float m, uint32_t (&p)[32])
+// The same of V, with the elements of each 32 in an order of their own: pair k of word c (of four) is columns 8 k + 2 c and the
+// next, so that a lane that reads those of k = 0 ... 3 from the accumulators has a word's eight elements
+template <bool E2M1, int D>
+__device__ __forceinline__ void store_values(uint8_t* operand, int row, const uint32_t (&code)[D / 8], const PairScale (&g)[D / 16])
 {
-    uint32_t s[2][32];
-    QLI_TMEM_LD_X32(cols, s[0]);
-    wait_loaded(s[0]);
-    QLI_TMEM_LD_X32(cols + 32, s[1]);
-    uint64_t part[2] = {0, 0};
+    uint8_t* dst = operand + row * 128;
+    const int flip = (row & 7) << 4;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) decode_pairs<E2M1>(code[4 * b + c], g[2 * b + c / 2], o[c]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(dst + (b >> 1) * Sizes<D>::atom + ((((b & 1) * 4 + k) << 4) ^ flip)) =
+                make_uint4(o[0][k], o[1][k], o[2][k], o[3][k]);
+    }
+}
+
+// Probabilities 2^(s f - m) of 32 of a row's logits, in fp16 pairs, and their sum onto `part`
+__device__ __forceinline__ void soft_part(const uint32_t (&s)[32], float f, float m, uint32_t* p, uint64_t (&part)[2])
+{
     const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m, -m);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (c == 1) wait_loaded(s[1]);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
-            float zx, zy;
-            ptx::unpack2(ptx::fma2(ptx::pack2(x, y), F, M), zx, zy);
-            const float px = ptx::ex2(zx), py = ptx::ex2(zy);
-            part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
-            p[16 * c + e / 2] = float2_to_act2<true>(px, py);
-        }
+    for (int e = 0; e < 32; e += 2) {
+        float zx, zy;
+        ptx::unpack2(ptx::fma2(ptx::pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), F, M), zx, zy);
+        const float px = ptx::ex2(zx), py = ptx::ex2(zy);
+        part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
+        p[e / 2] = float2_to_act2<true>(px, py);
     }
+}
+__device__ __forceinline__ float sum_of(const uint64_t (&part)[2])
+{
     float sum, other;
     ptx::unpack2(ptx::add2(part[0], part[1]), sum, other);
     return sum + other;
@@ -222,6 +238,22 @@ __device__ __noinline__ float max_half(uint32_t cols)
 #pragma unroll
     for (int e = 0; e < 32; ++e) top = ptx::max3(top, __uint_as_float(s[0][e]), __uint_as_float(s[1][e]));
     return top;
+}
+
+// The probabilities of a row's 64 logits from column `cols` on into the 32 columns from `to` on, and their sum
+__device__ __noinline__ float soft_half(uint32_t cols, uint32_t to, float f, float m)
+{
+    uint32_t s[2][32], p[32];
+    QLI_TMEM_LD_X32(cols, s[0]);
+    QLI_TMEM_LD_X32(cols + 32, s[1]);
+    wait_loaded(s[0]);
+    wait_loaded(s[1]);
+    uint64_t part[2] = {0, 0};
+    soft_part(s[0], f, m, p, part);
+    soft_part(s[1], f, m, p + 16, part);
+    QLI_TMEM_ST_X32(to, p);
+    ptx::tmem_wait_st();
+    return sum_of(part);
 }
 
 // -infinity for those of a row's 64 logits whose bit is not set
@@ -269,70 +301,78 @@ __device__ __noinline__ void scale_half(uint32_t cols, float g)
     QLI_TMEM_ST_X32(cols, o);
 }
 
-// Four rows' worth of 64 bytes: lane k of each four holds four 16-byte pieces of row k and gets piece k of the four rows
-__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16])
+// A lane's eight elements of a row (of 32 columns, in the order of store_values), times f
+template <bool E2M1>
+__device__ __forceinline__ float element(const uint32_t (&o)[16], int half, int e)
 {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int bit = 1; bit <= 2; bit <<= 1) {
-        const bool odd = lane & bit;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & bit) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // piece i of the odd lane against piece i + bit of the even one
-                const uint32_t out = odd ? w[4 * i + e] : w[4 * (i + bit) + e];
-                const uint32_t in = __shfl_xor_sync(0xffffffffu, out, bit);
-                if (odd) w[4 * i + e] = in;
-                else w[4 * (i + bit) + e] = in;
-            }
-        }
-    }
+    return __uint_as_float(E2M1 ? o[4 * (e >> 1) + 2 * half + (e & 1)] : o[4 * (e & 3) + 2 * half + (e >> 2)]);
 }
 
-// Columns [32 from, 32 to) of a row's accumulators from `acc` on (with `both`, joined with those D further, weighted g0 and
-// g1; without `some`, zeros) into the output, times inv, or as they are into `partial`.  Four neighbouring lanes write 64
-// bytes of each other's rows, which begin at elements at0 ... at3 (-1: none).
+// Columns [32 from, 32 to) of a warp's 32 rows' accumulators from `acc` on, times f0 (with `both`, and those D further times
+// f1; without `some`, zeros): into the output, or as fp32 into `partial`.  A lane has eight elements of rows lane / 4 + 8 i, which
+// begin at elements at0 ... at3 (-1: none); f0 and f1 are those of row `lane`.
 template <bool F16, bool E2M1, int D>
-__device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool both, bool some, float g0, float g1, float inv, uint16_t* dst,
-                                        int64_t at0, int64_t at1, int64_t at2, int64_t at3, float* partial)
+__device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool both, bool some, float f0, float f1, uint16_t* dst, int64_t at0,
+                                        int64_t at1, int64_t at2, int64_t at3, float* partial)
 {
-#pragma unroll 1
-    for (int x = from; x < to; ++x) {
-        uint32_t o[32];
+    constexpr int kStride = D + 4;
+    const int lane = threadIdx.x & 31, r = lane >> 2;
+    const int64_t at[4] = {at0, at1, at2, at3};
+    float a0[4], a1[4];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+    for (int i = 0; i < 4; ++i) {
+        a0[i] = __shfl_sync(0xffffffffu, f0, r + 8 * i);
+        a1[i] = __shfl_sync(0xffffffffu, f1, r + 8 * i);
+    }
+    auto put = [&](int x, int i, const float (&v)[8]) {
+        if (partial) {
+            float4* to4 = reinterpret_cast<float4*>(partial + (r + 8 * i) * kStride + 32 * x + 8 * (lane & 3));
+            to4[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to4[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else if (at[i] >= 0) {
+            *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) =
+                make_uint4(float2_to_act2<F16>(v[0], v[1]), float2_to_act2<F16>(v[2], v[3]), float2_to_act2<F16>(v[4], v[5]),
+                           float2_to_act2<F16>(v[6], v[7]));
+        }
+    };
+    // two blocks of 32 columns, or one of both accumulators
+#pragma unroll 1
+    for (int x = from; x < to; x += both ? 1 : 2) {
+        uint32_t o[2][2][16];
+        const uint32_t second = both ? acc + D + 32 * x : acc + 32 * x + 32;
         if (some) {
-            QLI_TMEM_LD_X32(acc + 32 * x, o);
-            wait_loaded(o);
+            QLI_TMEM_LD_16X256_X4(acc + 32 * x, o[0][0]);
+            QLI_TMEM_LD_16X256_X4(acc + 32 * x + (16u << 16), o[0][1]);
+            QLI_TMEM_LD_16X256_X4(second, o[1][0]);
+            QLI_TMEM_LD_16X256_X4(second + (16u << 16), o[1][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wait_loaded(o[i >> 1][i & 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) o[i >> 5][i >> 4 & 1][i & 15] = 0;
         }
         if (both) {
-            uint32_t o2[32];
-            QLI_TMEM_LD_X32(acc + D + 32 * x, o2);
-            wait_loaded(o2);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(g0, __uint_as_float(o[e]), g1 * __uint_as_float(o2[e])));
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = fmaf(a0[i], element<E2M1>(o[0][i >> 1], i & 1, e), a1[i] * element<E2M1>(o[1][i >> 1], i & 1, e));
+                put(x, i, v);
+            }
+        } else {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = a0[i] * element<E2M1>(o[y][i >> 1], i & 1, e);
+                    put(x + y, i, v);
+                }
         }
-        // (int4: the values' elements come in the order 0 4 1 5 2 6 3 7)
-        auto el = [&](int e) { return __uint_as_float(E2M1 ? o[e] : o[(e & ~7) + ((e & 3) << 1) + (e >> 2 & 1)]); };
-        if (partial) {
-            float4* to4 = reinterpret_cast<float4*>(partial + 32 * x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) to4[e] = make_float4(el(4 * e), el(4 * e + 1), el(4 * e + 2), el(4 * e + 3));
-            __syncwarp();
-            continue;
-        }
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = inv == 0.0f ? 0u : float2_to_act2<F16>(el(2 * e) * inv, el(2 * e + 1) * inv);
-        transpose_pieces(w);
-        const int64_t at[4] = {at0, at1, at2, at3};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (at[i] >= 0)
-                *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
+    __syncwarp();
 }
 
 // The block number `slot`, found by a warp (as find_rows); false: the prefix sums are invalid
@@ -363,6 +403,44 @@ __device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot
     }
     rows_of_block(a, b, block, M, group, lane == 0, r);
     return true;
+}
+
+template <bool F16, bool E2M1, int D>
+__device__ __noinline__ uint32_t turn_row(uint8_t* base, int row)
+{
+    constexpr int kPieces = D / 8;
+    uint32_t ex = 127;
+    uint4 w[kPieces];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) w[p] = *reinterpret_cast<const uint4*>(base + operand_at<D>(row, p));
+    float down = 1.0f;
+    if constexpr (!F16) {
+        uint32_t most = 0;                                 // magnitudes order like integers
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            most = __vmaxu2(most, __vmaxu2(w[p].x & 0x7FFF7FFFu, w[p].y & 0x7FFF7FFFu));
+            most = __vmaxu2(most, __vmaxu2(w[p].z & 0x7FFF7FFFu, w[p].w & 0x7FFF7FFFu));
+        }
+        most = max(most & 0xFFFFu, most >> 16);
+        ex = min(max(most >> 7, 1u), 253u);
+        down = __uint_as_float((254u - ex) << 23);         // 2^-(exponent of the largest)
+    }
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        uint32_t o[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
+        if constexpr (!F16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = act2_to_float2<F16>(o[e]);
+                o[e] = float2_to_act2<true>(v.x * down, v.y * down);
+            }
+        }
+        *reinterpret_cast<uint4*>(base + operand_at<D>(row, p)) =
+            E2M1 ? make_uint4(o[0], o[1], o[2], o[3])
+                 : make_uint4(__byte_perm(o[0], o[2], 0x5410), __byte_perm(o[0], o[2], 0x7632), __byte_perm(o[1], o[3], 0x5410),
+                              __byte_perm(o[1], o[3], 0x7632));
+    }
+    return ex;
 }
 
 template <bool F16, bool E2M1, int D>
@@ -424,18 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tile_of = [&](const Task& k, int q, int j) { return shares(k) ? 2 * j + q : j; };
     // global head row of a task's row i: `base` + i + (tokens before it) (heads_q - group)
     const uint32_t recip = (1u << 22) / group + 1;         // exact quotients of numbers below 512 by up to 256
-    struct Heads {
-        int64_t base;
-        uint32_t rest;
+    auto set_heads = [&](Task& k) {
+        k.tok0 = k.blk.first / group;
+        k.rest = (uint32_t)(k.blk.first - k.tok0 * group);
+        k.base = (k.blk.row0 + k.tok0) * a.heads_q + k.kvh * group + k.rest;
     };
-    auto heads_of = [&](const Task& k) {
-        const int tok0 = k.blk.first / group;
-        Heads h;
-        h.rest = (uint32_t)(k.blk.first - tok0 * group);
-        h.base = (k.blk.row0 + tok0) * a.heads_q + k.kvh * group + h.rest;
-        return h;
-    };
-    auto head_of = [&](const Heads& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 22) * (a.heads_q - group); };
+    auto head_of = [&](const Task& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 22) * (a.heads_q - group); };
     // the next task; false when a wait gave up.  (The softmax warps read theirs in place and hand it back at its end.)
     auto next_task = [&](int it, Task& k) {
         if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err)) return false;
@@ -467,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -FLT_MAX, l_run = 0.0f;
             bool ok = true;
             if (task.n > 0) {
-                const int hi = seen_end(a, task.blk, (task.blk.first + row) / group);
+                const int hi = seen_end(a, task.blk, task.tok0 + (int)((task.rest + row) * recip >> 22));
                 if (!wait_bounded(&sh.qfull, turn & 1, &sh.abort, a.err)) break;
                 const float f = sh.factor[turn & 1][row];
                 for (int j = 0; j < steps; ++j, ++step) {
@@ -483,11 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t valid = sh.valid[(tiles + t) & 7];
                     const bool whole = valid == 0xFFu && task.range.all_see(ch, kTileChunks);
-                    // half a tile at a time
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
-                        if (!whole) {
+                    if (!whole) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
                             uint32_t bits[2];
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
@@ -498,28 +568,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             mask_half(cols + 64 * h, bits[0], bits[1]);
                         }
-                        while (true) {
-                            const float sum = soft_half(cols + 64 * h, f, m_run, p);
-                            if (!__any_sync(0xffffffffu, sum > kMostSum)) {
-                                l_run += sum;
-                                break;
-                            }
-                            // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's
-                            // first half of P.  (The stream's last product was issued before these logits, and has ended.)
+                    }
+                    if (j == 0) m_run = fmaxf(m_run, max_half(cols) * f);          // (of the first logits: as they are)
+                    // half a tile at a time, each 32 logits on their way while those before are worked on
+                    uint32_t s[2][32];
+                    QLI_TMEM_LD_X32(cols, s[0]);
+                    wait_loaded(s[0]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+                        uint64_t part[2] = {0, 0};
+                        QLI_TMEM_LD_X32(cols + 64 * h + 32, s[1]);
+                        soft_part(s[0], f, m_run, p, part);
+                        wait_loaded(s[1]);
+                        if (h == 0) QLI_TMEM_LD_X32(cols + 64, s[0]);
+                        soft_part(s[1], f, m_run, p + 16, part);
+                        if (h == 0) wait_loaded(s[0]);
+                        const float sum = sum_of(part);
+                        if (__any_sync(0xffffffffu, sum > kMostSum)) {
+                            // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's first
+                            // half of P, and begin again.  (The stream's last product was issued before these logits, and has
+                            // ended.  What is in registers does not live through the calls.)
                             const float up = max_half(cols + 64 * h) * f;
                             const bool over = sum > kMostSum && up > m_run;
-                            if (!__any_sync(0xffffffffu, over)) {
-                                l_run += sum;
-                                break;
-                            }
                             const float g = over ? ptx::ex2(m_run - up) : 1.0f;
                             if (over) m_run = up;
-                            l_run *= g;
                             if (h == 1) scale_half(cols, g);
                             if (j > 0) scale_row(out + D * q, D / 32, g);
+                            l_run = l_run * g + soft_half(cols + 64 * h, cols + 32 * h, f, m_run);
+                            QLI_TMEM_LD_X32(cols + 64, s[0]);
+                            wait_loaded(s[0]);
+                        } else {
+                            l_run += sum;
+                            QLI_TMEM_ST_X32(cols + 32 * h, p);     // in the place of the logits that are through
                         }
-                        // in the place of the logits that are through
-                        QLI_TMEM_ST_X32(cols + 32 * h, p);
                     }
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
@@ -549,13 +631,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool writes = !shared || both || q == 0;
             const int from = both ? q * (D / 64) : 0, to = both ? from + D / 64 : D / 32;
             const uint32_t acc = out + (shared ? 0 : D * q);
-            const Heads heads = heads_of(task);
-            int64_t at[4];                                 // of the rows that these four lanes write
+            int64_t at[4];                                 // of the rows that this lane writes
 #pragma unroll
-            for (int i = 0; i < 4; ++i) at[i] = (row & ~3) + i < task.blk.rows ? head_of(heads, (row & ~3) + i) * D + 8 * (lane & 3) : -1;
-            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            for (int i = 0; i < 4; ++i) {
+                const int w = (row & ~31) + (lane >> 2) + 8 * i;
+                at[i] = w < task.blk.rows ? head_of(task, w) * D + 8 * (lane & 3) : -1;
+            }
+            const float inv = L.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : a.v_scale / sum;
             if (L.splits == 1 && writes && from == 0 && row < task.blk.rows && a.lse)
-                a.lse[head_of(heads, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                a.lse[head_of(task, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             if (task.n > 0) {
                 if (!wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
                 ptx::tc_fence_after();
@@ -563,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the operands' place is free now)
             if (L.splits > 1 && writes && from == 0) part_ml[row] = make_float2(top, sum);
             if (writes && !idle)
-                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0], g[1], inv, dst, at[0], at[1], at[2], at[3],
-                                         L.splits > 1 ? part_o + row * kStride : nullptr);
+                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0] * inv, g[1] * inv, dst, at[0], at[1], at[2], at[3],
+                                         L.splits > 1 ? part_o + (row & ~31) * kStride : nullptr);
             if (task.n > 0) {
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -582,57 +666,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         int rs = 0;
         uint32_t rp = 0, tiles = 0, turn = 0;
         // the task's queries as operands: row m is row blk.first + m of the sequence, in fp16 (float16 as it is, bfloat16
-        // times a power of two of its largest magnitude)
+        // times a power of two of its largest magnitude; for int4 each eight elements in the order 0 4 1 5 2 6 3 7, as its
+        // codes come).  They are copied into place, and what there is to change is changed there, a row per thread.
         auto queries = [&](const Task& task) {
             if (turn > 0 && !wait_bounded(&sh.qfree, turn - 1 & 1, &sh.abort, a.err)) return false;
-            constexpr int kPerWarp = 32;
-            // a lane's four (D = 64: two) elements; for int4 those of each eight in the order 0 4 1 5 2 6 3 7, as its
-            // codes come
-            const int el = D == 128 ? 4 * lane : 2 * lane, e8 = el & 7;
-            const int x0 = E2M1 ? el : (el & ~7) + e8 / 2, x1 = E2M1 ? el + 2 : (el & ~7) + e8 / 2 + 1;
-            const int tok0 = task.blk.first / group, rest0 = task.blk.first - tok0 * group;
-            for (int m0 = (warp - kConvWarp) * kPerWarp; m0 < (shares(task) ? kM : 2 * kM); m0 += kConvWarps * kPerWarp) {
-                uint32_t w[kPerWarp][2];
-#pragma unroll
-                for (int x = 0; x < kPerWarp; ++x) {
-                    const uint32_t i = rest0 + m0 + x, tok = i * recip >> 22;
-                    w[x][0] = w[x][1] = 0;
-                    if (m0 + x < task.blk.rows) {
-                        const uint16_t* src = static_cast<const uint16_t*>(a.query) + (task.blk.row0 + tok0 + tok) * a.q_stride +
-                                              (task.kvh * group + (int)(i - tok * group)) * D;
-                        if (!E2M1) {
-                            w[x][0] = src[x0] | (uint32_t)src[x0 + 4] << 16;
-                            if (D == 128) w[x][1] = src[x1] | (uint32_t)src[x1 + 4] << 16;
-                        } else if (D == 128) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(src + x0);
-                            w[x][0] = v.x, w[x][1] = v.y;
-                        } else {
-                            w[x][0] = *reinterpret_cast<const uint32_t*>(src + x0);
-                        }
-                    }
+            constexpr int kPieces = D / 8;
+            const int mine = 32 * (warp - kConvWarp), halves = shares(task) ? 1 : 2;
+            const int64_t first = task.tok0;
+            for (int h = 0; h < halves; ++h)
+#pragma unroll 4
+                for (int x = lane / kPieces; x < 32; x += 32 / kPieces) {
+                    const int m = kM * h + mine + x, piece = lane % kPieces;
+                    const uint32_t i = task.rest + m, tok = i * recip >> 22;
+                    const bool some = m < task.blk.rows;
+                    const uint16_t* src = static_cast<const uint16_t*>(a.query);
+                    if (some) src += (task.blk.row0 + first + tok) * a.q_stride + (task.kvh * group + (int)(i - tok * group)) * D + 8 * piece;
+                    ptx::cp_async16(smem + h * Z::operand + operand_at<D>(mine + x, piece), src, some);
                 }
-#pragma unroll
-                for (int x = 0; x < kPerWarp; ++x) {
-                    const int m = m0 + x;
-                    uint32_t ex = 127;
-                    if constexpr (!F16) {
-                        const float2 u = act2_to_float2<F16>(w[x][0]), v = act2_to_float2<F16>(w[x][1]);
-                        // the largest magnitude's bits: non-negative floats order like integers
-                        const float big = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
-                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-                        ex = min(max(most >> 23, 1u), 253u);
-                        const float down = __uint_as_float((254u - ex) << 23);          // 2^-(exponent of the largest)
-                        w[x][0] = float2_to_act2<true>(u.x * down, u.y * down);
-                        w[x][1] = float2_to_act2<true>(v.x * down, v.y * down);
-                    }
-                    uint8_t* to = smem + (m >> 7) * Z::operand + operand_at<D>(m & 127, el >> 3) + 2 * e8;
-                    if constexpr (D == 128) *reinterpret_cast<uint2*>(to) = make_uint2(w[x][0], w[x][1]);
-                    else *reinterpret_cast<uint32_t*>(to) = w[x][0];
-                    // (above zero: the mask's -infinity times it stays -infinity)
-                    if (lane == 0)
-                        sh.factor[turn & 1][m] = fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f),
-                                                             1.0e-30f), 3.0e38f);
-                }
+            ptx::cp_async_wait_all();
+            __syncwarp();
+            for (int h = 0; h < halves; ++h) {
+                uint8_t* const base = smem + h * Z::operand;
+                const uint32_t ex = F16 && E2M1 ? 127u : turn_row<F16, E2M1, D>(base, row);
+                // (above zero: the mask's -infinity times it stays -infinity)
+                sh.factor[turn & 1][kM * h + row] =
+                    fminf(fmaxf(__uint_as_float(ex << 23) * (a.softmax_scale * a.k_scale * 1.4426950408889634f), 1.0e-30f), 3.0e38f);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -643,8 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!next_task(it, task) || task.n < 0) break;
             if (task.n == 0) continue;
             const int lo = task.kvh * kv_unit_bytes(D) & 8;                    // (heads of 72 bytes)
-            bool ok = turn > 0 || queries(task);
-            for (int t = 0; ok && t < task.n; ++t, ++tiles) {
+            bool ok = true;
+            for (int t = 0;; ++t, ++tiles) {
+                // (behind the first tile, or before it: the queries of the task before are needed until its last logits are there)
+                if (t == (turn > 0)) ok = queries(task);
+                if (!ok || t == task.n) break;
                 // the position's bytes into registers: the next tile's may land
                 const uint8_t* src = raw + rs * Z::raw + row * Z::raw_row + lo;
                 ok = wait_bounded(&sh.rawfull[rs], rp, &sh.abort, a.err);
@@ -676,12 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scale_pairs<E2M1>(vs, true, g);
                 ok = wait_bounded(&sh.opfree[sv], free_phase, &sh.abort, a.err);
                 if (!ok) break;
-                store_row<E2M1, D>(ring + sv * Z::operand, row, vc, g);
+                store_values<E2M1, D>(ring + sv * Z::operand, row, vc, g);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && !stall) ptx::mbar_arrive(&sh.opfull[sv]);
-                // (behind the first tile: the queries of the task before are needed until its last logits are there)
-                if (t == 0 && turn > 0) ok = queries(task);
             }
             if (!ok) break;
             ++turn;
@@ -805,14 +864,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 k.n = max(0, (all - rank + L.splits - 1) / L.splits);
             }
             if (k.n < 0 || k.blk.rows > 0) {
+                set_heads(k);
                 if (k.n > 0 && it > 0) {
                     // the queries on their way to L2
-                    const Heads heads = heads_of(k);
-                    const int64_t first = k.blk.first / group;
+                    const int64_t first = k.tok0;
                     for (int i = lane; i < k.blk.rows; i += 32) {
-                        const uint32_t tok = (heads.rest + i) * recip >> 22;
+                        const uint32_t tok = (k.rest + i) * recip >> 22;
                         const uint16_t* src = static_cast<const uint16_t*>(a.query) + (k.blk.row0 + first + tok) * a.q_stride +
-                                              (k.kvh * group + (int)(heads.rest + i - tok * group)) * D;
+                                              (k.kvh * group + (int)(k.rest + i - tok * group)) * D;
 #pragma unroll
                         for (int x = 0; x < D; x += 64) ptx::prefetch_l2(src + x);
                     }
@@ -877,12 +936,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         // NaN for the rows of every task that this CTA may have left
         auto fail_rows = [&](const Task& k) {
-            const Heads heads = heads_of(k);
             for (int i = tid; i < k.blk.rows * (D / 8); i += kThreads)
-                reinterpret_cast<uint4*>(dst + head_of(heads, i / (D / 8)) * D)[i % (D / 8)] =
+                reinterpret_cast<uint4*>(dst + head_of(k, i / (D / 8)) * D)[i % (D / 8)] =
                     make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
             if (a.lse)
-                for (int i = tid; i < k.blk.rows; i += kThreads) a.lse[head_of(heads, i)] = __int_as_float(0x7FC00000);
+                for (int i = tid; i < k.blk.rows; i += kThreads) a.lse[head_of(k, i)] = __int_as_float(0x7FC00000);
         };
         if (rank == 0) {
             fail_rows(sh.task[0]);
@@ -892,7 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (held > 0) {
                 const uint32_t at = gridDim.x / (uint32_t)L.splits - held, slot = at / (uint32_t)a.heads_kv;
                 task.kvh = (int)(at - slot * a.heads_kv);
-                if (find_rows_warp(a, slot, L.blocks, L.rows, group, task.blk)) fail_rows(task);
+                if (find_rows_warp(a, slot, L.blocks, L.rows, group, task.blk)) {
+                    set_heads(task);
+                    fail_rows(task);
+                }
             }
         }
     } else if (sh.task[0].n == kBadSums) {
@@ -902,7 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // join the cluster's partial results (of its only task)
         const bool failed = sh.abort != 0;
         const Task& k = sh.task[0];
-        const Heads heads = heads_of(k);
         if (failed) {
             for (int i = tid; i < 2 * kM; i += kThreads) part_ml[i] = make_float2(0.0f, __int_as_float(0x7FC00000));
         }
@@ -931,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.x = fmaf(g, v[x].x, acc.x), acc.y = fmaf(g, v[x].y, acc.y);
                 acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
             }
-            const int64_t head = head_of(heads, i);
+            const int64_t head = head_of(k, i);
             const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
             *reinterpret_cast<uint2*>(dst + head * D + 4 * d4) =
                 make_uint2(float2_to_act2<F16>(acc.x * inv, acc.y * inv), float2_to_act2<F16>(acc.z * inv, acc.w * inv));
@@ -954,10 +1014,13 @@ cudaError_t launch_shape(const PagedArgs& a, int64_t most_rows, int sms, cudaStr
     L.rows = most_rows <= kM ? kM : 2 * kM;
     const int64_t slots = row_slots(a, L.rows, group, &L.blocks);
     const int64_t tiles = ceil_div64(most_positions(a, L.rows, group), kTile);
+    // blocks that hold rows (TND: most of the numbers past these have none)
+    const int64_t full = a.p.layout_tnd ? std::min<int64_t>(slots, a.p.batch * ceil_div64(most_rows, L.rows)) : slots;
+    // CTAs that all run at once: clusters leave some SMs of each group of 18 to 20 out.  us for splits 2 / 4 / 8: 4 sequences of
+    // 16k-32k positions (32 blocks and heads) 122 / 69 / -, 2 of 30000 and 9000 (16) 126 / 70 / 66, one of 16384 (16) - / 66 / 82
     L.splits = 1;
-    // (clusters of more than two leave some SMs of each group of 18 to 20 out)
-    while (L.splits < kMaxSplits && slots * a.heads_kv * L.splits * 2 <= (L.splits == 1 ? sms : sms * 5 / 6) && tiles >= 4 * L.splits)
-        L.splits *= 2;
+    auto room = [&](int splits) { return splits == 2 ? sms : splits == 4 ? sms * 27 / 32 : sms * 3 / 4; };
+    while (L.splits < kMaxSplits && full * a.heads_kv * L.splits * 2 <= room(2 * L.splits) && tiles >= 4 * L.splits) L.splits *= 2;
     const int64_t grid = slots * a.heads_kv * L.splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     CUtensorMap pages;

@@ -275,6 +275,15 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src)
                  : "memory");
 }
 
+// The same of 16 bytes, or zeros if not `some` (src stays a valid address), and the wait for this thread's copies
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool some)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(some ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Arrive on `bar` once this thread's earlier cp.async copies have landed (the barrier's expected
 // arrival count includes this arrival)
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar)
@@ -419,6 +428,17 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t m, uint32_t n)
           "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),            \
           "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]),            \
           "=r"(r[62]), "=r"(r[63])                                                                 \
+        : "r"(taddr))
+
+// 16 lanes x 32 columns, spread as a product's accumulators: thread i gets columns 8 k + 2 (i % 4) and the next of lane
+// base + i / 4 in r[4 k] and r[4 k + 1], and of the lane 8 further in r[4 k + 2] and r[4 k + 3]
+#define QLI_TMEM_LD_16X256_X4(taddr, r)                                                            \
+    asm volatile(                                                                                  \
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"   \
+        "%14,%15}, [%16];"                                                                         \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),      \
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),  \
+          "=r"(r[14]), "=r"(r[15])                                                                 \
         : "r"(taddr))
 
 #define QLI_TMEM_ST_X32(taddr, r)                                                                  \
