@@ -10,6 +10,10 @@
 // before the first is used, the token's places (batch, position, block_table: three dependent loads) behind
 // them.  The rotation wants a lane to hold elements i and R / 2 + i, the quantiser eight consecutive ones (half
 // a block): a key's vector changes hands through shared memory.
+//
+// 15360 tokens of 64 + 8 + 8 heads of 128: 584 MB in 118 us, 4.9 TB/s (0.73 of a copy; 65 % of the issue slots: norm, rotation and
+// quantisation, no pipe above 46 %); as two calls 96 and 18 us, the keys going out and in again in 16 bits between them (and
+// rounded to them).  One token, with a call that reads it back: 4.1 us, a launch and three dependent loads each.
 #include <cuda_runtime.h>
 
 #include "qli_norm_rope.cuh"

@@ -11,8 +11,8 @@
 // the rows, each takes every other tile, and their results are joined at the end.  Roles:
 //   * one warp copies the KV head's bytes of a tile's positions by TMA, 16 positions of a page a box;
 //   * 4 converter warps, a position per thread, decode them into fp16 operands in shared memory: rows of positions
-//     for K and for V (V enters the product with its positions as the K dimension, "MN-major"); they also bring the
-//     queries in;
+//     for K and for V (V enters the product with its positions as the K dimension, "MN-major"; its elements come in the
+//     order in which a lane of the output's warps reads them); they also copy the queries in and turn them into fp16 there;
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
 //   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64
@@ -21,6 +21,17 @@
 //     come first), and the next block's positions and queries are under way while the last one's rows are written.
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
 // through distributed shared memory in a fixed order.
+//
+// Bound by the products (4 D operations a logit): 4 prompts of 15360 tokens in all, 64 / 8 heads of 128, 1.46e12 operations over what
+// the rows see, 1077 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
+// heads, 822 us, 1.50 PFLOP/s (0.78); the prompts with windows of 1024, 488 us, 0.93 PFLOP/s.  What is above the products' time: the
+// chain from a stream's logits through its softmax to its next logits, about 3400 cycles a tile for two streams of which the products
+// 2048 (tensor memory holds two of S and two of O, so that a stream's S waits for its P to be used), and about 5 us a block of rows
+// (the queries, the first and last tiles' masks, 2 us for the output).  So the logits' loads run beside the exponentials (each wait
+// for tensor memory costs about 260 cycles), a block's queries and tiles are under way while the last one's rows are written, and
+// what is rare stands in calls.  Measured and not kept: S in two halves of 64 positions (1101 us for the chunks, then 925: an operand
+// of 128 rows is read from shared memory again for each), two warps that issue products (1190, then 849), P handed on in halves
+// (909, then 848), quarters of a tile at a time (1011, then 854), outputs in pieces of 32 bytes a lane (826, then 817).
 //
 // Masks, pages outside the pool and NaN scales as in qli_paged_attention.cu.  Every wait is bounded (0.2 s, those for
 // the end of a whole task 100 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
