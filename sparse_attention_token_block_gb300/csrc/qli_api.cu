@@ -888,7 +888,8 @@ qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int
     A.entry_bytes = (int32_t)entry_bytes_of(a);
     A.heads_q = a->num_heads_q;
     A.heads_kv = a->num_heads_kv;
-    A.window = window;
+    // (one that no sequence reaches hides nothing, and the masks need not add it up)
+    A.window = window < compressed_keys(p->max_seqlen_k, p->cmp_ratio) ? window : 0;
     A.sinks = sinks;
     A.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : 1.0f / sqrtf((float)a->head_dim);
     A.k_scale = a->k_scale;
@@ -952,7 +953,7 @@ int qli_testing_paged_chunks(const qli_problem* p, const qli_attention* a, int32
     A.p = params_of(p);
     A.heads_q = a->num_heads_q;
     A.heads_kv = a->num_heads_kv;
-    A.window = window;
+    A.window = window < compressed_keys(p->max_seqlen_k, p->cmp_ratio) ? window : 0;
     A.sinks = sinks;
     return A.p.rows > 0 && paged_in_chunks(A) ? 1 : 0;
 }

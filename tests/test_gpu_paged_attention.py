@@ -73,6 +73,13 @@ def test_windows(Q, window, sinks):
     _both(Q, case, 8, 2, 128, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window", [699, 700, 701, 2 ** 31 - 1])
+@pytest.mark.parametrize("sinks", [0, 2 ** 31 - 1])
+def test_windows_as_long_as_the_sequences(Q, window, sinks):
+    case = cache_case(layout_q="TND", q_lens=[40, 3, 1], seq_lens_k=[700, 2, 130], block_size=16, sparse_count=1, sparse_mode=3, seed=6)
+    _both(Q, case, 8, 2, 64, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("q_lens,lens", [([1, 1, 1], [40, 1, 600]), ([5, 0, 3, 0, 0, 17], [5, 3, 900, 0, 7, 17]),
                                          ([0, 0], [0, 5]), ([33, 200], [33, 1000]), ([7], [3])])
 @pytest.mark.parametrize("spare", [0, 1, 40])
