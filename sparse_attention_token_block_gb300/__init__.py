@@ -388,15 +388,21 @@ def _pool(t, p, a):
 
 def _here(*tensors):
     """ValueError unless every tensor given lies on the current CUDA device (the one that the call runs on)."""
-    at = None
-    for t in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        if at is None:
-            import torch
-            at = torch.cuda.current_device()
-        if t.get_device() != at:
-            raise ValueError("expected tensors on the current device cuda:%d, got %s" % (at, t.device))
+    global _cuda
+    if _cuda is None:
+        import torch
+        _cuda = torch.cuda
+    try:
+        found = {t.get_device() for t in tensors if t is not None}
+    except AttributeError:                             # (plain addresses among them)
+        found = {t.get_device() for t in tensors if t is not None and not isinstance(t, int)}
+    if found:
+        at = _cuda.current_device()
+        if found != {at}:
+            raise ValueError("expected tensors on the current device cuda:%d, got devices %s" % (at, sorted(found)))
+
+
+_cuda = None
 
 
 def _workspace(t):
