@@ -5,7 +5,7 @@ import pytest
 
 from attention_tools import cache, cache_case
 from oracle import attention as A
-from paged_tools import attend, check, dev, queries, settings
+from paged_tools import attend, check, dev, queries, round_to, settings
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +78,33 @@ def test_windows(Q, window, sinks):
 def test_windows_as_long_as_the_sequences(Q, window, sinks):
     case = cache_case(layout_q="TND", q_lens=[40, 3, 1], seq_lens_k=[700, 2, 130], block_size=16, sparse_count=1, sparse_mode=3, seed=6)
     _both(Q, case, 8, 2, 64, window=window, sinks=sinks)
+
+
+def _check_finite(Q, case, q, pool, e2m1, f16, scale=0.0):
+    """Rows and heads whose queries hold NaN or infinities are NaN, the others as if those were zeros."""
+    bad = ~np.isfinite(q).all(-1)
+    out, lse, bits = attend(Q, case, q, pool, 2, e2m1, f16, scale=scale)
+    assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+    clean = np.where(bad[..., None], np.float32(0), q)
+    want = attend(Q, case, clean, pool, 2, e2m1, f16, scale=scale)
+    out[bad], lse[bad] = want[0][bad], want[1][bad]
+    check(case, (out, lse, bits), clean, pool, 2, e2m1, f16, scale=scale)
+
+
+@pytest.mark.parametrize("e2m1,f16", [(True, False), (False, True), (True, True), (False, False)])
+def test_queries_of_no_numbers(Q, e2m1, f16):
+    case = cache_case(layout_q="TND", q_lens=[40, 3], seq_lens_k=[300, 77], block_size=32, sparse_count=1, sparse_mode=3, seed=7)
+    pool, q = cache(case, 2, 64, e2m1, 1), queries(case.rows, 8, 64, f16, 2)
+    q[1] = 0
+    q[5, 3, 7], q[9, 2], q[41, 0, 0], q[39, 6, 63] = np.nan, np.inf, -np.inf, np.nan
+    _check_finite(Q, case, q, pool, e2m1, f16)
+
+
+@pytest.mark.parametrize("size,scale", [(1e38, 2e-39), (1e-38, 1e37), (2.0 ** -130, 2.0 ** 120)])
+def test_queries_of_any_size(Q, size, scale):
+    case = cache_case(layout_q="TND", q_lens=[40, 3], seq_lens_k=[300, 77], block_size=32, sparse_count=1, sparse_mode=3, seed=8)
+    pool, q = cache(case, 2, 64, True, 1), round_to(queries(case.rows, 8, 64, False, 2) * np.float64(size), False)
+    _check_finite(Q, case, q, pool, True, False, scale=scale)            # (a few of the largest are infinite)
 
 
 @pytest.mark.parametrize("q_lens,lens", [([1, 1, 1], [40, 1, 600]), ([5, 0, 3, 0, 0, 17], [5, 3, 900, 0, 7, 17]),
