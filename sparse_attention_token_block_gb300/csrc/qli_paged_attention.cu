@@ -13,11 +13,11 @@
 // of a page by one TMA box; warps that are left over (`parts`) and the CTAs of a cluster (`splits`) share the
 // steps in turn, and their partial results are joined in shared memory in a fixed order.
 //
-// Bound by the cache's bytes: 32 sequences of 8k-32k positions, 64 / 8 heads of 128, 732 MB in 169 us, 4.3 TB/s (0.64 of a copy); the
+// Bound by the cache's bytes: 32 sequences of 8k-32k positions, 64 / 8 heads of 128, 732 MB in 163 us, 4.5 TB/s (0.66 of a copy); the
 // steady state reads 6.9 TB/s.  The rest is what a CTA does once (its rows 1 us, the first bytes 3 us, the join 1 to 5 us) and
 // sequences of uneven length: clusters of CTAs on a sequence even these out and pay the join.  Entries are decoded in registers, each
 // key once for its 8 or 16 rows: with the entries on the M side no part of a product is padding, and 8 rows cost what one does.
-// Windows of 4096 of the same batch 39 us (3.9 TB/s); 96 rows of 512 positions 15 us and one row of 256 6 us are latency.  Measured
+// Windows of 4096 of the same batch 37 us (4.1 TB/s: 256 CTAs, two on some SMs, where instructions count: shorter tests for NaN and masks gave 5 %); 96 rows of 512 positions 15 us and one row of 256 6 us are latency.  Measured
 // and not kept: the pages' numbers and queries loaded before the lengths are known (no gain), copies by lanes on their own (slower).
 //
 // Positions that a step holds beyond what a row sees are masked, and so are those on pages outside the pool (of
@@ -269,6 +269,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         const uint8_t* ks0 = head + r * row + D + (D == 128 ? 2 * c : c);
         const uint8_t* vc0 = head + 2 * c * row + D / 2 + (D / 16) * r;               // value codes and scales
         const uint8_t* vs0 = head + 2 * c * row + D + D / 16 + (D == 128 ? r : r >> 1);
+        // steps that every row sees whole (of those behind the sinks')
+        const int whole_from = range.sink_chunks + (max(0, range.high - range.base) + kChunk - 1) / kChunk;
+        const int whole_to = range.sink_chunks + max(0, range.low - range.base) / kChunk - 1;
         int stage = 0, parity = 0;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st) {
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                     if constexpr (D == 128) {
                         uint32_t b = *reinterpret_cast<const uint16_t*>(x);
                         const uint32_t v = *reinterpret_cast<const uint16_t*>(x + D / 16);
-                        if (__vcmpeq4(v & 0x7F7Fu, 0x00007F7Fu) & 0xFFFFu) b = 0x7F7Fu;
+                        if ((v & 0x7F7Fu) + 0x0101u & 0x8080u) b = 0x7F7Fu;
                         const uint32_t h = e4m3x2_to_f16x2(b);
                         g[u][y][0] = pair_scale<E2M1>(__byte_perm(h, 0, 0x1010));
                         g[u][y][1] = pair_scale<E2M1>(__byte_perm(h, 0, 0x3232));
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[u][t][e] = fmaf(s[u][t][e], f[t][e & 1], -m[t][e & 1]);
-            if (mask != 3u || !range.all_see(ch, 2)) {
+            if (mask != 3u || ch < whole_from || ch >= whole_to) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int pos = range.position(ch + u), limit = mask >> u & 1 ? range.limit(ch + u) : 0;

@@ -23,8 +23,8 @@
 // through distributed shared memory in a fixed order.
 //
 // Bound by the products (4 D operations a logit): 4 prompts of 15360 tokens in all, 64 / 8 heads of 128, 1.46e12 operations over what
-// the rows see, 1077 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
-// heads, 822 us, 1.50 PFLOP/s (0.78); the prompts with windows of 1024, 488 us, 0.93 PFLOP/s.  What is above the products' time: the
+// the rows see, 1073 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
+// heads, 818 us, 1.51 PFLOP/s (0.79); the prompts with windows of 1024, 487 us, 0.93 PFLOP/s.  What is above the products' time: the
 // chain from a stream's logits through its softmax to its next logits, about 3400 cycles a tile for two streams of which the products
 // 2048 (tensor memory holds two of S and two of O, so that a stream's S waits for its P to be used), and about 5 us a block of rows
 // (the queries, the first and last tiles' masks, 2 us for the output).  So the logits' loads run beside the exponentials (each wait
