@@ -467,9 +467,8 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
  * invalid (as for qli_metadata; all rows, for bad TND prefix sums).  Positions on a page outside the pool are left
  * out, with error bit 2; pages of positions that no row sees are not looked at.  sparse_count is not used.
  * QLI_ERR_UNSUPPORTED from 2^28 rows x query heads and from 2^31 - 1024 positions (of max_seqlen_k) on.
- * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention (float16 outputs too have their
- * probabilities rounded to fp16 once).  A scale byte of NaN gives NaN in the rows and heads that see the position,
- * in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
+ * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention.  A scale byte of NaN gives NaN in the rows
+ * and heads that see the position, in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
  * does not depend on scheduling.
  */
 qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks, const void* query,

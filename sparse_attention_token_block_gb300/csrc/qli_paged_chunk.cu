@@ -16,7 +16,9 @@
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
 //   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64
-//     probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16.
+//     probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16;
+//     for float16 outputs what that rounding drops stands beside P in the logits' place and is a product of its own with V
+//     (chunks 828 -> 1155 us, prompts 1074 -> 1451: half as many products again).
 //   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
 //     come first), and the next block's positions and queries are under way while the last one's rows are written.
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
@@ -215,8 +217,9 @@ __device__ __forceinline__ void store_values(uint8_t* operand, int row, const ui
     }
 }
 
-// Probabilities 2^(s f - m) of 32 of a row's logits, in fp16 pairs, and their sum onto `part`
-__device__ __forceinline__ void soft_part(const uint32_t (&s)[32], float f, float m, uint32_t* p, uint64_t (&part)[2])
+// Probabilities 2^(s f - m) of 32 of a row's logits, in fp16 pairs, and their sum onto `part`; F16: what the rounding dropped, too
+template <bool F16>
+__device__ __forceinline__ void soft_part(const uint32_t (&s)[32], float f, float m, uint32_t* p, uint32_t* rest, uint64_t (&part)[2])
 {
     const uint64_t F = ptx::pack2(f, f), M = ptx::pack2(-m, -m);
 #pragma unroll
@@ -226,6 +229,7 @@ __device__ __forceinline__ void soft_part(const uint32_t (&s)[32], float f, floa
         const float px = ptx::ex2(zx), py = ptx::ex2(zy);
         part[e >> 1 & 1] = ptx::add2(part[e >> 1 & 1], ptx::pack2(px, py));
         p[e / 2] = float2_to_act2<true>(px, py);
+        if constexpr (F16) rest[e / 2] = remainder_f16x2(px, py, p[e / 2]);
     }
 }
 __device__ __forceinline__ float sum_of(const uint64_t (&part)[2])
@@ -251,18 +255,21 @@ __device__ __noinline__ float max_half(uint32_t cols)
     return top;
 }
 
-// The probabilities of a row's 64 logits from column `cols` on into the 32 columns from `to` on, and their sum
+// The probabilities of a row's 64 logits from column `cols` on into the 32 columns from `to` on (F16: what their rounding dropped
+// into the 32 behind these), and their sum
+template <bool F16>
 __device__ __noinline__ float soft_half(uint32_t cols, uint32_t to, float f, float m)
 {
-    uint32_t s[2][32], p[32];
+    uint32_t s[2][32], p[32], rest[32];
     QLI_TMEM_LD_X32(cols, s[0]);
     QLI_TMEM_LD_X32(cols + 32, s[1]);
     wait_loaded(s[0]);
     wait_loaded(s[1]);
     uint64_t part[2] = {0, 0};
-    soft_part(s[0], f, m, p, part);
-    soft_part(s[1], f, m, p + 16, part);
+    soft_part<F16>(s[0], f, m, p, rest, part);
+    soft_part<F16>(s[1], f, m, p + 16, rest + 16, part);
     QLI_TMEM_ST_X32(to, p);
+    if constexpr (F16) QLI_TMEM_ST_X32(to + 32, rest);
     ptx::tmem_wait_st();
     return sum_of(part);
 }
@@ -297,19 +304,28 @@ __device__ __noinline__ void scale_row(uint32_t cols, int n, float g)
     }
 }
 
-// A row's 64 probabilities times g
+// A row's 64 probabilities times g (F16: with what their rounding dropped, rounded anew)
+template <bool F16>
 __device__ __noinline__ void scale_half(uint32_t cols, float g)
 {
-    uint32_t o[32];
+    uint32_t o[32], rest[32];
     ptx::tmem_wait_st();
     QLI_TMEM_LD_X32(cols, o);
+    if constexpr (F16) QLI_TMEM_LD_X32(cols + 32, rest);
     wait_loaded(o);
+    if constexpr (F16) wait_loaded(rest);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-        const float2 v = act2_to_float2<true>(o[e]);
+        float2 v = act2_to_float2<true>(o[e]);
+        if constexpr (F16) {
+            const float2 r = act2_to_float2<true>(rest[e]);
+            v.x += r.x, v.y += r.y;                        // (exact: 22 bits)
+        }
         o[e] = float2_to_act2<true>(v.x * g, v.y * g);
+        if constexpr (F16) rest[e] = remainder_f16x2(v.x * g, v.y * g, o[e]);
     }
     QLI_TMEM_ST_X32(cols, o);
+    if constexpr (F16) QLI_TMEM_ST_X32(cols + 32, rest);
 }
 
 // A lane's eight elements of a row (of 32 columns, in the order of store_values), times f
@@ -533,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* const part_ml = reinterpret_cast<float2*>(part_o + 2 * kM * kStride);
     static_assert(2 * kM * (kStride * 4 + 8) <= Z::shared_at, "partial results in the operands' place");
     Task task;
+    // columns from the probabilities of a tile's first 64 positions to the others': F16, what their rounding dropped stands between
+    constexpr int kHalfCols = F16 ? 64 : 32;
 
     if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax
@@ -587,13 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_loaded(s[0]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
+                        uint32_t p[32], rest[32];
                         uint64_t part[2] = {0, 0};
                         QLI_TMEM_LD_X32(cols + 64 * h + 32, s[1]);
-                        soft_part(s[0], f, m_run, p, part);
+                        soft_part<F16>(s[0], f, m_run, p, rest, part);
                         wait_loaded(s[1]);
                         if (h == 0) QLI_TMEM_LD_X32(cols + 64, s[0]);
-                        soft_part(s[1], f, m_run, p + 16, part);
+                        soft_part<F16>(s[1], f, m_run, p + 16, rest + 16, part);
                         if (h == 0) wait_loaded(s[0]);
                         const float sum = sum_of(part);
                         if (__any_sync(0xffffffffu, sum > kMostSum)) {
@@ -604,14 +622,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const bool over = sum > kMostSum && up > m_run;
                             const float g = over ? ptx::ex2(m_run - up) : 1.0f;
                             if (over) m_run = up;
-                            if (h == 1) scale_half(cols, g);
+                            if (h == 1) scale_half<F16>(cols, g);
                             if (j > 0) scale_row(out + D * q, D / 32, g);
-                            l_run = l_run * g + soft_half(cols + 64 * h, cols + 32 * h, f, m_run);
+                            l_run = l_run * g + soft_half<F16>(cols + 64 * h, cols + kHalfCols * h, f, m_run);
                             QLI_TMEM_LD_X32(cols + 64, s[0]);
                             wait_loaded(s[0]);
                         } else {
                             l_run += sum;
-                            QLI_TMEM_ST_X32(cols + 32 * h, p);     // in the place of the logits that are through
+                            QLI_TMEM_ST_X32(cols + kHalfCols * h, p);     // in the place of the logits that are through
+                            if constexpr (F16) QLI_TMEM_ST_X32(cols + kHalfCols * h + 32, rest);
                         }
                     }
                     ptx::tmem_wait_st();
@@ -833,7 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t vo = vd + (stage * Z::operand >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + 8 * kk, vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0);
+#pragma unroll
+                        for (int e = 0; e < (F16 ? 2 : 1); ++e)
+                            ptx::mma_f16_ts(tm + kColO + D * q, tm + kTile * q + kHalfCols * (kk >> 2) + 8 * (kk & 3) + 32 * e,
+                                            vo + (kk * 16 * 128 >> 4), idesc_o, j > 0 || kk > 0 || e > 0);
                     if (shared || q == 1) ptx::mma_commit(&sh.opfree[stage]);
                 }
                 __syncwarp();
