@@ -467,7 +467,9 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
  * invalid (as for qli_metadata; all rows, for bad TND prefix sums).  Positions on a page outside the pool are left
  * out, with error bit 2; pages of positions that no row sees are not looked at.  sparse_count is not used.
  * QLI_ERR_UNSUPPORTED from 2^28 rows x query heads and from 2^31 - 1024 positions (of max_seqlen_k) on.
- * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention.  A scale byte of NaN gives NaN in the rows
+ * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention, with probabilities held so that each is within
+ * 2^-33 of its row's largest besides the rounding named there: n positions far below one add at most n 2^-33 of the
+ * largest value to the output's error.  A scale byte of NaN gives NaN in the rows
  * and heads that see the position, in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
  * does not depend on scheduling.
  */

@@ -7,7 +7,7 @@
 // share of the positions, 32 a step:
 //   * logits:  S^T (16 positions x 8 rows) = K Q^T, keys decoded from shared memory straight into the fragment;
 //   * softmax: running maximum and sum per row in fp32 (base 2); the accumulators are rescaled only when a logit
-//     exceeds the maximum in use by more than 8;
+//     exceeds the maximum in use by more than 15;
 //   * output:  O^T (D x 8 rows) += V^T P^T, P rounded to fp16 (values of codes times scales are exact in fp16), for float16
 //     outputs with a second product of what that rounding dropped (decode 173 -> 186 us, over int4 218 -> 236).
 // The units of `per_cta` KV heads of the same rows share a CTA, and a copy warp brings their bytes of 16 positions
@@ -49,7 +49,11 @@ constexpr int kMaxStages = 6;
 constexpr int kHalfSmem = 112 * 1024;             // dynamic, of one of two CTAs on an SM
 constexpr int kMostSmem = 220 * 1024;
 constexpr uint64_t kWaitLimitNs = 200000000ull;
-constexpr float kRescale = 8.0f;                  // logits (base 2) above the maximum in use
+// Probabilities enter the products in fp16, where a row's largest stands between 2^11 and 2^15: the maximum in use is raised to 11
+// below the largest logit (base 2) when one lies more than 15 above it.  So fp16's normal range (2^-14) reaches 2^-25 of the largest
+// at least, and 2^-36 of it is what becomes 0: however many positions lie 27 bits down, they count.  (Raised to the largest logit
+// itself 2^-25 became 0: 50000 positions below one whose value is 0 were lost.)
+constexpr float kRescale = 15.0f, kBelow = 11.0f, kUnit11 = 1.0f / 2048.0f;
 
 // How a launch is laid out (host)
 struct Layout {
@@ -85,6 +89,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
 {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return wait_slow(bar, parity, abort, err);
+}
+
+// ln of a row's sum of exponentials, held as `sum` of 2^(z - m)
+__device__ __forceinline__ float lse_of(float m, float sum)
+{
+    return sum == 0.0f ? -INFINITY : (m + kBelow + log2f(sum * kUnit11)) * 0.6931471805599453f;
 }
 
 template <int N>
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = m[t][e];
+                        float top = -FLT_MAX;
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -364,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        // (rounded up: logits that fp32 holds in steps of 16 have their largest at 2^0, not at 2^16)
+                        top = fmaxf(m[t][e], __fadd_ru(top, -kBelow));
                         const float down = ptx::ex2(m[t][e] - top);
                         m[t][e] = top;
                         l[t][e] *= down;
@@ -474,15 +486,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
                 const int i = 8 * t + 2 * c + e;
                 if (i >= blk.rows) continue;
                 const float sum = l[t][e];
-                const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 uint32_t w[MO];
 #pragma unroll
-                for (int x = 0; x < MO; ++x) w[x] = float2_to_act2<F16>(o[t][x][e] * inv, o[t][x][e + 2] * inv);
+                for (int x = 0; x < MO; ++x) w[x] = float2_to_act2<F16>(o[t][x][e] * inv * a.v_scale, o[t][x][e + 2] * inv * a.v_scale);
                 const int64_t at = out_head(unit, i);
                 uint4* dst = reinterpret_cast<uint4*>(out + at * D + r * (D / 8));
 #pragma unroll
                 for (int x = 0; x < MO / 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-                if (a.lse && r == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (m[t][e] + log2f(sum)) * 0.6931471805599453f;
+                if (a.lse && r == 0) a.lse[at] = lse_of(m[t][e], sum);
             }
         return;
     }
@@ -509,10 +521,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         const int un = hh / M, i = hh - un * M;
         if (i >= blk.rows) return;
         const int64_t at = out_head(un, i);
-        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        // (two steps: a factor near the smallest number over the sum would not be one that fp32 holds)
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, g = a.v_scale;
         *reinterpret_cast<uint2*>(out + at * D + 4 * d4) =
-            make_uint2(float2_to_act2<F16>(v.x * inv, v.y * inv), float2_to_act2<F16>(v.z * inv, v.w * inv));
-        if (a.lse && d4 == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            make_uint2(float2_to_act2<F16>(v.x * inv * g, v.y * inv * g), float2_to_act2<F16>(v.z * inv * g, v.w * inv * g));
+        if (a.lse && d4 == 0) a.lse[at] = lse_of(top, sum);
     };
     if (L.parts > 1) {
         // the warps of each unit; the joined result replaces the first warp's

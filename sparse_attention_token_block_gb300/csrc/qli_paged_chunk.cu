@@ -15,8 +15,8 @@
 //     order in which a lane of the output's warps reads them); they also copy the queries in and turn them into fp16 there;
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
-//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64
-//     probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16;
+//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (8 below the largest, raised only when the sum
+//     of 64 probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16;
 //     for float16 outputs what that rounding drops stands beside P in the logits' place and is a product of its own with V
 //     (chunks 828 -> 1155 us, prompts 1074 -> 1451: half as many products again).
 //   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
@@ -59,6 +59,10 @@ constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
 constexpr float kMostSum = 32768.0f;                   // of 64 probabilities, which then fit fp16
+// The maximum in use is set to 8 below the largest of 64 logits (base 2), whose probabilities then add up to 2^14 at most: a row's
+// largest stands at 2^8 or above, and what becomes 0 in fp16 lies 2^-33 below it (at 2^0, 2^-25: 100000 positions below one
+// whose value is 0 were lost).
+constexpr float kBelow = 8.0f, kUnit8 = 1.0f / 256.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 100000000000ull;     // (the length of a task: 2^31 positions)
 
 struct Layout {
@@ -120,6 +124,15 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
         }
     }
     return true;
+}
+
+// `kBelow` under a logit, rounded up: logits that fp32 holds in steps of 16 have their largest at 2^0, not at 2^16
+__device__ __forceinline__ float below(float top) { return __fadd_ru(top, -kBelow); }
+
+// ln of a row's sum of exponentials, held as `sum` of 2^(z - m)
+__device__ __forceinline__ float lse_of(float m, float sum)
+{
+    return sum == 0.0f ? -INFINITY : (m + kBelow + log2f(sum * kUnit8)) * 0.6931471805599453f;
 }
 
 // Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
@@ -336,10 +349,10 @@ __device__ __forceinline__ float element(const uint32_t (&o)[16], int half, int 
 }
 
 // Columns [32 from, 32 to) of a warp's 32 rows' accumulators from `acc` on, times f0 (with `both`, and those D further times
-// f1; without `some`, zeros): into the output, or as fp32 into `partial`.  A lane has eight elements of rows lane / 4 + 8 i, which
+// f1; without `some`, zeros): times g into the output, or as fp32 into `partial`.  A lane has eight elements of rows lane / 4 + 8 i, which
 // begin at elements at0 ... at3 (-1: none); f0 and f1 are those of row `lane`.
 template <bool F16, bool E2M1, int D>
-__device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool both, bool some, float f0, float f1, uint16_t* dst, int64_t at0,
+__device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool both, bool some, float f0, float f1, float g, uint16_t* dst, int64_t at0,
                                         int64_t at1, int64_t at2, int64_t at3, float* partial)
 {
     constexpr int kStride = D + 4;
@@ -358,8 +371,8 @@ __device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool bot
             to4[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else if (at[i] >= 0) {
             *reinterpret_cast<uint4*>(dst + at[i] + 32 * x) =
-                make_uint4(float2_to_act2<F16>(v[0], v[1]), float2_to_act2<F16>(v[2], v[3]), float2_to_act2<F16>(v[4], v[5]),
-                           float2_to_act2<F16>(v[6], v[7]));
+                make_uint4(float2_to_act2<F16>(v[0] * g, v[1] * g), float2_to_act2<F16>(v[2] * g, v[3] * g),
+                           float2_to_act2<F16>(v[4] * g, v[5] * g), float2_to_act2<F16>(v[6] * g, v[7] * g));
         }
     };
     // two blocks of 32 columns, or one of both accumulators
@@ -598,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mask_half(cols + 64 * h, bits[0], bits[1]);
                         }
                     }
-                    if (j == 0) m_run = fmaxf(m_run, max_half(cols) * f);          // (of the first logits: as they are)
+                    if (j == 0) m_run = fmaxf(m_run, below(max_half(cols) * f));   // (of the first logits: as they are)
                     // half a tile at a time, each 32 logits on their way while those before are worked on
                     uint32_t s[2][32];
                     QLI_TMEM_LD_X32(cols, s[0]);
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's first
                             // half of P, and begin again.  (The stream's last product was issued before these logits, and has
                             // ended.  What is in registers does not live through the calls.)
-                            const float up = max_half(cols + 64 * h) * f;
+                            const float up = below(max_half(cols + 64 * h) * f);
                             const bool over = sum > kMostSum && up > m_run;
                             const float g = over ? ptx::ex2(m_run - up) : 1.0f;
                             if (over) m_run = up;
@@ -667,9 +680,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int w = (row & ~31) + (lane >> 2) + 8 * i;
                 at[i] = w < task.blk.rows ? head_of(task, w) * D + 8 * (lane & 3) : -1;
             }
-            const float inv = L.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : a.v_scale / sum;
+            const float inv = L.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             if (L.splits == 1 && writes && from == 0 && row < task.blk.rows && a.lse)
-                a.lse[head_of(task, row)] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                a.lse[head_of(task, row)] = lse_of(top, sum);
             if (task.n > 0) {
                 if (!wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
                 ptx::tc_fence_after();
@@ -677,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the operands' place is free now)
             if (L.splits > 1 && writes && from == 0) part_ml[row] = make_float2(top, sum);
             if (writes && !idle)
-                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0] * inv, g[1] * inv, dst, at[0], at[1], at[2], at[3],
+                write_rows<F16, E2M1, D>(acc, from, to, both, task.n > 0, g[0] * inv, g[1] * inv, a.v_scale, dst, at[0], at[1], at[2], at[3],
                                          L.splits > 1 ? part_o + (row & ~31) * kStride : nullptr);
             if (task.n > 0) {
                 ptx::tc_fence_before();
@@ -1025,10 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
             }
             const int64_t head = head_of(k, i);
-            const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, g = a.v_scale;
             *reinterpret_cast<uint2*>(dst + head * D + 4 * d4) =
-                make_uint2(float2_to_act2<F16>(acc.x * inv, acc.y * inv), float2_to_act2<F16>(acc.z * inv, acc.w * inv));
-            if (a.lse && d4 == 0) a.lse[head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                make_uint2(float2_to_act2<F16>(acc.x * inv * g, acc.y * inv * g), float2_to_act2<F16>(acc.z * inv * g, acc.w * inv * g));
+            if (a.lse && d4 == 0) a.lse[head] = lse_of(top, sum);
         }
         __syncwarp();
         ptx::cluster_sync();                               // no CTA leaves while another reads its partial results

@@ -1,5 +1,6 @@
 """The probabilities of the dense paged attention, through both of its kernels, against the 64-bit oracle (needs a
-GB300): with float16 activations they enter the products with the bits that fp16 drops of them."""
+GB300): with float16 activations they enter the products with the bits that fp16 drops of them, and those far below a
+row's largest count whatever the number of positions."""
 import math
 
 import numpy as np
@@ -28,7 +29,7 @@ def Q(request):
     Q._lib_handle, Q._lib_path = saved
 
 
-def _bounds(ref, spread, f16, terms):
+def _bounds(ref, spread, f16, terms, depth=25):
     """Bound of |out - ref| for exact queries (powers of two times integers below 2^11) of which `terms` elements are not
     zero, the other products adding nothing:
       * logits: `terms` - 1 additions of a product's sum (each within 2^-23 of the sum of magnitudes, truncation allowed), the
@@ -38,20 +39,21 @@ def _bounds(ref, spread, f16, terms):
         2^-19;
       * n + 64 additions of a sum and of an output, 2^-23 each;
       * a probability within 2^-22 of itself (float16: fp16's half step of a remainder of at most 2^-11) or 2^-11 (bfloat16:
-        one rounding to fp16), 2^-25 below fp16's normal range;
+        one rounding to fp16), and within 2^-`depth` of a row's largest: 2^-25 is fp16's half step below its normal range, of
+        numbers among which the largest stands at 2^0 at least (both kernels: at 2^8, so that depth is 33);
       * the output's own rounding."""
     n = np.maximum(spread["n"], 1)[:, None]
     dz = spread["qk"] * (2 * terms + 4) * 2.0 ** -24
     rel = (2.0 ** -22 if f16 else 2.0 ** -11) + 2 * dz + 2.0 ** -19 + (n + 64) * 2.0 ** -23
-    err = rel[..., None] * (spread["wv"] + np.abs(ref)) + (n * 2.0 ** -25 * spread["vmax"])[..., None]
+    err = rel[..., None] * (spread["wv"] + np.abs(ref)) + (n * 2.0 ** -depth * spread["vmax"])[..., None]
     return err + half_step(f16) * (np.abs(ref) + err) + smallest_step(f16)
 
 
-def _check(case, got, q, pool, hkv, e2m1, f16, scale, terms, **kw):
+def _check(case, got, q, pool, hkv, e2m1, f16, scale, terms, depth=25, **kw):
     out, lse, bits = got
     ref, rl, err, spread = A.paged_attention(case, q, pool, hkv, e2m1, scale, **kw)
     assert bits == err == 0
-    bad = ~(np.abs(out - ref) <= _bounds(ref, spread, f16, terms))
+    bad = ~(np.abs(out - ref) <= _bounds(ref, spread, f16, terms, depth))
     assert not bad.any(), (int(bad.sum()), bad.size, np.argwhere(bad)[:3], out[bad][:3], ref[bad][:3])
     n = np.maximum(spread["n"], 1)[:, None]
     ltol = spread["qk"] * (2 * terms + 4) * 2.0 ** -24 + 2.0 ** -19 + n * 2.0 ** -23 + 2.0 ** -22 * np.abs(rl)
@@ -74,3 +76,52 @@ def test_float16_outputs_are_off_by_their_rounding(Q, hq, hkv, dim, e2m1, terms)
     for scale, window, sinks in ((1 / math.sqrt(terms), 8, 0), (1 / math.sqrt(terms), 6, 2), (20.0, 40, 3)):
         got = attend(Q, case, q, pool, hkv, e2m1, True, window=window, sinks=sinks, scale=scale)
         _check(case, got, q, pool, hkv, e2m1, True, scale, terms, window=window, sinks=sinks)
+
+
+def _one_far_above(n, dim, gap, spread, e2m1, seed):
+    """A case and a pool of one KV head: position 0 has a logit of 0 and a value of zeros, the n others logits about `gap` bits
+    lower, spread over about `spread` bits, and values about 1."""
+    case = cache_case(batch=1, s1=1, seq_lens_k=[n + 1], block_size=64, sparse_count=1, sparse_mode=3, seed=seed, permute=False)
+    slots = case.num_blocks * case.block_size
+    rng = np.random.default_rng(seed)
+    k, v = np.zeros((slots, 1, dim), np.float32), np.zeros((slots, 1, dim), np.float32)
+    at = (case.block_table[0][:, None] * 64 + np.arange(64)).reshape(-1)[:n + 1]
+    k[at[1:], 0, 0] = -gap * math.log(2.0)
+    k[at[1:], 0, 16] = rng.uniform(-0.5, 0.5, n) * spread * math.log(2.0)
+    v[at[1:]] = 1 + 0.25 * rng.normal(size=(n, 1, dim))
+    return case, A.encode(k, v, e2m1).reshape(case.num_blocks, 64, -1)
+
+
+@pytest.mark.parametrize("gap", [20, 22, 24, 25, 26, 27])
+@pytest.mark.parametrize("spread", [1, 0])
+@pytest.mark.parametrize("f16", [False, True])
+def test_one_position_far_above_many(Q, gap, spread, f16):
+    dim, e2m1 = (64, True) if gap % 2 else (128, False)
+    case, pool = _one_far_above(100000, dim, gap, spread, e2m1, gap)
+    q = np.zeros((1, 2, dim), np.float32)
+    q[:, :, 0] = 1
+    q[:, 1, 16] = 1
+    _check(case, attend(Q, case, q, pool, 1, e2m1, f16, scale=1.0), q, pool, 1, e2m1, f16, 1.0, 2, depth=33)
+
+
+@pytest.mark.parametrize("gap", [24, 27])
+@pytest.mark.parametrize("f16", [False, True])
+def test_one_position_far_above_many_in_one_warp(Q, gap, f16):
+    """The same where a warp carries all positions of a sequence: more sequences than the GPU holds CTAs, of the same pages."""
+    dim, hkv, sequences = 64, 8, 640
+    case, one = _one_far_above(50000, dim, gap, 1, True, gap)
+    unit = A.unit_bytes(dim)
+    pool = np.tile(one[..., :unit], hkv)
+    q = np.zeros((sequences, hkv, dim), np.float32)
+    q[:, :, 0] = 1
+    q[sequences // 2:, :, 16] = 1
+    many = cache_case(batch=sequences, s1=1, seq_lens_k=[1] * sequences, block_size=64, sparse_count=1, sparse_mode=3, seed=1)
+    many.seq_lens_k = np.repeat(case.seq_lens_k, sequences)
+    many.block_table = np.repeat(case.block_table, sequences, 0)
+    many.num_blocks, many.max_blocks_per_seq = case.num_blocks, case.max_blocks_per_seq
+    out, lse, bits = attend(Q, many, q, pool, hkv, True, f16, scale=1.0)
+    for b in (0, sequences - 1):
+        got = out[b:b + 1, :1], lse[b:b + 1, :1], bits
+        _check(case, got, q[b:b + 1, :1], one, 1, True, f16, 1.0, 2, depth=33)
+    for half in (slice(0, sequences // 2), slice(sequences // 2, None)):         # every head and sequence the same
+        assert (out[half] == out[half][:1, :1]).all() and (lse[half] == lse[half][:1, :1]).all()
