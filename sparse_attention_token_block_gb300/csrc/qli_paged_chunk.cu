@@ -36,7 +36,7 @@
 // (909, then 848), quarters of a tile at a time (1011, then 854), outputs in pieces of 32 bytes a lane (826, then 817).
 //
 // Masks, pages outside the pool and NaN scales as in qli_paged_attention.cu.  Every wait is bounded (0.2 s, those for
-// the end of a whole task 100 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
+// a task and for the end of one 100 s); on expiry the kernel records kErrTimeout, writes NaN and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -415,8 +415,11 @@ __device__ __noinline__ void write_rows(uint32_t acc, int from, int to, bool bot
     __syncwarp();
 }
 
-// The block number `slot`, found by a warp (as find_rows); false: the prefix sums are invalid
-__device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot, int blocks, int M, int group, RowBlock& r)
+// The block number `slot`, found by a warp (as find_rows); false: the prefix sums are invalid.  `checked`: they have been looked
+// at as a whole (and will have been), so that a search finds the sequence: of 50000 without new tokens each number costs a few
+// loads, not 1563.
+__device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot, int blocks, int M, int group, bool& checked,
+                                               RowBlock& r)
 {
     const Params& p = a.p;
     const int lane = threadIdx.x & 31;
@@ -424,6 +427,19 @@ __device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot
     if (!p.layout_tnd) {
         b = (int)(slot / (uint32_t)blocks);
         block = (int)(slot - (uint32_t)b * blocks);
+    } else if (checked) {
+        // the number of sequences that begin at or before the block lies in [b, b + n]: each lane asks for the last of a piece
+        b = 0;
+        for (uint32_t n = (uint32_t)p.batch; n > 0;) {
+            const uint32_t step = (n + 31) / 32;
+            const int i = b + (int)min((lane + 1) * step, n) - 1;
+            const bool before = (int64_t)a.seq_lens_q[i] * group / M + i + 1 <= (int64_t)slot;
+            const uint32_t past = min(__popc(__ballot_sync(0xffffffffu, before)) * step, n);
+            b += (int)past;
+            n = past < n ? min(step, n - past) - 1 : 0;    // (that piece's last is not among them)
+        }
+        const int64_t done = b > 0 ? a.seq_lens_q[b - 1] : 0;
+        block = (int)((int64_t)slot - (done * group / M + b));
     } else {
         bool bad = false;
         b = 0;
@@ -438,6 +454,7 @@ __device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot
             b += __popc(__ballot_sync(0xffffffffu, before));
         }
         if (__any_sync(0xffffffffu, bad)) return false;
+        checked = true;
         const int64_t done = b > 0 ? a.seq_lens_q[b - 1] : 0;
         block = (int)((int64_t)slot - (done * group / M + b));
     }
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto head_of = [&](const Task& h, int i) { return h.base + i + (int)((h.rest + i) * recip >> 22) * (a.heads_q - group); };
     // the next task; false when a wait gave up.  (The softmax warps read theirs in place and hand it back at its end.)
     auto next_task = [&](int it, Task& k) {
-        if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err)) return false;
+        if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err, kTaskLimitNs)) return false;
         k = sh.task[it & 1];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.taskfree[it & 1]);
@@ -573,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t joins = 0;
         for (int it = 0;; ++it) {
             const Task& task = sh.task[it & 1];
-            if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err) || task.n < 0) break;
+            if (!wait_bounded(&sh.taskfull[it & 1], it >> 1 & 1, &sh.abort, a.err, kTaskLimitNs) || task.n < 0) break;
 
             const bool shared = shares(task);
             const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
@@ -895,13 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // they start first.
         const uint32_t tasks = gridDim.x / (uint32_t)L.splits;
         uint32_t id = blockIdx.x / (uint32_t)L.splits, asked = 0;
-        bool more = true, ok = true;
+        bool more = true, ok = true, checked = false;
         for (int it = 0; more; ++it) {
             Task k;
             k.n = k.blk.rows = 0;
             const uint32_t at = tasks - 1 - id, slot = at / (uint32_t)a.heads_kv;
             k.kvh = (int)(at - slot * a.heads_kv);
-            if (!find_rows_warp(a, slot, L.blocks, L.rows, group, k.blk)) {
+            if (!find_rows_warp(a, slot, L.blocks, L.rows, group, checked, k.blk)) {
                 k.n = kBadSums;
                 more = false;
             } else if (k.blk.rows > 0) {
@@ -996,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (held > 0) {
                 const uint32_t at = gridDim.x / (uint32_t)L.splits - held, slot = at / (uint32_t)a.heads_kv;
                 task.kvh = (int)(at - slot * a.heads_kv);
-                if (find_rows_warp(a, slot, L.blocks, L.rows, group, task.blk)) {
+                bool checked = false;
+                if (find_rows_warp(a, slot, L.blocks, L.rows, group, checked, task.blk)) {
                     set_heads(task);
                     fail_rows(task);
                 }
