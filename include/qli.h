@@ -468,7 +468,7 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
  * out, with error bit 2; pages of positions that no row sees are not looked at.  sparse_count is not used.
  * QLI_ERR_UNSUPPORTED from 2^28 rows x query heads and from 2^31 - 1024 positions (of max_seqlen_k) on.
  * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention, with probabilities held so that each is within
- * 2^-33 of its row's largest besides the rounding named there: n positions far below one add at most n 2^-33 of the
+ * 2^-31 of its row's sum besides the rounding named there: n positions far below others add at most n 2^-31 of the
  * largest value to the output's error.  A scale byte of NaN gives NaN in the rows
  * and heads that see the position, in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
  * does not depend on scheduling.

@@ -15,8 +15,8 @@
 //     order in which a lane of the output's warps reads them); they also copy the queries in and turn them into fp16 there;
 //   * one warp issues the products: Q, K and V from shared memory, logits and accumulators in tensor memory, P in the
 //     place of the logits it came from;
-//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (8 below the largest, raised only when the sum
-//     of 64 probabilities passes 2^15, which P would not hold much longer: then the row of O is rescaled), sum in fp32, P to fp16;
+//   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64 probabilities
+//     passes 65000, which P would not hold much longer: then the rows of O are rescaled), sum in fp32, P to fp16;
 //     for float16 outputs what that rounding drops stands beside P in the logits' place and is a product of its own with V
 //     (chunks 828 -> 1155 us, prompts 1074 -> 1451: half as many products again).
 //   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
@@ -58,11 +58,14 @@ constexpr int kThreads = 32 * 15;
 constexpr int kRing = 4, kMaxRaw = 2;
 constexpr int kMaxSplits = 8;
 constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 128 q
-constexpr float kMostSum = 32768.0f;                   // of 64 probabilities, which then fit fp16
-// The maximum in use is set to 8 below the largest of 64 logits (base 2), whose probabilities then add up to 2^14 at most: a row's
-// largest stands at 2^8 or above, and what becomes 0 in fp16 lies 2^-33 below it (at 2^0, 2^-25: 100000 positions below one
-// whose value is 0 were lost).
-constexpr float kBelow = 8.0f, kUnit8 = 1.0f / 256.0f;
+// Probabilities enter the second product in fp16.  The maximum in use is set to 6 below the largest of a row's first 128 logits
+// (base 2), so that its sum stands at 2^6 or above from the first tile on, and what becomes 0 (2^-25) lies 2^-31 below it: 100000
+// positions 25 bits below one whose value is 0 count (from 2^0 on they were lost).  It is raised when 64 probabilities add up to more
+// than fp16 is sure to hold; the warp's other rows then catch up with their largest sum so far, since their next records are near.
+// us for 8 / 7 / 6 / 5 below, chunks and prompts: queries of the tests' spread 837 / 837 / 837 / 850 and 1097 / 1095 / 1097 / 1104, of
+// twice the spread 884 / 872 / 859 / 855 and 1223 / 1164 / 1130 / 1122 (each row raised alone, 8 below, 1081 and 1672).
+constexpr float kBelow = 6.0f, kUnit6 = 1.0f / 64.0f;
+constexpr float kMostSum = 65000.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 100000000000ull;     // (the length of a task: 2^31 positions)
 
 struct Layout {
@@ -132,7 +135,7 @@ __device__ __forceinline__ float below(float top) { return __fadd_ru(top, -kBelo
 // ln of a row's sum of exponentials, held as `sum` of 2^(z - m)
 __device__ __forceinline__ float lse_of(float m, float sum)
 {
-    return sum == 0.0f ? -INFINITY : (m + kBelow + log2f(sum * kUnit8)) * 0.6931471805599453f;
+    return sum == 0.0f ? -INFINITY : (m + kBelow + log2f(sum * kUnit6)) * 0.6931471805599453f;
 }
 
 // Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool shared = shares(task);
             const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
             const bool idle = (row & ~31) >= task.blk.rows;
-            float m_run = -FLT_MAX, l_run = 0.0f;
+            float m_run = -FLT_MAX, l_run = 0.0f, best = 0.0f;         // (best: the largest sum of 64)
             bool ok = true;
             if (task.n > 0) {
                 const int hi = seen_end(a, task.blk, task.tok0 + (int)((task.rest + row) * recip >> 22));
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mask_half(cols + 64 * h, bits[0], bits[1]);
                         }
                     }
-                    if (j == 0) m_run = fmaxf(m_run, below(max_half(cols) * f));   // (of the first logits: as they are)
+                    if (j == 0) m_run = fmaxf(m_run, below(fmaxf(max_half(cols), max_half(cols + 64)) * f));
                     // half a tile at a time, each 32 logits on their way while those before are worked on
                     uint32_t s[2][32];
                     QLI_TMEM_LD_X32(cols, s[0]);
@@ -645,20 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (h == 0) wait_loaded(s[0]);
                         const float sum = sum_of(part);
                         if (__any_sync(0xffffffffu, sum > kMostSum)) {
-                            // raise the maximum of the rows that need it, rescale their sums, accumulators and the tile's first
-                            // half of P, and begin again.  (The stream's last product was issued before these logits, and has
-                            // ended.  What is in registers does not live through the calls.)
-                            const float up = below(max_half(cols + 64 * h) * f);
-                            const bool over = sum > kMostSum && up > m_run;
-                            const float g = over ? ptx::ex2(m_run - up) : 1.0f;
-                            if (over) m_run = up;
+                            // raise the maximum to the logits that are left of the tile, of rows that do not need it also so that
+                            // their largest sum stands near 2^6, rescale sums, accumulators and the tile's first half of P, and
+                            // begin again.  (The stream's last product was issued before these logits, and has ended.  What is in
+                            // registers does not live through the calls.)
+                            const float top = below((h == 0 ? fmaxf(max_half(cols), max_half(cols + 64)) : max_half(cols + 64)) * f);
+                            const float more = best > 2 / kUnit6 ? (float)(int)(__float_as_uint(best) >> 23) - (127 + kBelow) : 0.0f;
+                            const float up = fmaxf(top, sum > kMostSum ? m_run : __fadd_rd(m_run, more));
+                            const float g = ptx::ex2(m_run - up);
+                            m_run = up;
                             if (h == 1) scale_half<F16>(cols, g);
                             if (j > 0) scale_row(out + D * q, D / 32, g);
-                            l_run = l_run * g + soft_half<F16>(cols + 64 * h, cols + kHalfCols * h, f, m_run);
+                            const float now = soft_half<F16>(cols + 64 * h, cols + kHalfCols * h, f, m_run);
+                            l_run = l_run * g + now;
+                            best = fmaxf(best * g, now);
                             QLI_TMEM_LD_X32(cols + 64, s[0]);
                             wait_loaded(s[0]);
                         } else {
                             l_run += sum;
+                            best = fmaxf(best, sum);
                             QLI_TMEM_ST_X32(cols + kHalfCols * h, p);     // in the place of the logits that are through
                             if constexpr (F16) QLI_TMEM_ST_X32(cols + kHalfCols * h + 32, rest);
                         }

@@ -8,7 +8,7 @@ import pytest
 
 from attention_tools import cache, cache_case, half_step, round_to, smallest_step
 from oracle import attention as A
-from paged_tools import attend
+from paged_tools import attend, check, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -39,8 +39,9 @@ def _bounds(ref, spread, f16, terms, depth=25):
         2^-19;
       * n + 64 additions of a sum and of an output, 2^-23 each;
       * a probability within 2^-22 of itself (float16: fp16's half step of a remainder of at most 2^-11) or 2^-11 (bfloat16:
-        one rounding to fp16), and within 2^-`depth` of a row's largest: 2^-25 is fp16's half step below its normal range, of
-        numbers among which the largest stands at 2^0 at least (both kernels: at 2^8, so that depth is 33);
+        one rounding to fp16), and within 2^-`depth` of a row's sum: 2^-25 is fp16's half step below its normal range, of
+        numbers among which the largest stands at 2^0 at least (in the kernels a row's sum stands at 2^6 at least, the lower of 2^11
+        and 2^6: depth 31);
       * the output's own rounding."""
     n = np.maximum(spread["n"], 1)[:, None]
     dz = spread["qk"] * (2 * terms + 4) * 2.0 ** -24
@@ -101,7 +102,7 @@ def test_one_position_far_above_many(Q, gap, spread, f16):
     q = np.zeros((1, 2, dim), np.float32)
     q[:, :, 0] = 1
     q[:, 1, 16] = 1
-    _check(case, attend(Q, case, q, pool, 1, e2m1, f16, scale=1.0), q, pool, 1, e2m1, f16, 1.0, 2, depth=33)
+    _check(case, attend(Q, case, q, pool, 1, e2m1, f16, scale=1.0), q, pool, 1, e2m1, f16, 1.0, 2, depth=31)
 
 
 @pytest.mark.parametrize("gap", [24, 27])
@@ -122,6 +123,27 @@ def test_one_position_far_above_many_in_one_warp(Q, gap, f16):
     out, lse, bits = attend(Q, many, q, pool, hkv, True, f16, scale=1.0)
     for b in (0, sequences - 1):
         got = out[b:b + 1, :1], lse[b:b + 1, :1], bits
-        _check(case, got, q[b:b + 1, :1], one, 1, True, f16, 1.0, 2, depth=33)
+        _check(case, got, q[b:b + 1, :1], one, 1, True, f16, 1.0, 2, depth=31)
     for half in (slice(0, sequences // 2), slice(sequences // 2, None)):         # every head and sequence the same
         assert (out[half] == out[half][:1, :1]).all() and (lse[half] == lse[half][:1, :1]).all()
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -124, 2.0 ** 100])
+def test_factors_near_the_ends_of_the_range(Q, factor):
+    case = cache_case(layout_q="TND", q_lens=[150, 1], seq_lens_k=[900, 5000], block_size=64, sparse_count=1, sparse_mode=3, seed=2)
+    pool, q = cache(case, 2, 64, True, 1, 1.0, factor), queries(case.rows, 8, 64, False, 2)
+    got = attend(Q, case, q, pool, 2, True, False, factors=(1.0, factor))
+    check(case, got, q, pool, 2, True, False, factors=(1.0, factor))
+
+
+@pytest.mark.parametrize("std", [3.0, 10.0])
+@pytest.mark.parametrize("e2m1,f16", [(True, False), (False, True)])
+def test_logits_that_spread_widely(Q, std, e2m1, f16):
+    """Rows whose maximum rises again and again, in first and second halves of tiles, beside others whose does not."""
+    case = cache_case(layout_q="TND", q_lens=[260, 40], seq_lens_k=[2500, 1200], block_size=64, sparse_count=1, sparse_mode=3, seed=2)
+    pool, q = cache(case, 2, 64, e2m1, 1), queries(case.rows, 4, 64, f16, 2)
+    q[::3] *= np.float32(std)
+    q = round_to(q, f16)
+    for window, sinks in ((0, 0), (200, 3)):
+        got = attend(Q, case, q, pool, 2, e2m1, f16, window=window, sinks=sinks)
+        check(case, got, q, pool, 2, e2m1, f16, window=window, sinks=sinks)
