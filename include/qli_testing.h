@@ -27,6 +27,8 @@ extern "C" {
  * memory before it exits, so the CUDA context stays usable.  Other values select 0.
  * Mode 1 also holds for qli_sparse_attention's and qli_paged_attention's kernels: no entry is copied or
  * handed on, the waits run out (0.2 s) and the outputs are NaN.
+ *   3  (qli_paged_attention's kernel of few rows) every second copying lane's own test for a free stage
+ *      fails.  A pair of lanes goes by its first lane's test, so nothing changes; other kernels run as in 0.
  */
 void qli_testing_set_stall(int mode);
 

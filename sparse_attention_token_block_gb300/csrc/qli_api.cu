@@ -942,7 +942,7 @@ const char* qli_status_string(qli_status s)
 int qli_version(void) { return 100; }
 
 #ifdef QLI_TESTING
-void qli_testing_set_stall(int mode) { g_test_stall.store(mode == 1 || mode == 2 ? mode : 0); }
+void qli_testing_set_stall(int mode) { g_test_stall.store(mode >= 1 && mode <= 3 ? mode : 0); }
 void qli_testing_set_topk_ctas(int ctas) { g_test_topk_ctas.store(ctas > 0 ? ctas : 0); }
 void qli_testing_set_paged(int kernel) { g_test_paged.store(kernel == 1 || kernel == 2 ? kernel : 0); }
 int qli_testing_paged_chunks(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks)

@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     if (wid == kWarps) {
         // ---------------------------------------------------------------- copies: a lane per part and chunk of its steps
         const int p = min(lane >> 1, L.parts - 1), x = lane & 1, n = lane < 2 * L.parts ? steps_of(p) : 0, lo = u0 * kUnit & ~15;
-        const bool stall = a.p.test_stall == 1;                // test switch: nothing arrives, the waits run out
+        const bool stall = a.p.test_stall == 1;                // test switches: nothing arrives, the waits run out
+        const bool late = a.p.test_stall == 3;                 // second lanes' own tests of a stage fail
         const int32_t* table = a.block_table + (int64_t)blk.batch * a.p.max_blocks_per_seq;
         const uint32_t bytes = kChunk * L.row_bytes;
         uint8_t* const ring = smem + p * L.stages * 2 * bytes + x * bytes;
@@ -175,8 +176,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         uint32_t parity = 1;
         uint64_t since = ptx::globaltimer();
         while (__any_sync(0xffffffffu, i < n)) {
-            // those parts whose next stage is free go on
-            const bool ready = i < n && ptx::mbar_test_wait(&freed[p][stage], parity);
+            // those parts whose next stage is free go on: the first lane of the pair that copies for a part tells (two tests of
+            // a barrier that is about to change may differ, and a lane that went on alone would arm it for half the bytes)
+            bool ready = i < n && !(late && x) && ptx::mbar_test_wait(&freed[p][stage], parity);
+            ready = __shfl_sync(0xffffffffu, ready, lane & ~1);
             if (!__any_sync(0xffffffffu, ready)) {
                 if (__any_sync(0xffffffffu, *(volatile uint32_t*)&abort != 0)) break;
                 if (__any_sync(0xffffffffu, ptx::globaltimer() - since > kWaitLimitNs)) {
