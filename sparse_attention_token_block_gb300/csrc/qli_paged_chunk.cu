@@ -18,15 +18,17 @@
 //   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64 probabilities
 //     passes 65000, which P would not hold much longer: then the rows of O are rescaled), sum in fp32, P to fp16;
 //     for float16 outputs what that rounding drops stands beside P in the logits' place and is a product of its own with V
-//     (chunks 828 -> 1155 us, prompts 1074 -> 1451: half as many products again).
-//   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun (the longest
-//     come first), and the next block's positions and queries are under way while the last one's rows are written.
+//     (chunks 828 -> 1147 us, prompts 1071 -> 1447: half as many products again).
+//   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun, and the next block's
+//     positions and queries are under way while the last one's rows are written.  A sequence's later rows, which see more, begin
+//     first; sequences begin in the reverse of the batch's order, whatever their length (chunks of 512, 1000, 33 and 2047 tokens
+//     behind 8k to 30k 828 us, the same four in the opposite order 882).
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
 // through distributed shared memory in a fixed order.
 //
 // Bound by the products (4 D operations a logit): 4 prompts of 15360 tokens in all, 64 / 8 heads of 128, 1.46e12 operations over what
-// the rows see, 1073 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
-// heads, 818 us, 1.51 PFLOP/s (0.79); the prompts with windows of 1024, 487 us, 0.93 PFLOP/s.  What is above the products' time: the
+// the rows see, 1078 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
+// heads, 828 us, 1.49 PFLOP/s (0.78); the prompts with windows of 1024, 488 us, 0.93 PFLOP/s.  What is above the products' time: the
 // chain from a stream's logits through its softmax to its next logits, about 3400 cycles a tile for two streams of which the products
 // 2048 (tensor memory holds two of S and two of O, so that a stream's S waits for its P to be used), and about 5 us a block of rows
 // (the queries, the first and last tiles' masks, 2 us for the output).  So the logits' loads run beside the exponentials (each wait
@@ -62,8 +64,8 @@ constexpr uint32_t kTmemCols = 512, kColO = 256;       // logits of stream q at 
 // (base 2), so that its sum stands at 2^6 or above from the first tile on, and what becomes 0 (2^-25) lies 2^-31 below it: 100000
 // positions 25 bits below one whose value is 0 count (from 2^0 on they were lost).  It is raised when 64 probabilities add up to more
 // than fp16 is sure to hold; the warp's other rows then catch up with their largest sum so far, since their next records are near.
-// us for 8 / 7 / 6 / 5 below, chunks and prompts: queries of the tests' spread 837 / 837 / 837 / 850 and 1097 / 1095 / 1097 / 1104, of
-// twice the spread 884 / 872 / 859 / 855 and 1223 / 1164 / 1130 / 1122 (each row raised alone, 8 below, 1081 and 1672).
+// us for 8 / 7 / 6 / 5 below, chunks and prompts: queries of normal values 837 / 837 / 837 / 850 and 1097 / 1095 / 1097 / 1104, with
+// twice that spread 884 / 872 / 859 / 855 and 1223 / 1164 / 1130 / 1122 (each row raised alone, 8 below, 1081 and 1672).
 constexpr float kBelow = 6.0f, kUnit6 = 1.0f / 64.0f;
 constexpr float kMostSum = 65000.0f;
 constexpr uint64_t kWaitLimitNs = 200000000ull, kTaskLimitNs = 100000000000ull;     // (the length of a task: 2^31 positions)
@@ -465,6 +467,28 @@ __device__ __forceinline__ bool find_rows_warp(const PagedArgs& a, uint32_t slot
     return true;
 }
 
+// The rare step of a row's 64 logits at cols + 64 h, whose probabilities add up to too much for fp16 in some row of the warp: raise the
+// maximum to the logits that are left of the tile, of rows that do not need it also so that their largest sum stands near 2^6,
+// rescale sums, accumulators (32 n columns from `acc` on) and the tile's first half of P, and take the probabilities again.
+struct Running {
+    float m, l, best;                                      // maximum in use, sum, largest sum of 64
+};
+template <bool F16>
+__device__ __noinline__ Running raise_rows(uint32_t cols, int h, int half_cols, uint32_t acc, int n, float f, float sum, Running r)
+{
+    const float top = below((h == 0 ? fmaxf(max_half(cols), max_half(cols + 64)) : max_half(cols + 64)) * f);
+    const float more = r.best > 2 / kUnit6 ? (float)(int)(__float_as_uint(r.best) >> 23) - (127 + kBelow) : 0.0f;
+    const float up = fmaxf(top, sum > kMostSum ? r.m : __fadd_rd(r.m, more));
+    const float g = ptx::ex2(r.m - up);
+    r.m = up;
+    if (h == 1) scale_half<F16>(cols, g);
+    scale_row(acc, n, g);
+    const float now = soft_half<F16>(cols + 64 * h, cols + half_cols * h, f, up);
+    r.l = r.l * g + now;
+    r.best = fmaxf(r.best * g, now);
+    return r;
+}
+
 template <bool F16, bool E2M1, int D>
 __device__ __noinline__ uint32_t turn_row(uint8_t* base, int row)
 {
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool shared = shares(task);
             const int row = (shared ? 0 : q * kM) + lane_row, steps = steps_of(task, q);
             const bool idle = (row & ~31) >= task.blk.rows;
-            float m_run = -FLT_MAX, l_run = 0.0f, best = 0.0f;         // (best: the largest sum of 64)
+            Running run = {-FLT_MAX, 0.0f, 0.0f};
             bool ok = true;
             if (task.n > 0) {
                 const int hi = seen_end(a, task.blk, task.tok0 + (int)((task.rest + row) * recip >> 22));
@@ -631,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mask_half(cols + 64 * h, bits[0], bits[1]);
                         }
                     }
-                    if (j == 0) m_run = fmaxf(m_run, below(fmaxf(max_half(cols), max_half(cols + 64)) * f));
+                    if (j == 0) run.m = fmaxf(run.m, below(fmaxf(max_half(cols), max_half(cols + 64)) * f));
                     // half a tile at a time, each 32 logits on their way while those before are worked on
                     uint32_t s[2][32];
                     QLI_TMEM_LD_X32(cols, s[0]);
@@ -641,32 +665,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t p[32], rest[32];
                         uint64_t part[2] = {0, 0};
                         QLI_TMEM_LD_X32(cols + 64 * h + 32, s[1]);
-                        soft_part<F16>(s[0], f, m_run, p, rest, part);
+                        soft_part<F16>(s[0], f, run.m, p, rest, part);
                         wait_loaded(s[1]);
                         if (h == 0) QLI_TMEM_LD_X32(cols + 64, s[0]);
-                        soft_part<F16>(s[1], f, m_run, p + 16, rest + 16, part);
+                        soft_part<F16>(s[1], f, run.m, p + 16, rest + 16, part);
                         if (h == 0) wait_loaded(s[0]);
                         const float sum = sum_of(part);
                         if (__any_sync(0xffffffffu, sum > kMostSum)) {
-                            // raise the maximum to the logits that are left of the tile, of rows that do not need it also so that
-                            // their largest sum stands near 2^6, rescale sums, accumulators and the tile's first half of P, and
-                            // begin again.  (The stream's last product was issued before these logits, and has ended.  What is in
-                            // registers does not live through the calls.)
-                            const float top = below((h == 0 ? fmaxf(max_half(cols), max_half(cols + 64)) : max_half(cols + 64)) * f);
-                            const float more = best > 2 / kUnit6 ? (float)(int)(__float_as_uint(best) >> 23) - (127 + kBelow) : 0.0f;
-                            const float up = fmaxf(top, sum > kMostSum ? m_run : __fadd_rd(m_run, more));
-                            const float g = ptx::ex2(m_run - up);
-                            m_run = up;
-                            if (h == 1) scale_half<F16>(cols, g);
-                            if (j > 0) scale_row(out + D * q, D / 32, g);
-                            const float now = soft_half<F16>(cols + 64 * h, cols + kHalfCols * h, f, m_run);
-                            l_run = l_run * g + now;
-                            best = fmaxf(best * g, now);
+                            // (The stream's last product was issued before these logits, and has ended.  What is in registers
+                            // does not live through the call.)
+                            run = raise_rows<F16>(cols, h, kHalfCols, out + D * q, j > 0 ? D / 32 : 0, f, sum, run);
                             QLI_TMEM_LD_X32(cols + 64, s[0]);
                             wait_loaded(s[0]);
                         } else {
-                            l_run += sum;
-                            best = fmaxf(best, sum);
+                            run.l += sum;
+                            run.best = fmaxf(run.best, sum);
                             QLI_TMEM_ST_X32(cols + kHalfCols * h, p);     // in the place of the logits that are through
                             if constexpr (F16) QLI_TMEM_ST_X32(cols + kHalfCols * h + 32, rest);
                         }
@@ -681,10 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the rows' outputs.  Shared rows: each stream's warps join half of the elements of both accumulators.
             // (What there is to know before the last products end.)
             float g[2] = {1.0f, 0.0f};
-            float top = m_run, sum = l_run;
+            float top = run.m, sum = run.l;
             const bool both = shared && steps_of(task, 1) > 0;
             if (both) {
-                sh.ml[joins & 1][q][lane_row] = make_float2(m_run, l_run);
+                sh.ml[joins & 1][q][lane_row] = make_float2(run.m, run.l);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sh.joined);
                 if (!wait_bounded(&sh.joined, joins & 1, &sh.abort, a.err)) break;
