@@ -12,8 +12,9 @@
 // a block): a key's vector changes hands through shared memory.
 //
 // 15360 tokens of 64 + 8 + 8 heads of 128: 584 MB in 118 us, 4.9 TB/s (0.73 of a copy; 65 % of the issue slots: norm, rotation and
-// quantisation, no pipe above 46 %); as two calls 96 and 18 us, the keys going out and in again in 16 bits between them (and
-// rounded to them).  One token, with a call that reads it back: 4.1 us, a launch and three dependent loads each.
+// quantisation, no pipe above 46 %); as two calls 94.6 and 23.5 us, 118 together, the keys going out and in again in 16 bits
+// between them: for many tokens the pass saves the keys' rounding to 16 bits, not time.  One token 2.5 us, as two calls 3.5; with a
+// call that reads it back 4.0, a launch and three dependent loads each.
 #include <cuda_runtime.h>
 
 #include "qli_norm_rope.cuh"

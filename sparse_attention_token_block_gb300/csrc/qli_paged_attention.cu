@@ -9,17 +9,19 @@
 //   * softmax: running maximum and sum per row in fp32 (base 2); the accumulators are rescaled only when a logit
 //     exceeds the maximum in use by more than 15;
 //   * output:  O^T (D x 8 rows) += V^T P^T, P rounded to fp16 (values of codes times scales are exact in fp16), for float16
-//     outputs with a second product of what that rounding dropped (decode 173 -> 186 us, over int4 218 -> 236).
+//     outputs with a second product of what that rounding dropped (decode 162 -> 179 us, over int4 206 -> 233).
 // The units of `per_cta` KV heads of the same rows share a CTA, and a copy warp brings their bytes of 16 positions
 // of a page by one TMA box; warps that are left over (`parts`) and the CTAs of a cluster (`splits`) share the
 // steps in turn, and their partial results are joined in shared memory in a fixed order.
 //
-// Bound by the cache's bytes: 32 sequences of 8k-32k positions, 64 / 8 heads of 128, 732 MB in 163 us, 4.5 TB/s (0.66 of a copy); the
+// Bound by the cache's bytes: 32 sequences of 8k-32k positions, 64 / 8 heads of 128, 732 MB in 164 us, 4.5 TB/s (0.66 of a copy); the
 // steady state reads 6.9 TB/s.  The rest is what a CTA does once (its rows 1 us, the first bytes 3 us, the join 1 to 5 us) and
 // sequences of uneven length: clusters of CTAs on a sequence even these out and pay the join.  Entries are decoded in registers, each
 // key once for its 8 or 16 rows: with the entries on the M side no part of a product is padding, and 8 rows cost what one does.
-// Windows of 4096 of the same batch 37 us (4.1 TB/s: 256 CTAs, two on some SMs, where instructions count: shorter tests for NaN and masks gave 5 %); 96 rows of 512 positions 15 us and one row of 256 6 us are latency.  Measured
-// and not kept: the pages' numbers and queries loaded before the lengths are known (no gain), copies by lanes on their own (slower).
+// Windows of 4096 of the same batch 37 us (4.1 TB/s: 256 CTAs, two on some SMs, where instructions count: shorter tests for NaN and
+// masks gave 5 %).  96 tokens' rows over 128 / 512 / 1024 positions of an int4 cache, float16, 10 / 16 / 25 us: 2.1 us a step of a warp;
+// one row of 256, one step a warp, 6 us.  Measured and not kept: the pages' numbers and queries loaded before the lengths are known
+// (no gain), copies by lanes on their own (slower).
 //
 // Positions that a step holds beyond what a row sees are masked, and so are those on pages outside the pool (of
 // which nothing is copied).  What lies there is arbitrary: scales of NaN among the values are taken as numbers
