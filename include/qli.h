@@ -469,9 +469,10 @@ qli_status qli_sparse_attention(const qli_problem* p, const qli_attention* a, co
  * QLI_ERR_UNSUPPORTED from 2^28 rows x query heads and from 2^31 - 1024 positions (of max_seqlen_k) on.
  * `query`, `out`, `lse`, types and numerics as in qli_sparse_attention, with probabilities held so that each is within
  * 2^-31 of its row's sum besides the rounding named there: n positions far below others add at most n 2^-31 of the
- * largest value to the output's error.  A scale byte of NaN gives NaN in the rows and heads that see the position,
- * in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result does
- * not depend on scheduling.  The choice is the whole call's, by its longest sequence (max_seqlen_q): single tokens
+ * largest value to the output's error.  Logits are fp32: a row and head whose largest is below 2^27 in magnitude is as
+ * above, one whose largest is beyond 1.87e8 gets NaN.  A scale byte of NaN gives NaN in the rows and heads that see the
+ * position, in some or all of their elements, and nowhere else.  One kernel on `stream`, chosen by the sizes; the result
+ * does not depend on scheduling.  The choice is the whole call's, by its longest sequence (max_seqlen_q): single tokens
  * beside a prompt's chunk in one TND call run as a chunk's rows do; as two calls they cost less.
  */
 qli_status qli_paged_attention(const qli_problem* p, const qli_attention* a, int32_t window, int32_t sinks, const void* query,

@@ -2,6 +2,8 @@
 // positions they see.
 #pragma once
 
+#include <cfloat>
+
 #include "qli_kv.cuh"
 
 namespace qli {
@@ -167,6 +169,13 @@ inline int64_t most_positions(const PagedArgs& a, int M, int group)
     int64_t n = compressed_keys(a.p.max_seqlen_k, a.p.cmp_ratio);
     if (a.window > 0 && (int64_t)a.window + a.sinks + M / group + 32 < n) n = (int64_t)a.window + a.sinks + M / group + 32;
     return n;
+}
+
+// A row's sum as it counts.  Exponentials take s f - m at once, with m near the largest s f in fp32: from 2^28 on (base 2) fp32 holds
+// every 32nd number, and 2^(s f - m) of the largest itself leaves fp16's range.  Such rows are NaN (m = -FLT_MAX: nothing seen).
+__device__ __forceinline__ float sum_that_counts(float m, float sum)
+{
+    return fabsf(m) < 268435456.0f || m == -FLT_MAX ? sum : __int_as_float(0x7FC00000);
 }
 
 // Every row zero, shared between all threads of the launch (`thread` of `threads`)

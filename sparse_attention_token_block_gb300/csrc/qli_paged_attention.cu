@@ -9,7 +9,7 @@
 //   * softmax: running maximum and sum per row in fp32 (base 2); the accumulators are rescaled only when a logit
 //     exceeds the maximum in use by more than 15;
 //   * output:  O^T (D x 8 rows) += V^T P^T, P rounded to fp16 (values of codes times scales are exact in fp16), for float16
-//     outputs with a second product of what that rounding dropped (decode 162 -> 179 us, over int4 206 -> 233).
+//     outputs with a second product of what that rounding dropped (decode 162 -> 177 us, over int4 206 -> 231).
 // The units of `per_cta` KV heads of the same rows share a CTA, and a copy warp brings their bytes of 16 positions
 // of a page by one TMA box; warps that are left over (`parts`) and the CTAs of a cluster (`splits`) share the
 // steps in turn, and their partial results are joined in shared memory in a fixed order.
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             for (int e = 0; e < 2; ++e) {
                 const int i = 8 * t + 2 * c + e;
                 if (i >= blk.rows) continue;
-                const float sum = l[t][e];
+                const float sum = sum_that_counts(m[t][e], l[t][e]);
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 uint32_t w[MO];
 #pragma unroll
@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     auto finish = [&](int hh, int d4, const float4& v, float top, float sum) {
         const int un = hh / M, i = hh - un * M;
         if (i >= blk.rows) return;
+        sum = sum_that_counts(top, sum);
         const int64_t at = out_head(un, i);
         // (two steps: a factor near the smallest number over the sum would not be one that fp32 holds)
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, g = a.v_scale;

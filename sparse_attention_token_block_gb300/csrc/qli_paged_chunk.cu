@@ -18,17 +18,17 @@
 //   * 4 softmax warps per stream, a row per thread: masked logits, running maximum (raised only when the sum of 64 probabilities
 //     passes 65000, which P would not hold much longer: then the rows of O are rescaled), sum in fp32, P to fp16;
 //     for float16 outputs what that rounding drops stands beside P in the logits' place and is a product of its own with V
-//     (chunks 828 -> 1147 us, prompts 1071 -> 1447: half as many products again).
+//     (chunks 828 -> 1138 us, prompts 1071 -> 1443: half as many products again).
 //   * one warp looks after the work: a CTA that is through takes over CTAs of the grid that have not begun, and the next block's
 //     positions and queries are under way while the last one's rows are written.  A sequence's later rows, which see more, begin
 //     first; sequences begin in the reverse of the batch's order, whatever their length (chunks of 512, 1000, 33 and 2047 tokens
-//     behind 8k to 30k 828 us, the same four in the opposite order 882).
+//     behind 8k to 30k 821 us, the same four in the opposite order 879).
 // Where there are few blocks of rows a cluster of CTAs shares a block's tiles, and the partial results are joined
 // through distributed shared memory in a fixed order.
 //
 // Bound by the products (4 D operations a logit): 4 prompts of 15360 tokens in all, 64 / 8 heads of 128, 1.46e12 operations over what
-// the rows see, 1078 us, 1.36 PFLOP/s (0.71 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
-// heads, 828 us, 1.49 PFLOP/s (0.78); the prompts with windows of 1024, 488 us, 0.93 PFLOP/s.  What is above the products' time: the
+// the rows see, 1086 us, 1.35 PFLOP/s (0.70 of a library's large product); chunks of 3592 tokens behind 67000 cached ones, 32 / 8
+// heads, 821 us, 1.51 PFLOP/s (0.78); the prompts with windows of 1024, 495 us, 0.92 PFLOP/s.  What is above the products' time: the
 // chain from a stream's logits through its softmax to its next logits, about 3400 cycles a tile for two streams of which the products
 // 2048 (tensor memory holds two of S and two of O, so that a stream's S waits for its P to be used), and about 5 us a block of rows
 // (the queries, the first and last tiles' masks, 2 us for the output).  So the logits' loads run beside the exponentials (each wait
@@ -138,6 +138,13 @@ __device__ __forceinline__ float below(float top) { return __fadd_ru(top, -kBelo
 __device__ __forceinline__ float lse_of(float m, float sum)
 {
     return sum == 0.0f ? -INFINITY : (m + kBelow + log2f(sum * kUnit6)) * 0.6931471805599453f;
+}
+
+// What a row's accumulators are multiplied by, and its lse
+__device__ __noinline__ float2 end_of_row(float m, float sum)
+{
+    sum = sum_that_counts(m, sum);
+    return make_float2(sum == 0.0f ? 0.0f : 1.0f / sum, lse_of(m, sum));
 }
 
 // Wait for this thread's loads from tensor memory; the registers pass through it, so that nothing that uses
@@ -718,9 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int w = (row & ~31) + (lane >> 2) + 8 * i;
                 at[i] = w < task.blk.rows ? head_of(task, w) * D + 8 * (lane & 3) : -1;
             }
-            const float inv = L.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float2 end = L.splits > 1 ? make_float2(1.0f, 0.0f) : end_of_row(top, sum);
+            const float inv = end.x;
             if (L.splits == 1 && writes && from == 0 && row < task.blk.rows && a.lse)
-                a.lse[head_of(task, row)] = lse_of(top, sum);
+                a.lse[head_of(task, row)] = end.y;
             if (task.n > 0) {
                 if (!wait_bounded(&sh.odone, turn & 1, &sh.abort, a.err)) break;
                 ptx::tc_fence_after();
@@ -1077,6 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.z = fmaf(g, v[x].z, acc.z), acc.w = fmaf(g, v[x].w, acc.w);
             }
             const int64_t head = head_of(k, i);
+            sum = sum_that_counts(top, sum);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, g = a.v_scale;
             *reinterpret_cast<uint2*>(dst + head * D + 4 * d4) =
                 make_uint2(float2_to_act2<F16>(acc.x * inv * g, acc.y * inv * g), float2_to_act2<F16>(acc.z * inv * g, acc.w * inv * g));

@@ -147,3 +147,40 @@ def test_logits_that_spread_widely(Q, std, e2m1, f16):
     for window, sinks in ((0, 0), (200, 3)):
         got = attend(Q, case, q, pool, 2, e2m1, f16, window=window, sinks=sinks)
         check(case, got, q, pool, 2, e2m1, f16, window=window, sinks=sinks)
+
+
+def _sized_logits(scale, f16):
+    """Queries with one element that is not zero, of 0.7 to 1.3: equal codes and scales give equal logits, others differ by more
+    than any rounding, and a row's largest is 2.1 to 7.8 times `scale`."""
+    dim, hkv, hq, rows = 64, 2, 4, 150
+    case = cache_case(layout_q="TND", q_lens=[rows, 1], seq_lens_k=[700, 333], block_size=16, sparse_count=1, sparse_mode=3, seed=3)
+    rng = np.random.default_rng(5)
+    n = case.num_blocks * case.block_size
+    k = rng.choice([-3.0, -1.0, 0.5, 1.0, 2.0, 6.0], size=(n, hkv, dim)).astype(np.float32)
+    k[..., ::16] = 6.0                                      # (every block's scale is 1)
+    pool = A.encode(k, rng.normal(size=(n, hkv, dim)).astype(np.float32), True).reshape(case.num_blocks, 16, -1)
+    q = np.zeros((case.rows, hq, dim), np.float32)
+    q[..., 5] = round_to(rng.uniform(0.7, 1.3, size=(case.rows, hq)) * rng.choice([-1, 1], size=(case.rows, hq)), f16)
+    return case, q, pool, hkv
+
+
+@pytest.mark.parametrize("scale", [2.0 ** e for e in (8, 16, 20, 22, 24)])
+@pytest.mark.parametrize("f16", [False, True])
+def test_large_logits(Q, scale, f16):
+    """Up to 2^27, of which fp32 holds every 16th: the positions of the largest share the weight."""
+    case, q, pool, hkv = _sized_logits(scale, f16)
+    out, lse, bits = attend(Q, case, q, pool, hkv, True, f16, scale=scale)
+    ref, rl, err, spread = A.paged_attention(case, q, pool, hkv, True, scale)
+    assert bits == err == 0
+    spread["qk"] = np.zeros_like(spread["qk"])              # (equal logits have equal errors)
+    assert (np.abs(out - ref) <= _bounds(ref, spread, f16, 1)).all()
+    # (the factor's three roundings, the product's and those of the way to the natural logarithm: 2^-24 each)
+    assert (np.abs(lse - rl) <= 7 * 2.0 ** -24 * np.abs(rl) + 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** e for e in (28, 30, 40, 60, 120)])
+@pytest.mark.parametrize("f16", [False, True])
+def test_logits_beyond_the_range_are_no_numbers(Q, scale, f16):
+    case, q, pool, hkv = _sized_logits(scale, f16)
+    out, lse, bits = attend(Q, case, q, pool, hkv, True, f16, scale=scale)
+    assert bits == 0 and np.isnan(out).all() and np.isnan(lse).all()
